@@ -26,7 +26,7 @@ ARM_AUTO, ARM_DECODE, ARM_TENSOR = 0, 1, 2
 _ARMS = {None: ARM_AUTO, "auto": ARM_AUTO, "decode": ARM_DECODE, "tensor": ARM_TENSOR}
 
 __all__ = ["GROUP", "pack", "gemm", "gemm_partials", "gemm_grouped", "gemm_batched", "plan_batched", "dequant_fp32", "dequant_bf16",
-           "splitk_reduce", "plan", "packed_weight_bytes", "layout_version", "read_error_word",
+           "splitk_reduce", "dispatch", "dispatch_backward", "combine", "combine_backward", "plan", "packed_weight_bytes", "layout_version", "read_error_word",
            "ERROR_WAIT_TIMEOUT", "W4A16Error"]
 
 
@@ -421,3 +421,129 @@ def splitk_reduce(ws: torch.Tensor, out: torch.Tensor | None = None) -> torch.Te
         _lib.check(_lib.lib().w4a16_splitk_reduce(ws.data_ptr(), out.data_ptr(), S, M, N,
                                                   _stream_ptr(ws.device)), "w4a16_splitk_reduce")
     return out
+
+
+def _launch(name: str, dev: torch.device, *args) -> None:
+    """One library call on ``dev``'s current torch stream."""
+    fn = getattr(_lib.lib(), name)
+    if dev.index == torch.cuda.current_device():
+        status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if status:
+        _lib.check(status, name)
+
+
+def _on_device_of(x: torch.Tensor, **others) -> None:
+    for name, t in others.items():
+        if t is not None and t.device != x.device:
+            raise ValueError(f"{name} must be on {x.device}, got {t.device}")
+
+
+_sort_bytes_cache: dict = {}
+
+
+def _sort_bytes(tokens: int, top_k: int, num_groups: int) -> int:
+    key = (tokens, top_k, num_groups)
+    need = _sort_bytes_cache.get(key)
+    if need is None:
+        nb = ctypes.c_size_t(0)
+        _lib.check(_lib.lib().w4a16_dispatch_workspace_bytes(tokens, top_k, num_groups, ctypes.byref(nb)),
+                   "w4a16_dispatch_workspace_bytes")
+        need = _sort_bytes_cache[key] = int(nb.value)
+    return need
+
+
+def dispatch(x: torch.Tensor, ids: torch.Tensor, num_groups: int):
+    """Copy every token's row to the groups (experts) its ids name, in group order.
+
+    x: bf16 [T, K]; ids: int32 or int64 [T, k], an id outside [0, num_groups)
+    drops its slot.  Returns (xs bf16 [T*k, K], m_sizes int32 [num_groups],
+    slots int32 [T, k]): xs and m_sizes are what gemm_grouped takes; slots[t, j]
+    is the row of xs that holds the copy, or ~row (negative) for a dropped slot,
+    whose row lies past the groups and holds zeros.  The order is stable: inside
+    a group rows stand by token, then slot."""
+    _need_cuda(x, "x", torch.bfloat16)
+    _need_cuda(ids, "ids")
+    if x.dim() != 2 or ids.dim() != 2 or ids.shape[0] != x.shape[0]:
+        raise ValueError("x must be [T, K] and ids [T, k]")
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise ValueError(f"ids must be int32 or int64, got {ids.dtype}")
+    _on_device_of(x, ids=ids)
+    T, K = x.shape
+    k = ids.shape[1]
+    dev = x.device
+    need = _sort_bytes(T, k, num_groups)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    xs = torch.empty((T * k, K), dtype=torch.bfloat16, device=dev)
+    m_sizes = torch.empty(num_groups, dtype=torch.int32, device=dev)
+    slots = torch.empty((T, k), dtype=torch.int32, device=dev)
+    _launch("w4a16_dispatch", dev, x.data_ptr(), ids.data_ptr(), ids.element_size(), xs.data_ptr(),
+            m_sizes.data_ptr(), slots.data_ptr(), T, k, K, num_groups,
+            ws.data_ptr() if need else None, need)
+    return xs, m_sizes, slots
+
+
+_WEIGHT_DTYPES = (torch.float32, torch.bfloat16)
+
+
+def _need_slots(rows: torch.Tensor, slots: torch.Tensor, weights, name: str):
+    _need_cuda(rows, name, torch.bfloat16)
+    _need_cuda(slots, "slots", torch.int32)
+    if rows.dim() != 2 or slots.dim() != 2 or rows.shape[0] != slots.numel():
+        raise ValueError(f"{name} must be [T*k, N] for slots [T, k]")
+    if weights is not None:
+        _need_cuda(weights, "weights")
+        if weights.dtype not in _WEIGHT_DTYPES or weights.shape != slots.shape:
+            raise ValueError("weights must be float32 or bfloat16 with the shape of slots")
+    _on_device_of(rows, slots=slots, weights=weights)
+
+
+def _combine(ys, slots, weights, name) -> torch.Tensor:
+    _need_slots(ys, slots, weights, name)
+    T, k = slots.shape
+    y = torch.empty((T, ys.shape[1]), dtype=torch.bfloat16, device=ys.device)
+    _launch("w4a16_combine", ys.device, ys.data_ptr(), slots.data_ptr(),
+            None if weights is None else weights.data_ptr(),
+            0 if weights is None else weights.element_size(), y.data_ptr(), T, k, ys.shape[1])
+    return y
+
+
+def combine(ys: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor) -> torch.Tensor:
+    """y[t] = sum over j of weights[t, j] * ys[slots[t, j]] (dropped slots left out).
+
+    ys: bf16 [T*k, N], rows in group order (the grouped product of dispatch's
+    rows); slots: from dispatch; weights: float32 or bfloat16 [T, k].  fp32 sums,
+    rounded once; returns bf16 [T, N]."""
+    if weights is None:
+        raise ValueError("weights must be a CUDA tensor")
+    return _combine(ys, slots, weights, "ys")
+
+
+def dispatch_backward(dxs: torch.Tensor, slots: torch.Tensor) -> torch.Tensor:
+    """The gradient of dispatch: dx[t] = sum over the kept slots of dxs[slots[t, j]].
+
+    dxs: bf16 [T*k, K]; returns bf16 [T, K] (fp32 sums, rounded once)."""
+    return _combine(dxs, slots, None, "dxs")
+
+
+def combine_backward(dy: torch.Tensor, ys: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor):
+    """The gradients of combine: (dys bf16 [T*k, N], dweights [T, k] in the weights' type).
+
+    dys[slots[t, j]] = weights[t, j] * dy[t], zeros in the rows of dropped slots;
+    dweights[t, j] = <dy[t], ys[slots[t, j]]>, 0 for a dropped slot."""
+    if weights is None:
+        raise ValueError("weights must be a CUDA tensor")
+    _need_cuda(dy, "dy", torch.bfloat16)
+    _need_slots(ys, slots, weights, "ys")
+    T, k = slots.shape
+    N = ys.shape[1]
+    if tuple(dy.shape) != (T, N):
+        raise ValueError("dy must be [T, N]")
+    _on_device_of(ys, dy=dy)
+    dys = torch.empty_like(ys)
+    dweights = torch.empty_like(weights)
+    _launch("w4a16_combine_backward", ys.device, dy.data_ptr(), ys.data_ptr(), slots.data_ptr(),
+            weights.data_ptr(), weights.element_size(), dys.data_ptr(), dweights.data_ptr(), T, k, N)
+    return dys, dweights

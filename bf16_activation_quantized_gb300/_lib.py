@@ -52,6 +52,10 @@ SIGNATURES = {
     "w4a16_dequant_zp_bf16": (I, [P, P, P, P, I, I, I, P]),
     "w4a16_splitk_reduce": (I, [P, P, I, I, I, P]),
     "w4a16_gemm_noalloc": (I, [P, P, P, P, I, I, I, I, P]),
+    "w4a16_dispatch_workspace_bytes": (I, [I, I, I, ctypes.POINTER(SZ)]),
+    "w4a16_dispatch": (I, [P, P, I, P, P, P, I, I, I, I, P, SZ, P]),
+    "w4a16_combine": (I, [P, P, P, I, P, I, I, I, P]),
+    "w4a16_combine_backward": (I, [P, P, P, P, I, P, P, I, I, I, P]),
 }
 
 

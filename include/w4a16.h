@@ -358,6 +358,60 @@ w4a16_status w4a16_gemm_noalloc(const w4a16_bf16 *X, const uint8_t *W_packed,
                                 const w4a16_bf16 *scales, w4a16_bf16 *Y, int M, int N, int K,
                                 int group_size, void *stream);
 
+/* Rows in group order for w4a16_gemm_grouped, and back: token t's slots
+ * f = t * top_k + j name the groups (experts) its row goes to.  With key(f) =
+ * ids[f], or num_groups when ids[f] is outside [0, num_groups),
+ *   row(f) = #{f' : key(f') < key(f)} + #{f' < f : key(f') = key(f)},
+ * i.e. a stable sort by group.  Slots with an id outside the range are
+ * dropped: they come last, in the rows that no group covers.  The pages'
+ * grouped product starts from sorted rows and device-side sizes; these calls
+ * are the library's own.  None of them reads anything on the host, so all
+ * are capturable; their results do not depend on timing.
+ *
+ * w4a16_dispatch:
+ *  X:           device bf16 [tokens][width].
+ *  ids_dev:     device int32 (id_bytes 4) or int64 (id_bytes 8) [tokens][top_k].
+ *  Xs:          device bf16 [tokens * top_k][width]: Xs[row(f)] = X[f / top_k],
+ *               zeros for a dropped slot.  Must not overlap X.
+ *  M_sizes_dev: device int32 [num_groups], written: slots of each group, the
+ *               sizes w4a16_gemm_grouped takes with M_total = tokens * top_k.
+ *  slots_dev:   device int32 [tokens][top_k], written: row(f), or ~row(f) (a
+ *               negative number) for a dropped slot.
+ *  workspace:   at least w4a16_dispatch_workspace_bytes (may be NULL when that
+ *               is 0); contents need no initialisation.
+ * X, Xs and workspace 16-byte aligned, ids and the int32 outputs to their
+ * element.  1 <= num_groups <= 1024, top_k >= 1, tokens * top_k <= 2^24,
+ * 1 <= width <= 2^20; tokens == 0 only writes the sizes.  id_bytes other than
+ * 4 and 8 is W4A16_ERR_UNSUPPORTED. */
+w4a16_status w4a16_dispatch_workspace_bytes(int tokens, int top_k, int num_groups, size_t *bytes);
+w4a16_status w4a16_dispatch(const w4a16_bf16 *X, const void *ids_dev, int id_bytes, w4a16_bf16 *Xs,
+                            int32_t *M_sizes_dev, int32_t *slots_dev, int tokens, int top_k, int width,
+                            int num_groups, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Y[t] = sum over j of w[t][j] * Ys[slots[t][j]], dropped slots (negative)
+ * left out; fp32, j ascending, rounded once to bf16.  A token with no slot
+ * left gets zeros; rows of dropped slots are never read.
+ *  Ys:          device bf16 [tokens * top_k][width], rows in group order.
+ *  slots_dev:   what w4a16_dispatch wrote (a slot at or past tokens * top_k is
+ *               treated as dropped).
+ *  weights_dev: device fp32 (weight_bytes 4) or bf16 (2) [tokens][top_k]; NULL
+ *               for weights of one, which makes the call the gradient of
+ *               w4a16_dispatch (dX from dXs).
+ *  Y:           device bf16 [tokens][width]; must not overlap Ys.
+ * Element alignment is enough; 16-byte aligned Ys and Y with width a multiple
+ * of 8 take the wide path.  Limits as for w4a16_dispatch. */
+w4a16_status w4a16_combine(const w4a16_bf16 *Ys, const int32_t *slots_dev, const void *weights_dev,
+                           int weight_bytes, w4a16_bf16 *Y, int tokens, int top_k, int width,
+                           void *stream);
+
+/* The gradients of w4a16_combine: dYs[slots[t][j]] = w[t][j] * dY[t] (the rows
+ * of dropped slots are written as zeros) and dweights[t][j] = <dY[t],
+ * Ys[slots[t][j]]> (0 for a dropped slot), summed in fp32 and written in the
+ * weights' type. */
+w4a16_status w4a16_combine_backward(const w4a16_bf16 *dY, const w4a16_bf16 *Ys, const int32_t *slots_dev,
+                                    const void *weights_dev, int weight_bytes, w4a16_bf16 *dYs,
+                                    void *dweights_dev, int tokens, int top_k, int width, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
