@@ -26,7 +26,8 @@ ARM_AUTO, ARM_DECODE, ARM_TENSOR = 0, 1, 2
 _ARMS = {None: ARM_AUTO, "auto": ARM_AUTO, "decode": ARM_DECODE, "tensor": ARM_TENSOR}
 
 __all__ = ["GROUP", "pack", "gemm", "gemm_partials", "gemm_grouped", "gemm_batched", "plan_batched", "dequant_fp32", "dequant_bf16",
-           "splitk_reduce", "dispatch", "dispatch_backward", "combine", "combine_backward", "plan", "packed_weight_bytes", "layout_version", "read_error_word",
+           "splitk_reduce", "dispatch", "dispatch_backward", "combine", "combine_backward",
+           "lora_add", "lora_add_backward", "plan", "packed_weight_bytes", "layout_version", "read_error_word",
            "ERROR_WAIT_TIMEOUT", "W4A16Error"]
 
 
@@ -547,3 +548,101 @@ def combine_backward(dy: torch.Tensor, ys: torch.Tensor, slots: torch.Tensor, we
     _launch("w4a16_combine_backward", ys.device, dy.data_ptr(), ys.data_ptr(), slots.data_ptr(),
             weights.data_ptr(), weights.element_size(), dys.data_ptr(), dweights.data_ptr(), T, k, N)
     return dys, dweights
+
+
+_lora_bytes_cache: dict = {}
+
+
+def _lora_workspace(dev, tokens: int, adapters: int, rank: int, backward: int):
+    key = (tokens, adapters, rank, backward)
+    need = _lora_bytes_cache.get(key)
+    if need is None:
+        nb = ctypes.c_size_t(0)
+        _lib.check(_lib.lib().w4a16_lora_workspace_bytes(tokens, adapters, rank, backward, ctypes.byref(nb)),
+                   "w4a16_lora_workspace_bytes")
+        need = _lora_bytes_cache[key] = int(nb.value)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    return ws, need
+
+
+def _need_lora(x, lora_a, lora_b, adapters, lora_scales):
+    """Checks of what lora_add and its gradient share: (T, L, r, N, K)."""
+    _need_cuda(x, "x", torch.bfloat16)
+    _need_cuda(lora_a, "lora_a", torch.bfloat16)
+    _need_cuda(lora_b, "lora_b", torch.bfloat16)
+    _need_cuda(adapters, "adapters")
+    _need_cuda(lora_scales, "lora_scales", torch.float32)
+    if x.dim() != 2 or lora_a.dim() != 3 or lora_b.dim() != 3:
+        raise ValueError("x must be [T, K], lora_a [L, r, K] and lora_b [L, N, r]")
+    T, K = x.shape
+    L, r, ka = lora_a.shape
+    N = lora_b.shape[1]
+    if ka != K or lora_b.shape[0] != L or lora_b.shape[2] != r:
+        raise ValueError("lora_a must be [L, r, K] and lora_b [L, N, r] for x [T, K]")
+    if adapters.dtype not in (torch.int32, torch.int64) or tuple(adapters.shape) != (T,):
+        raise ValueError("adapters must be int32 or int64 [T]")
+    if tuple(lora_scales.shape) != (L,):
+        raise ValueError("lora_scales must be float32 [L]")
+    _on_device_of(x, lora_a=lora_a, lora_b=lora_b, adapters=adapters, lora_scales=lora_scales)
+    return T, L, r, N, K
+
+
+def _need_rows(t, name, shape, x, dtype=torch.bfloat16):
+    _need_cuda(t, name, dtype)
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}")
+    _on_device_of(x, **{name: t})
+
+
+def lora_add(x: torch.Tensor, lora_a: torch.Tensor, lora_b: torch.Tensor, adapters: torch.Tensor,
+             lora_scales: torch.Tensor, base: torch.Tensor | None = None, *,
+             out: torch.Tensor | None = None, return_hidden: bool = False):
+    """y[t] = base[t] + s_a * B_a . (A_a . x[t]), a = adapters[t]: the low-rank
+    adapters of many requests at once, beside a shared projection's result.
+
+    x: bf16 [T, K]; lora_a: bf16 [L, r, K]; lora_b: bf16 [L, N, r] (r a multiple
+    of 8, at most 128); adapters: int32 or int64 [T], an id outside [0, L) leaves
+    the token as it is; lora_scales: float32 [L]; base: bf16 [T, N] (gemm's
+    result) or None for zeros.  ``out`` may be base itself.  Returns y bf16
+    [T, N], with ``return_hidden`` also A . x (float32 [T, r]), which
+    lora_add_backward takes."""
+    T, L, r, N, K = _need_lora(x, lora_a, lora_b, adapters, lora_scales)
+    dev = x.device
+    if base is not None:
+        _need_rows(base, "base", (T, N), x)
+    if out is None:
+        out = torch.empty((T, N), dtype=torch.bfloat16, device=dev)
+    else:
+        _need_rows(out, "out", (T, N), x)
+    hidden = torch.empty((T, r), dtype=torch.float32, device=dev) if return_hidden else None
+    ws, need = _lora_workspace(dev, T, L, r, 0)
+    _launch("w4a16_lora_add", dev, x.data_ptr(), lora_a.data_ptr(), lora_b.data_ptr(), adapters.data_ptr(),
+            adapters.element_size(), lora_scales.data_ptr(), None if base is None else base.data_ptr(),
+            out.data_ptr(), hidden.data_ptr() if return_hidden else None, T, L, r, N, K,
+            ws.data_ptr() if need else None, need)
+    return (out, hidden) if return_hidden else out
+
+
+def lora_add_backward(dy: torch.Tensor, x: torch.Tensor, hidden: torch.Tensor, lora_a: torch.Tensor,
+                      lora_b: torch.Tensor, adapters: torch.Tensor, lora_scales: torch.Tensor, *,
+                      dx_base: torch.Tensor | None = None):
+    """The gradients of lora_add: (dx bf16 [T, K], d_lora_a, d_lora_b), the latter
+    in the shapes and type of the adapters, zeros for an adapter without tokens.
+
+    dy: bf16 [T, N]; hidden: what lora_add returned; dx_base: bf16 [T, K], the
+    shared projection's own gradient, which the adapters' part is added to.
+    base's gradient is dy."""
+    T, L, r, N, K = _need_lora(x, lora_a, lora_b, adapters, lora_scales)
+    _need_rows(dy, "dy", (T, N), x)
+    _need_rows(hidden, "hidden", (T, r), x, torch.float32)
+    if dx_base is not None:
+        _need_rows(dx_base, "dx_base", (T, K), x)
+    dev = x.device
+    dx = torch.empty((T, K), dtype=torch.bfloat16, device=dev)
+    da, db = torch.empty_like(lora_a), torch.empty_like(lora_b)
+    ws, need = _lora_workspace(dev, T, L, r, 1)
+    _launch("w4a16_lora_add_backward", dev, dy.data_ptr(), x.data_ptr(), hidden.data_ptr(), lora_a.data_ptr(),
+            lora_b.data_ptr(), adapters.data_ptr(), adapters.element_size(), lora_scales.data_ptr(),
+            None if dx_base is None else dx_base.data_ptr(), dx.data_ptr(), da.data_ptr(), db.data_ptr(),
+            T, L, r, N, K, ws.data_ptr() if need else None, need)
+    return dx, da, db

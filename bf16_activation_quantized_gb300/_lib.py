@@ -56,6 +56,9 @@ SIGNATURES = {
     "w4a16_dispatch": (I, [P, P, I, P, P, P, I, I, I, I, P, SZ, P]),
     "w4a16_combine": (I, [P, P, P, I, P, I, I, I, P]),
     "w4a16_combine_backward": (I, [P, P, P, P, I, P, P, I, I, I, P]),
+    "w4a16_lora_workspace_bytes": (I, [I, I, I, I, ctypes.POINTER(SZ)]),
+    "w4a16_lora_add": (I, [P, P, P, P, I, P, P, P, P, I, I, I, I, I, P, SZ, P]),
+    "w4a16_lora_add_backward": (I, [P, P, P, P, P, P, I, P, P, P, P, P, I, I, I, I, I, P, SZ, P]),
 }
 
 

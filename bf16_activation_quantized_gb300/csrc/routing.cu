@@ -14,6 +14,7 @@
 #include "w4a16.h"
 #include "common.cuh"
 #include "internal.h"
+#include "launch.cuh"
 
 namespace w4a16 {
 namespace {
@@ -22,6 +23,8 @@ constexpr int kRouteThreads = 256;
 constexpr int kRouteWarps = kRouteThreads / 32;
 // Ids one CTA of the sort ranks; 8 warps of 256.
 constexpr int kSortChunk = 2048;
+// Up to this many ids the ranking CTAs count all ids themselves (one launch).
+constexpr int kSortDirect = 8 * kSortChunk;
 // Up to this many ids every CTA ranks its own token's by counting over all of
 // them (one launch); beyond, the counting sort runs first.
 constexpr int kCountIds = 4096;
@@ -138,6 +141,13 @@ __global__ void __launch_bounds__(kRouteThreads)
     }
 }
 
+// counter[key] += 1 for every lane with a key (-1: none), one shared-memory
+// atomic per distinct key of the warp: ids are often all alike (one adapter).
+__device__ __forceinline__ void count_key(int *counter, int key) {
+    const unsigned same = __match_any_sync(0xffffffffu, key);
+    if (key >= 0 && (threadIdx.x & 31) == __ffs(same) - 1) atomicAdd(&counter[key], __popc(same));
+}
+
 // The sort's first pass: counts[c][key] over the ids of chunk c.
 template <bool I64>
 __global__ void __launch_bounds__(kRouteThreads)
@@ -147,10 +157,10 @@ __global__ void __launch_bounds__(kRouteThreads)
     pdl_launch_dependents();
     for (int e = threadIdx.x; e <= groups; e += kRouteThreads) s_count[e] = 0;
     __syncthreads();
-    const int f0 = blockIdx.x * kSortChunk;
-    const int f1 = min(n, f0 + kSortChunk);
-    for (int f = f0 + threadIdx.x; f < f1; f += kRouteThreads)
-        atomicAdd(&s_count[load_key<I64>(ids, f, groups)], 1);
+    const int f0 = blockIdx.x * kSortChunk + threadIdx.x;
+    #pragma unroll
+    for (int i = 0; i < kSortChunk; i += kRouteThreads)
+        count_key(s_count, f0 + i < n ? load_key<I64>(ids, f0 + i, groups) : -1);
     __syncthreads();
     for (int e = threadIdx.x; e <= groups; e += kRouteThreads)
         counts[(long long)blockIdx.x * (groups + 1) + e] = s_count[e];
@@ -158,13 +168,16 @@ __global__ void __launch_bounds__(kRouteThreads)
 
 // The second pass: a chunk's ids in order.  Its CTA sums the chunks' counts
 // (all of them for the groups' starts, the earlier ones for its own place in
-// each group), each warp counts its 256 ids, and the warps then rank their ids
-// 32 at a time: equal ids of a step find each other by match, the lowest lane
-// moves the group's counter.
+// each group; with counts == nullptr it counts all ids itself), each warp
+// counts its 256 ids, and the warps then rank their ids 32 at a time: equal
+// ids of a step find each other by match, the lowest lane moves the group's
+// counter.  slots[f] receives the place, order[place] the id's index; either
+// may be nullptr.
 template <bool I64>
 __global__ void __launch_bounds__(kRouteThreads)
     sort_rank_kernel(const void *__restrict__ ids, const int *__restrict__ counts,
-                     int *__restrict__ sizes, int *__restrict__ slots, int n, int groups, int chunks) {
+                     int *__restrict__ sizes, int *__restrict__ slots, int *__restrict__ order, int n,
+                     int groups, int chunks) {
     __shared__ int s_total[kMaxGroups + 1];
     __shared__ int s_next[kRouteWarps][kMaxGroups + 1];
     __shared__ int s_scan[kRouteWarps];
@@ -176,12 +189,24 @@ __global__ void __launch_bounds__(kRouteThreads)
     for (int i = threadIdx.x; i < kRouteWarps * keys; i += kRouteThreads) s_next[i / keys][i % keys] = 0;
     __syncthreads();
     // s_next[0][e]: ids of key e in earlier chunks
-    const int all = chunks * keys, before = blockIdx.x * keys;
-    for (int i = threadIdx.x; i < all; i += kRouteThreads) {
-        const int v = counts[i];
-        if (v) {
-            atomicAdd(&s_total[i % keys], v);
-            if (i < before) atomicAdd(&s_next[0][i % keys], v);
+    if (counts) {
+        const int all = chunks * keys, before = blockIdx.x * keys;
+        for (int i = threadIdx.x; i < all; i += kRouteThreads) {
+            const int v = counts[i];
+            if (v) {
+                atomicAdd(&s_total[i % keys], v);
+                if (i < before) atomicAdd(&s_next[0][i % keys], v);
+            }
+        }
+    } else {
+        for (int f0 = 0; f0 < n; f0 += kSortChunk) {
+            #pragma unroll
+            for (int i = 0; i < kSortChunk; i += kRouteThreads) {
+                const int f = f0 + i + threadIdx.x;
+                const int key = f < n ? load_key<I64>(ids, f, groups) : -1;
+                count_key(s_total, key);
+                if (f0 < int(blockIdx.x) * kSortChunk) count_key(s_next[0], key);
+            }
         }
     }
     __syncthreads();
@@ -215,7 +240,7 @@ __global__ void __launch_bounds__(kRouteThreads)
     for (int i = 0; i < kSteps; ++i) {
         const int f = f0 + 32 * i + lane;
         key[i] = f < n ? load_key<I64>(ids, f, groups) : -1;
-        if (warp + 1 < kRouteWarps && key[i] >= 0) atomicAdd(&s_next[warp + 1][key[i]], 1);
+        if (warp + 1 < kRouteWarps) count_key(s_next[warp + 1], key[i]);
     }
     __syncthreads();
     for (int e = threadIdx.x; e < keys; e += kRouteThreads) {
@@ -240,7 +265,8 @@ __global__ void __launch_bounds__(kRouteThreads)
         __syncwarp();
         if (key[i] >= 0) {
             const int row = base + __popc(same & ((1u << lane) - 1));
-            slots[f0 + 32 * i + lane] = key[i] < groups ? row : ~row;
+            if (slots) slots[f0 + 32 * i + lane] = key[i] < groups ? row : ~row;
+            if (order) order[row] = f0 + 32 * i + lane;
         }
     }
 }
@@ -385,22 +411,6 @@ __global__ void __launch_bounds__(kRouteThreads)
     }
 }
 
-// A launch chained to the previous kernel on the stream: its CTAs may be
-// scheduled while that kernel drains, and wait for it before touching memory.
-template <typename... Params, typename... Args>
-cudaError_t launch_chained(void (*kernel)(Params...), dim3 grid, int threads, cudaStream_t s, Args... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, Params(args)...);
-}
-
 bool aligned(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
 int ceil_div(long long a, long long b) { return int((a + b - 1) / b); }
@@ -426,9 +436,29 @@ w4a16_status check_routing(int tokens, int top_k, int width) {
 
 w4a16_status from_cuda(cudaError_t e) { return e == cudaSuccess ? W4A16_OK : W4A16_ERR_CUDA; }
 
+size_t dispatch_sort_bytes(int n, int groups) { return n <= kCountIds ? 0 : sort_bytes(n, groups); }
+
+}  // namespace
+
 size_t sort_bytes(int n, int groups) {
-    return n <= kCountIds ? 0 : size_t(ceil_div(n, kSortChunk)) * size_t(groups + 1) * sizeof(int);
+    return n <= kSortDirect ? 0 : size_t(ceil_div(n, kSortChunk)) * size_t(groups + 1) * sizeof(int);
 }
+
+cudaError_t launch_sort(const void *ids, int id_bytes, int n, int groups, int *counts, int *sizes,
+                        int *slots, int *order, cudaStream_t s) {
+    const int chunks = ceil_div(n, kSortChunk);
+    if (n <= kSortDirect) {
+        counts = nullptr;
+    } else {
+        const cudaError_t e = launch_chained(id_bytes == 8 ? sort_count_kernel<true> : sort_count_kernel<false>,
+                                             dim3(chunks), kRouteThreads, 0, 1, s, ids, counts, n, groups);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_chained(id_bytes == 8 ? sort_rank_kernel<true> : sort_rank_kernel<false>, dim3(chunks),
+                          kRouteThreads, 0, 1, s, ids, counts, sizes, slots, order, n, groups, chunks);
+}
+
+namespace {
 
 template <bool I64>
 cudaError_t launch_dispatch(const uint16_t *X, const void *ids, uint16_t *Xs, int *sizes, int *slots,
@@ -439,17 +469,12 @@ cudaError_t launch_dispatch(const uint16_t *X, const void *ids, uint16_t *Xs, in
     if (n <= kCountIds) {
         const dim3 grid(tokens + 1, c.blocks);
         return launch_chained(vec ? dispatch_few_kernel<I64, 8> : dispatch_few_kernel<I64, 1>, grid,
-                              c.threads, s, X, ids, Xs, sizes, slots, tokens, top_k, width, groups);
+                              c.threads, 0, 1, s, X, ids, Xs, sizes, slots, tokens, top_k, width, groups);
     }
-    const int chunks = ceil_div(n, kSortChunk);
-    cudaError_t e = launch_chained(sort_count_kernel<I64>, dim3(chunks), kRouteThreads, s, ids, counts,
-                                   n, groups);
-    if (e != cudaSuccess) return e;
-    e = launch_chained(sort_rank_kernel<I64>, dim3(chunks), kRouteThreads, s, ids, counts, sizes, slots,
-                       n, groups, chunks);
+    cudaError_t e = launch_sort(ids, I64 ? 8 : 4, n, groups, counts, sizes, slots, nullptr, s);
     if (e != cudaSuccess) return e;
     return launch_chained(vec ? dispatch_copy_kernel<8> : dispatch_copy_kernel<1>,
-                          dim3(tokens, c.blocks), c.threads, s, X, slots, Xs, top_k, width);
+                          dim3(tokens, c.blocks), c.threads, 0, 1, s, X, slots, Xs, top_k, width);
 }
 
 }  // namespace
@@ -463,7 +488,7 @@ w4a16_status w4a16_dispatch_workspace_bytes(int tokens, int top_k, int num_group
     if (!bytes || num_groups < 1 || num_groups > kMaxGroups) return W4A16_ERR_INVALID_ARG;
     const w4a16_status st = check_routing(tokens, top_k, 1);
     if (st != W4A16_OK) return st;
-    *bytes = sort_bytes(tokens * top_k, num_groups);
+    *bytes = dispatch_sort_bytes(tokens * top_k, num_groups);
     return W4A16_OK;
 }
 
@@ -480,7 +505,7 @@ w4a16_status w4a16_dispatch(const w4a16_bf16 *X, const void *ids_dev, int id_byt
         if (!aligned(X, 16) || !aligned(Xs, 16) || !aligned(ids_dev, id_bytes) || !aligned(slots_dev, 4))
             return W4A16_ERR_INVALID_ARG;
     }
-    const size_t need = sort_bytes(tokens * top_k, num_groups);
+    const size_t need = dispatch_sort_bytes(tokens * top_k, num_groups);
     if (need > 0) {
         if (!workspace || workspace_bytes < need) return W4A16_ERR_WORKSPACE_TOO_SMALL;
         if (!aligned(workspace, 16)) return W4A16_ERR_INVALID_ARG;
@@ -507,7 +532,7 @@ w4a16_status w4a16_combine(const w4a16_bf16 *Ys, const int32_t *slots_dev, const
     const bool vec = width % 8 == 0 && aligned(Ys, 16) && aligned(Y, 16);
     const ColSplit c = col_split(width, vec ? 8 : 1);
     return from_cuda(launch_chained(vec ? combine_kernel<8> : combine_kernel<1>, dim3(tokens, c.blocks),
-                                    c.threads, static_cast<cudaStream_t>(stream), Ys, slots_dev,
+                                    c.threads, 0, 1, static_cast<cudaStream_t>(stream), Ys, slots_dev,
                                     weights_dev, weight_bytes, Y, top_k, tokens * top_k, width));
 }
 
@@ -525,7 +550,7 @@ w4a16_status w4a16_combine_backward(const w4a16_bf16 *dY, const w4a16_bf16 *Ys, 
     const bool vec = width % 8 == 0 && aligned(dY, 16) && aligned(Ys, 16) && aligned(dYs, 16);
     const ColSplit c = col_split(width, vec ? 8 : 1);
     return from_cuda(launch_chained(vec ? combine_backward_kernel<8> : combine_backward_kernel<1>,
-                                    dim3(tokens), c.threads, static_cast<cudaStream_t>(stream), dY, Ys,
+                                    dim3(tokens), c.threads, 0, 1, static_cast<cudaStream_t>(stream), dY, Ys,
                                     slots_dev, weights_dev, weight_bytes, dYs, dweights_dev, top_k,
                                     tokens * top_k, width));
 }

@@ -412,6 +412,56 @@ w4a16_status w4a16_combine_backward(const w4a16_bf16 *dY, const w4a16_bf16 *Ys, 
                                     const void *weights_dev, int weight_bytes, w4a16_bf16 *dYs,
                                     void *dweights_dev, int tokens, int top_k, int width, void *stream);
 
+/* Low-rank adapters of many requests beside a shared projection: token t with
+ * adapter a = adapters[t] gets
+ *   Y[t] = base[t] + lora_scales[a] * B[a] . (A[a] . X[t]);
+ * a token whose adapter id is outside [0, num_adapters) has none: Y[t] =
+ * base[t] bit for bit, and its X row is never read.  The pages have no
+ * adapters; the call is the library's own.
+ *  X:            device bf16 [tokens][K].   base, Y: device bf16 [tokens][N];
+ *                base is what w4a16_gemm wrote, or NULL for zeros; Y may be
+ *                base itself (in place), and overlaps nothing else.
+ *  A:            device bf16 [num_adapters][rank][K].
+ *  B:            device bf16 [num_adapters][N][rank].
+ *  adapters_dev: device int32 (id_bytes 4) or int64 (8) [tokens].
+ *  lora_scales:  device fp32 [num_adapters].
+ *  hidden:       device fp32 [tokens][rank] or NULL: A . X before the scale
+ *                (zeros without an adapter), kept for the gradient.
+ *  workspace:    at least w4a16_lora_workspace_bytes(..., backward 0) bytes;
+ *                contents need no initialisation.
+ * The inner A . X stays in fp32; Y is rounded once.  rank: a multiple of 8, 8 to
+ * 128 (W4A16_ERR_UNSUPPORTED otherwise); adapters of a smaller rank are padded
+ * with zeros by the caller.  1 <= num_adapters <= 1024, K a positive multiple
+ * of 128, N >= 1, 0 <= tokens <= 2^24.  X, A, B, hidden and workspace 16-byte
+ * aligned, base and Y 2-byte; with N a multiple of 8 and 16-byte aligned base
+ * and Y the rows move 16 bytes at a time.  Nothing is read on the host, so the
+ * call is capturable; the result does not depend on timing. */
+w4a16_status w4a16_lora_workspace_bytes(int tokens, int num_adapters, int rank, int backward,
+                                        size_t *bytes);
+w4a16_status w4a16_lora_add(const w4a16_bf16 *X, const w4a16_bf16 *A, const w4a16_bf16 *B,
+                            const void *adapters_dev, int id_bytes, const float *lora_scales,
+                            const w4a16_bf16 *base, w4a16_bf16 *Y, float *hidden, int tokens,
+                            int num_adapters, int rank, int N, int K, void *workspace,
+                            size_t workspace_bytes, void *stream);
+
+/* The gradients of w4a16_lora_add for dY, with g[t] = s_a B[a]^T dY[t] (fp32):
+ *   dX[t] = dX_base[t] + A[a]^T g[t]      (dX_base[t] without an adapter),
+ *   dA[a] = sum over a's tokens of g[t] X[t]^T,
+ *   dB[a] = s_a * sum over a's tokens of dY[t] hidden[t]^T;
+ * zeros for an adapter without tokens.  base's gradient is dY itself.
+ *  hidden:  what w4a16_lora_add wrote.   dX_base: device bf16 [tokens][K] (the
+ *           shared projection's own gradient) or NULL for zeros; dX may be
+ *           dX_base itself, and overlaps nothing else.
+ *  dA, dB:  device bf16, the shapes of A and B, 16-byte aligned, written fully.
+ *  workspace: w4a16_lora_workspace_bytes(..., backward 1).
+ * All sums are fp32 in a fixed order; each output is rounded once. */
+w4a16_status w4a16_lora_add_backward(const w4a16_bf16 *dY, const w4a16_bf16 *X, const float *hidden,
+                                     const w4a16_bf16 *A, const w4a16_bf16 *B, const void *adapters_dev,
+                                     int id_bytes, const float *lora_scales, const w4a16_bf16 *dX_base,
+                                     w4a16_bf16 *dX, w4a16_bf16 *dA, w4a16_bf16 *dB, int tokens,
+                                     int num_adapters, int rank, int N, int K, void *workspace,
+                                     size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
