@@ -106,12 +106,11 @@ cudaError_t launch_tensor(const TensorPlan &p, const uint16_t *X, const uint8_t 
 cudaError_t launch_reduce(const float *ws, uint16_t *Y, int splits, long long count, bool pdl,
                           cudaStream_t s);
 
-// Stable counting sort of n ids by group (routing.cu): sizes[groups]; slots[f] =
-// place of id f, ~place where the id lies outside [0, groups) (those come last);
-// order[place] = f.  slots and order may be nullptr.  counts: sort_bytes of
-// scratch.  ids: int32 (id_bytes 4) or int64 (8).  n >= 1.
+// Stable counting sort of n >= 1 ids by group (routing.cu): sizes[groups];
+// order[place] = the id's index, ids outside [0, groups) last.  counts:
+// sort_bytes of scratch.  ids: int32 (id_bytes 4) or int64 (8).
 size_t sort_bytes(int n, int groups);
-cudaError_t launch_sort(const void *ids, int id_bytes, int n, int groups, int *counts, int *sizes,
-                        int *slots, int *order, cudaStream_t s);
+cudaError_t launch_sort(const void *ids, int id_bytes, int n, int groups, int *counts, int *sizes, int *order,
+                        cudaStream_t s);
 
 }  // namespace w4a16

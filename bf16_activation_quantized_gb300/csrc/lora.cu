@@ -853,7 +853,7 @@ w4a16_status w4a16_lora_add(const w4a16_bf16 *X, const w4a16_bf16 *A, const w4a1
     char *ws = static_cast<char *>(workspace);
     int *order = reinterpret_cast<int *>(ws + w.order), *sizes = reinterpret_cast<int *>(ws + w.sizes);
     cudaError_t e = launch_sort(adapters_dev, id_bytes, tokens, num_adapters,
-                                reinterpret_cast<int *>(ws + w.counts), sizes, nullptr, order, s);
+                                reinterpret_cast<int *>(ws + w.counts), sizes, order, s);
     if (e != cudaSuccess) return W4A16_ERR_CUDA;
     p.order = order, p.sizes = sizes;
     return from_cuda(launch_lora<false>(p, false, tile_cluster(tokens, rank, sms), s));
@@ -888,7 +888,7 @@ w4a16_status w4a16_lora_add_backward(const w4a16_bf16 *dY, const w4a16_bf16 *X, 
     int *order = reinterpret_cast<int *>(ws + w.order), *sizes = reinterpret_cast<int *>(ws + w.sizes);
     float *g = reinterpret_cast<float *>(ws + w.g);
     cudaError_t e = launch_sort(adapters_dev, id_bytes, tokens, num_adapters,
-                                reinterpret_cast<int *>(ws + w.counts), sizes, nullptr, order, s);
+                                reinterpret_cast<int *>(ws + w.counts), sizes, order, s);
     if (e != cudaSuccess) return W4A16_ERR_CUDA;
     LoraArgs p = {};
     p.x = dY, p.w1 = B, p.w2 = A, p.ids = adapters_dev, p.id_bytes = id_bytes, p.scale = lora_scales;

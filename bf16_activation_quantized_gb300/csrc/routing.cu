@@ -21,13 +21,18 @@ namespace {
 
 constexpr int kRouteThreads = 256;
 constexpr int kRouteWarps = kRouteThreads / 32;
-// Ids one CTA of the sort ranks; 8 warps of 256.
-constexpr int kSortChunk = 2048;
-// Up to this many ids the ranking CTAs count all ids themselves (one launch).
-constexpr int kSortDirect = 8 * kSortChunk;
-// Up to this many ids every CTA ranks its own token's by counting over all of
-// them (one launch); beyond, the counting sort runs first.
-constexpr int kCountIds = 4096;
+// Ids one CTA ranks at most.
+constexpr int kRankIds = 256;
+// Up to this many ids every ranking CTA counts all ids itself (one launch).
+// Beyond, a counting kernel cuts them into at most kMaxChunks chunks first.
+constexpr int kDirectIds = 16384;
+constexpr int kMinChunk = 2048;
+constexpr int kMaxChunks = 64;
+constexpr int kMaxTopK = 256;
+// Rows a thread of the combine kernels holds at once.  Four rather than eight
+// lets twice the warps reside: 8192 tokens of 8 rows of 4096 columns took 91.5
+// against 101.5 us, the gradients of 4096 of 4 rows of 5120 59.7 against 86.4.
+constexpr int kSlotsAtOnce = 4;
 constexpr int kMaxSlots = 1 << 24;     // tokens * top_k
 
 template <bool I64>
@@ -72,202 +77,147 @@ struct Cols<1> {
     __device__ __forceinline__ void pack(const float (&f)[1]) { v = f32_to_bf16_rn(f[0]); }
 };
 
-// Few ids: one launch.  CTA (t, c) copies its columns of token t to the rows
-// of the token's slots, which it finds by counting: with c(f) = key(f) * 2^13
-// + f, row(f) is the number of ids with a smaller c.  CTA (tokens, 0) counts
-// the group sizes.
-template <bool I64, int VEC>
-__global__ void __launch_bounds__(kRouteThreads)
-    dispatch_few_kernel(const uint16_t *__restrict__ X, const void *__restrict__ ids,
-                        uint16_t *__restrict__ Xs, int *__restrict__ sizes, int *__restrict__ slots,
-                        int tokens, int top_k, int width, int groups) {
-    __shared__ int s_place[8];
-    __shared__ int s_sizes[kMaxGroups];
-    pdl_wait();
-    pdl_launch_dependents();
-    const int n = tokens * top_k;
-    const int t = blockIdx.x;
-    if (t == tokens) {
-        if (blockIdx.y != 0) return;
-        for (int e = threadIdx.x; e < groups; e += blockDim.x) s_sizes[e] = 0;
-        __syncthreads();
-        for (int f = threadIdx.x; f < n; f += blockDim.x) {
-            const int key = load_key<I64>(ids, f, groups);
-            if (key < groups) atomicAdd(&s_sizes[key], 1);
-        }
-        __syncthreads();
-        for (int e = threadIdx.x; e < groups; e += blockDim.x) sizes[e] = s_sizes[e];
-        return;
-    }
-    const int col = (blockIdx.y * blockDim.x + threadIdx.x) * VEC;
-    Cols<VEC> x;
-    x.zero();
-    if (col < width) x.load(X + (long long)t * width + col);
-    for (int j0 = 0; j0 < top_k; j0 += 8) {
-        const int jn = min(8, top_k - j0);
-        int mine[8], below[8];
-        #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int f = t * top_k + j0 + j;
-            mine[j] = j < jn ? (load_key<I64>(ids, f, groups) << 13) + f : 0;
-            below[j] = 0;
-        }
-        if (threadIdx.x < 8) s_place[threadIdx.x] = 0;
-        __syncthreads();
-        for (int f = threadIdx.x; f < n; f += blockDim.x) {
-            const int c = (load_key<I64>(ids, f, groups) << 13) + f;
-            #pragma unroll
-            for (int j = 0; j < 8; ++j) below[j] += c < mine[j] ? 1 : 0;
-        }
-        #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int sum = __reduce_add_sync(0xffffffffu, below[j]);
-            if ((threadIdx.x & 31) == j && j < jn && sum) atomicAdd(&s_place[j], sum);
-        }
-        __syncthreads();
-        #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            if (j >= jn) break;
-            const int row = s_place[j];
-            const bool kept = (mine[j] >> 13) < groups;
-            if (blockIdx.y == 0 && threadIdx.x == 0) slots[t * top_k + j0 + j] = kept ? row : ~row;
-            if (col < width) {
-                Cols<VEC> v = x;
-                if (!kept) v.zero();
-                v.store(Xs + (long long)row * width + col);
-            }
-        }
-        __syncthreads();
-    }
+// The ids' chunks of the counting kernel (n > kDirectIds).
+__host__ __device__ __forceinline__ int chunk_ids(int n) {
+    const int even = (n + kMaxChunks - 1) / kMaxChunks;
+    return even > kMinChunk ? even : kMinChunk;
 }
 
-// counter[key] += 1 for every lane with a key (-1: none), one shared-memory
-// atomic per distinct key of the warp: ids are often all alike (one adapter).
-__device__ __forceinline__ void count_key(int *counter, int key) {
-    const unsigned same = __match_any_sync(0xffffffffu, key);
-    if (key >= 0 && (threadIdx.x & 31) == __ffs(same) - 1) atomicAdd(&counter[key], __popc(same));
-}
-
-// The sort's first pass: counts[c][key] over the ids of chunk c.
+// counts[c][key] over the ids of chunk c.
 template <bool I64>
-__global__ void __launch_bounds__(kRouteThreads)
+__global__ void __launch_bounds__(4 * kRouteThreads)
     sort_count_kernel(const void *__restrict__ ids, int *__restrict__ counts, int n, int groups) {
     __shared__ int s_count[kMaxGroups + 1];
     pdl_wait();
     pdl_launch_dependents();
-    for (int e = threadIdx.x; e <= groups; e += kRouteThreads) s_count[e] = 0;
+    for (int e = threadIdx.x; e <= groups; e += blockDim.x) s_count[e] = 0;
     __syncthreads();
-    const int f0 = blockIdx.x * kSortChunk + threadIdx.x;
-    #pragma unroll
-    for (int i = 0; i < kSortChunk; i += kRouteThreads)
-        count_key(s_count, f0 + i < n ? load_key<I64>(ids, f0 + i, groups) : -1);
+    const int chunk = chunk_ids(n);
+    const int f0 = blockIdx.x * chunk, f1 = min(n, f0 + chunk);
+    #pragma unroll 4
+    for (int f = f0 + threadIdx.x; f < f1; f += blockDim.x)
+        atomicAdd(&s_count[load_key<I64>(ids, f, groups)], 1);
     __syncthreads();
-    for (int e = threadIdx.x; e <= groups; e += kRouteThreads)
+    for (int e = threadIdx.x; e <= groups; e += blockDim.x)
         counts[(long long)blockIdx.x * (groups + 1) + e] = s_count[e];
 }
 
-// The second pass: a chunk's ids in order.  Its CTA sums the chunks' counts
-// (all of them for the groups' starts, the earlier ones for its own place in
-// each group; with counts == nullptr it counts all ids itself), each warp
-// counts its 256 ids, and the warps then rank their ids 32 at a time: equal
-// ids of a step find each other by match, the lowest lane moves the group's
-// counter.  slots[f] receives the place, order[place] the id's index; either
-// may be nullptr.
+struct RankSmem {
+    int total[kMaxGroups + 1];   // ids of each key
+    int next[kMaxGroups + 1];    // place of the key's next id
+    int scan[kRouteWarps];
+    int place[kRankIds];         // ~place for a dropped id
+};
+
+// The CTA (kRouteThreads threads) gets the places of ids f0, f0 + 1, ... ready:
+// next[key] = ids with a smaller key + ids of this key before f0.  counts (of
+// the counting kernel, or nullptr: all ids are counted here) makes a CTA read
+// only its own chunk's ids.  Block 0 writes the sizes.
 template <bool I64>
-__global__ void __launch_bounds__(kRouteThreads)
-    sort_rank_kernel(const void *__restrict__ ids, const int *__restrict__ counts,
-                     int *__restrict__ sizes, int *__restrict__ slots, int *__restrict__ order, int n,
-                     int groups, int chunks) {
-    __shared__ int s_total[kMaxGroups + 1];
-    __shared__ int s_next[kRouteWarps][kMaxGroups + 1];
-    __shared__ int s_scan[kRouteWarps];
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int keys = groups + 1;
-    pdl_wait();
-    pdl_launch_dependents();
-    for (int e = threadIdx.x; e < keys; e += kRouteThreads) s_total[e] = 0;
-    for (int i = threadIdx.x; i < kRouteWarps * keys; i += kRouteThreads) s_next[i / keys][i % keys] = 0;
+__device__ void rank_prepare(RankSmem &sm, const void *ids, const int *counts, int *sizes, int n, int groups,
+                             int f0) {
+    const int keys = groups + 1, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    for (int e = threadIdx.x; e < keys; e += kRouteThreads) sm.total[e] = sm.next[e] = 0;
     __syncthreads();
-    // s_next[0][e]: ids of key e in earlier chunks
     if (counts) {
-        const int all = chunks * keys, before = blockIdx.x * keys;
-        for (int i = threadIdx.x; i < all; i += kRouteThreads) {
-            const int v = counts[i];
-            if (v) {
-                atomicAdd(&s_total[i % keys], v);
-                if (i < before) atomicAdd(&s_next[0][i % keys], v);
+        const int chunk = chunk_ids(n), chunks = (n + chunk - 1) / chunk, mine = f0 / chunk;
+        for (int e = threadIdx.x; e < keys; e += kRouteThreads) {
+            int total = 0, before = 0;
+            #pragma unroll 16
+            for (int c = 0; c < chunks; ++c) {
+                const int v = counts[c * keys + e];
+                total += v;
+                before += c < mine ? v : 0;
             }
+            sm.total[e] = total;
+            sm.next[e] = before;
         }
+        __syncthreads();
+        #pragma unroll 4
+        for (int f = mine * chunk + threadIdx.x; f < f0; f += kRouteThreads)
+            atomicAdd(&sm.next[load_key<I64>(ids, f, groups)], 1);
     } else {
-        for (int f0 = 0; f0 < n; f0 += kSortChunk) {
-            #pragma unroll
-            for (int i = 0; i < kSortChunk; i += kRouteThreads) {
-                const int f = f0 + i + threadIdx.x;
-                const int key = f < n ? load_key<I64>(ids, f, groups) : -1;
-                count_key(s_total, key);
-                if (f0 < int(blockIdx.x) * kSortChunk) count_key(s_next[0], key);
-            }
+        #pragma unroll 4
+        for (int f = threadIdx.x; f < n; f += kRouteThreads) {
+            const int key = load_key<I64>(ids, f, groups);
+            atomicAdd(&sm.total[key], 1);
+            if (f < f0) atomicAdd(&sm.next[key], 1);
         }
     }
     __syncthreads();
-    if (blockIdx.x == 0)
-        for (int e = threadIdx.x; e < groups; e += kRouteThreads) sizes[e] = s_total[e];
-    // the groups' starts: exclusive scan over the keys, a run of them per thread
+    if (blockIdx.x == 0 && blockIdx.y == 0)
+        for (int e = threadIdx.x; e < groups; e += kRouteThreads) sizes[e] = sm.total[e];
+    // exclusive scan over the keys, a run of them per thread
     const int per = (keys + kRouteThreads - 1) / kRouteThreads;
     const int e0 = min(keys, int(threadIdx.x) * per), e1 = min(keys, e0 + per);
-    int mine = 0;
-    for (int e = e0; e < e1; ++e) mine += s_total[e];
-    int scan = mine;
+    int sum = 0;
+    for (int e = e0; e < e1; ++e) sum += sm.total[e];
+    int scan = sum;
     #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
         const int v = __shfl_up_sync(0xffffffffu, scan, d);
         if (lane >= d) scan += v;
     }
-    if (lane == 31) s_scan[warp] = scan;
+    if (lane == 31) sm.scan[warp] = scan;
     __syncthreads();
-    int start = scan - mine;
-    for (int w = 0; w < warp; ++w) start += s_scan[w];
+    int start = scan - sum;
+    for (int w = 0; w < warp; ++w) start += sm.scan[w];
     for (int e = e0; e < e1; ++e) {
-        s_next[0][e] += start;
-        start += s_total[e];
+        sm.next[e] += start;
+        start += sm.total[e];
     }
     __syncthreads();
-    // each warp's own counts, in the row after its own; then their prefix
-    const int f0 = blockIdx.x * kSortChunk + warp * (kSortChunk / kRouteWarps);
-    constexpr int kSteps = kSortChunk / kRouteWarps / 32;
-    int key[kSteps];
-    #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-        const int f = f0 + 32 * i + lane;
-        key[i] = f < n ? load_key<I64>(ids, f, groups) : -1;
-        if (warp + 1 < kRouteWarps) count_key(s_next[warp + 1], key[i]);
+}
+
+// Places of the next m <= kRankIds ids from f0, into place[].  A warp takes 32
+// of them; equal keys find each other through one ballot per key bit (a
+// match.any over mostly different keys took several times as long), and the
+// warps move the keys' counters one after the other.
+template <bool I64>
+__device__ void rank_ids(RankSmem &sm, const void *ids, int groups, int f0, int m) {
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int i = threadIdx.x;
+    const int key = i < m ? load_key<I64>(ids, f0 + i, groups) : -1;
+    unsigned same = __ballot_sync(0xffffffffu, key >= 0);
+    if (key < 0) same = ~same;
+    for (int bit = 0; groups >> bit; ++bit) {
+        const bool set = (key >> bit) & 1;
+        const unsigned with = __ballot_sync(0xffffffffu, set);
+        same &= set ? with : ~with;
     }
-    __syncthreads();
-    for (int e = threadIdx.x; e < keys; e += kRouteThreads) {
-        int run = s_next[0][e];
-        #pragma unroll
-        for (int w = 1; w < kRouteWarps; ++w) {
-            run += s_next[w][e];
-            s_next[w][e] = run;
-        }
-    }
-    __syncthreads();
-    #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-        const unsigned same = __match_any_sync(0xffffffffu, key[i]);
-        const int lead = __ffs(same) - 1;
-        int base = 0;
-        if (key[i] >= 0 && lane == lead) {
-            base = s_next[warp][key[i]];
-            s_next[warp][key[i]] = base + __popc(same);
-        }
-        base = __shfl_sync(0xffffffffu, base, lead);
-        __syncwarp();
-        if (key[i] >= 0) {
+    const int lead = __ffs(same) - 1;
+    for (int w = 0; w < (m + 31) / 32; ++w) {
+        if (w == warp) {
+            int base = 0;
+            if (key >= 0 && lane == lead) {
+                base = sm.next[key];
+                sm.next[key] = base + __popc(same);
+            }
+            base = __shfl_sync(0xffffffffu, base, lead);
             const int row = base + __popc(same & ((1u << lane) - 1));
-            if (slots) slots[f0 + 32 * i + lane] = key[i] < groups ? row : ~row;
-            if (order) order[row] = f0 + 32 * i + lane;
+            if (key >= 0) sm.place[i] = key < groups ? row : ~row;
         }
+        __syncthreads();
+    }
+}
+
+// The sort alone: slots[f] = place (~place for a dropped id), order[place] = f;
+// either may be nullptr.
+template <bool I64>
+__global__ void __launch_bounds__(kRouteThreads)
+    sort_rank_kernel(const void *__restrict__ ids, const int *__restrict__ counts,
+                     int *__restrict__ sizes, int *__restrict__ slots, int *__restrict__ order, int n,
+                     int groups) {
+    __shared__ RankSmem sm;
+    pdl_wait();
+    pdl_launch_dependents();
+    const int f0 = blockIdx.x * kRankIds, m = min(kRankIds, n - f0);
+    rank_prepare<I64>(sm, ids, counts, sizes, n, groups, f0);
+    rank_ids<I64>(sm, ids, groups, f0, m);
+    if (int(threadIdx.x) < m) {
+        const int place = sm.place[threadIdx.x];
+        if (slots) slots[f0 + threadIdx.x] = place;
+        if (order) order[place < 0 ? ~place : place] = f0 + threadIdx.x;
     }
 }
 
@@ -293,6 +243,43 @@ __global__ void __launch_bounds__(kRouteThreads)
     }
 }
 
+// CTA (b, c) ranks the slots of tokens [b * per, ...) and copies their columns
+// of part c: each row is read once and written top_k times.
+template <bool I64, int VEC>
+__global__ void __launch_bounds__(kRouteThreads)
+    dispatch_few_kernel(const uint16_t *__restrict__ X, const void *__restrict__ ids,
+                        uint16_t *__restrict__ Xs, int *__restrict__ sizes, int *__restrict__ slots,
+                        int tokens, int top_k, int width, int groups, int per) {
+    __shared__ RankSmem sm;
+    pdl_wait();
+    pdl_launch_dependents();
+    const int t0 = blockIdx.x * per, t1 = min(tokens, t0 + per);
+    const int items = (width + VEC - 1) / VEC;
+    const int c0 = int((long long)items * blockIdx.y / gridDim.y);
+    const int c1 = int((long long)items * (blockIdx.y + 1) / gridDim.y);
+    const int f0 = t0 * top_k, m = (t1 - t0) * top_k;
+    rank_prepare<I64>(sm, ids, nullptr, sizes, tokens * top_k, groups, f0);
+    rank_ids<I64>(sm, ids, groups, f0, m);
+    if (blockIdx.y == 0 && int(threadIdx.x) < m) slots[f0 + threadIdx.x] = sm.place[threadIdx.x];
+    int t = t0, c = c0 + threadIdx.x;
+    while (t < t1) {
+        while (c >= c1 && t < t1) c -= c1 - c0, ++t;
+        if (t >= t1) break;
+        const long long col = (long long)c * VEC;
+        Cols<VEC> x;
+        x.load(X + (long long)t * width + col);
+        const int *mine = sm.place + (t - t0) * top_k;
+        #pragma unroll 8
+        for (int j = 0; j < top_k; ++j) {
+            const int place = mine[j];
+            Cols<VEC> v = x;
+            if (place < 0) v.zero();
+            v.store(Xs + (long long)(place < 0 ? ~place : place) * width + col);
+        }
+        c += kRouteThreads;
+    }
+}
+
 __device__ __forceinline__ float load_weight(const void *w, int bytes, long long i) {
     return bytes == 4 ? static_cast<const float *>(w)[i]
                       : bf16_bits_to_f32(static_cast<const uint16_t *>(w)[i]);
@@ -315,18 +302,18 @@ __global__ void __launch_bounds__(kRouteThreads)
     float sum[VEC];
     #pragma unroll
     for (int i = 0; i < VEC; ++i) sum[i] = 0.f;
-    for (int j0 = 0; j0 < top_k; j0 += 8) {
-        Cols<VEC> v[8];
-        bool kept[8];
+    for (int j0 = 0; j0 < top_k; j0 += kSlotsAtOnce) {
+        Cols<VEC> v[kSlotsAtOnce];
+        bool kept[kSlotsAtOnce];
         #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < kSlotsAtOnce; ++j) {
             const int slot = j0 + j < top_k ? slots[f0 + j0 + j] : -1;
             kept[j] = slot >= 0 && slot < rows;
             v[j].zero();
             if (kept[j]) v[j].load(Ys + (long long)slot * width + col);
         }
         #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < kSlotsAtOnce; ++j) {
             if (!kept[j]) continue;
             const float w = weights ? load_weight(weights, weight_bytes, f0 + j0 + j) : 1.f;
             float f[VEC];
@@ -341,34 +328,34 @@ __global__ void __launch_bounds__(kRouteThreads)
 }
 
 // One CTA per token: dys[row] = w * dy (zeros for a dropped slot's own row),
-// dw[t][j] = <dy[t], ys[row]> in fp32.  Eight slots a pass.
+// dw[t][j] = <dy[t], ys[row]> in fp32.  kSlotsAtOnce slots a pass.
 template <int VEC>
 __global__ void __launch_bounds__(kRouteThreads)
     combine_backward_kernel(const uint16_t *__restrict__ dY, const uint16_t *__restrict__ Ys,
                             const int *__restrict__ slots, const void *__restrict__ weights,
                             int weight_bytes, uint16_t *__restrict__ dYs, void *__restrict__ dW,
                             int top_k, int rows, int width) {
-    __shared__ float s_dot[8][kRouteWarps];
+    __shared__ float s_dot[kSlotsAtOnce][kRouteWarps];
     pdl_wait();
     pdl_launch_dependents();
     const int t = blockIdx.x, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int warps = blockDim.x / 32;
-    for (int j0 = 0; j0 < top_k; j0 += 8) {
-        const int jn = min(8, top_k - j0);
+    for (int j0 = 0; j0 < top_k; j0 += kSlotsAtOnce) {
+        const int jn = min(kSlotsAtOnce, top_k - j0);
         const long long f0 = (long long)t * top_k + j0;
-        int slot[8];
-        float w[8], dot[8];
+        int slot[kSlotsAtOnce];
+        float w[kSlotsAtOnce], dot[kSlotsAtOnce];
         #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < kSlotsAtOnce; ++j) {
             slot[j] = j < jn ? slots[f0 + j] : 0;
             w[j] = j < jn ? load_weight(weights, weight_bytes, f0 + j) : 0.f;
             dot[j] = 0.f;
         }
         for (int col = threadIdx.x * VEC; col < width; col += blockDim.x * VEC) {
-            Cols<VEC> g, v[8];
+            Cols<VEC> g, v[kSlotsAtOnce];
             g.load(dY + (long long)t * width + col);
             #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < kSlotsAtOnce; ++j) {
                 v[j].zero();
                 if (j < jn && slot[j] >= 0 && slot[j] < rows)
                     v[j].load(Ys + (long long)slot[j] * width + col);
@@ -376,7 +363,7 @@ __global__ void __launch_bounds__(kRouteThreads)
             float gf[VEC];
             g.unpack(gf);
             #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < kSlotsAtOnce; ++j) {
                 if (j >= jn) break;
                 const bool kept = slot[j] >= 0 && slot[j] < rows;
                 const int row = slot[j] >= 0 ? slot[j] : ~slot[j];
@@ -393,7 +380,7 @@ __global__ void __launch_bounds__(kRouteThreads)
             }
         }
         #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < kSlotsAtOnce; ++j) {
             #pragma unroll
             for (int d = 16; d > 0; d /= 2) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], d);
             if (lane == 0) s_dot[j][warp] = dot[j];
@@ -428,7 +415,7 @@ ColSplit col_split(int width, int vec) {
 }
 
 w4a16_status check_routing(int tokens, int top_k, int width) {
-    if (tokens < 0 || top_k < 1 || width < 1 || width > (1 << 20)) return W4A16_ERR_INVALID_ARG;
+    if (tokens < 0 || top_k < 1 || top_k > kMaxTopK || width < 1 || width > (1 << 20)) return W4A16_ERR_INVALID_ARG;
     if ((long long)tokens * top_k > kMaxSlots) return W4A16_ERR_INVALID_ARG;
     if (ceil_div(width, kRouteThreads) > 65535) return W4A16_ERR_INVALID_ARG;
     return W4A16_OK;
@@ -436,48 +423,66 @@ w4a16_status check_routing(int tokens, int top_k, int width) {
 
 w4a16_status from_cuda(cudaError_t e) { return e == cudaSuccess ? W4A16_OK : W4A16_ERR_CUDA; }
 
-size_t dispatch_sort_bytes(int n, int groups) { return n <= kCountIds ? 0 : sort_bytes(n, groups); }
-
 }  // namespace
 
 size_t sort_bytes(int n, int groups) {
-    return n <= kSortDirect ? 0 : size_t(ceil_div(n, kSortChunk)) * size_t(groups + 1) * sizeof(int);
-}
-
-cudaError_t launch_sort(const void *ids, int id_bytes, int n, int groups, int *counts, int *sizes,
-                        int *slots, int *order, cudaStream_t s) {
-    const int chunks = ceil_div(n, kSortChunk);
-    if (n <= kSortDirect) {
-        counts = nullptr;
-    } else {
-        const cudaError_t e = launch_chained(id_bytes == 8 ? sort_count_kernel<true> : sort_count_kernel<false>,
-                                             dim3(chunks), kRouteThreads, 0, 1, s, ids, counts, n, groups);
-        if (e != cudaSuccess) return e;
-    }
-    return launch_chained(id_bytes == 8 ? sort_rank_kernel<true> : sort_rank_kernel<false>, dim3(chunks),
-                          kRouteThreads, 0, 1, s, ids, counts, sizes, slots, order, n, groups, chunks);
+    return n <= kDirectIds ? 0 : size_t(ceil_div(n, chunk_ids(n))) * size_t(groups + 1) * sizeof(int);
 }
 
 namespace {
 
 template <bool I64>
-cudaError_t launch_dispatch(const uint16_t *X, const void *ids, uint16_t *Xs, int *sizes, int *slots,
-                            int tokens, int top_k, int width, int groups, int *counts, cudaStream_t s) {
-    const bool vec = width % 8 == 0;
-    const ColSplit c = col_split(width, vec ? 8 : 1);
-    const int n = tokens * top_k;
-    if (n <= kCountIds) {
-        const dim3 grid(tokens + 1, c.blocks);
-        return launch_chained(vec ? dispatch_few_kernel<I64, 8> : dispatch_few_kernel<I64, 1>, grid,
-                              c.threads, 0, 1, s, X, ids, Xs, sizes, slots, tokens, top_k, width, groups);
+cudaError_t launch_sort_ids(const void *ids, int n, int groups, int *counts, int *sizes, int *slots,
+                            int *order, cudaStream_t s) {
+    if (n <= kDirectIds) {
+        counts = nullptr;
+    } else {
+        const cudaError_t e = launch_chained(sort_count_kernel<I64>, dim3(ceil_div(n, chunk_ids(n))),
+                                             4 * kRouteThreads, 0, 1, s, ids, counts, n, groups);
+        if (e != cudaSuccess) return e;
     }
-    cudaError_t e = launch_sort(ids, I64 ? 8 : 4, n, groups, counts, sizes, slots, nullptr, s);
-    if (e != cudaSuccess) return e;
-    return launch_chained(vec ? dispatch_copy_kernel<8> : dispatch_copy_kernel<1>,
-                          dim3(tokens, c.blocks), c.threads, 0, 1, s, X, slots, Xs, top_k, width);
+    return launch_chained(sort_rank_kernel<I64>, dim3(ceil_div(n, kRankIds)), kRouteThreads, 0, 1, s, ids,
+                          counts, sizes, slots, order, n, groups);
+}
+
+// Few ids: one launch, whose CTAs each count all ids, so there are only about
+// three per SM (1322 tokens of 2 ids and 2560 columns: 5.7 us, with six per SM
+// 8.0), each with at most kRankIds ids; few tokens also split their columns.
+// Many ids: the sort, then a copy in token order, whose writes advance through
+// every group together (8192 tokens of 8 ids and 4096 columns: 100 us; 911
+// CTAs that rank and copy nine tokens each took 111).
+template <bool I64>
+cudaError_t launch_dispatch(const uint16_t *X, const void *ids, uint16_t *Xs, int *sizes, int *slots,
+                            int tokens, int top_k, int width, int groups, int *counts, int sms,
+                            cudaStream_t s) {
+    const int n = tokens * top_k;
+    const bool vec = width % 8 == 0;
+    if (n > kDirectIds) {
+        const cudaError_t e = launch_sort_ids<I64>(ids, n, groups, counts, sizes, slots, nullptr, s);
+        if (e != cudaSuccess) return e;
+        const ColSplit c = col_split(width, vec ? 8 : 1);
+        return launch_chained(vec ? dispatch_copy_kernel<8> : dispatch_copy_kernel<1>,
+                              dim3(tokens, c.blocks), c.threads, 0, 1, s, X, slots, Xs, top_k, width);
+    }
+    const int items = ceil_div(width, vec ? 8 : 1);
+    int per = ceil_div(tokens, 3 * sms);
+    if (per * top_k > kRankIds) per = kRankIds / top_k;
+    if (per < 1) per = 1;
+    const int blocks = tokens > 0 ? ceil_div(tokens, per) : 1;
+    int parts = ceil_div(2 * sms, blocks);
+    if (parts > ceil_div(items, kRouteThreads)) parts = ceil_div(items, kRouteThreads);
+    return launch_chained(vec ? dispatch_few_kernel<I64, 8> : dispatch_few_kernel<I64, 1>, dim3(blocks, parts),
+                          kRouteThreads, 0, 1, s, X, ids, Xs, sizes, slots, tokens, top_k, width, groups, per);
 }
 
 }  // namespace
+
+cudaError_t launch_sort(const void *ids, int id_bytes, int n, int groups, int *counts, int *sizes, int *order,
+                        cudaStream_t s) {
+    return id_bytes == 8 ? launch_sort_ids<true>(ids, n, groups, counts, sizes, nullptr, order, s)
+                         : launch_sort_ids<false>(ids, n, groups, counts, sizes, nullptr, order, s);
+}
+
 }  // namespace w4a16
 
 using namespace w4a16;
@@ -488,7 +493,7 @@ w4a16_status w4a16_dispatch_workspace_bytes(int tokens, int top_k, int num_group
     if (!bytes || num_groups < 1 || num_groups > kMaxGroups) return W4A16_ERR_INVALID_ARG;
     const w4a16_status st = check_routing(tokens, top_k, 1);
     if (st != W4A16_OK) return st;
-    *bytes = dispatch_sort_bytes(tokens * top_k, num_groups);
+    *bytes = sort_bytes(tokens * top_k, num_groups);
     return W4A16_OK;
 }
 
@@ -505,17 +510,19 @@ w4a16_status w4a16_dispatch(const w4a16_bf16 *X, const void *ids_dev, int id_byt
         if (!aligned(X, 16) || !aligned(Xs, 16) || !aligned(ids_dev, id_bytes) || !aligned(slots_dev, 4))
             return W4A16_ERR_INVALID_ARG;
     }
-    const size_t need = dispatch_sort_bytes(tokens * top_k, num_groups);
+    const size_t need = sort_bytes(tokens * top_k, num_groups);
     if (need > 0) {
         if (!workspace || workspace_bytes < need) return W4A16_ERR_WORKSPACE_TOO_SMALL;
         if (!aligned(workspace, 16)) return W4A16_ERR_INVALID_ARG;
     }
+    int sms = 0;
+    if (device_sm_count(&sms) != 0 || sms < 1) return W4A16_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     int *counts = static_cast<int *>(workspace);
     return from_cuda(id_bytes == 8 ? launch_dispatch<true>(X, ids_dev, Xs, M_sizes_dev, slots_dev, tokens,
-                                                           top_k, width, num_groups, counts, s)
+                                                           top_k, width, num_groups, counts, sms, s)
                                    : launch_dispatch<false>(X, ids_dev, Xs, M_sizes_dev, slots_dev, tokens,
-                                                            top_k, width, num_groups, counts, s));
+                                                            top_k, width, num_groups, counts, sms, s));
 }
 
 w4a16_status w4a16_combine(const w4a16_bf16 *Ys, const int32_t *slots_dev, const void *weights_dev,
@@ -549,8 +556,7 @@ w4a16_status w4a16_combine_backward(const w4a16_bf16 *dY, const w4a16_bf16 *Ys, 
         return W4A16_ERR_INVALID_ARG;
     const bool vec = width % 8 == 0 && aligned(dY, 16) && aligned(Ys, 16) && aligned(dYs, 16);
     const ColSplit c = col_split(width, vec ? 8 : 1);
-    return from_cuda(launch_chained(vec ? combine_backward_kernel<8> : combine_backward_kernel<1>,
-                                    dim3(tokens), c.threads, 0, 1, static_cast<cudaStream_t>(stream), dY, Ys,
+    return from_cuda(launch_chained(vec ? combine_backward_kernel<8> : combine_backward_kernel<1>, dim3(tokens), c.threads, 0, 1, static_cast<cudaStream_t>(stream), dY, Ys,
                                     slots_dev, weights_dev, weight_bytes, dYs, dweights_dev, top_k,
                                     tokens * top_k, width));
 }
