@@ -37,6 +37,24 @@ __device__ __forceinline__ uint64_t tc_sdesc_sw128(uint32_t smem_addr) {
     return d;
 }
 
+// Instruction descriptor bits: the operand lies along M (or N) instead of K.
+constexpr uint32_t kTcAMajorM = 1u << 15;
+constexpr uint32_t kTcBMajorN = 1u << 16;
+
+// Shared-memory matrix descriptor for an operand that lies along M or N, with
+// the 128-byte swizzle: each K index is a row of 128 bytes (64 elements of M or
+// N), 8-row atoms of 1024 bytes.  `block_bytes`: from one block of 64 elements
+// to the next.  Advancing K by 16 adds two atoms (2048 bytes) to the address.
+__device__ __forceinline__ uint64_t tc_sdesc_sw128_mn(uint32_t smem_addr, uint32_t block_bytes) {
+    uint64_t d = 0;
+    d |= uint64_t((smem_addr >> 4) & 0x3FFF);
+    d |= uint64_t(block_bytes >> 4) << 16;           // leading byte offset: next 64 elements
+    d |= uint64_t(1024 >> 4) << 32;                  // stride byte offset: next 8 of K
+    d |= uint64_t(1) << 46;
+    d |= uint64_t(2) << 61;
+    return d;
+}
+
 __device__ __forceinline__ void tc_alloc(uint32_t dst_smem, uint32_t ncols) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem),
                  "r"(ncols)
@@ -67,6 +85,16 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+// D[tmem] (+)= A[smem] . B[smem]^T ; accumulate when `acc` is nonzero.
+__device__ __forceinline__ void tc_mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                          uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(acc)
         : "memory");
 }
 
@@ -106,6 +134,16 @@ __device__ __forceinline__ void tc_ld_32x32b_x32(uint32_t taddr, uint32_t (&v)[3
           "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
           "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]),
           "=r"(v[31])
+        : "r"(taddr)
+        : "memory");
+}
+
+// 32 lanes x 32 bits, 8 repetitions: thread i gets columns c .. c+7 of lane i.
+__device__ __forceinline__ void tc_ld_32x32b_x8(uint32_t taddr, uint32_t (&v)[8]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+          "=r"(v[7])
         : "r"(taddr)
         : "memory");
 }
