@@ -25,6 +25,7 @@ struct LoraArgs {
     uint16_t *y;             // [tokens][out]
     float *hidden;           // [tokens][r]: forward h, written (or nullptr); gradient: read
     uint16_t *pg, *ph;       // gradient: g and s h of the sorted tokens, written (see plane_pitch)
+    float *partial;          // partial sums of h (many tokens)
     int *err;
     int id_bytes, tokens, adapters, rank, in, out;
     int vec_in, vec_out;     // rows of x / of base and y start on 16 bytes
@@ -258,7 +259,8 @@ cudaError_t allow_smem(size_t bytes) {
     return e;
 }
 
-// lora_tensor.cu: the tcgen05 kernels.  ranks up to 64 for the first.
+// lora_tensor.cu.  lora_partial_bytes: the workspace of the partial sums.
+size_t lora_partial_bytes(int tokens, int adapters, int rank);
 cudaError_t launch_lora_tensor(const LoraArgs &p, bool trans, int sms, cudaStream_t s);
 cudaError_t launch_wgrad(const WgradArgs &p, int adapters, int sms, cudaStream_t s);
 

@@ -1,20 +1,23 @@
 // lora_tensor.cu -- adapters for many tokens, on the tensor cores.
 //
-// lora_tensor_kernel: y = base + s B (A x) and, with the weights read along the
-// other axis, dx = dx_base + A^T (s B^T dy), for tiles of 128 sorted tokens of one
-// adapter (the formulas and the precision: lora.cu).  A cluster of CTAs owns a
-// tile and splits first the input columns, then the output columns.  Four
-// producer warps gather the rows of X (then of base) and the weights with
-// 16-byte asynchronous copies into a ring of 128-column stages, in the 128-byte
-// swizzle that tcgen05.mma reads; one warp issues the MMAs.  D1 = X W1^T (128
-// tokens x rank, in TMEM) is read once, its partial sums are added over the
-// cluster in CTA order, each CTA a share of the rows, and the result returns to
-// every CTA as two bf16 planes, the A operand of D2 = H W2^T.  Eight epilogue
-// warps add base in shared memory and store whole 128-byte pieces of rows.
+// lora_down_kernel: partial sums of h = A x (or, with the weight read along its
+// other axis, of B^T dy); lora_up_kernel: y = base + s B h (dx = dx_base + A^T g).
+// The formulas and the precision are in lora.cu.  Both walk tiles of 128 sorted
+// tokens of one adapter in steps of 128 columns; the (tile, column step) pairs
+// are cut into one even run per CTA, one CTA per SM, so every SM moves the same
+// bytes whatever the adapters' sizes.  A run that covers part of a tile's input
+// columns leaves its sum in a workspace slot (tile + CTA, unique along the
+// walk), and the second kernel adds a tile's slots in CTA order.
 //
-// What bounds it: HBM.  At rank 64 the legacy MMA pipe would need two thirds of
-// the memory's time and left a 64-token mma.sync version of this kernel waiting
-// on MMA latency (78 us for 4096 tokens, 8192 x 8192); tcgen05 needs a tenth.
+// In each CTA four producer warps gather rows of X (of base) and the weights
+// with 16-byte asynchronous copies into a ring of stages, in the 128-byte
+// swizzle that tcgen05.mma reads; one warp issues the MMAs; the other warps
+// empty TMEM, and in the second kernel add base in shared memory and store
+// whole 128-byte pieces of rows.  h enters the second product as two bf16 planes.
+//
+// What bounds them: HBM.  At rank 64 the legacy MMA pipe would need two thirds of
+// the memory's time and left a 64-token mma.sync version waiting on MMA latency
+// (78 us for 4096 tokens, 8192 x 8192); tcgen05 needs a tenth.
 //
 // lora_wgrad_kernel: dA = g^T X and dB = s dY^T h.  The tokens are the MMA's K;
 // rows of X or dY lie along M, rows of g or s h along N, as they come, so nothing
@@ -40,363 +43,505 @@ constexpr int kCols = 128;             // columns of a stage: two blocks of 64
 constexpr int kBlock = kTile * 128;    // bytes of 128 rows x 64 columns
 constexpr int kSmemMax = 226 * 1024;
 constexpr int kTmemCols = 512;
-constexpr int kTmemD1 = 256;           // D2's two buffers take columns 0..255
+constexpr int kMaxRuns = 160;          // CTAs of the two products: one per SM (152)
 
 __device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kEpiThreads) : "memory"); }
 
 // Byte of piece p (16 bytes) of row `row` in a block of 128-byte rows.
 __device__ __forceinline__ uint32_t sw128(int row, int p) { return uint32_t(row * 128 + ((p ^ (row & 7)) << 4)); }
 
-template <int RP>
-struct TensorShape {
-    static constexpr int kW = 2 * RP * 128 > kBlock ? 2 * RP * 128 : kBlock;   // weights of a stage
+// The walk: unit u = tile * per + step; CTA b of n takes units [run(b), run(b + 1)).
+__device__ __forceinline__ long long run_start(long long units, int n, int b) { return units * b / n; }
+// The CTA whose run holds unit u.
+__device__ __forceinline__ int run_owner(long long units, int n, long long u) {
+    return int(((u + 1) * n - 1) / units);
+}
+struct Walk {
+    long long units;
+    int per, ctas;          // steps of a tile; CTAs with a run
+    long long u0, u1;       // this CTA's run
+};
+__device__ __forceinline__ Walk make_walk(int tiles, int per, int b) {
+    Walk w;
+    w.units = (long long)tiles * per;
+    w.per = per;
+    w.ctas = int(w.units < gridDim.x ? w.units : gridDim.x);
+    w.u0 = w.u1 = 0;
+    if (b < w.ctas) w.u0 = run_start(w.units, w.ctas, b), w.u1 = run_start(w.units, w.ctas, b + 1);
+    return w;
+}
+
+// One warp: tiles of all adapters and, past those, of the tokens without one.
+__device__ void count_tiles(const LoraArgs &p, int *out) {
+    const int lane = threadIdx.x & 31;
+    int tiles = 0, rows = 0;
+    for (int a = lane; a < p.adapters; a += 32) {
+        const int size = p.sizes[a];
+        tiles += (size + kTile - 1) / kTile;
+        rows += size;
+    }
+    tiles = __reduce_add_sync(0xffffffffu, tiles);
+    rows = __reduce_add_sync(0xffffffffu, rows);
+    if (lane == 0) out[0] = tiles, out[1] = (p.tokens - rows + kTile - 1) / kTile;
+}
+
+// Two tiles' tokens, filled by the first producer warp ahead of the others.
+struct TileSlots {
+    int rows[2][kTile];
+    int info[2][3];         // adapter (-1: none), tokens, first place in the sort
+};
+
+// Bytes of a stage's weights: along, rows of RP ranks x 128 columns; across, rows
+// of 128 columns x RP ranks (in blocks of 64 elements either way).
+constexpr int weight_bytes(int RP, bool along) { return along ? 2 * RP * 128 : (RP + 63) / 64 * kBlock; }
+constexpr int plane_bytes(int RP) { return (RP + 63) / 64 * kBlock; }
+
+// A producer thread's part of a stage: column piece `piece` of rows row0 + 8 j,
+// whose swizzled places are 1024 bytes apart.
+struct Producer {
+    int piece, row0;
+    uint32_t dst;
+};
+__device__ __forceinline__ Producer make_producer() {
+    Producer t;
+    const int pt = threadIdx.x - kEpiThreads;
+    t.piece = pt % 16;
+    t.row0 = pt / 16;
+    t.dst = (t.piece / 8) * kBlock + sw128(t.row0, t.piece % 8);
+    return t;
+}
+
+// Rows of x or base: src[j] points at this thread's piece of column 0 of its
+// row; columns past n are zeros.
+__device__ __forceinline__ void stage_rows(const Producer &t, unsigned char *xs, const uint16_t *const (&src)[kTile / 8],
+                                           int rows, long long col, int n, int vec) {
+    const uint32_t dst = smem_u32(xs) + t.dst;
+    const bool in = 8 * t.piece < n;
+    if (vec) {
+        const long long at = in ? col : 0;
+        #pragma unroll
+        for (int j = 0; j < kTile / 8; ++j)
+            if (j < rows) cp_async16z(dst + 1024 * j, src[j] + at, in);
+    } else {
+        #pragma unroll
+        for (int j = 0; j < kTile / 8; ++j)
+            if (j < rows) *reinterpret_cast<uint4 *>(xs + t.dst + 1024 * j) = load_cols8(src[j] + col, n - 8 * t.piece, 0);
+    }
+}
+
+// Weights of a stage.  [r][cols]: this thread's piece of the ranks row0 + 8 j;
+// [cols][r]: pieces of the columns' rows.  Past the last rank or column: zeros
+// (they are summed over).
+template <int RP, bool ALONG>
+__device__ __forceinline__ void stage_weights(const Producer &t, uint32_t ws, const uint16_t *w, int r, int cols, int col,
+                                              int n) {
+    if (ALONG) {
+        const bool in = 8 * t.piece < n;
+        const uint32_t dst = ws + (t.piece / 8) * (RP * 128) + sw128(t.row0, t.piece % 8);
+        const uint16_t *src = w + (long long)t.row0 * cols + (in ? col + 8 * t.piece : 0);
+        const long long step = 8LL * cols;
+        #pragma unroll
+        for (int j = 0; j < RP / 8; ++j) {
+            const bool ok = in && 8 * j < r;             // r is a multiple of 8
+            cp_async16z(dst + 1024 * j, ok ? src : w, ok);
+            src += step;
+        }
+    } else {
+        constexpr int kPieces = RP / 8, kRows = kProducers / kPieces;   // rows in one go
+        const int pt = threadIdx.x - kEpiThreads, q = pt % kPieces, row0 = pt / kPieces;
+        const uint16_t *src = w + (long long)(col + row0) * r + 8 * q;
+        #pragma unroll
+        for (int j = 0; j < kCols / kRows; ++j) {
+            const int row = row0 + kRows * j;
+            const bool ok = row < n && 8 * q < r;
+            cp_async16z(ws + (q / 8) * kBlock + sw128(row, q % 8), ok ? src + kRows * j * r : w, ok);
+        }
+    }
+}
+
+// The first producer warp fills segment seg's slot; everyone waits for it.
+__device__ __forceinline__ bool tile_ready(const LoraArgs &p, TileSlots &ts, int seg, int tile, uint32_t tfull,
+                                           uint32_t tempty, bool writer, volatile int *abort_flag) {
+    const int slot = seg & 1;
+    bool ok = true;
+    if (writer) {
+        if (seg >= 2) ok = mbar_wait(tempty + 8 * slot, ((seg >> 1) - 1) & 1, abort_flag, p.err);
+        if (__all_sync(0xffffffffu, ok)) {
+            find_tile_sorted<kTile>(p, tile, ts.rows[slot], ts.info[slot]);
+            __syncwarp();
+            if ((threadIdx.x & 31) == 0) mbar_arrive(tfull + 8 * slot);
+        }
+    }
+    ok = ok && mbar_wait(tfull + 8 * slot, (seg >> 1) & 1, abort_flag, p.err);
+    return __all_sync(0xffffffffu, ok);
+}
+__device__ __forceinline__ void tile_done(int seg, uint32_t tempty) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(tempty + 8 * (seg & 1));
+}
+
+// ------------------------------------------------------------ first product
+template <int RP, bool TRANS>
+struct DownShape {
+    static constexpr int kW = weight_bytes(RP, !TRANS);
     static constexpr int kStage = 2 * kBlock + kW;
-    static constexpr int PS = RP + 4;                       // floats of a row of partial sums
-    static constexpr int kH = 2 * kBlock;                   // the planes of h
-    static constexpr int kFixed = kH + kTile * PS * 4;
-    static constexpr int kStages = (kSmemMax - 1024 - kFixed) / kStage;
-    static constexpr int kSmem = kStages * kStage + kFixed + 1024;
-    static_assert(RP <= 64 && kStages >= 2, "the ring does not fit");
+    static constexpr int kStages = (kSmemMax - 1024) / kStage < 6 ? (kSmemMax - 1024) / kStage : 6;
+    static constexpr int kSmem = kStages * kStage + 1024;
+    static_assert(kStages >= 3, "the ring does not fit");
 };
 
 template <int RP, bool TRANS>
-__global__ void __launch_bounds__(kThreads, 1) lora_tensor_kernel(const LoraArgs p) {
-    using S = TensorShape<RP>;
-    constexpr int NS = S::kStages, PS = S::PS, KS = RP / 16;
+__global__ void __launch_bounds__(kThreads, 1) lora_down_kernel(const LoraArgs p) {
+    using S = DownShape<RP, TRANS>;
+    constexpr int NS = S::kStages;
     extern __shared__ unsigned char s_raw[];
-    __shared__ uint64_t s_bar[3 * NS + 8];
-    __shared__ int s_rows[kTile];
-    __shared__ int s_tile[3];
+    __shared__ uint64_t s_bar[2 * NS + 8];
+    __shared__ TileSlots s_tiles;
+    __shared__ int s_count[2];
     __shared__ int s_abort;
     __shared__ uint32_t s_tmem;
     unsigned char *s_mem = s_raw + (-smem_u32(s_raw) & 1023);
-    unsigned char *s_hi = s_mem + NS * S::kStage, *s_lo = s_hi + kBlock;
-    float *s_part = reinterpret_cast<float *>(s_lo + kBlock);            // [kTile][PS]
-
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int C = cluster_size(), c = cluster_rank();
-    const uint32_t full = smem_u32(s_bar), empty1 = full + 8 * NS, empty2 = empty1 + 8 * NS;
-    const uint32_t d1full = empty2 + 8 * NS, ready = d1full + 8, hready = ready + 8;
-    const uint32_t dfull = hready + 8, dempty = dfull + 16, done = dempty + 16;
+    const uint32_t full = smem_u32(s_bar), empty = full + 8 * NS, tfull = empty + 8 * NS, tempty = tfull + 16;
+    const uint32_t dfull = tempty + 16, dempty = dfull + 16;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < NS; ++i) {
-            mbar_init(full + 8 * i, kProducers);
-            mbar_init(empty1 + 8 * i, 1);            // first product: the MMAs have read it
-            mbar_init(empty2 + 8 * i, kEpiWarps);    // second: the epilogue has
+        for (int i = 0; i < NS; ++i) mbar_init(full + 8 * i, kProducers), mbar_init(empty + 8 * i, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(tfull + 8 * i, 1), mbar_init(tempty + 8 * i, kThreads / 32);
+            mbar_init(dfull + 8 * i, 1), mbar_init(dempty + 8 * i, kEpiWarps);
         }
-        mbar_init(d1full, 1);
-        mbar_init(ready, C);
-        mbar_init(hready, C);
-        for (int i = 0; i < 2; ++i) mbar_init(dfull + 8 * i, 1), mbar_init(dempty + 8 * i, kEpiWarps);
-        mbar_init(done, 1);
         s_abort = 0;
         fence_barrier_init();
     }
-    pdl_wait();
-    if (warp == 0) find_tile_sorted<kTile>(p, blockIdx.x / C, s_rows, s_tile);
-    __syncthreads();
-    const int adapter = s_tile[0], count = s_tile[1];
-    if (count == 0) return;                          // the same in every CTA of the cluster
-    if (adapter < 0) {
-        // no adapter: y = base, h = 0
-        if (p.y != p.base) {
-            const int items = (p.out + 7) / 8;
-            const int i0 = int((long long)items * c / C), i1 = int((long long)items * (c + 1) / C);
-            for (int r = warp; r < count; r += kThreads / 32) {
-                const long long at = (long long)s_rows[r] * p.out;
-                #pragma unroll 8
-                for (int i = i0 + lane; i < i1; i += 32) {
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (p.base) v = load_cols8(p.base + at + 8 * i, p.out - 8 * i, p.vec_out);
-                    store_cols8(p.y + at + 8 * i, p.out - 8 * i, p.vec_out, v);
-                }
-            }
-        }
-        if (!TRANS && p.hidden && c == 0)
-            for (int i = threadIdx.x; i < count * p.rank; i += kThreads)
-                p.hidden[(long long)s_rows[i / p.rank] * p.rank + i % p.rank] = 0.f;
-        return;
-    }
-    // Dependents may start only when every CTA holds its TMEM, so that an
-    // allocation never waits for a kernel that waits for this one.
     if (warp == kMmaWarp) {
         tc_alloc(smem_u32(&s_tmem), kTmemCols);
         tc_relinquish();
     }
+    pdl_wait();
+    if (warp == 0) count_tiles(p, s_count);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     pdl_launch_dependents();
-    if (C > 1) cluster_arrive();                     // barriers initialised
     const uint32_t tmem = s_tmem;
-
     const int r = p.rank;
-    const int kin = (p.in + kCols - 1) / kCols, kout = (p.out + kCols - 1) / kCols;
-    const int in0 = int((long long)kin * c / C), out0 = int((long long)kout * c / C);
-    const int nin = int((long long)kin * (c + 1) / C) - in0;
-    const int nall = nin + int((long long)kout * (c + 1) / C) - out0;
+    const Walk w = make_walk(s_count[0], (p.in + kCols - 1) / kCols, blockIdx.x);
     volatile int *abort_flag = &s_abort;
 
-    if (warp >= kEpiWarps && warp < kMmaWarp) {
-        // ---- producers: the stages of both products in order
-        const uint16_t *w1 = p.w1 + (long long)adapter * r * p.in, *w2 = p.w2 + (long long)adapter * r * p.out;
-        const int pt = threadIdx.x - kEpiThreads, piece = pt % 16, row0 = pt / 16;
-        constexpr int kRows = kProducers / 16;       // rows in one go
-        for (int i = 0; i < nall; ++i) {
-            const int s = i % NS;
-            bool ok = true;
-            if (i >= NS) {
-                const int before = i - NS, use = before / NS;
-                if (before < nin) {
-                    ok = mbar_wait(empty1 + 8 * s, use & 1, abort_flag, p.err);
-                } else {
-                    const int uses1 = (nin - s + NS - 1) / NS;   // of this stage, in the first product
-                    ok = mbar_wait(empty2 + 8 * s, (use - uses1) & 1, abort_flag, p.err);
-                }
-            }
-            if (!__all_sync(0xffffffffu, ok)) break;
-            const bool first = i < nin;
-            const int cols = first ? p.in : p.out, col = (first ? in0 + i : out0 + i - nin) * kCols;
-            const int n = min(kCols, cols - col), vec = first ? p.vec_in : p.vec_out;
-            const uint16_t *rows = first ? p.x : p.base, *w = first ? w1 : w2;
-            const uint32_t xs = smem_u32(s_mem) + s * S::kStage, ws = xs + 2 * kBlock;
-            const bool in = 8 * piece < n;
-            if (rows) {
-                // columns past the end are zeros: they are summed over in the first product
-                const uint32_t dst = xs + (piece / 8) * kBlock;
-                if (vec) {
-                    #pragma unroll 4
-                    for (int k = row0; k < count; k += kRows) {
-                        const uint16_t *src = rows + (long long)s_rows[k] * cols + (in ? col + 8 * piece : 0);
-                        cp_async16z(dst + sw128(k, piece % 8), src, in);
-                    }
-                } else {
-                    for (int k = row0; k < count; k += kRows) {
-                        const uint4 v = load_cols8(rows + (long long)s_rows[k] * cols + col + 8 * piece,
-                                                   n - 8 * piece, 0);
-                        *reinterpret_cast<uint4 *>(s_mem + s * S::kStage + (piece / 8) * kBlock +
-                                                   sw128(k, piece % 8)) = v;
-                    }
-                }
-            }
-            if (first != TRANS) {
-                // [r][cols]: rows of ranks.  Ranks past r are summed over in the second product.
-                const int rows_w = first ? r : RP;
-                const uint32_t dst = ws + (piece / 8) * (RP * 128);
-                #pragma unroll 4
-                for (int k = row0; k < rows_w; k += kRows) {
-                    const bool ok_w = in && k < r;
-                    cp_async16z(dst + sw128(k, piece % 8), ok_w ? w + (long long)k * cols + col + 8 * piece : w, ok_w);
-                }
-            } else {
-                // [cols][r]: rows of columns, zeros past the end and past r
-                #pragma unroll 4
-                for (int k = pt; k < kCols * (RP / 8); k += kProducers) {
-                    const int row = k / (RP / 8), q = k % (RP / 8);
-                    const bool ok_w = row < n && 8 * q < r;
-                    cp_async16z(ws + sw128(row, q), ok_w ? w + (long long)(col + row) * r + 8 * q : w, ok_w);
-                }
-            }
-            stage_done(full + 8 * s, vec);
-        }
-        cp_async_wait_all();
-    } else if (warp == kMmaWarp) {
-        // ---- MMA issuer
-        constexpr uint32_t idesc1 = tc_idesc_bf16(kTile, RP) | (TRANS ? kTcBMajorN : 0);
-        constexpr uint32_t idesc2 = tc_idesc_bf16(kTile, kCols) | (TRANS ? kTcBMajorN : 0);
-        bool ok = true;
-        for (int i = 0; i < nin && ok; ++i) {
-            const int s = i % NS;
-            ok = __all_sync(0xffffffffu, mbar_wait(full + 8 * s, (i / NS) & 1, abort_flag, p.err));
-            if (!ok) break;
-            fence_proxy_async();
-            tc_fence_after();
-            const uint32_t xs = smem_u32(s_mem) + s * S::kStage, ws = xs + 2 * kBlock;
-            if (elect_one()) {
-                #pragma unroll
-                for (int k = 0; k < kCols / 16; ++k) {
-                    const uint64_t a = tc_sdesc_sw128(xs + (k / 4) * kBlock + (k % 4) * 32);
-                    const uint64_t b = TRANS ? tc_sdesc_sw128_mn(ws + k * 2048, kBlock)
-                                             : tc_sdesc_sw128(ws + (k / 4) * (RP * 128) + (k % 4) * 32);
-                    tc_mma_ss(tmem + kTmemD1, a, b, idesc1, i > 0 || k > 0);
-                }
-                tc_commit(empty1 + 8 * s);
-            }
-            __syncwarp();
-        }
-        if (ok && nin > 0 && elect_one()) tc_commit(d1full);
-        __syncwarp();
-        ok = ok && __all_sync(0xffffffffu, mbar_wait_cluster(hready, 0, abort_flag, p.err));
-        for (int i = nin; i < nall && ok; ++i) {
-            const int s = i % NS, j = i - nin, buf = j & 1;
-            ok = j < 2 || mbar_wait(dempty + 8 * buf, ((j >> 1) - 1) & 1, abort_flag, p.err);
-            ok = ok && mbar_wait(full + 8 * s, (i / NS) & 1, abort_flag, p.err);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            fence_proxy_async();
-            tc_fence_after();
-            const uint32_t ws = smem_u32(s_mem) + s * S::kStage + 2 * kBlock;
-            if (elect_one()) {
-                #pragma unroll
-                for (int part = 0; part < 2; ++part)     // the low plane first
-                    #pragma unroll
-                    for (int k = 0; k < KS; ++k) {
-                        const uint64_t a = tc_sdesc_sw128(smem_u32(part ? s_hi : s_lo) + k * 32);
-                        const uint64_t b = TRANS ? tc_sdesc_sw128_mn(ws + k * 2048, RP * 128)
-                                                 : tc_sdesc_sw128(ws + k * 32);
-                        tc_mma_ss(tmem + buf * kCols, a, b, idesc2, part > 0 || k > 0);
-                    }
-                tc_commit(dfull + 8 * buf);
-            }
-            __syncwarp();
-        }
-        // every MMA issued has completed before TMEM is freed
-        if (elect_one()) tc_commit(done);
-        __syncwarp();
-        drain_wait(done, 0);
-        if (!ok) drain_wait(hready, 0);              // the others may still read this CTA's sums
-    } else {
-        // ---- h: D1's rows to shared memory, summed over the cluster
-        const int sub = warp % 4, half = warp / 4;
-        const int my_row = 32 * sub + lane;
-        const uint32_t lanes = tmem + (uint32_t(32 * sub) << 16);
-        const float scale = p.scale[adapter];
-        bool bad = false;
-        if (nin > 0) {
-            bad = !__all_sync(0xffffffffu, mbar_wait(d1full, 0, abort_flag, p.err));
-            tc_fence_after();
-        }
-        #pragma unroll
-        for (int k = 0; k < RP / 16; ++k) {
-            const int rank = half * (RP / 2) + 8 * k;
-            uint32_t v[8];
-            if (nin > 0 && !bad) {
-                tc_ld_32x32b_x8(lanes + kTmemD1 + rank, v);
-                tc_wait_ld();
-            } else {
-                #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = bad ? 0x7fffffffu : 0u;
-            }
-            float *d = s_part + my_row * PS + rank;
-            *reinterpret_cast<uint4 *>(d) = make_uint4(v[0], v[1], v[2], v[3]);
-            *reinterpret_cast<uint4 *>(d + 4) = make_uint4(v[4], v[5], v[6], v[7]);
-        }
-        epi_sync();
-        if (C > 1) {
-            cluster_wait();
-            if (threadIdx.x < C) mbar_arrive_cluster(ready, threadIdx.x);
-            bad |= !mbar_wait_cluster(ready, 0, abort_flag, p.err);
-        }
-        // this CTA's share of the rows; the planes go to every CTA
-        constexpr int kPieces = RP / 8;
-        const int r0 = kTile / C * c;
-        for (int i = threadIdx.x; i < kTile / C * kPieces; i += kEpiThreads) {
-            const int row = r0 + i / kPieces, rank = 8 * (i % kPieces);
-            const float *d = s_part + row * PS + rank;
-            float v[8];
+    int i = 0, seg = 0;                              // steps and tiles so far
+    for (long long u = w.u0; u < w.u1; ++seg) {
+        const int tile = int(u / w.per), k0 = int(u - (long long)tile * w.per);
+        const int n_steps = int(w.u1 - u < w.per - k0 ? w.u1 - u : w.per - k0);
+        u += n_steps;
+        if (!tile_ready(p, s_tiles, seg, tile, tfull, tempty, warp == kEpiWarps, abort_flag)) break;
+        const int *rows = s_tiles.rows[seg & 1];
+        const int adapter = s_tiles.info[seg & 1][0], count = s_tiles.info[seg & 1][1];
+        if (warp >= kEpiWarps && warp < kMmaWarp) {
+            const Producer t = make_producer();
+            const uint16_t *wt = p.w1 + (long long)adapter * r * p.in, *src[kTile / 8];
+            const int mine = (count - t.row0 + 7) / 8;
             #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = 0.f;
-            for (int k = 0; k < C; ++k) {
-                const float4 a = C > 1 ? ld_cluster4(d, k) : *reinterpret_cast<const float4 *>(d);
-                const float4 b = C > 1 ? ld_cluster4(d + 4, k) : *reinterpret_cast<const float4 *>(d + 4);
-                v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
-                v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+            for (int j = 0; j < kTile / 8; ++j)
+                src[j] = p.x + (long long)rows[j < mine ? t.row0 + 8 * j : 0] * p.in + 8 * t.piece;
+            for (int k = 0; k < n_steps; ++k, ++i) {
+                const int s = i % NS, col = (k0 + k) * kCols, n = min(kCols, p.in - col);
+                const bool ok = i < NS || mbar_wait(empty + 8 * s, (i / NS - 1) & 1, abort_flag, p.err);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                unsigned char *xs = s_mem + s * S::kStage;
+                stage_rows(t, xs, src, mine, col, n, p.vec_in);
+                stage_weights<RP, !TRANS>(t, smem_u32(xs) + 2 * kBlock, wt, r, p.in, col, n);
+                stage_done(full + 8 * s, p.vec_in);
             }
-            const bool token = row < count, in = rank < r;
-            if (bad) {
-                #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = __int_as_float(0x7fffffff);
-            }
-            if (!TRANS && p.hidden && token && in) {
-                float4 *h = reinterpret_cast<float4 *>(p.hidden + (long long)s_rows[row] * r + rank);
-                h[0] = make_float4(v[0], v[1], v[2], v[3]);
-                h[1] = make_float4(v[4], v[5], v[6], v[7]);
-            }
-            // ranks past r are zeros: what was staged for them is not
-            uint4 hi = make_uint4(0, 0, 0, 0), lo = hi;
-            if (in) {
-                split2(scale * v[0], scale * v[1], hi.x, lo.x), split2(scale * v[2], scale * v[3], hi.y, lo.y);
-                split2(scale * v[4], scale * v[5], hi.z, lo.z), split2(scale * v[6], scale * v[7], hi.w, lo.w);
-            }
-            for (int k = 0; k < C; ++k) {
-                const int to = (c + k) % C;
-                st_cluster16(smem_u32(s_hi) + sw128(row, i % kPieces), to, hi);
-                st_cluster16(smem_u32(s_lo) + sw128(row, i % kPieces), to, lo);
-            }
-            if (TRANS && token) {
-                // g and s h of the sorted token, for the weight gradients
-                const long long at = (long long)(s_tile[2] + row) * (plane_pitch(RP) / 2) + rank;
-                *reinterpret_cast<uint4 *>(p.pg + at) = hi, *reinterpret_cast<uint4 *>(p.pg + at + RP) = lo;
-                hi = lo = make_uint4(0, 0, 0, 0);
-                if (in) {
-                    const float4 *h = reinterpret_cast<const float4 *>(p.hidden + (long long)s_rows[row] * r + rank);
-                    const float4 a = h[0], b = h[1];
-                    split2(scale * a.x, scale * a.y, hi.x, lo.x), split2(scale * a.z, scale * a.w, hi.y, lo.y);
-                    split2(scale * b.x, scale * b.y, hi.z, lo.z), split2(scale * b.z, scale * b.w, hi.w, lo.w);
-                }
-                *reinterpret_cast<uint4 *>(p.ph + at) = hi, *reinterpret_cast<uint4 *>(p.ph + at + RP) = lo;
-            }
-        }
-        fence_proxy_async();
-        epi_sync();
-        if (threadIdx.x < C) mbar_arrive_cluster(hready, threadIdx.x);
-
-        // ---- y: this warp's 32 rows x 64 columns of every stage
-        for (int i = nin; i < nall; ++i) {
-            const int s = i % NS, j = i - nin, buf = j & 1;
-            const int col = (out0 + j) * kCols + 64 * half;
-            unsigned char *bs = s_mem + s * S::kStage + half * kBlock;
-            bool ok = mbar_wait(full + 8 * s, (i / NS) & 1, abort_flag, p.err);
-            ok = ok && mbar_wait(dfull + 8 * buf, (j >> 1) & 1, abort_flag, p.err);
-            bad |= !__all_sync(0xffffffffu, ok);
-            tc_fence_after();
-            if (col < p.out && 32 * sub < count) {
-                uint32_t acc[2][32];
-                tc_ld_32x32b_x32(lanes + buf * kCols + 64 * half, acc[0]);
-                tc_ld_32x32b_x32(lanes + buf * kCols + 64 * half + 32, acc[1]);
-                tc_wait_ld();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(dempty + 8 * buf);
-                #pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    uint4 *at = reinterpret_cast<uint4 *>(bs + sw128(my_row, q));
-                    uint4 b = make_uint4(0, 0, 0, 0);
-                    if (p.base) b = *at;
-                    const uint32_t *d = &acc[q / 4][8 * (q % 4)];
-                    uint4 v;
-                    v.x = pack_bf16x2_rn(bf16_lo_to_f32(b.x) + __uint_as_float(d[0]), bf16_hi_to_f32(b.x) + __uint_as_float(d[1]));
-                    v.y = pack_bf16x2_rn(bf16_lo_to_f32(b.y) + __uint_as_float(d[2]), bf16_hi_to_f32(b.y) + __uint_as_float(d[3]));
-                    v.z = pack_bf16x2_rn(bf16_lo_to_f32(b.z) + __uint_as_float(d[4]), bf16_hi_to_f32(b.z) + __uint_as_float(d[5]));
-                    v.w = pack_bf16x2_rn(bf16_lo_to_f32(b.w) + __uint_as_float(d[6]), bf16_hi_to_f32(b.w) + __uint_as_float(d[7]));
-                    if (bad) v = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
-                    *at = v;
-                }
-                __syncwarp();
-                #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const int row = 32 * sub + 4 * k + lane / 8, q = lane % 8;
-                    if (row < count) {
-                        const uint4 v = *reinterpret_cast<const uint4 *>(bs + sw128(row, q));
-                        store_cols8(p.y + (long long)s_rows[row] * p.out + col + 8 * q, p.out - col - 8 * q, p.vec_out, v);
+        } else if (warp == kMmaWarp) {
+            constexpr uint32_t idesc = tc_idesc_bf16(kTile, RP) | (TRANS ? kTcBMajorN : 0);
+            const uint32_t d = tmem + (seg & 1) * 128;
+            bool ok = seg < 2 || mbar_wait(dempty + 8 * (seg & 1), ((seg >> 1) - 1) & 1, abort_flag, p.err);
+            ok = __all_sync(0xffffffffu, ok);
+            for (int k = 0; k < n_steps && ok; ++k, ++i) {
+                const int s = i % NS;
+                ok = __all_sync(0xffffffffu, mbar_wait(full + 8 * s, (i / NS) & 1, abort_flag, p.err));
+                if (!ok) break;
+                fence_proxy_async();
+                tc_fence_after();
+                const uint32_t xs = smem_u32(s_mem) + s * S::kStage, ws = xs + 2 * kBlock;
+                if (elect_one()) {
+                    #pragma unroll
+                    for (int m = 0; m < kCols / 16; ++m) {
+                        const uint64_t a = tc_sdesc_sw128(xs + (m / 4) * kBlock + (m % 4) * 32);
+                        const uint64_t b = TRANS ? tc_sdesc_sw128_mn(ws + m * 2048, kBlock)
+                                                 : tc_sdesc_sw128(ws + (m / 4) * (RP * 128) + (m % 4) * 32);
+                        tc_mma_ss(d, a, b, idesc, k > 0 || m > 0);
                     }
+                    tc_commit(empty + 8 * s);
                 }
-            } else {
-                tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(dempty + 8 * buf);
             }
+            if (elect_one()) tc_commit(dfull + 8 * (seg & 1));
             __syncwarp();
-            if (lane == 0) mbar_arrive(empty2 + 8 * s);
+        } else {
+            // this run's sum over the tile's columns, to its slot
+            const int sub = warp % 4, half = warp / 4, row = 32 * sub + lane;
+            const bool ok = __all_sync(0xffffffffu, mbar_wait(dfull + 8 * (seg & 1), (seg >> 1) & 1, abort_flag, p.err));
+            tc_fence_after();
+            float *out = p.partial + ((long long)(tile + blockIdx.x) * kTile + row) * RP + half * (RP / 2);
+            #pragma unroll
+            for (int k = 0; k < RP / 16; ++k) {
+                uint32_t v[8];
+                tc_ld_32x32b_x8(tmem + (uint32_t(32 * sub) << 16) + (seg & 1) * 128 + half * (RP / 2) + 8 * k, v);
+                tc_wait_ld();
+                if (!ok || *abort_flag) {
+                    #pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] = 0x7fffffffu;
+                }
+                if (row < count) {
+                    *reinterpret_cast<uint4 *>(out + 8 * k) = make_uint4(v[0], v[1], v[2], v[3]);
+                    *reinterpret_cast<uint4 *>(out + 8 * k + 4) = make_uint4(v[4], v[5], v[6], v[7]);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(dempty + 8 * (seg & 1));
         }
+        tile_done(seg, tempty);
     }
+    cp_async_wait_all();
+    if (warp == kMmaWarp && seg > 0) drain_wait(dfull + 8 * ((seg - 1) & 1), ((seg - 1) >> 1) & 1);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     if (warp == kMmaWarp) tc_dealloc(tmem, kTmemCols);
-    // every thread that arrived waits (the epilogue's did); no CTA is read or
-    // written after its own hready, which it has passed
-    if (C > 1 && warp >= kEpiWarps) cluster_wait();
+}
+
+// ----------------------------------------------------------- second product
+template <int RP, bool TRANS>
+struct UpShape {
+    static constexpr int kW = weight_bytes(RP, TRANS);
+    static constexpr int kStage = 2 * kBlock + kW;
+    static constexpr int kH = 2 * plane_bytes(RP);
+    static constexpr int kStages = (kSmemMax - 1024 - kH) / kStage < 5 ? (kSmemMax - 1024 - kH) / kStage : 5;
+    static constexpr int kSmem = kStages * kStage + kH + 1024;
+    static_assert(kStages >= 2, "the ring does not fit");
+};
+
+template <int RP, bool TRANS>
+__global__ void __launch_bounds__(kThreads, 1) lora_up_kernel(const LoraArgs p) {
+    using S = UpShape<RP, TRANS>;
+    constexpr int NS = S::kStages, KS = RP / 16;
+    extern __shared__ unsigned char s_raw[];
+    __shared__ uint64_t s_bar[2 * NS + 9];
+    __shared__ TileSlots s_tiles;
+    __shared__ int s_count[2];
+    __shared__ int s_abort;
+    __shared__ uint32_t s_tmem;
+    unsigned char *s_mem = s_raw + (-smem_u32(s_raw) & 1023);
+    unsigned char *s_hi = s_mem + NS * S::kStage, *s_lo = s_hi + plane_bytes(RP);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t full = smem_u32(s_bar), empty = full + 8 * NS, tfull = empty + 8 * NS, tempty = tfull + 16;
+    const uint32_t dfull = tempty + 16, dempty = dfull + 16, hready = dempty + 16;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NS; ++i) mbar_init(full + 8 * i, kProducers), mbar_init(empty + 8 * i, kEpiWarps);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(tfull + 8 * i, 1), mbar_init(tempty + 8 * i, kThreads / 32);
+            mbar_init(dfull + 8 * i, 1), mbar_init(dempty + 8 * i, kEpiWarps);
+        }
+        mbar_init(hready, kEpiThreads);
+        s_abort = 0;
+        fence_barrier_init();
+    }
+    if (warp == kMmaWarp) {
+        tc_alloc(smem_u32(&s_tmem), kTmemCols);
+        tc_relinquish();
+    }
+    // The first product's CTAs waited for what came before them when they let
+    // this kernel start, so the sort, base and the weights may be read at once;
+    // only their sums (read by the epilogue) and what overwrites something wait.
+    if (warp == 0) count_tiles(p, s_count);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    const int r = p.rank;
+    const Walk w = make_walk(s_count[0] + s_count[1], (p.out + kCols - 1) / kCols, blockIdx.x);
+    volatile int *abort_flag = &s_abort;
+
+    int i = 0, j = 0, seg = 0, h_seg = 0;            // steps, multiplied steps, tiles, multiplied tiles
+    for (long long u = w.u0; u < w.u1; ++seg) {
+        const int tile = int(u / w.per), k0 = int(u - (long long)tile * w.per);
+        const int n_steps = int(w.u1 - u < w.per - k0 ? w.u1 - u : w.per - k0);
+        u += n_steps;
+        if (!tile_ready(p, s_tiles, seg, tile, tfull, tempty, warp == kEpiWarps, abort_flag)) break;
+        const int *rows = s_tiles.rows[seg & 1];
+        const int adapter = s_tiles.info[seg & 1][0], count = s_tiles.info[seg & 1][1];
+        const bool in_place = adapter < 0 && p.y == p.base;      // nothing to do
+        if (warp >= kEpiWarps && warp < kMmaWarp) {
+            const Producer t = make_producer();
+            const uint16_t *wt = p.w2 + (long long)max(adapter, 0) * r * p.out, *src[kTile / 8];
+            const int mine = p.base ? (count - t.row0 + 7) / 8 : 0;
+            #pragma unroll
+            for (int m = 0; m < kTile / 8; ++m)
+                src[m] = p.base + (long long)rows[m < mine ? t.row0 + 8 * m : 0] * p.out + 8 * t.piece;
+            for (int k = 0; k < n_steps && !in_place; ++k, ++i) {
+                const int s = i % NS, col = (k0 + k) * kCols, n = min(kCols, p.out - col);
+                const bool ok = i < NS || mbar_wait(empty + 8 * s, (i / NS - 1) & 1, abort_flag, p.err);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                unsigned char *xs = s_mem + s * S::kStage;
+                stage_rows(t, xs, src, mine, col, n, p.vec_out);
+                if (adapter >= 0) stage_weights<RP, TRANS>(t, smem_u32(xs) + 2 * kBlock, wt, r, p.out, col, n);
+                stage_done(full + 8 * s, p.vec_out);
+            }
+        } else if (warp == kMmaWarp) {
+            constexpr uint32_t idesc = tc_idesc_bf16(kTile, kCols) | (TRANS ? kTcBMajorN : 0);
+            if (adapter >= 0) {
+                bool ok = __all_sync(0xffffffffu, mbar_wait(hready, h_seg & 1, abort_flag, p.err));
+                ++h_seg;
+                for (int k = 0; k < n_steps && ok; ++k, ++i, ++j) {
+                    const int s = i % NS, buf = j & 1;
+                    ok = j < 2 || mbar_wait(dempty + 8 * buf, ((j >> 1) - 1) & 1, abort_flag, p.err);
+                    ok = ok && mbar_wait(full + 8 * s, (i / NS) & 1, abort_flag, p.err);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    fence_proxy_async();
+                    tc_fence_after();
+                    const uint32_t ws = smem_u32(s_mem) + s * S::kStage + 2 * kBlock;
+                    if (elect_one()) {
+                        #pragma unroll
+                        for (int part = 0; part < 2; ++part)     // the low plane first
+                            #pragma unroll
+                            for (int m = 0; m < KS; ++m) {
+                                const uint32_t at = (m / 4) * kBlock + (m % 4) * 32;
+                                const uint64_t a = tc_sdesc_sw128(smem_u32(part ? s_hi : s_lo) + at);
+                                const uint64_t b = TRANS ? tc_sdesc_sw128_mn(ws + m * 2048, RP * 128)
+                                                         : tc_sdesc_sw128(ws + at);
+                                tc_mma_ss(tmem + buf * kCols, a, b, idesc, part > 0 || m > 0);
+                            }
+                        tc_commit(dfull + 8 * buf);
+                    }
+                    __syncwarp();
+                }
+            } else if (!in_place) {
+                i += n_steps;
+            }
+        } else {
+            const int sub = warp % 4, half = warp / 4, my_row = 32 * sub + lane;
+            const uint32_t lanes = tmem + (uint32_t(32 * sub) << 16);
+            bool bad = false;
+            if (seg == 0) pdl_wait();
+            if (adapter >= 0) {
+                // h: the tile's slots in CTA order
+                const Walk d = make_walk(s_count[0], (p.in + kCols - 1) / kCols, 0);
+                const long long first = (long long)tile * d.per;
+                const int b0 = run_owner(d.units, d.ctas, first), b1 = run_owner(d.units, d.ctas, first + d.per - 1);
+                const float scale = p.scale[adapter];
+                constexpr int kPieces = RP / 8;
+                #pragma unroll 2
+                for (int m = threadIdx.x; m < kTile * kPieces; m += kEpiThreads) {
+                    const int row = m / kPieces, rank = 8 * (m % kPieces);
+                    const bool token = row < count, in = rank < r;
+                    float v[8];
+                    #pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] = 0.f;
+                    if (token && in) {
+                        const float *at = p.partial + ((long long)(tile + b0) * kTile + row) * RP + rank;
+                        #pragma unroll 4
+                        for (int b = b0; b <= b1; ++b, at += kTile * RP) {
+                            const float4 x = __ldcg(reinterpret_cast<const float4 *>(at));
+                            const float4 y = __ldcg(reinterpret_cast<const float4 *>(at) + 1);
+                            v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+                            v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
+                        }
+                    }
+                    if (!TRANS && p.hidden && token && in && k0 == 0) {
+                        float4 *h = reinterpret_cast<float4 *>(p.hidden + (long long)rows[row] * r + rank);
+                        h[0] = make_float4(v[0], v[1], v[2], v[3]);
+                        h[1] = make_float4(v[4], v[5], v[6], v[7]);
+                    }
+                    // rows past the tile's tokens and ranks past r are zeros
+                    uint4 hi, lo;
+                    split2(scale * v[0], scale * v[1], hi.x, lo.x), split2(scale * v[2], scale * v[3], hi.y, lo.y);
+                    split2(scale * v[4], scale * v[5], hi.z, lo.z), split2(scale * v[6], scale * v[7], hi.w, lo.w);
+                    const uint32_t to = (rank / 64) * kBlock + sw128(row, (rank / 8) % 8);
+                    *reinterpret_cast<uint4 *>(s_hi + to) = hi;
+                    *reinterpret_cast<uint4 *>(s_lo + to) = lo;
+                    if (TRANS && token && k0 == 0) {
+                        // g and s h of the sorted token, for the weight gradients
+                        const long long out = (long long)(s_tiles.info[seg & 1][2] + row) * (plane_pitch(RP) / 2) + rank;
+                        *reinterpret_cast<uint4 *>(p.pg + out) = hi, *reinterpret_cast<uint4 *>(p.pg + out + RP) = lo;
+                        hi = lo = make_uint4(0, 0, 0, 0);
+                        if (in) {
+                            const float4 *h = reinterpret_cast<const float4 *>(p.hidden + (long long)rows[row] * r + rank);
+                            const float4 x = h[0], y = h[1];
+                            split2(scale * x.x, scale * x.y, hi.x, lo.x), split2(scale * x.z, scale * x.w, hi.y, lo.y);
+                            split2(scale * y.x, scale * y.y, hi.z, lo.z), split2(scale * y.z, scale * y.w, hi.w, lo.w);
+                        }
+                        *reinterpret_cast<uint4 *>(p.ph + out) = hi, *reinterpret_cast<uint4 *>(p.ph + out + RP) = lo;
+                    }
+                }
+                fence_proxy_async();
+                mbar_arrive(hready);
+            } else if (!TRANS && p.hidden && k0 == 0) {
+                for (int m = threadIdx.x; m < count * r; m += kEpiThreads)
+                    p.hidden[(long long)rows[m / r] * r + m % r] = 0.f;
+            }
+            for (int k = 0; k < n_steps && !in_place; ++k, ++i) {
+                const int s = i % NS, buf = j & 1, col = (k0 + k) * kCols + 64 * half;
+                unsigned char *bs = s_mem + s * S::kStage + half * kBlock;
+                bool ok = mbar_wait(full + 8 * s, (i / NS) & 1, abort_flag, p.err);
+                uint32_t acc[2][32];
+                if (adapter >= 0) {
+                    ok = ok && mbar_wait(dfull + 8 * buf, (j >> 1) & 1, abort_flag, p.err);
+                    ++j;
+                    tc_fence_after();
+                    tc_ld_32x32b_x32(lanes + buf * kCols + 64 * half, acc[0]);
+                    tc_ld_32x32b_x32(lanes + buf * kCols + 64 * half + 32, acc[1]);
+                    tc_wait_ld();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(dempty + 8 * buf);
+                } else {
+                    #pragma unroll
+                    for (int e = 0; e < 32; ++e) acc[0][e] = acc[1][e] = 0x80000000u;   // -0: base as it is
+                }
+                bad |= !__all_sync(0xffffffffu, ok);
+                if (col < p.out && 32 * sub < count) {
+                    #pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        uint4 *at = reinterpret_cast<uint4 *>(bs + sw128(my_row, q));
+                        uint4 b = make_uint4(0, 0, 0, 0);
+                        if (p.base) b = *at;
+                        const uint32_t *d = &acc[q / 4][8 * (q % 4)];
+                        uint4 v;
+                        v.x = pack_bf16x2_rn(bf16_lo_to_f32(b.x) + __uint_as_float(d[0]), bf16_hi_to_f32(b.x) + __uint_as_float(d[1]));
+                        v.y = pack_bf16x2_rn(bf16_lo_to_f32(b.y) + __uint_as_float(d[2]), bf16_hi_to_f32(b.y) + __uint_as_float(d[3]));
+                        v.z = pack_bf16x2_rn(bf16_lo_to_f32(b.z) + __uint_as_float(d[4]), bf16_hi_to_f32(b.z) + __uint_as_float(d[5]));
+                        v.w = pack_bf16x2_rn(bf16_lo_to_f32(b.w) + __uint_as_float(d[6]), bf16_hi_to_f32(b.w) + __uint_as_float(d[7]));
+                        if (adapter < 0) v = b;                  // bit for bit, a NaN's too
+                        if (bad) v = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+                        *at = v;
+                    }
+                    __syncwarp();
+                    #pragma unroll
+                    for (int m = 0; m < 8; ++m) {
+                        const int row = 32 * sub + 4 * m + lane / 8, q = lane % 8;
+                        if (row < count) {
+                            const uint4 v = *reinterpret_cast<const uint4 *>(bs + sw128(row, q));
+                            store_cols8(p.y + (long long)rows[row] * p.out + col + 8 * q, p.out - col - 8 * q, p.vec_out, v);
+                        }
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(empty + 8 * s);
+            }
+        }
+        tile_done(seg, tempty);
+    }
+    pdl_wait();
+    pdl_launch_dependents();
+    cp_async_wait_all();
+    if (warp == kMmaWarp && j > 0) drain_wait(dfull + 8 * ((j - 1) & 1), ((j - 1) >> 1) & 1);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kMmaWarp) tc_dealloc(tmem, kTmemCols);
 }
 
 // ---------------------------------------------------------- weight gradients
@@ -443,38 +588,48 @@ __device__ __forceinline__ void wgrad_tile(const WgradArgs &p, int slice, int ad
     volatile int *abort_flag = s_abort;
 
     if (warp >= kEpiWarps && warp < kMmaWarp) {
-        constexpr int kRows = kStageTokens / kProducerWarps;     // rows of a producer warp
-        const int first = (warp - kEpiWarps) * kRows;
+        // Rows row0 + 8 j, column pieces piece + 16 e: their places are 1024 and 2
+        // blocks apart.  The rows of the next stage are looked up one stage ahead.
+        const int pt = threadIdx.x - kEpiThreads, piece = pt % 16, row0 = pt / 16;
+        constexpr int kJ = kStageTokens / 8, kE = S::kCols / 128;
+        const uint32_t dst = (piece / 8) * S::kQBlock + sw128(row0, piece % 8);
+        int next[kJ];
+        #pragma unroll
+        for (int j = 0; j < kJ; ++j) next[j] = t0 + row0 + 8 * j < t1 ? rows[t0 + row0 + 8 * j] : -1;
         for (int i = 0; i < stages; ++i) {
             const int s = i % NS, tok = t0 + i * kStageTokens, n = min(kStageTokens, t1 - tok);
-            const int row = lane < kRows && first + lane < n ? rows[tok + first + lane] : 0;
+            int row[kJ];
+            #pragma unroll
+            for (int j = 0; j < kJ; ++j) {
+                const int t = tok + kStageTokens + row0 + 8 * j;
+                row[j] = next[j];
+                next[j] = t < t1 ? rows[t] : -1;
+            }
             const bool ok = i < NS || mbar_wait(empty + 8 * s, (i / NS - 1) & 1, abort_flag, p.err);
             if (!__all_sync(0xffffffffu, ok)) break;
             const uint32_t qs = ring + s * S::kStage, ps = qs + S::kQ;
             // tokens past the end are zeros on both sides: they are summed over
             #pragma unroll
-            for (int k = 0; k < kRows; ++k) {
-                const bool in = first + k < n;
-                const uint16_t *src = q + (long long)__shfl_sync(0xffffffffu, row, k) * cols + col0;
+            for (int j = 0; j < kJ; ++j) {
+                const bool in = row[j] >= 0;
+                const uint16_t *src = q + (long long)max(row[j], 0) * cols + col0 + 8 * piece;
                 #pragma unroll
-                for (int b = lane; b < S::kCols / 8; b += 32) {
-                    const uint32_t dst = (b / 8) * S::kQBlock + sw128(first + k, b % 8);
-                    const bool ok_q = in && 8 * b < width;
-                    if (vec) {
-                        if (8 * b < width) cp_async16z(qs + dst, ok_q ? src + 8 * b : q, ok_q);
-                    } else if (8 * b < width) {
-                        *reinterpret_cast<uint4 *>(s_mem + s * S::kStage + dst) =
-                            load_cols8(src + 8 * b, in ? width - 8 * b : 0, 0);
-                    }
+                for (int e = 0; e < kE; ++e) {
+                    const int left = width - 8 * piece - 128 * e;
+                    const uint32_t at = dst + 1024 * j + 2 * S::kQBlock * e;
+                    if (left <= 0) continue;
+                    if (vec) cp_async16z(qs + at, in ? src + 128 * e : q, in);
+                    else *reinterpret_cast<uint4 *>(s_mem + s * S::kStage + at) = load_cols8(src + 128 * e, in ? left : 0, 0);
                 }
             }
-            const uint16_t *src = planes + (long long)(start + tok) * (plane_pitch(RP) / 2);
-            constexpr int kPieces = RP / 4;                      // 16-byte pieces of both planes
-            #pragma unroll 4
-            for (int k = threadIdx.x - kEpiThreads; k < kStageTokens * kPieces; k += kProducers) {
-                const int t = k / kPieces, b = k % kPieces, plane = b / (RP / 8), e = b % (RP / 8);
-                cp_async16z(ps + plane * S::kP + (e / 8) * S::kQBlock + sw128(t, e % 8),
-                            t < n ? src + (long long)t * (plane_pitch(RP) / 2) + 8 * b : planes, t < n);
+            constexpr int kPieces = RP / 4, kTokens = kProducers / kPieces;   // both planes' pieces; tokens in one go
+            const int b = pt % kPieces, tk = pt / kPieces, plane = b / (RP / 8), e = b % (RP / 8);
+            const uint16_t *src = planes + (long long)(start + tok + tk) * (plane_pitch(RP) / 2) + 8 * b;
+            const uint32_t pdst = ps + plane * S::kP + (e / 8) * S::kQBlock;
+            #pragma unroll
+            for (int j = 0; j < kStageTokens / kTokens; ++j) {
+                const bool in = tk + kTokens * j < n;
+                cp_async16z(pdst + sw128(tk + kTokens * j, e % 8), in ? src + kTokens * j * (plane_pitch(RP) / 2) : planes, in);
             }
             stage_done(full + 8 * s, vec);
         }
@@ -613,18 +768,15 @@ int ceil_div(long long a, long long b) { return int((a + b - 1) / b); }
 
 template <int RP, bool TRANS>
 cudaError_t launch_tensor_rank(const LoraArgs &p, int sms, cudaStream_t s) {
-    using S = TensorShape<RP>;
-    const cudaError_t e = allow_smem<lora_tensor_kernel<RP, TRANS>>(S::kSmem);
+    using D = DownShape<RP, TRANS>;
+    using U = UpShape<RP, TRANS>;
+    cudaError_t e = allow_smem<lora_down_kernel<RP, TRANS>>(D::kSmem);
+    if (e == cudaSuccess) e = allow_smem<lora_up_kernel<RP, TRANS>>(U::kSmem);
     if (e != cudaSuccess) return e;
-    // CTAs per tile: as many as leave one CTA per SM (the adapters' last tiles
-    // counted as half there), so that few tiles use every SM and many split nothing
-    const int whole = ceil_div(p.tokens, kTile);
-    const int tiles = whole + (p.adapters < whole ? p.adapters : whole) / 2;
-    int cluster = kMaxCluster;
-    while (cluster > 1 && tiles * cluster > sms) cluster /= 2;
-    const int extra = p.adapters + 1 < p.tokens ? p.adapters + 1 : p.tokens;
-    return launch_chained(lora_tensor_kernel<RP, TRANS>, dim3(unsigned(whole + extra) * cluster), kThreads, S::kSmem,
-                          cluster, s, p);
+    const int ctas = sms < kMaxRuns ? sms : kMaxRuns;
+    e = launch_chained(lora_down_kernel<RP, TRANS>, dim3(ctas), kThreads, D::kSmem, 1, s, p);
+    if (e != cudaSuccess) return e;
+    return launch_chained(lora_up_kernel<RP, TRANS>, dim3(ctas), kThreads, U::kSmem, 1, s, p);
 }
 
 template <int RP>
@@ -641,12 +793,17 @@ cudaError_t launch_wgrad_rank(WgradArgs p, int adapters, int sms, cudaStream_t s
 
 }  // namespace
 
+size_t lora_partial_bytes(int tokens, int adapters, int rank) {
+    const size_t tiles = size_t(ceil_div(tokens, kTile)) + (adapters < tokens ? adapters : tokens);
+    return (tiles + kMaxRuns) * kTile * padded_rank(rank) * sizeof(float);
+}
+
 cudaError_t launch_lora_tensor(const LoraArgs &p, bool trans, int sms, cudaStream_t s) {
     switch (padded_rank(p.rank)) {
         case 16: return trans ? launch_tensor_rank<16, true>(p, sms, s) : launch_tensor_rank<16, false>(p, sms, s);
         case 32: return trans ? launch_tensor_rank<32, true>(p, sms, s) : launch_tensor_rank<32, false>(p, sms, s);
         case 64: return trans ? launch_tensor_rank<64, true>(p, sms, s) : launch_tensor_rank<64, false>(p, sms, s);
-        default: return cudaErrorInvalidValue;
+        default: return trans ? launch_tensor_rank<128, true>(p, sms, s) : launch_tensor_rank<128, false>(p, sms, s);
     }
 }
 
