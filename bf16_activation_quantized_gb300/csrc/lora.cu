@@ -283,7 +283,7 @@ cudaError_t launch_lora_few(const LoraArgs &p, cudaStream_t s) {
 size_t round16(size_t b) { return (b + 15) / 16 * 16; }
 
 // Workspace: order [tokens], sizes [adapters], the sort's counts, the partial
-// sums of h, and for the gradient the planes of g and of s h.
+// sums of h, its planes, and in the gradient s h's planes.
 struct LoraWorkspace {
     size_t order, sizes, counts, partial, g, h, total;
 };
@@ -295,7 +295,7 @@ LoraWorkspace lora_workspace(int tokens, int adapters, int rank, bool backward) 
     w.partial = w.counts + round16(sort_bytes(tokens, adapters));
     w.g = w.partial + lora_partial_bytes(tokens, adapters, rank);
     w.h = w.g + size_t(tokens) * plane_pitch(padded_rank(rank));
-    w.total = backward ? w.h + size_t(tokens) * plane_pitch(padded_rank(rank)) : w.g;
+    w.total = w.h + (backward ? size_t(tokens) * plane_pitch(padded_rank(rank)) : 0);
     if (!backward && tokens <= kFewTokens) w.total = 0;
     return w;
 }
@@ -308,6 +308,12 @@ w4a16_status check_lora(int tokens, int adapters, int rank, int N, int K) {
 }
 
 w4a16_status from_cuda(cudaError_t e) { return e == cudaSuccess ? W4A16_OK : W4A16_ERR_CUDA; }
+
+void place_workspace(LoraArgs *p, char *ws, const LoraWorkspace &w) {
+    p->partial = reinterpret_cast<float *>(ws + w.partial);
+    p->pg = reinterpret_cast<uint16_t *>(ws + w.g);
+    p->ph = reinterpret_cast<uint16_t *>(ws + w.h);
+}
 
 w4a16_status check_workspace(const LoraWorkspace &w, const void *ws, size_t bytes) {
     if (w.total == 0) return W4A16_OK;
@@ -361,7 +367,8 @@ w4a16_status w4a16_lora_add(const w4a16_bf16 *X, const w4a16_bf16 *A, const w4a1
     cudaError_t e = launch_sort(adapters_dev, id_bytes, tokens, num_adapters,
                                 reinterpret_cast<int *>(ws + w.counts), sizes, order, s);
     if (e != cudaSuccess) return W4A16_ERR_CUDA;
-    p.order = order, p.sizes = sizes, p.partial = reinterpret_cast<float *>(ws + w.partial);
+    p.order = order, p.sizes = sizes;
+    place_workspace(&p, ws, w);
     return from_cuda(launch_lora_tensor(p, false, sms, s));
 }
 
@@ -398,12 +405,11 @@ w4a16_status w4a16_lora_add_backward(const w4a16_bf16 *dY, const w4a16_bf16 *X, 
     LoraArgs p = {};
     p.x = dY, p.w1 = B, p.w2 = A, p.ids = adapters_dev, p.id_bytes = id_bytes, p.scale = lora_scales;
     p.order = order, p.sizes = sizes, p.base = dX_base, p.y = dX, p.hidden = const_cast<float *>(hidden);
-    p.pg = reinterpret_cast<uint16_t *>(ws + w.g), p.ph = reinterpret_cast<uint16_t *>(ws + w.h);
     p.err = device_error_word();
     p.tokens = tokens, p.adapters = num_adapters, p.rank = rank, p.in = N, p.out = K;
     p.vec_in = N % 8 == 0 && aligned(dY, 16);
     p.vec_out = aligned(dX_base, 16) && aligned(dX, 16);
-    p.partial = reinterpret_cast<float *>(ws + w.partial);
+    place_workspace(&p, ws, w);
     e = launch_lora_tensor(p, true, sms, s);
     if (e != cudaSuccess) return W4A16_ERR_CUDA;
     WgradArgs q = {};

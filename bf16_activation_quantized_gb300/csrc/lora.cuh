@@ -24,7 +24,7 @@ struct LoraArgs {
     const uint16_t *base;    // [tokens][out] or nullptr
     uint16_t *y;             // [tokens][out]
     float *hidden;           // [tokens][r]: forward h, written (or nullptr); gradient: read
-    uint16_t *pg, *ph;       // gradient: g and s h of the sorted tokens, written (see plane_pitch)
+    uint16_t *pg, *ph;       // planes of the sorted tokens: s h or g; in the gradient also s h
     float *partial;          // partial sums of h (many tokens)
     int *err;
     int id_bytes, tokens, adapters, rank, in, out;

@@ -1,13 +1,15 @@
 // lora_tensor.cu -- adapters for many tokens, on the tensor cores.
 //
 // lora_down_kernel: partial sums of h = A x (or, with the weight read along its
-// other axis, of B^T dy); lora_up_kernel: y = base + s B h (dx = dx_base + A^T g).
-// The formulas and the precision are in lora.cu.  Both walk tiles of 128 sorted
-// tokens of one adapter in steps of 128 columns; the (tile, column step) pairs
-// are cut into one even run per CTA, one CTA per SM, so every SM moves the same
-// bytes whatever the adapters' sizes.  A run that covers part of a tile's input
-// columns leaves its sum in a workspace slot (tile + CTA, unique along the
-// walk), and the second kernel adds a tile's slots in CTA order.
+// other axis, of B^T dy); lora_sum_kernel: h; lora_up_kernel: y = base + s B h (dx
+// = dx_base + A^T g).  The formulas and the precision are in lora.cu.  The two
+// products walk tiles of 128 sorted tokens of one adapter in steps of 128
+// columns; the (tile, column step) pairs are cut into one even run per CTA, one
+// CTA per SM, so every SM moves the same bytes whatever the adapters' sizes.  A
+// run that covers part of a tile's input columns leaves its sum in a workspace
+// slot (tile + CTA, unique along the walk), and a tile's slots are added in CTA
+// order.  The three launches are chained: the second product's CTAs stream base
+// and weights while the sums are made.
 //
 // In each CTA four producer warps gather rows of X (of base) and the weights
 // with 16-byte asynchronous copies into a ring of stages, in the 128-byte
@@ -61,11 +63,11 @@ struct Walk {
     int per, ctas;          // steps of a tile; CTAs with a run
     long long u0, u1;       // this CTA's run
 };
-__device__ __forceinline__ Walk make_walk(int tiles, int per, int b) {
+__device__ __forceinline__ Walk make_walk(int tiles, int per, int b, int ctas) {
     Walk w;
     w.units = (long long)tiles * per;
     w.per = per;
-    w.ctas = int(w.units < gridDim.x ? w.units : gridDim.x);
+    w.ctas = int(w.units < ctas ? w.units : ctas);
     w.u0 = w.u1 = 0;
     if (b < w.ctas) w.u0 = run_start(w.units, w.ctas, b), w.u1 = run_start(w.units, w.ctas, b + 1);
     return w;
@@ -225,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1) lora_down_kernel(const LoraArgs p
     pdl_launch_dependents();
     const uint32_t tmem = s_tmem;
     const int r = p.rank;
-    const Walk w = make_walk(s_count[0], (p.in + kCols - 1) / kCols, blockIdx.x);
+    const Walk w = make_walk(s_count[0], (p.in + kCols - 1) / kCols, blockIdx.x, gridDim.x);
     volatile int *abort_flag = &s_abort;
 
     int i = 0, seg = 0;                              // steps and tiles so far
@@ -312,6 +314,62 @@ __global__ void __launch_bounds__(kThreads, 1) lora_down_kernel(const LoraArgs p
     if (warp == kMmaWarp) tc_dealloc(tmem, kTmemCols);
 }
 
+// ------------------------------------------------------------------ its sums
+// h of every tile: its slots in CTA order, to the planes p.pg (scaled) and
+// p.hidden; in the gradient also s h's planes from p.hidden.  Four ranks a
+// thread, all of a tile's slots (5 of them at 4096 tokens) on their way at once.
+constexpr int kSumThreads = 256;
+
+template <int RP, bool TRANS>
+__global__ void __launch_bounds__(kSumThreads) lora_sum_kernel(const LoraArgs p, int down_ctas) {
+    constexpr int kPieces = RP / 4, kRows = kSumThreads / kPieces, kBlocks = kTile / kRows, kSlots = 8;
+    __shared__ int s_rows[kTile];
+    __shared__ int s_info[3], s_count[2];
+    // The first product's CTAs let this kernel start after the sort had ended.
+    pdl_launch_dependents();
+    const int tile = blockIdx.x / kBlocks, row0 = blockIdx.x % kBlocks * kRows;
+    if (threadIdx.x < 32) {
+        count_tiles(p, s_count);
+        find_tile_sorted<kTile>(p, tile, s_rows, s_info);
+    }
+    __syncthreads();
+    const int adapter = s_info[0], count = s_info[1], r = p.rank;
+    const int row = row0 + threadIdx.x / kPieces, rank = 4 * (threadIdx.x % kPieces);
+    pdl_wait();
+    if (row >= count) return;
+    float4 *hidden = reinterpret_cast<float4 *>(p.hidden + (long long)s_rows[row] * r + rank);
+    if (adapter < 0) {
+        if (!TRANS && p.hidden && rank < r) *hidden = make_float4(0.f, 0.f, 0.f, 0.f);
+        return;
+    }
+    const Walk d = make_walk(s_count[0], (p.in + kCols - 1) / kCols, 0, down_ctas);
+    const long long first = (long long)tile * d.per;
+    const int b0 = run_owner(d.units, d.ctas, first), b1 = run_owner(d.units, d.ctas, first + d.per - 1);
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f), w = v;
+    if (TRANS && rank < r) w = *hidden;
+    const float *at = p.partial + ((long long)(tile + b0) * kTile + row) * RP + rank;
+    for (int b = b0; b <= b1; b += kSlots) {
+        float4 u[kSlots];
+        #pragma unroll
+        for (int k = 0; k < kSlots; ++k)
+            if (b + k <= b1) u[k] = *reinterpret_cast<const float4 *>(at + (long long)(b - b0 + k) * kTile * RP);
+        #pragma unroll
+        for (int k = 0; k < kSlots; ++k)
+            if (b + k <= b1) v.x += u[k].x, v.y += u[k].y, v.z += u[k].z, v.w += u[k].w;
+    }
+    if (!TRANS && p.hidden && rank < r) *hidden = v;
+    if (rank >= r) v = make_float4(0.f, 0.f, 0.f, 0.f);  // also where x holds infinities (0 * inf)
+    const float scale = p.scale[adapter];
+    const long long out = (long long)(s_info[2] + row) * (plane_pitch(RP) / 2) + rank;
+    uint2 hi, lo;
+    split2(scale * v.x, scale * v.y, hi.x, lo.x), split2(scale * v.z, scale * v.w, hi.y, lo.y);
+    *reinterpret_cast<uint2 *>(p.pg + out) = hi, *reinterpret_cast<uint2 *>(p.pg + out + RP) = lo;
+    if (TRANS) {
+        split2(scale * w.x, scale * w.y, hi.x, lo.x), split2(scale * w.z, scale * w.w, hi.y, lo.y);
+        *reinterpret_cast<uint2 *>(p.ph + out) = hi, *reinterpret_cast<uint2 *>(p.ph + out + RP) = lo;
+    }
+}
+
 // ----------------------------------------------------------- second product
 template <int RP, bool TRANS>
 struct UpShape {
@@ -352,16 +410,16 @@ __global__ void __launch_bounds__(kThreads, 1) lora_up_kernel(const LoraArgs p) 
         tc_alloc(smem_u32(&s_tmem), kTmemCols);
         tc_relinquish();
     }
-    // The first product's CTAs waited for what came before them when they let
-    // this kernel start, so the sort, base and the weights may be read at once;
-    // only their sums (read by the epilogue) and what overwrites something wait.
+    // The first product's CTAs had waited for what came before them when they let
+    // the sums start, and those this kernel: the sort, base and the weights may be
+    // read at once; only h (read by the epilogue) and what overwrites anything wait.
     if (warp == 0) count_tiles(p, s_count);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s_tmem;
     const int r = p.rank;
-    const Walk w = make_walk(s_count[0] + s_count[1], (p.out + kCols - 1) / kCols, blockIdx.x);
+    const Walk w = make_walk(s_count[0] + s_count[1], (p.out + kCols - 1) / kCols, blockIdx.x, gridDim.x);
     volatile int *abort_flag = &s_abort;
 
     int i = 0, j = 0, seg = 0, h_seg = 0;            // steps, multiplied steps, tiles, multiplied tiles
@@ -427,60 +485,27 @@ __global__ void __launch_bounds__(kThreads, 1) lora_up_kernel(const LoraArgs p) 
             bool bad = false;
             if (seg == 0) pdl_wait();
             if (adapter >= 0) {
-                // h: the tile's slots in CTA order
-                const Walk d = make_walk(s_count[0], (p.in + kCols - 1) / kCols, 0);
-                const long long first = (long long)tile * d.per;
-                const int b0 = run_owner(d.units, d.ctas, first), b1 = run_owner(d.units, d.ctas, first + d.per - 1);
-                const float scale = p.scale[adapter];
-                constexpr int kPieces = RP / 8;
-                #pragma unroll 2
-                for (int m = threadIdx.x; m < kTile * kPieces; m += kEpiThreads) {
-                    const int row = m / kPieces, rank = 8 * (m % kPieces);
-                    const bool token = row < count, in = rank < r;
-                    float v[8];
+                // h's planes of the tile; rows past its tokens are zeros
+                const int start = s_tiles.info[seg & 1][2];
+                constexpr int kPieces = RP / 4, kOnce = RP >= 64 ? 8 : RP / 8;
+                #pragma unroll 1
+                for (int m0 = threadIdx.x; m0 < kTile * kPieces; m0 += kOnce * kEpiThreads) {
+                    uint4 v[kOnce];
                     #pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] = 0.f;
-                    if (token && in) {
-                        const float *at = p.partial + ((long long)(tile + b0) * kTile + row) * RP + rank;
-                        #pragma unroll 4
-                        for (int b = b0; b <= b1; ++b, at += kTile * RP) {
-                            const float4 x = __ldcg(reinterpret_cast<const float4 *>(at));
-                            const float4 y = __ldcg(reinterpret_cast<const float4 *>(at) + 1);
-                            v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
-                            v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
-                        }
+                    for (int e = 0; e < kOnce; ++e) {
+                        const int m = m0 + e * kEpiThreads, row = m / kPieces, b = m % kPieces;
+                        v[e] = make_uint4(0, 0, 0, 0);
+                        if (row < count)
+                            v[e] = *(reinterpret_cast<const uint4 *>(p.pg + (long long)(start + row) * (plane_pitch(RP) / 2)) + b);
                     }
-                    if (!TRANS && p.hidden && token && in && k0 == 0) {
-                        float4 *h = reinterpret_cast<float4 *>(p.hidden + (long long)rows[row] * r + rank);
-                        h[0] = make_float4(v[0], v[1], v[2], v[3]);
-                        h[1] = make_float4(v[4], v[5], v[6], v[7]);
-                    }
-                    // rows past the tile's tokens and ranks past r are zeros
-                    uint4 hi, lo;
-                    split2(scale * v[0], scale * v[1], hi.x, lo.x), split2(scale * v[2], scale * v[3], hi.y, lo.y);
-                    split2(scale * v[4], scale * v[5], hi.z, lo.z), split2(scale * v[6], scale * v[7], hi.w, lo.w);
-                    const uint32_t to = (rank / 64) * kBlock + sw128(row, (rank / 8) % 8);
-                    *reinterpret_cast<uint4 *>(s_hi + to) = hi;
-                    *reinterpret_cast<uint4 *>(s_lo + to) = lo;
-                    if (TRANS && token && k0 == 0) {
-                        // g and s h of the sorted token, for the weight gradients
-                        const long long out = (long long)(s_tiles.info[seg & 1][2] + row) * (plane_pitch(RP) / 2) + rank;
-                        *reinterpret_cast<uint4 *>(p.pg + out) = hi, *reinterpret_cast<uint4 *>(p.pg + out + RP) = lo;
-                        hi = lo = make_uint4(0, 0, 0, 0);
-                        if (in) {
-                            const float4 *h = reinterpret_cast<const float4 *>(p.hidden + (long long)rows[row] * r + rank);
-                            const float4 x = h[0], y = h[1];
-                            split2(scale * x.x, scale * x.y, hi.x, lo.x), split2(scale * x.z, scale * x.w, hi.y, lo.y);
-                            split2(scale * y.x, scale * y.y, hi.z, lo.z), split2(scale * y.z, scale * y.w, hi.w, lo.w);
-                        }
-                        *reinterpret_cast<uint4 *>(p.ph + out) = hi, *reinterpret_cast<uint4 *>(p.ph + out + RP) = lo;
+                    #pragma unroll
+                    for (int e = 0; e < kOnce; ++e) {
+                        const int m = m0 + e * kEpiThreads, row = m / kPieces, b = m % kPieces, q = b % (RP / 8);
+                        *reinterpret_cast<uint4 *>((b < RP / 8 ? s_hi : s_lo) + (q / 8) * kBlock + sw128(row, q % 8)) = v[e];
                     }
                 }
                 fence_proxy_async();
                 mbar_arrive(hready);
-            } else if (!TRANS && p.hidden && k0 == 0) {
-                for (int m = threadIdx.x; m < count * r; m += kEpiThreads)
-                    p.hidden[(long long)rows[m / r] * r + m % r] = 0.f;
             }
             for (int k = 0; k < n_steps && !in_place; ++k, ++i) {
                 const int s = i % NS, buf = j & 1, col = (k0 + k) * kCols + 64 * half;
@@ -546,14 +571,16 @@ __global__ void __launch_bounds__(kThreads, 1) lora_up_kernel(const LoraArgs p) 
 
 // ---------------------------------------------------------- weight gradients
 constexpr int kStageTokens = 32;
+// Eight warps produce and then store; the ninth issues the MMAs.
+constexpr int kWgradWarps = 8, kWgradProducers = kWgradWarps * 32, kWgradThreads = kWgradProducers + 32;
 
 template <int RP>
 struct WgradShape {
     static constexpr int kCols = RP <= 64 ? 512 : 256;      // columns of a CTA
     static constexpr int kQBlock = kStageTokens * 128;      // bytes of 32 tokens x 64 columns
     static constexpr int kQ = kCols / 64 * kQBlock;
-    static constexpr int kP = (RP + 63) / 64 * kQBlock;     // of one plane
-    static constexpr int kStage = kQ + 2 * kP;
+    static constexpr int kP = (2 * RP + 63) / 64 * kQBlock; // both planes: rows of 2 RP, in blocks of 64
+    static constexpr int kStage = kQ + kP;
     static constexpr int kSumsA = RP * (kCols + 4) * 4, kSumsB = kCols * (RP + 4) * 4;
     static constexpr int kSums = kSumsA > kSumsB ? kSumsA : kSumsB;
     static constexpr int kStages = (kSmemMax - 1024) / kStage;
@@ -563,7 +590,8 @@ struct WgradShape {
 
 // Grid (slices * cluster, adapters): a cluster owns kCols columns of one
 // adapter's dA (or rows of dB), D[column][rank] in TMEM in blocks of 128
-// columns; its CTAs split the adapter's tokens, 32 to a stage, and add their
+// columns, once for each plane of g or s h (one MMA takes both as its N; two of
+// half the N took twice the time); its CTAs split the adapter's tokens, 32 to a stage, and add their
 // sums through distributed shared memory, in CTA order.
 template <int RP, bool DB>
 __device__ __forceinline__ void wgrad_tile(const WgradArgs &p, int slice, int adapter, unsigned char *s_mem,
@@ -587,21 +615,21 @@ __device__ __forceinline__ void wgrad_tile(const WgradArgs &p, int slice, int ad
     const int *rows = p.order + start;
     volatile int *abort_flag = s_abort;
 
-    if (warp >= kEpiWarps && warp < kMmaWarp) {
-        // Rows row0 + 8 j, column pieces piece + 16 e: their places are 1024 and 2
-        // blocks apart.  The rows of the next stage are looked up one stage ahead.
-        const int pt = threadIdx.x - kEpiThreads, piece = pt % 16, row0 = pt / 16;
-        constexpr int kJ = kStageTokens / 8, kE = S::kCols / 128;
+    if (warp < kWgradWarps) {
+        // Rows row0 + 16 j, column pieces piece + 16 e: their places are 2048 bytes and
+        // 2 blocks apart.  The rows of the next stage are looked up one stage ahead.
+        const int pt = threadIdx.x, piece = pt % 16, row0 = pt / 16;
+        constexpr int kRows = kWgradProducers / 16, kJ = kStageTokens / kRows, kE = S::kCols / 128;
         const uint32_t dst = (piece / 8) * S::kQBlock + sw128(row0, piece % 8);
         int next[kJ];
         #pragma unroll
-        for (int j = 0; j < kJ; ++j) next[j] = t0 + row0 + 8 * j < t1 ? rows[t0 + row0 + 8 * j] : -1;
+        for (int j = 0; j < kJ; ++j) next[j] = t0 + row0 + kRows * j < t1 ? rows[t0 + row0 + kRows * j] : -1;
         for (int i = 0; i < stages; ++i) {
             const int s = i % NS, tok = t0 + i * kStageTokens, n = min(kStageTokens, t1 - tok);
             int row[kJ];
             #pragma unroll
             for (int j = 0; j < kJ; ++j) {
-                const int t = tok + kStageTokens + row0 + 8 * j;
+                const int t = tok + kStageTokens + row0 + kRows * j;
                 row[j] = next[j];
                 next[j] = t < t1 ? rows[t] : -1;
             }
@@ -616,26 +644,25 @@ __device__ __forceinline__ void wgrad_tile(const WgradArgs &p, int slice, int ad
                 #pragma unroll
                 for (int e = 0; e < kE; ++e) {
                     const int left = width - 8 * piece - 128 * e;
-                    const uint32_t at = dst + 1024 * j + 2 * S::kQBlock * e;
+                    const uint32_t at = dst + kRows * 128 * j + 2 * S::kQBlock * e;
                     if (left <= 0) continue;
                     if (vec) cp_async16z(qs + at, in ? src + 128 * e : q, in);
                     else *reinterpret_cast<uint4 *>(s_mem + s * S::kStage + at) = load_cols8(src + 128 * e, in ? left : 0, 0);
                 }
             }
-            constexpr int kPieces = RP / 4, kTokens = kProducers / kPieces;   // both planes' pieces; tokens in one go
-            const int b = pt % kPieces, tk = pt / kPieces, plane = b / (RP / 8), e = b % (RP / 8);
-            const uint16_t *src = planes + (long long)(start + tok + tk) * (plane_pitch(RP) / 2) + 8 * b;
-            const uint32_t pdst = ps + plane * S::kP + (e / 8) * S::kQBlock;
+            constexpr int kPieces = RP / 4, kAll = kStageTokens * kPieces;   // both planes' pieces
+            const uint16_t *src = planes + (long long)(start + tok) * (plane_pitch(RP) / 2);
             #pragma unroll
-            for (int j = 0; j < kStageTokens / kTokens; ++j) {
-                const bool in = tk + kTokens * j < n;
-                cp_async16z(pdst + sw128(tk + kTokens * j, e % 8), in ? src + kTokens * j * (plane_pitch(RP) / 2) : planes, in);
+            for (int k = pt; k < kAll; k += kWgradProducers) {
+                const int tk = k / kPieces, b = k % kPieces;
+                const bool in = tk < n;
+                cp_async16z(ps + (b / 8) * S::kQBlock + sw128(tk, b % 8), in ? src + 8 * k : planes, in);
             }
             stage_done(full + 8 * s, vec);
         }
         cp_async_wait_all();
-    } else if (warp == kMmaWarp) {
-        constexpr uint32_t idesc = tc_idesc_bf16(128, RP) | kTcAMajorM | kTcBMajorN;
+    } else {
+        constexpr uint32_t idesc = tc_idesc_bf16(128, 2 * RP) | kTcAMajorM | kTcBMajorN;
         bool ok = true;
         for (int i = 0; i < stages; ++i) {
             const int s = i % NS;
@@ -648,13 +675,11 @@ __device__ __forceinline__ void wgrad_tile(const WgradArgs &p, int slice, int ad
                 #pragma unroll
                 for (int m = 0; m < S::kCols / 128; ++m)
                     #pragma unroll
-                    for (int part = 0; part < 2; ++part)         // the low plane first
-                        #pragma unroll
-                        for (int k = 0; k < kStageTokens / 16; ++k) {
-                            const uint64_t a = tc_sdesc_sw128_mn(qs + m * 2 * S::kQBlock + k * 2048, S::kQBlock);
-                            const uint64_t b = tc_sdesc_sw128_mn(ps + (part ? 0 : S::kP) + k * 2048, S::kQBlock);
-                            tc_mma_ss(tmem + m * RP, a, b, idesc, i > 0 || part > 0 || k > 0);
-                        }
+                    for (int k = 0; k < kStageTokens / 16; ++k) {
+                        const uint64_t a = tc_sdesc_sw128_mn(qs + m * 2 * S::kQBlock + k * 2048, S::kQBlock);
+                        const uint64_t b = tc_sdesc_sw128_mn(ps + k * 2048, S::kQBlock);
+                        tc_mma_ss(tmem + m * 2 * RP, a, b, idesc, i > 0 || k > 0);
+                    }
                 tc_commit(empty + 8 * s);
             }
             __syncwarp();
@@ -670,16 +695,20 @@ __device__ __forceinline__ void wgrad_tile(const WgradArgs &p, int slice, int ad
     const bool bad = *abort_flag != 0;
     float *s_sum = reinterpret_cast<float *>(s_mem);
     constexpr int kPitch = DB ? RP + 4 : S::kCols + 4;
-    if (warp < kEpiWarps) {
+    if (warp < kWgradWarps) {
         const int sub = warp % 4;
         for (int m = warp / 4; m < S::kCols / 128; m += 2) {
             const int col = 128 * m + 32 * sub + lane;
-            #pragma unroll
+            #pragma unroll 2
             for (int k = 0; k < RP / 8; ++k) {
-                uint32_t v[8];
+                uint32_t v[8], w[8];
                 if (stages > 0 && !bad) {
-                    tc_ld_32x32b_x8(tmem + (uint32_t(32 * sub) << 16) + m * RP + 8 * k, v);
+                    const uint32_t at = tmem + (uint32_t(32 * sub) << 16) + m * 2 * RP + 8 * k;
+                    tc_ld_32x32b_x8(at, v);
+                    tc_ld_32x32b_x8(at + RP, w);
                     tc_wait_ld();
+                    #pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) + __uint_as_float(w[e]));
                 } else {
                     #pragma unroll
                     for (int e = 0; e < 8; ++e) v[e] = bad ? 0x7fffffffu : 0u;
@@ -703,15 +732,25 @@ __device__ __forceinline__ void wgrad_tile(const WgradArgs &p, int slice, int ad
     const int n_rows = DB ? width : r, per = (DB ? r : width) / 8;   // rows, 8-element pieces of one
     const int items = n_rows * per;
     const int i0 = int((long long)items * c / C), i1 = int((long long)items * (c + 1) / C);
-    for (int i = i0 + threadIdx.x; i < i1; i += kThreads) {
+    for (int i = i0 + threadIdx.x; i < i1; i += kWgradThreads) {
         const int row = i / per, col = 8 * (i % per);
         const float *at = s_sum + row * kPitch + col;
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-        for (int k = 0; k < C; ++k) {
-            const float4 u = C > 1 ? ld_cluster4(at, k) : *reinterpret_cast<const float4 *>(at);
-            const float4 v = C > 1 ? ld_cluster4(at + 4, k) : *reinterpret_cast<const float4 *>(at + 4);
-            a.x += u.x, a.y += u.y, a.z += u.z, a.w += u.w;
-            b.x += v.x, b.y += v.y, b.z += v.z, b.w += v.w;
+        if (C > 1) {
+            for (int k0 = 0; k0 < C; k0 += 4) {          // clusters of 2, 4 or 8
+                float4 x[4], y[4];
+                #pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (k0 + k < C) x[k] = ld_cluster4(at, k0 + k), y[k] = ld_cluster4(at + 4, k0 + k);
+                #pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (k0 + k < C) {
+                        a.x += x[k].x, a.y += x[k].y, a.z += x[k].z, a.w += x[k].w;
+                        b.x += y[k].x, b.y += y[k].y, b.z += y[k].z, b.w += y[k].w;
+                    }
+            }
+        } else {
+            a = *reinterpret_cast<const float4 *>(at), b = *reinterpret_cast<const float4 *>(at + 4);
         }
         uint4 o;
         o.x = pack_bf16x2_rn(a.x, a.y), o.y = pack_bf16x2_rn(a.z, a.w);
@@ -728,7 +767,7 @@ __device__ __forceinline__ void wgrad_tile(const WgradArgs &p, int slice, int ad
 }
 
 template <int RP>
-__global__ void __launch_bounds__(kThreads, 1) lora_wgrad_kernel(const WgradArgs p) {
+__global__ void __launch_bounds__(kWgradThreads, 1) lora_wgrad_kernel(const WgradArgs p) {
     using S = WgradShape<RP>;
     constexpr int NS = S::kStages;
     extern __shared__ unsigned char s_raw[];
@@ -739,12 +778,12 @@ __global__ void __launch_bounds__(kThreads, 1) lora_wgrad_kernel(const WgradArgs
     const int warp = threadIdx.x / 32;
     if (threadIdx.x == 0) {
         const uint32_t bar = smem_u32(s_bar);
-        for (int i = 0; i < NS; ++i) mbar_init(bar + 8 * i, kProducers), mbar_init(bar + 8 * (NS + i), 1);
+        for (int i = 0; i < NS; ++i) mbar_init(bar + 8 * i, kWgradProducers), mbar_init(bar + 8 * (NS + i), 1);
         mbar_init(bar + 16 * NS, 1);
         s_abort = 0;
         fence_barrier_init();
     }
-    if (warp == kMmaWarp) {
+    if (warp == kWgradWarps) {
         tc_alloc(smem_u32(&s_tmem), kTmemCols);
         tc_relinquish();
     }
@@ -760,11 +799,16 @@ __global__ void __launch_bounds__(kThreads, 1) lora_wgrad_kernel(const WgradArgs
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == kMmaWarp) tc_dealloc(tmem, kTmemCols);
+    if (warp == kWgradWarps) tc_dealloc(tmem, kTmemCols);
 }
 
 // ---------------------------------------------------------------- host side
 int ceil_div(long long a, long long b) { return int((a + b - 1) / b); }
+
+// Tiles at most: the adapters' and the adapterless tokens' last may be part empty.
+int lora_max_tiles(int tokens, int adapters) {
+    return ceil_div(tokens, kTile) + (adapters < tokens ? adapters : tokens);
+}
 
 template <int RP, bool TRANS>
 cudaError_t launch_tensor_rank(const LoraArgs &p, int sms, cudaStream_t s) {
@@ -775,6 +819,9 @@ cudaError_t launch_tensor_rank(const LoraArgs &p, int sms, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     const int ctas = sms < kMaxRuns ? sms : kMaxRuns;
     e = launch_chained(lora_down_kernel<RP, TRANS>, dim3(ctas), kThreads, D::kSmem, 1, s, p);
+    if (e != cudaSuccess) return e;
+    const int blocks = lora_max_tiles(p.tokens, p.adapters) * (kTile * (RP / 4) / kSumThreads);
+    e = launch_chained(lora_sum_kernel<RP, TRANS>, dim3(blocks), kSumThreads, 0, 1, s, p, ctas);
     if (e != cudaSuccess) return e;
     return launch_chained(lora_up_kernel<RP, TRANS>, dim3(ctas), kThreads, U::kSmem, 1, s, p);
 }
@@ -788,14 +835,13 @@ cudaError_t launch_wgrad_rank(WgradArgs p, int adapters, int sms, cudaStream_t s
     const int slices = p.slices_x + ceil_div(p.N, S::kCols);
     int cluster = 1;
     while (cluster < kMaxCluster && 2LL * slices * adapters * cluster <= sms) cluster *= 2;
-    return launch_chained(lora_wgrad_kernel<RP>, dim3(slices * cluster, adapters), kThreads, S::kSmem, cluster, s, p);
+    return launch_chained(lora_wgrad_kernel<RP>, dim3(slices * cluster, adapters), kWgradThreads, S::kSmem, cluster, s, p);
 }
 
 }  // namespace
 
 size_t lora_partial_bytes(int tokens, int adapters, int rank) {
-    const size_t tiles = size_t(ceil_div(tokens, kTile)) + (adapters < tokens ? adapters : tokens);
-    return (tiles + kMaxRuns) * kTile * padded_rank(rank) * sizeof(float);
+    return (size_t(lora_max_tiles(tokens, adapters)) + kMaxRuns) * kTile * padded_rank(rank) * sizeof(float);
 }
 
 cudaError_t launch_lora_tensor(const LoraArgs &p, bool trans, int sms, cudaStream_t s) {
