@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1) lora_up_kernel(const LoraArgs p) 
     using S = UpShape<RP, TRANS>;
     constexpr int NS = S::kStages, KS = RP / 16;
     extern __shared__ unsigned char s_raw[];
-    __shared__ uint64_t s_bar[2 * NS + 9];
+    __shared__ uint64_t s_bar[2 * NS + 13];
     __shared__ TileSlots s_tiles;
     __shared__ int s_count[2];
     __shared__ int s_abort;
@@ -395,13 +395,13 @@ __global__ void __launch_bounds__(kThreads, 1) lora_up_kernel(const LoraArgs p) 
     unsigned char *s_hi = s_mem + NS * S::kStage, *s_lo = s_hi + plane_bytes(RP);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t full = smem_u32(s_bar), empty = full + 8 * NS, tfull = empty + 8 * NS, tempty = tfull + 16;
-    const uint32_t dfull = tempty + 16, dempty = dfull + 16, hready = dempty + 16;
+    const uint32_t dfull = tempty + 16, dempty = dfull + 32, hready = dempty + 32;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < NS; ++i) mbar_init(full + 8 * i, kProducers), mbar_init(empty + 8 * i, kEpiWarps);
+        for (int i = 0; i < NS; ++i) mbar_init(full + 8 * i, kProducers), mbar_init(empty + 8 * i, kEpiWarps / 2);
         for (int i = 0; i < 2; ++i) {
             mbar_init(tfull + 8 * i, 1), mbar_init(tempty + 8 * i, kThreads / 32);
-            mbar_init(dfull + 8 * i, 1), mbar_init(dempty + 8 * i, kEpiWarps);
         }
+        for (int i = 0; i < 4; ++i) mbar_init(dfull + 8 * i, 1), mbar_init(dempty + 8 * i, kEpiWarps / 2);
         mbar_init(hready, kEpiThreads);
         s_abort = 0;
         fence_barrier_init();
@@ -422,7 +422,10 @@ __global__ void __launch_bounds__(kThreads, 1) lora_up_kernel(const LoraArgs p) 
     const Walk w = make_walk(s_count[0] + s_count[1], (p.out + kCols - 1) / kCols, blockIdx.x, gridDim.x);
     volatile int *abort_flag = &s_abort;
 
-    int i = 0, j = 0, seg = 0, h_seg = 0;            // steps, multiplied steps, tiles, multiplied tiles
+    // steps, tiles, multiplied tiles; step i multiplies into buffer i % 4 of D2
+    int i = 0, seg = 0, h_seg = 0;
+    uint32_t uses = 0;                               // a bit per buffer: the parity of its next use
+    uint32_t used = 0;
     for (long long u = w.u0; u < w.u1; ++seg) {
         const int tile = int(u / w.per), k0 = int(u - (long long)tile * w.per);
         const int n_steps = int(w.u1 - u < w.per - k0 ? w.u1 - u : w.per - k0);
@@ -452,9 +455,11 @@ __global__ void __launch_bounds__(kThreads, 1) lora_up_kernel(const LoraArgs p) 
             if (adapter >= 0) {
                 bool ok = __all_sync(0xffffffffu, mbar_wait(hready, h_seg & 1, abort_flag, p.err));
                 ++h_seg;
-                for (int k = 0; k < n_steps && ok; ++k, ++i, ++j) {
-                    const int s = i % NS, buf = j & 1;
-                    ok = j < 2 || mbar_wait(dempty + 8 * buf, ((j >> 1) - 1) & 1, abort_flag, p.err);
+                for (int k = 0; k < n_steps && ok; ++k, ++i) {
+                    const int s = i % NS, buf = i & 3;
+                    if ((used >> buf) & 1) ok = mbar_wait(dempty + 8 * buf, (~uses >> buf) & 1, abort_flag, p.err);
+                    used |= 1u << buf;
+                    uses ^= 1u << buf;
                     ok = ok && mbar_wait(full + 8 * s, (i / NS) & 1, abort_flag, p.err);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
@@ -480,10 +485,13 @@ __global__ void __launch_bounds__(kThreads, 1) lora_up_kernel(const LoraArgs p) 
                 i += n_steps;
             }
         } else {
-            const int sub = warp % 4, half = warp / 4, my_row = 32 * sub + lane;
-            const uint32_t lanes = tmem + (uint32_t(32 * sub) << 16);
+            // Two groups of four warps take the steps in turn, two buffers of D2 each (with
+            // one the MMA's latency stood in the way: 2650 cycles a step, with two 2300 --
+            // see the figures above); a warp has 32 rows.
+            const int sub = warp % 4, group = warp / 4, my_row = 32 * sub + lane;
             bool bad = false;
             if (seg == 0) pdl_wait();
+            else epi_sync();                         // the MMAs of the tile before have ended
             if (adapter >= 0) {
                 // h's planes of the tile; rows past its tokens are zeros
                 const int start = s_tiles.info[seg & 1][2];
@@ -508,40 +516,44 @@ __global__ void __launch_bounds__(kThreads, 1) lora_up_kernel(const LoraArgs p) 
                 mbar_arrive(hready);
             }
             for (int k = 0; k < n_steps && !in_place; ++k, ++i) {
-                const int s = i % NS, buf = j & 1, col = (k0 + k) * kCols + 64 * half;
-                unsigned char *bs = s_mem + s * S::kStage + half * kBlock;
+                if ((i & 1) != group) continue;
+                const int s = i % NS;
+                const uint32_t lanes = tmem + (uint32_t(32 * sub) << 16) + (i & 3) * kCols;
                 bool ok = mbar_wait(full + 8 * s, (i / NS) & 1, abort_flag, p.err);
-                uint32_t acc[2][32];
                 if (adapter >= 0) {
-                    ok = ok && mbar_wait(dfull + 8 * buf, (j >> 1) & 1, abort_flag, p.err);
-                    ++j;
+                    ok = ok && mbar_wait(dfull + 8 * (i & 3), (uses >> (i & 3)) & 1, abort_flag, p.err);
+                    uses ^= 1u << (i & 3);
                     tc_fence_after();
-                    tc_ld_32x32b_x32(lanes + buf * kCols + 64 * half, acc[0]);
-                    tc_ld_32x32b_x32(lanes + buf * kCols + 64 * half + 32, acc[1]);
-                    tc_wait_ld();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(dempty + 8 * buf);
-                } else {
-                    #pragma unroll
-                    for (int e = 0; e < 32; ++e) acc[0][e] = acc[1][e] = 0x80000000u;   // -0: base as it is
                 }
                 bad |= !__all_sync(0xffffffffu, ok);
-                if (col < p.out && 32 * sub < count) {
-                    #pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        uint4 *at = reinterpret_cast<uint4 *>(bs + sw128(my_row, q));
-                        uint4 b = make_uint4(0, 0, 0, 0);
-                        if (p.base) b = *at;
-                        const uint32_t *d = &acc[q / 4][8 * (q % 4)];
-                        uint4 v;
-                        v.x = pack_bf16x2_rn(bf16_lo_to_f32(b.x) + __uint_as_float(d[0]), bf16_hi_to_f32(b.x) + __uint_as_float(d[1]));
-                        v.y = pack_bf16x2_rn(bf16_lo_to_f32(b.y) + __uint_as_float(d[2]), bf16_hi_to_f32(b.y) + __uint_as_float(d[3]));
-                        v.z = pack_bf16x2_rn(bf16_lo_to_f32(b.z) + __uint_as_float(d[4]), bf16_hi_to_f32(b.z) + __uint_as_float(d[5]));
-                        v.w = pack_bf16x2_rn(bf16_lo_to_f32(b.w) + __uint_as_float(d[6]), bf16_hi_to_f32(b.w) + __uint_as_float(d[7]));
-                        if (adapter < 0) v = b;                  // bit for bit, a NaN's too
-                        if (bad) v = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
-                        *at = v;
+                #pragma unroll 1
+                for (int half = 0; half < 2; ++half) {
+                    const int col = (k0 + k) * kCols + 64 * half;
+                    if (col >= p.out || 32 * sub >= count) break;
+                    unsigned char *bs = s_mem + s * S::kStage + half * kBlock;
+                    if (adapter >= 0 && !bad) {
+                        uint32_t acc[2][32];
+                        tc_ld_32x32b_x32(lanes + 64 * half, acc[0]);
+                        tc_ld_32x32b_x32(lanes + 64 * half + 32, acc[1]);
+                        tc_wait_ld();
+                        #pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            uint4 *at = reinterpret_cast<uint4 *>(bs + sw128(my_row, q));
+                            uint4 b = make_uint4(0, 0, 0, 0);
+                            if (p.base) b = *at;
+                            const uint32_t *d = &acc[q / 4][8 * (q % 4)];
+                            uint4 v;
+                            v.x = pack_bf16x2_rn(bf16_lo_to_f32(b.x) + __uint_as_float(d[0]), bf16_hi_to_f32(b.x) + __uint_as_float(d[1]));
+                            v.y = pack_bf16x2_rn(bf16_lo_to_f32(b.y) + __uint_as_float(d[2]), bf16_hi_to_f32(b.y) + __uint_as_float(d[3]));
+                            v.z = pack_bf16x2_rn(bf16_lo_to_f32(b.z) + __uint_as_float(d[4]), bf16_hi_to_f32(b.z) + __uint_as_float(d[5]));
+                            v.w = pack_bf16x2_rn(bf16_lo_to_f32(b.w) + __uint_as_float(d[6]), bf16_hi_to_f32(b.w) + __uint_as_float(d[7]));
+                            *at = v;
+                        }
+                    } else if (bad || !p.base) {
+                        const uint32_t fill = bad ? 0x7fff7fffu : 0u;
+                        #pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            *reinterpret_cast<uint4 *>(bs + sw128(my_row, q)) = make_uint4(fill, fill, fill, fill);
                     }
                     __syncwarp();
                     #pragma unroll
@@ -553,8 +565,12 @@ __global__ void __launch_bounds__(kThreads, 1) lora_up_kernel(const LoraArgs p) 
                         }
                     }
                 }
+                tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(empty + 8 * s);
+                if (lane == 0) {
+                    if (adapter >= 0) mbar_arrive(dempty + 8 * (i & 3));
+                    mbar_arrive(empty + 8 * s);
+                }
             }
         }
         tile_done(seg, tempty);
@@ -562,7 +578,9 @@ __global__ void __launch_bounds__(kThreads, 1) lora_up_kernel(const LoraArgs p) 
     pdl_wait();
     pdl_launch_dependents();
     cp_async_wait_all();
-    if (warp == kMmaWarp && j > 0) drain_wait(dfull + 8 * ((j - 1) & 1), ((j - 1) >> 1) & 1);
+    if (warp == kMmaWarp)
+        for (int buf = 0; buf < 4; ++buf)
+            if ((used >> buf) & 1) drain_wait(dfull + 8 * buf, (~uses >> buf) & 1);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
