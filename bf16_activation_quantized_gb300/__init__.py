@@ -424,22 +424,37 @@ def splitk_reduce(ws: torch.Tensor, out: torch.Tensor | None = None) -> torch.Te
     return out
 
 
-def _launch(name: str, dev: torch.device, *args) -> None:
-    """One library call on ``dev``'s current torch stream."""
-    fn = getattr(_lib.lib(), name)
-    if dev.index == torch.cuda.current_device():
-        status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+# The current stream's handle and the current device without the objects around
+# them: a call of a few microseconds spends a third of its time there otherwise.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+
+
+def _launch(name: str, index: int, *args) -> None:
+    """One library call on the current torch stream of device ``index``."""
+    fn = getattr(_lib._lib or _lib.lib(), name)
+    if index == _current_device():
+        status = fn(*args, _raw_stream(index))
     else:
-        with torch.cuda.device(dev):
-            status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+        with torch.cuda.device(index):
+            status = fn(*args, _raw_stream(index))
     if status:
         _lib.check(status, name)
 
 
-def _on_device_of(x: torch.Tensor, **others) -> None:
-    for name, t in others.items():
-        if t is not None and t.device != x.device:
-            raise ValueError(f"{name} must be on {x.device}, got {t.device}")
+def _need_on(index: int, t: torch.Tensor, name: str, dtype=None) -> None:
+    """``t`` is a contiguous tensor of ``dtype`` on CUDA device ``index``."""
+    if (isinstance(t, torch.Tensor) and (dtype is None or t.dtype == dtype) and t.is_contiguous()
+            and t.get_device() == index):
+        return
+    _need_cuda(t, name, dtype)
+    raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
+
+
+def _index_of(t: torch.Tensor, name: str, dtype) -> int:
+    """The CUDA device of ``t``, a contiguous tensor of ``dtype``."""
+    _need_cuda(t, name, dtype)
+    return t.get_device()
 
 
 _sort_bytes_cache: dict = {}
@@ -465,49 +480,49 @@ def dispatch(x: torch.Tensor, ids: torch.Tensor, num_groups: int):
     is the row of xs that holds the copy, or ~row (negative) for a dropped slot,
     whose row lies past the groups and holds zeros.  The order is stable: inside
     a group rows stand by token, then slot."""
-    _need_cuda(x, "x", torch.bfloat16)
-    _need_cuda(ids, "ids")
+    dev = _index_of(x, "x", torch.bfloat16)
+    _need_on(dev, ids, "ids")
     if x.dim() != 2 or ids.dim() != 2 or ids.shape[0] != x.shape[0]:
         raise ValueError("x must be [T, K] and ids [T, k]")
-    if ids.dtype not in (torch.int32, torch.int64):
+    if ids.dtype not in _ID_DTYPES:
         raise ValueError(f"ids must be int32 or int64, got {ids.dtype}")
-    _on_device_of(x, ids=ids)
     T, K = x.shape
     k = ids.shape[1]
-    dev = x.device
     need = _sort_bytes(T, k, num_groups)
-    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    xs = torch.empty((T * k, K), dtype=torch.bfloat16, device=dev)
-    m_sizes = torch.empty(num_groups, dtype=torch.int32, device=dev)
-    slots = torch.empty((T, k), dtype=torch.int32, device=dev)
+    ws = x.new_empty(need, dtype=torch.uint8) if need else None
+    xs = x.new_empty((T * k, K))
+    m_sizes = x.new_empty(num_groups, dtype=torch.int32)
+    slots = x.new_empty((T, k), dtype=torch.int32)
     _launch("w4a16_dispatch", dev, x.data_ptr(), ids.data_ptr(), ids.element_size(), xs.data_ptr(),
             m_sizes.data_ptr(), slots.data_ptr(), T, k, K, num_groups,
             ws.data_ptr() if need else None, need)
     return xs, m_sizes, slots
 
 
+_ID_DTYPES = (torch.int32, torch.int64)
 _WEIGHT_DTYPES = (torch.float32, torch.bfloat16)
 
 
-def _need_slots(rows: torch.Tensor, slots: torch.Tensor, weights, name: str):
-    _need_cuda(rows, name, torch.bfloat16)
-    _need_cuda(slots, "slots", torch.int32)
+def _need_slots(rows: torch.Tensor, slots: torch.Tensor, weights, name: str) -> int:
+    dev = _index_of(rows, name, torch.bfloat16)
+    _need_on(dev, slots, "slots", torch.int32)
     if rows.dim() != 2 or slots.dim() != 2 or rows.shape[0] != slots.numel():
         raise ValueError(f"{name} must be [T*k, N] for slots [T, k]")
     if weights is not None:
-        _need_cuda(weights, "weights")
+        _need_on(dev, weights, "weights")
         if weights.dtype not in _WEIGHT_DTYPES or weights.shape != slots.shape:
             raise ValueError("weights must be float32 or bfloat16 with the shape of slots")
-    _on_device_of(rows, slots=slots, weights=weights)
+    return dev
 
 
 def _combine(ys, slots, weights, name) -> torch.Tensor:
-    _need_slots(ys, slots, weights, name)
+    dev = _need_slots(ys, slots, weights, name)
     T, k = slots.shape
-    y = torch.empty((T, ys.shape[1]), dtype=torch.bfloat16, device=ys.device)
-    _launch("w4a16_combine", ys.device, ys.data_ptr(), slots.data_ptr(),
+    N = ys.shape[1]
+    y = ys.new_empty((T, N))
+    _launch("w4a16_combine", dev, ys.data_ptr(), slots.data_ptr(),
             None if weights is None else weights.data_ptr(),
-            0 if weights is None else weights.element_size(), y.data_ptr(), T, k, ys.shape[1])
+            0 if weights is None else weights.element_size(), y.data_ptr(), T, k, N)
     return y
 
 
@@ -536,16 +551,15 @@ def combine_backward(dy: torch.Tensor, ys: torch.Tensor, slots: torch.Tensor, we
     dweights[t, j] = <dy[t], ys[slots[t, j]]>, 0 for a dropped slot."""
     if weights is None:
         raise ValueError("weights must be a CUDA tensor")
-    _need_cuda(dy, "dy", torch.bfloat16)
-    _need_slots(ys, slots, weights, "ys")
+    dev = _need_slots(ys, slots, weights, "ys")
     T, k = slots.shape
     N = ys.shape[1]
-    if tuple(dy.shape) != (T, N):
+    _need_on(dev, dy, "dy", torch.bfloat16)
+    if dy.shape != (T, N):
         raise ValueError("dy must be [T, N]")
-    _on_device_of(ys, dy=dy)
     dys = torch.empty_like(ys)
     dweights = torch.empty_like(weights)
-    _launch("w4a16_combine_backward", ys.device, dy.data_ptr(), ys.data_ptr(), slots.data_ptr(),
+    _launch("w4a16_combine_backward", dev, dy.data_ptr(), ys.data_ptr(), slots.data_ptr(),
             weights.data_ptr(), weights.element_size(), dys.data_ptr(), dweights.data_ptr(), T, k, N)
     return dys, dweights
 
@@ -553,7 +567,7 @@ def combine_backward(dy: torch.Tensor, ys: torch.Tensor, slots: torch.Tensor, we
 _lora_bytes_cache: dict = {}
 
 
-def _lora_workspace(dev, tokens: int, adapters: int, rank: int, backward: int):
+def _lora_workspace(x, tokens: int, adapters: int, rank: int, backward: int):
     key = (tokens, adapters, rank, backward)
     need = _lora_bytes_cache.get(key)
     if need is None:
@@ -561,37 +575,35 @@ def _lora_workspace(dev, tokens: int, adapters: int, rank: int, backward: int):
         _lib.check(_lib.lib().w4a16_lora_workspace_bytes(tokens, adapters, rank, backward, ctypes.byref(nb)),
                    "w4a16_lora_workspace_bytes")
         need = _lora_bytes_cache[key] = int(nb.value)
-    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    ws = x.new_empty(need, dtype=torch.uint8) if need else None
     return ws, need
 
 
 def _need_lora(x, lora_a, lora_b, adapters, lora_scales):
-    """Checks of what lora_add and its gradient share: (T, L, r, N, K)."""
-    _need_cuda(x, "x", torch.bfloat16)
-    _need_cuda(lora_a, "lora_a", torch.bfloat16)
-    _need_cuda(lora_b, "lora_b", torch.bfloat16)
-    _need_cuda(adapters, "adapters")
-    _need_cuda(lora_scales, "lora_scales", torch.float32)
+    """Checks of what lora_add and its gradient share: (device, T, L, r, N, K)."""
+    dev = _index_of(x, "x", torch.bfloat16)
+    _need_on(dev, lora_a, "lora_a", torch.bfloat16)
+    _need_on(dev, lora_b, "lora_b", torch.bfloat16)
+    _need_on(dev, adapters, "adapters")
+    _need_on(dev, lora_scales, "lora_scales", torch.float32)
     if x.dim() != 2 or lora_a.dim() != 3 or lora_b.dim() != 3:
         raise ValueError("x must be [T, K], lora_a [L, r, K] and lora_b [L, N, r]")
     T, K = x.shape
     L, r, ka = lora_a.shape
-    N = lora_b.shape[1]
-    if ka != K or lora_b.shape[0] != L or lora_b.shape[2] != r:
+    lb, N, rb = lora_b.shape
+    if ka != K or lb != L or rb != r:
         raise ValueError("lora_a must be [L, r, K] and lora_b [L, N, r] for x [T, K]")
-    if adapters.dtype not in (torch.int32, torch.int64) or tuple(adapters.shape) != (T,):
+    if adapters.dtype not in _ID_DTYPES or adapters.shape != (T,):
         raise ValueError("adapters must be int32 or int64 [T]")
-    if tuple(lora_scales.shape) != (L,):
+    if lora_scales.shape != (L,):
         raise ValueError("lora_scales must be float32 [L]")
-    _on_device_of(x, lora_a=lora_a, lora_b=lora_b, adapters=adapters, lora_scales=lora_scales)
-    return T, L, r, N, K
+    return dev, T, L, r, N, K
 
 
-def _need_rows(t, name, shape, x, dtype=torch.bfloat16):
-    _need_cuda(t, name, dtype)
-    if tuple(t.shape) != shape:
+def _need_rows(index, t, name, shape, dtype=torch.bfloat16):
+    _need_on(index, t, name, dtype)
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}")
-    _on_device_of(x, **{name: t})
 
 
 def lora_add(x: torch.Tensor, lora_a: torch.Tensor, lora_b: torch.Tensor, adapters: torch.Tensor,
@@ -606,16 +618,15 @@ def lora_add(x: torch.Tensor, lora_a: torch.Tensor, lora_b: torch.Tensor, adapte
     result) or None for zeros.  ``out`` may be base itself.  Returns y bf16
     [T, N], with ``return_hidden`` also A . x (float32 [T, r]), which
     lora_add_backward takes."""
-    T, L, r, N, K = _need_lora(x, lora_a, lora_b, adapters, lora_scales)
-    dev = x.device
+    dev, T, L, r, N, K = _need_lora(x, lora_a, lora_b, adapters, lora_scales)
     if base is not None:
-        _need_rows(base, "base", (T, N), x)
+        _need_rows(dev, base, "base", (T, N))
     if out is None:
-        out = torch.empty((T, N), dtype=torch.bfloat16, device=dev)
+        out = x.new_empty((T, N))
     else:
-        _need_rows(out, "out", (T, N), x)
-    hidden = torch.empty((T, r), dtype=torch.float32, device=dev) if return_hidden else None
-    ws, need = _lora_workspace(dev, T, L, r, 0)
+        _need_rows(dev, out, "out", (T, N))
+    hidden = x.new_empty((T, r), dtype=torch.float32) if return_hidden else None
+    ws, need = _lora_workspace(x, T, L, r, 0)
     _launch("w4a16_lora_add", dev, x.data_ptr(), lora_a.data_ptr(), lora_b.data_ptr(), adapters.data_ptr(),
             adapters.element_size(), lora_scales.data_ptr(), None if base is None else base.data_ptr(),
             out.data_ptr(), hidden.data_ptr() if return_hidden else None, T, L, r, N, K,
@@ -632,15 +643,14 @@ def lora_add_backward(dy: torch.Tensor, x: torch.Tensor, hidden: torch.Tensor, l
     dy: bf16 [T, N]; hidden: what lora_add returned; dx_base: bf16 [T, K], the
     shared projection's own gradient, which the adapters' part is added to.
     base's gradient is dy."""
-    T, L, r, N, K = _need_lora(x, lora_a, lora_b, adapters, lora_scales)
-    _need_rows(dy, "dy", (T, N), x)
-    _need_rows(hidden, "hidden", (T, r), x, torch.float32)
+    dev, T, L, r, N, K = _need_lora(x, lora_a, lora_b, adapters, lora_scales)
+    _need_rows(dev, dy, "dy", (T, N))
+    _need_rows(dev, hidden, "hidden", (T, r), torch.float32)
     if dx_base is not None:
-        _need_rows(dx_base, "dx_base", (T, K), x)
-    dev = x.device
-    dx = torch.empty((T, K), dtype=torch.bfloat16, device=dev)
+        _need_rows(dev, dx_base, "dx_base", (T, K))
+    dx = torch.empty_like(x)
     da, db = torch.empty_like(lora_a), torch.empty_like(lora_b)
-    ws, need = _lora_workspace(dev, T, L, r, 1)
+    ws, need = _lora_workspace(x, T, L, r, 1)
     _launch("w4a16_lora_add_backward", dev, dy.data_ptr(), x.data_ptr(), hidden.data_ptr(), lora_a.data_ptr(),
             lora_b.data_ptr(), adapters.data_ptr(), adapters.element_size(), lora_scales.data_ptr(),
             None if dx_base is None else dx_base.data_ptr(), dx.data_ptr(), da.data_ptr(), db.data_ptr(),
