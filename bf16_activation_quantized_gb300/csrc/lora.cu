@@ -27,7 +27,12 @@ constexpr int kFewThreads = 256;
 constexpr int kFewWarps = kFewThreads / 32;
 constexpr int kStepCols = 32;          // columns of a step: 16 bytes per lane of a quad
 constexpr int kFewTile = 16;
-constexpr int kFewTokens = 128;        // up to this many tokens take this kernel
+// Up to kFewTokens tokens take this kernel, and up to kFewTokensEach while the
+// adapters have at most 16 each on average.  Measured at 8192 x 8192 and rank 16
+// (64), this kernel / the tensor core kernels: 192 tokens of 1 adapter 13.6 / 19.1
+// us (27.4 / 21.6), of 16 13.4 / 26.2 (23.0 / 30.5); 384 tokens of 16 19.2 / 27.6
+// (40.3 / 32.1); 512 tokens of 1 36.4 / 25.7, of 128 32.0 / 108 (78 / 118).
+constexpr int kFewTokens = 192, kFewTokensEach = 512;
 constexpr int kMaxRank = 128;
 
 __device__ __forceinline__ void mma_acc(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -52,7 +57,7 @@ __global__ void __launch_bounds__(kFewThreads, RP <= 32 ? 2 : 1) lora_few_kernel
     constexpr int TM = kFewTile, NT = RP / 8, QN = RP >= 32 ? RP / 32 : 1, KS = RP / 16;
     constexpr int PS = RP + 4;                           // floats of a row of h
     constexpr int U = RP <= 32 ? 4 : RP == 64 ? 2 : 1;   // steps of the first product loaded together
-    constexpr int PF = RP == 16 ? 4 : RP == 32 ? 2 : 1;  // steps of the second
+    constexpr int PF = RP <= 32 ? 4 : RP == 64 ? 2 : 1;  // steps of the second
     constexpr int kQuads = RP / 4;
     extern __shared__ float s_mem[];
     float *s_part = s_mem;                               // [kFewWarps][TM][PS]
@@ -97,15 +102,14 @@ __global__ void __launch_bounds__(kFewThreads, RP <= 32 ? 2 : 1) lora_few_kernel
     const long long row0 = g < count ? (long long)s_rows[g] * p.out : -1;
     const long long row1 = g + 8 < count ? (long long)s_rows[g + 8] * p.out : -1;
     uint32_t w[PF][RP / 2];
-    uint4 base[PF][2];
+    uint4 base[PF];                                      // of rows g; rows g + 8 come when they are needed
     const auto load_up = [&](int nb) {
         #pragma unroll
         for (int f = 0; f < PF; ++f) {
             if (nb + f >= n1) break;
             const int col = (nb + f) * kStepCols, mine = col + 8 * t;
-            base[f][0] = base[f][1] = make_uint4(0, 0, 0, 0);
-            if (p.base && row0 >= 0) base[f][0] = load_cols8(p.base + row0 + mine, p.out - mine, p.vec_out);
-            if (p.base && row1 >= 0) base[f][1] = load_cols8(p.base + row1 + mine, p.out - mine, p.vec_out);
+            base[f] = make_uint4(0, 0, 0, 0);
+            if (p.base && row0 >= 0) base[f] = load_cols8(p.base + row0 + mine, p.out - mine, p.vec_out);
             // B's rows of columns {8 (i/2) + 2 j + i%2}
             #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -193,9 +197,11 @@ __global__ void __launch_bounds__(kFewThreads, RP <= 32 ? 2 : 1) lora_few_kernel
         const int row = i / kQuads, rank = 4 * (i % kQuads);
         float4 part[kMaxCluster], v = make_float4(0.f, 0.f, 0.f, 0.f);
         #pragma unroll
-        for (int k = 0; k < kMaxCluster; ++k) part[k] = ld_cluster4(s_part + row * PS + rank, k);
+        for (int k = 0; k < kMaxCluster; ++k)
+            if (k < C) part[k] = ld_cluster4(s_part + row * PS + rank, k);
         #pragma unroll
-        for (int k = 0; k < kMaxCluster; ++k) v.x += part[k].x, v.y += part[k].y, v.z += part[k].z, v.w += part[k].w;
+        for (int k = 0; k < kMaxCluster; ++k)
+            if (k < C) v.x += part[k].x, v.y += part[k].y, v.z += part[k].z, v.w += part[k].w;
         // a rank past r is 0 also where x holds infinities (0 * inf)
         if (rank >= r) v = make_float4(0.f, 0.f, 0.f, 0.f);
         if (p.hidden && c == 0 && rank < r)
@@ -243,7 +249,11 @@ __global__ void __launch_bounds__(kFewThreads, RP <= 32 ? 2 : 1) lora_few_kernel
                 for (int h = 0; h < 2; ++h) {
                     const long long row = h ? row1 : row0;
                     if (row < 0) continue;
-                    const uint4 b = base[f][h];
+                    uint4 b = base[f];
+                    if (h) {
+                        b = make_uint4(0, 0, 0, 0);
+                        if (p.base) b = load_cols8(p.base + row1 + mine, p.out - mine, p.vec_out);
+                    }
                     uint4 v;
                     v.x = pack_bf16x2_rn(bf16_lo_to_f32(b.x) + acc[0][2 * h], bf16_hi_to_f32(b.x) + acc[0][2 * h + 1]);
                     v.y = pack_bf16x2_rn(bf16_lo_to_f32(b.y) + acc[1][2 * h], bf16_hi_to_f32(b.y) + acc[1][2 * h + 1]);
@@ -262,21 +272,38 @@ __global__ void __launch_bounds__(kFewThreads, RP <= 32 ? 2 : 1) lora_few_kernel
 bool aligned(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 int ceil_div(long long a, long long b) { return int((a + b - 1) / b); }
 
+bool takes_few(int tokens, int adapters) {
+    return tokens <= kFewTokens || (tokens <= kFewTokensEach && tokens <= kFewTile * adapters);
+}
+
+// CTAs of a cluster: eight where all clusters can be resident at once (two CTAs
+// per SM up to rank 32, else one), counting a cluster per adapter in use and one
+// per 16 tokens.  Measured at 8192 x 8192 with 64 adapters, 8 / 4 / 2 CTAs: rank
+// 16, 32 tokens 6.8 / 7.7 / 12.1 us, 64 tokens 12.6 / 10.2 / 12.8; rank 64, 16
+// tokens 10.7 / 15.6 / 26.6, 64 tokens 34.9 / 34.9 / 30.4.
+int few_cluster(int tokens, int adapters, int padded, int sms) {
+    const int used = adapters + tokens / kFewTile, clusters = tokens < used ? tokens : used;
+    const int slots = (padded <= 32 ? 2 : 1) * sms;
+    int c = kMaxCluster;
+    while (c > 2 && clusters * c > slots) c /= 2;
+    return c;
+}
+
 template <int RP>
-cudaError_t launch_few(const LoraArgs &p, cudaStream_t s) {
+cudaError_t launch_few(const LoraArgs &p, int sms, cudaStream_t s) {
     constexpr size_t smem = size_t(kFewWarps + 1) * kFewTile * (RP + 4) * 4;
     const cudaError_t e = allow_smem<lora_few_kernel<RP>>(smem);
     if (e != cudaSuccess) return e;
-    return launch_chained(lora_few_kernel<RP>, dim3(unsigned(p.tokens) * kMaxCluster), kFewThreads, smem, kMaxCluster,
-                          s, p);
+    const int cluster = few_cluster(p.tokens, p.adapters, RP, sms);
+    return launch_chained(lora_few_kernel<RP>, dim3(unsigned(p.tokens) * cluster), kFewThreads, smem, cluster, s, p);
 }
 
-cudaError_t launch_lora_few(const LoraArgs &p, cudaStream_t s) {
+cudaError_t launch_lora_few(const LoraArgs &p, int sms, cudaStream_t s) {
     switch (padded_rank(p.rank)) {
-        case 16: return launch_few<16>(p, s);
-        case 32: return launch_few<32>(p, s);
-        case 64: return launch_few<64>(p, s);
-        default: return launch_few<128>(p, s);
+        case 16: return launch_few<16>(p, sms, s);
+        case 32: return launch_few<32>(p, sms, s);
+        case 64: return launch_few<64>(p, sms, s);
+        default: return launch_few<128>(p, sms, s);
     }
 }
 
@@ -296,7 +323,7 @@ LoraWorkspace lora_workspace(int tokens, int adapters, int rank, bool backward) 
     w.g = w.partial + lora_partial_bytes(tokens, adapters, rank);
     w.h = w.g + size_t(tokens) * plane_pitch(padded_rank(rank));
     w.total = w.h + (backward ? size_t(tokens) * plane_pitch(padded_rank(rank)) : 0);
-    if (!backward && tokens <= kFewTokens) w.total = 0;
+    if (!backward && takes_few(tokens, adapters)) w.total = 0;
     return w;
 }
 
@@ -361,7 +388,7 @@ w4a16_status w4a16_lora_add(const w4a16_bf16 *X, const w4a16_bf16 *A, const w4a1
     p.tokens = tokens, p.adapters = num_adapters, p.rank = rank, p.in = K, p.out = N;
     p.vec_in = 1;
     p.vec_out = N % 8 == 0 && aligned(base, 16) && aligned(Y, 16);
-    if (tokens <= kFewTokens) return from_cuda(launch_lora_few(p, s));
+    if (takes_few(tokens, num_adapters)) return from_cuda(launch_lora_few(p, sms, s));
     char *ws = static_cast<char *>(workspace);
     int *order = reinterpret_cast<int *>(ws + w.order), *sizes = reinterpret_cast<int *>(ws + w.sizes);
     cudaError_t e = launch_sort(adapters_dev, id_bytes, tokens, num_adapters,

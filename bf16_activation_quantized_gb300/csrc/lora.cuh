@@ -178,6 +178,7 @@ __device__ void find_tile_few(const LoraArgs &p, int tile, int *rows, int *out) 
     const int lane = threadIdx.x & 31;
     const int key = adapter_of(p, tile);
     int before = 0, count = 0;
+    #pragma unroll 4
     for (int t0 = 0; t0 < p.tokens; t0 += 32) {
         const int t = t0 + lane;
         const bool same = t < p.tokens && adapter_of(p, t) == key;
