@@ -310,9 +310,10 @@ cudaError_t launch_lora_few(const LoraArgs &p, int sms, cudaStream_t s) {
 size_t round16(size_t b) { return (b + 15) / 16 * 16; }
 
 // Workspace: order [tokens], sizes [adapters], the sort's counts, the partial
-// sums of h, its planes, and in the gradient s h's planes.
+// sums (of h, then of the weight gradients), the planes of h or g, and in the
+// gradient the planes of g and s h by tile.
 struct LoraWorkspace {
-    size_t order, sizes, counts, partial, g, h, total;
+    size_t order, sizes, counts, partial, planes, tg, th, total;
 };
 LoraWorkspace lora_workspace(int tokens, int adapters, int rank, bool backward) {
     LoraWorkspace w;
@@ -320,9 +321,11 @@ LoraWorkspace lora_workspace(int tokens, int adapters, int rank, bool backward) 
     w.sizes = round16(size_t(tokens) * 4);
     w.counts = w.sizes + round16(size_t(adapters) * 4);
     w.partial = w.counts + round16(sort_bytes(tokens, adapters));
-    w.g = w.partial + lora_partial_bytes(tokens, adapters, rank);
-    w.h = w.g + size_t(tokens) * plane_pitch(padded_rank(rank));
-    w.total = w.h + (backward ? size_t(tokens) * plane_pitch(padded_rank(rank)) : 0);
+    w.planes = w.partial + lora_partial_bytes(tokens, adapters, rank, backward);
+    w.tg = w.planes + size_t(tokens) * plane_pitch(padded_rank(rank));
+    const size_t by_tile = backward ? size_t(lora_max_tiles(tokens, adapters)) * tile_planes(padded_rank(rank)) * 2 : 0;
+    w.th = w.tg + by_tile;
+    w.total = w.th + by_tile;
     if (!backward && takes_few(tokens, adapters)) w.total = 0;
     return w;
 }
@@ -338,8 +341,9 @@ w4a16_status from_cuda(cudaError_t e) { return e == cudaSuccess ? W4A16_OK : W4A
 
 void place_workspace(LoraArgs *p, char *ws, const LoraWorkspace &w) {
     p->partial = reinterpret_cast<float *>(ws + w.partial);
-    p->pg = reinterpret_cast<uint16_t *>(ws + w.g);
-    p->ph = reinterpret_cast<uint16_t *>(ws + w.h);
+    p->planes = reinterpret_cast<uint16_t *>(ws + w.planes);
+    p->tg = reinterpret_cast<uint16_t *>(ws + w.tg);
+    p->th = reinterpret_cast<uint16_t *>(ws + w.th);
 }
 
 w4a16_status check_workspace(const LoraWorkspace &w, const void *ws, size_t bytes) {
@@ -440,9 +444,10 @@ w4a16_status w4a16_lora_add_backward(const w4a16_bf16 *dY, const w4a16_bf16 *X, 
     e = launch_lora_tensor(p, true, sms, s);
     if (e != cudaSuccess) return W4A16_ERR_CUDA;
     WgradArgs q = {};
-    q.x = X, q.dy = dY, q.pg = p.pg, q.ph = p.ph, q.order = order, q.sizes = sizes, q.da = dA, q.db = dB;
-    q.err = p.err, q.rank = rank, q.K = K, q.N = N, q.vec_x = 1, q.vec_dy = p.vec_in;
-    return from_cuda(launch_wgrad(q, num_adapters, sms, s));
+    q.x = X, q.dy = dY, q.tg = p.tg, q.th = p.th, q.order = order, q.sizes = sizes, q.partial = p.partial;
+    q.da = dA, q.db = dB, q.err = p.err, q.adapters = num_adapters, q.rank = rank, q.K = K, q.N = N;
+    q.vec_x = 1, q.vec_dy = p.vec_in;
+    return from_cuda(launch_wgrad(q, sms, s));
 }
 
 }  // extern "C"

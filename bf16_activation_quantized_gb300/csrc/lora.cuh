@@ -11,8 +11,11 @@
 
 namespace w4a16 {
 
-// Bytes of a sorted token's row of g or s h: two bf16 planes (hi, lo) of RP.
+// Bytes of a sorted token's row of h or g: two bf16 planes (hi, lo) of RP ranks.
 __host__ __device__ constexpr int plane_pitch(int RP) { return 4 * RP; }
+// The same by tile of 128 tokens of an adapter, for the weight gradients: rows of
+// 128 tokens, RP of hi and RP of lo, zeros past the last token.  In elements.
+__host__ __device__ constexpr int tile_planes(int RP) { return 2 * RP * 128; }
 
 struct LoraArgs {
     const uint16_t *x;       // [tokens][in]
@@ -24,7 +27,8 @@ struct LoraArgs {
     const uint16_t *base;    // [tokens][out] or nullptr
     uint16_t *y;             // [tokens][out]
     float *hidden;           // [tokens][r]: forward h, written (or nullptr); gradient: read
-    uint16_t *pg, *ph;       // planes of the sorted tokens: s h or g; in the gradient also s h
+    uint16_t *planes;        // of the sorted tokens: s h (gradient: g), see plane_pitch
+    uint16_t *tg, *th;       // gradient: planes of g and of s h by tile, see tile_planes
     float *partial;          // partial sums of h (many tokens)
     int *err;
     int id_bytes, tokens, adapters, rank, in, out;
@@ -233,11 +237,13 @@ __device__ void find_tile_sorted(const LoraArgs &p, int tile, int *rows, int *ou
 
 struct WgradArgs {
     const uint16_t *x, *dy;        // [tokens][K], [tokens][N]
-    const uint16_t *pg, *ph;       // g and s h of the sorted tokens (plane_pitch rows)
+    const uint16_t *tg, *th;       // g and s h by tile (tile_planes)
     const int *order, *sizes;
+    float *partial;                // two tiles of sums per CTA
     uint16_t *da, *db;             // [L][r][K], [L][N][r]
     int *err;
-    int rank, K, N, slices_x;      // column slices of x, then of dy
+    int adapters, rank, K, N;
+    int slices_x, slices;          // column slices of x, of x and dy
     int vec_x, vec_dy;
 };
 
@@ -261,9 +267,10 @@ cudaError_t allow_smem(size_t bytes) {
 }
 
 // lora_tensor.cu.  lora_partial_bytes: the workspace of the partial sums.
-size_t lora_partial_bytes(int tokens, int adapters, int rank);
+size_t lora_partial_bytes(int tokens, int adapters, int rank, bool backward);
+int lora_max_tiles(int tokens, int adapters);
 cudaError_t launch_lora_tensor(const LoraArgs &p, bool trans, int sms, cudaStream_t s);
-cudaError_t launch_wgrad(const WgradArgs &p, int adapters, int sms, cudaStream_t s);
+cudaError_t launch_wgrad(const WgradArgs &p, int sms, cudaStream_t s);
 
 inline int padded_rank(int r) { return r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128; }
 

@@ -315,9 +315,10 @@ __global__ void __launch_bounds__(kThreads, 1) lora_down_kernel(const LoraArgs p
 }
 
 // ------------------------------------------------------------------ its sums
-// h of every tile: its slots in CTA order, to the planes p.pg (scaled) and
-// p.hidden; in the gradient also s h's planes from p.hidden.  Four ranks a
-// thread, all of a tile's slots (5 of them at 4096 tokens) on their way at once.
+// h of every tile: its slots in CTA order, to the planes (scaled) and p.hidden;
+// in the gradient the planes of g, and of s h from p.hidden, by tile too.  Four
+// ranks a thread, all of a tile's slots (5 of them at 4096 tokens) on their way
+// at once.
 constexpr int kSumThreads = 256;
 
 template <int RP, bool TRANS>
@@ -325,6 +326,7 @@ __global__ void __launch_bounds__(kSumThreads) lora_sum_kernel(const LoraArgs p,
     constexpr int kPieces = RP / 4, kRows = kSumThreads / kPieces, kBlocks = kTile / kRows, kSlots = 8;
     __shared__ int s_rows[kTile];
     __shared__ int s_info[3], s_count[2];
+    __shared__ uint16_t s_t[TRANS ? 2 : 1][TRANS ? 2 * RP : 1][kRows + 2];   // g, s h: [plane, rank][row]
     // The first product's CTAs let this kernel start after the sort had ended.
     pdl_launch_dependents();
     const int tile = blockIdx.x / kBlocks, row0 = blockIdx.x % kBlocks * kRows;
@@ -335,38 +337,57 @@ __global__ void __launch_bounds__(kSumThreads) lora_sum_kernel(const LoraArgs p,
     __syncthreads();
     const int adapter = s_info[0], count = s_info[1], r = p.rank;
     const int row = row0 + threadIdx.x / kPieces, rank = 4 * (threadIdx.x % kPieces);
+    const bool token = row < count, in = token && rank < r;
     pdl_wait();
-    if (row >= count) return;
-    float4 *hidden = reinterpret_cast<float4 *>(p.hidden + (long long)s_rows[row] * r + rank);
+    if (count == 0) return;
+    float4 *hidden = reinterpret_cast<float4 *>(p.hidden + (in ? (long long)s_rows[row] * r + rank : 0));
     if (adapter < 0) {
-        if (!TRANS && p.hidden && rank < r) *hidden = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (!TRANS && p.hidden && in) *hidden = make_float4(0.f, 0.f, 0.f, 0.f);
         return;
     }
-    const Walk d = make_walk(s_count[0], (p.in + kCols - 1) / kCols, 0, down_ctas);
-    const long long first = (long long)tile * d.per;
-    const int b0 = run_owner(d.units, d.ctas, first), b1 = run_owner(d.units, d.ctas, first + d.per - 1);
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f), w = v;
-    if (TRANS && rank < r) w = *hidden;
-    const float *at = p.partial + ((long long)(tile + b0) * kTile + row) * RP + rank;
-    for (int b = b0; b <= b1; b += kSlots) {
-        float4 u[kSlots];
-        #pragma unroll
-        for (int k = 0; k < kSlots; ++k)
-            if (b + k <= b1) u[k] = *reinterpret_cast<const float4 *>(at + (long long)(b - b0 + k) * kTile * RP);
-        #pragma unroll
-        for (int k = 0; k < kSlots; ++k)
-            if (b + k <= b1) v.x += u[k].x, v.y += u[k].y, v.z += u[k].z, v.w += u[k].w;
+    if (in) {
+        const Walk d = make_walk(s_count[0], (p.in + kCols - 1) / kCols, 0, down_ctas);
+        const long long first = (long long)tile * d.per;
+        const int b0 = run_owner(d.units, d.ctas, first), b1 = run_owner(d.units, d.ctas, first + d.per - 1);
+        if (TRANS) w = *hidden;
+        const float *at = p.partial + ((long long)(tile + b0) * kTile + row) * RP + rank;
+        for (int b = b0; b <= b1; b += kSlots) {
+            float4 u[kSlots];
+            #pragma unroll
+            for (int k = 0; k < kSlots; ++k)
+                if (b + k <= b1) u[k] = *reinterpret_cast<const float4 *>(at + (long long)(b - b0 + k) * kTile * RP);
+            #pragma unroll
+            for (int k = 0; k < kSlots; ++k)
+                if (b + k <= b1) v.x += u[k].x, v.y += u[k].y, v.z += u[k].z, v.w += u[k].w;
+        }
+        if (!TRANS && p.hidden) *hidden = v;
     }
-    if (!TRANS && p.hidden && rank < r) *hidden = v;
-    if (rank >= r) v = make_float4(0.f, 0.f, 0.f, 0.f);  // also where x holds infinities (0 * inf)
+    // ranks past r are zeros (also where x holds infinities: 0 * inf)
     const float scale = p.scale[adapter];
-    const long long out = (long long)(s_info[2] + row) * (plane_pitch(RP) / 2) + rank;
     uint2 hi, lo;
     split2(scale * v.x, scale * v.y, hi.x, lo.x), split2(scale * v.z, scale * v.w, hi.y, lo.y);
-    *reinterpret_cast<uint2 *>(p.pg + out) = hi, *reinterpret_cast<uint2 *>(p.pg + out + RP) = lo;
+    if (token) {
+        const long long out = (long long)(s_info[2] + row) * (plane_pitch(RP) / 2) + rank;
+        *reinterpret_cast<uint2 *>(p.planes + out) = hi, *reinterpret_cast<uint2 *>(p.planes + out + RP) = lo;
+    }
     if (TRANS) {
-        split2(scale * w.x, scale * w.y, hi.x, lo.x), split2(scale * w.z, scale * w.w, hi.y, lo.y);
-        *reinterpret_cast<uint2 *>(p.ph + out) = hi, *reinterpret_cast<uint2 *>(p.ph + out + RP) = lo;
+        const int mine = threadIdx.x / kPieces;
+        #pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            if (which) split2(scale * w.x, scale * w.y, hi.x, lo.x), split2(scale * w.z, scale * w.w, hi.y, lo.y);
+            #pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                s_t[which][rank + e][mine] = uint16_t((e < 2 ? hi.x : hi.y) >> (16 * (e & 1)));
+                s_t[which][RP + rank + e][mine] = uint16_t((e < 2 ? lo.x : lo.y) >> (16 * (e & 1)));
+            }
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < 2 * 2 * RP * kRows / 2; i += kSumThreads) {
+            const int pair = i % (kRows / 2), line = i / (kRows / 2) % (2 * RP), which = i / (kRows / 2) / (2 * RP);
+            uint16_t *out = (which ? p.th : p.tg) + (long long)tile * tile_planes(RP) + line * kTile + row0 + 2 * pair;
+            *reinterpret_cast<uint32_t *>(out) = *reinterpret_cast<const uint32_t *>(&s_t[which][line][2 * pair]);
+        }
     }
 }
 
@@ -486,8 +507,8 @@ __global__ void __launch_bounds__(kThreads, 1) lora_up_kernel(const LoraArgs p) 
             }
         } else {
             // Two groups of four warps take the steps in turn, two buffers of D2 each (with
-            // one the MMA's latency stood in the way: 2650 cycles a step, with two 2300 --
-            // see the figures above); a warp has 32 rows.
+            // one, 1100 to 1700 of a group's 5300 cycles a step went by waiting for the
+            // MMAs: 46.4 against 43.2 us for 2858 tokens at 17408 columns); a warp has 32 rows.
             const int sub = warp % 4, group = warp / 4, my_row = 32 * sub + lane;
             bool bad = false;
             if (seg == 0) pdl_wait();
@@ -504,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1) lora_up_kernel(const LoraArgs p) 
                         const int m = m0 + e * kEpiThreads, row = m / kPieces, b = m % kPieces;
                         v[e] = make_uint4(0, 0, 0, 0);
                         if (row < count)
-                            v[e] = *(reinterpret_cast<const uint4 *>(p.pg + (long long)(start + row) * (plane_pitch(RP) / 2)) + b);
+                            v[e] = *(reinterpret_cast<const uint4 *>(p.planes + (long long)(start + row) * (plane_pitch(RP) / 2)) + b);
                     }
                     #pragma unroll
                     for (int e = 0; e < kOnce; ++e) {
@@ -589,219 +610,103 @@ __global__ void __launch_bounds__(kThreads, 1) lora_up_kernel(const LoraArgs p) 
 
 // ---------------------------------------------------------- weight gradients
 constexpr int kStageTokens = 32;
-// Eight warps produce and then store; the ninth issues the MMAs.
-constexpr int kWgradWarps = 8, kWgradProducers = kWgradWarps * 32, kWgradThreads = kWgradProducers + 32;
+// Warps: eight producers, four that empty TMEM, one that issues the MMAs.
+constexpr int kWgradProducerWarps = 8, kWgradProducers = kWgradProducerWarps * 32, kWgradStore = 4;
+constexpr int kWgradMma = kWgradProducerWarps + kWgradStore, kWgradThreads = (kWgradMma + 1) * 32;
 
 template <int RP>
 struct WgradShape {
-    static constexpr int kCols = RP <= 64 ? 512 : 256;      // columns of a CTA
+    static constexpr int kCols = RP <= 64 ? 512 : 256;      // columns of a pair
     static constexpr int kQBlock = kStageTokens * 128;      // bytes of 32 tokens x 64 columns
     static constexpr int kQ = kCols / 64 * kQBlock;
-    static constexpr int kP = (2 * RP + 63) / 64 * kQBlock; // both planes: rows of 2 RP, in blocks of 64
+    static constexpr int kP = 2 * RP * 64;                  // both planes: rows of 32 tokens
     static constexpr int kStage = kQ + kP;
-    static constexpr int kSumsA = RP * (kCols + 4) * 4, kSumsB = kCols * (RP + 4) * 4;
-    static constexpr int kSums = kSumsA > kSumsB ? kSumsA : kSumsB;
-    static constexpr int kStages = (kSmemMax - 1024) / kStage;
+    static constexpr int kStages = (kSmemMax - 1024) / kStage < 6 ? (kSmemMax - 1024) / kStage : 6;
     static constexpr int kSmem = kStages * kStage + 1024;
-    static_assert(kStages >= 2 && kSums <= kStages * kStage, "the ring does not fit");
+    static constexpr int kD = kCols / 128 * 2 * RP;         // TMEM columns of a pair's sums
+    static constexpr int kBufs = 2 * kD <= kTmemCols ? 2 : 1;
+    static constexpr int kTileSums = kCols * RP;            // floats of a pair's sums
+    static_assert(kStages >= 3 && kD <= kTmemCols, "the ring does not fit");
 };
 
-// Grid (slices * cluster, adapters): a cluster owns kCols columns of one
-// adapter's dA (or rows of dB), D[column][rank] in TMEM in blocks of 128
-// columns, once for each plane of g or s h (one MMA takes both as its N; two of
-// half the N took twice the time); its CTAs split the adapter's tokens, 32 to a stage, and add their
-// sums through distributed shared memory, in CTA order.
-template <int RP, bool DB>
-__device__ __forceinline__ void wgrad_tile(const WgradArgs &p, int slice, int adapter, unsigned char *s_mem,
-                                           uint64_t *s_bar, int *s_abort, uint32_t tmem) {
-    using S = WgradShape<RP>;
-    constexpr int NS = S::kStages;
-    const uint16_t *q = DB ? p.dy : p.x, *planes = DB ? p.ph : p.pg;
-    const int cols = DB ? p.N : p.K, vec = DB ? p.vec_dy : p.vec_x, r = p.rank;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int C = cluster_size(), c = cluster_rank();
-    const uint32_t ring = smem_u32(s_mem), full = smem_u32(s_bar), empty = full + 8 * NS, dfull = empty + 8 * NS;
-    int start = 0;
-    for (int a = lane; a < adapter; a += 32) start += p.sizes[a];
-    start = __reduce_add_sync(0xffffffffu, start);
-    const int size = p.sizes[adapter];
-    const int blocks = (size + kStageTokens - 1) / kStageTokens;
-    const int t0 = kStageTokens * int((long long)blocks * c / C);
-    const int t1 = min(size, kStageTokens * int((long long)blocks * (c + 1) / C));
-    const int stages = t1 > t0 ? (t1 - t0 + kStageTokens - 1) / kStageTokens : 0;
-    const int col0 = slice * S::kCols, width = min(S::kCols, cols - col0);
-    const int *rows = p.order + start;
-    volatile int *abort_flag = s_abort;
-
-    if (warp < kWgradWarps) {
-        // Rows row0 + 16 j, column pieces piece + 16 e: their places are 2048 bytes and
-        // 2 blocks apart.  The rows of the next stage are looked up one stage ahead.
-        const int pt = threadIdx.x, piece = pt % 16, row0 = pt / 16;
-        constexpr int kRows = kWgradProducers / 16, kJ = kStageTokens / kRows, kE = S::kCols / 128;
-        const uint32_t dst = (piece / 8) * S::kQBlock + sw128(row0, piece % 8);
-        int next[kJ];
+// The walk: a pair is an adapter with tokens and a slice of columns of x or dy; a
+// unit is a block of 32 of its tokens; a CTA takes an even run of all units.
+struct Pair {
+    int adapter, slice, start, tile0, size, blocks;   // start, tile0: the adapter's first place and tile
+    long long first;                                  // its first unit
+};
+// Every warp finds its pairs itself.
+__device__ Pair find_pair(const WgradArgs &p, long long u) {
+    const int lane = threadIdx.x & 31;
+    Pair q = {};
+    long long units = 0;
+    int rows = 0, tiles = 0;
+    for (int a0 = 0; a0 < p.adapters; a0 += 32) {
+        const int size = a0 + lane < p.adapters ? p.sizes[a0 + lane] : 0;
+        const int blocks = (size + kStageTokens - 1) / kStageTokens, my_tiles = (size + kTile - 1) / kTile;
+        const long long mine = (long long)blocks * p.slices;
+        long long u_end = mine;
+        int r_end = size, t_end = my_tiles;
         #pragma unroll
-        for (int j = 0; j < kJ; ++j) next[j] = t0 + row0 + kRows * j < t1 ? rows[t0 + row0 + kRows * j] : -1;
-        for (int i = 0; i < stages; ++i) {
-            const int s = i % NS, tok = t0 + i * kStageTokens, n = min(kStageTokens, t1 - tok);
-            int row[kJ];
-            #pragma unroll
-            for (int j = 0; j < kJ; ++j) {
-                const int t = tok + kStageTokens + row0 + kRows * j;
-                row[j] = next[j];
-                next[j] = t < t1 ? rows[t] : -1;
-            }
-            const bool ok = i < NS || mbar_wait(empty + 8 * s, (i / NS - 1) & 1, abort_flag, p.err);
-            if (!__all_sync(0xffffffffu, ok)) break;
-            const uint32_t qs = ring + s * S::kStage, ps = qs + S::kQ;
-            // tokens past the end are zeros on both sides: they are summed over
-            #pragma unroll
-            for (int j = 0; j < kJ; ++j) {
-                const bool in = row[j] >= 0;
-                const uint16_t *src = q + (long long)max(row[j], 0) * cols + col0 + 8 * piece;
-                #pragma unroll
-                for (int e = 0; e < kE; ++e) {
-                    const int left = width - 8 * piece - 128 * e;
-                    const uint32_t at = dst + kRows * 128 * j + 2 * S::kQBlock * e;
-                    if (left <= 0) continue;
-                    if (vec) cp_async16z(qs + at, in ? src + 128 * e : q, in);
-                    else *reinterpret_cast<uint4 *>(s_mem + s * S::kStage + at) = load_cols8(src + 128 * e, in ? left : 0, 0);
-                }
-            }
-            constexpr int kPieces = RP / 4, kAll = kStageTokens * kPieces;   // both planes' pieces
-            const uint16_t *src = planes + (long long)(start + tok) * (plane_pitch(RP) / 2);
-            #pragma unroll
-            for (int k = pt; k < kAll; k += kWgradProducers) {
-                const int tk = k / kPieces, b = k % kPieces;
-                const bool in = tk < n;
-                cp_async16z(ps + (b / 8) * S::kQBlock + sw128(tk, b % 8), in ? src + 8 * k : planes, in);
-            }
-            stage_done(full + 8 * s, vec);
+        for (int d = 1; d < 32; d *= 2) {
+            const long long x = __shfl_up_sync(0xffffffffu, u_end, d);
+            const int y = __shfl_up_sync(0xffffffffu, r_end, d), z = __shfl_up_sync(0xffffffffu, t_end, d);
+            if (lane >= d) u_end += x, r_end += y, t_end += z;
         }
-        cp_async_wait_all();
-    } else {
-        constexpr uint32_t idesc = tc_idesc_bf16(128, 2 * RP) | kTcAMajorM | kTcBMajorN;
-        bool ok = true;
-        for (int i = 0; i < stages; ++i) {
-            const int s = i % NS;
-            ok = __all_sync(0xffffffffu, mbar_wait(full + 8 * s, (i / NS) & 1, abort_flag, p.err));
-            if (!ok) break;
-            fence_proxy_async();
-            tc_fence_after();
-            const uint32_t qs = ring + s * S::kStage, ps = qs + S::kQ;
-            if (elect_one()) {
-                #pragma unroll
-                for (int m = 0; m < S::kCols / 128; ++m)
-                    #pragma unroll
-                    for (int k = 0; k < kStageTokens / 16; ++k) {
-                        const uint64_t a = tc_sdesc_sw128_mn(qs + m * 2 * S::kQBlock + k * 2048, S::kQBlock);
-                        const uint64_t b = tc_sdesc_sw128_mn(ps + k * 2048, S::kQBlock);
-                        tc_mma_ss(tmem + m * 2 * RP, a, b, idesc, i > 0 || k > 0);
-                    }
-                tc_commit(empty + 8 * s);
-            }
-            __syncwarp();
+        const unsigned hit = __ballot_sync(0xffffffffu, u >= units + u_end - mine && u < units + u_end);
+        if (hit) {
+            const int src = __ffs(hit) - 1;
+            q.adapter = a0 + src;
+            q.size = __shfl_sync(0xffffffffu, size, src);
+            q.blocks = __shfl_sync(0xffffffffu, blocks, src);
+            q.start = __shfl_sync(0xffffffffu, rows + r_end - size, src);
+            q.tile0 = __shfl_sync(0xffffffffu, tiles + t_end - my_tiles, src);
+            const long long base = __shfl_sync(0xffffffffu, units + u_end - mine, src);
+            q.slice = int((u - base) / q.blocks);
+            q.first = base + (long long)q.slice * q.blocks;
+            return q;
         }
-        if (elect_one()) tc_commit(dfull);
-        __syncwarp();
-        drain_wait(dfull, 0);
+        units += __shfl_sync(0xffffffffu, u_end, 31);
+        rows += __shfl_sync(0xffffffffu, r_end, 31);
+        tiles += __shfl_sync(0xffffffffu, t_end, 31);
     }
-    // ---- sums: the tile as it will be stored, in fp32, where the ring was
-    tc_fence_before();
-    __syncthreads();                                             // every copy and MMA has ended
-    tc_fence_after();
-    const bool bad = *abort_flag != 0;
-    float *s_sum = reinterpret_cast<float *>(s_mem);
-    constexpr int kPitch = DB ? RP + 4 : S::kCols + 4;
-    if (warp < kWgradWarps) {
-        const int sub = warp % 4;
-        for (int m = warp / 4; m < S::kCols / 128; m += 2) {
-            const int col = 128 * m + 32 * sub + lane;
-            #pragma unroll 2
-            for (int k = 0; k < RP / 8; ++k) {
-                uint32_t v[8], w[8];
-                if (stages > 0 && !bad) {
-                    const uint32_t at = tmem + (uint32_t(32 * sub) << 16) + m * 2 * RP + 8 * k;
-                    tc_ld_32x32b_x8(at, v);
-                    tc_ld_32x32b_x8(at + RP, w);
-                    tc_wait_ld();
-                    #pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) + __uint_as_float(w[e]));
-                } else {
-                    #pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] = bad ? 0x7fffffffu : 0u;
-                }
-                if (DB) {
-                    float *d = s_sum + col * kPitch + 8 * k;
-                    *reinterpret_cast<uint4 *>(d) = make_uint4(v[0], v[1], v[2], v[3]);
-                    *reinterpret_cast<uint4 *>(d + 4) = make_uint4(v[4], v[5], v[6], v[7]);
-                } else {
-                    #pragma unroll
-                    for (int e = 0; e < 8; ++e) s_sum[(8 * k + e) * kPitch + col] = __uint_as_float(v[e]);
-                }
-            }
-        }
-    }
-    __syncthreads();
-    if (C > 1) {
-        cluster_arrive();
-        cluster_wait();
-    }
-    const int n_rows = DB ? width : r, per = (DB ? r : width) / 8;   // rows, 8-element pieces of one
-    const int items = n_rows * per;
-    const int i0 = int((long long)items * c / C), i1 = int((long long)items * (c + 1) / C);
-    for (int i = i0 + threadIdx.x; i < i1; i += kWgradThreads) {
-        const int row = i / per, col = 8 * (i % per);
-        const float *at = s_sum + row * kPitch + col;
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-        if (C > 1) {
-            for (int k0 = 0; k0 < C; k0 += 4) {          // clusters of 2, 4 or 8
-                float4 x[4], y[4];
-                #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (k0 + k < C) x[k] = ld_cluster4(at, k0 + k), y[k] = ld_cluster4(at + 4, k0 + k);
-                #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (k0 + k < C) {
-                        a.x += x[k].x, a.y += x[k].y, a.z += x[k].z, a.w += x[k].w;
-                        b.x += y[k].x, b.y += y[k].y, b.z += y[k].z, b.w += y[k].w;
-                    }
-            }
-        } else {
-            a = *reinterpret_cast<const float4 *>(at), b = *reinterpret_cast<const float4 *>(at + 4);
-        }
-        uint4 o;
-        o.x = pack_bf16x2_rn(a.x, a.y), o.y = pack_bf16x2_rn(a.z, a.w);
-        o.z = pack_bf16x2_rn(b.x, b.y), o.w = pack_bf16x2_rn(b.z, b.w);
-        uint16_t *d = DB ? p.db + ((long long)adapter * cols + col0 + row) * r + col
-                         : p.da + ((long long)adapter * r + row) * cols + col0 + col;
-        *reinterpret_cast<uint4 *>(d) = o;
-    }
-    if (C > 1) {
-        __syncwarp();
-        cluster_arrive();
-        cluster_wait();
-    }
+    return q;
+}
+__device__ __forceinline__ long long count_units(const WgradArgs &p) {
+    int blocks = 0;
+    for (int a = threadIdx.x & 31; a < p.adapters; a += 32) blocks += (p.sizes[a] + kStageTokens - 1) / kStageTokens;
+    return (long long)__reduce_add_sync(0xffffffffu, blocks) * p.slices;
 }
 
+// D[column][plane, rank] of a pair is summed in TMEM in blocks of 128 columns: x or
+// dy lies along M as it comes, both planes of g or s h along N, one MMA for the two.
+// A run that covers all of a pair's tokens stores the gradient, the others their
+// sums ([rank][column], slot 0: the pair began before the run, slot 1: it goes on
+// after it) for wgrad_sum_kernel.
+//
+// What bounds it: the MMAs, at 142 cycles for 128 x 128 x 16 with the rows along M
+// (a stage of 32 tokens and 512 columns at rank 64: 1150 of the 1750 cycles that
+// its copies and they take together).  Two MMAs for the planes took 90 each, x or dy
+// as the MMA's 256 columns 375.
 template <int RP>
 __global__ void __launch_bounds__(kWgradThreads, 1) lora_wgrad_kernel(const WgradArgs p) {
     using S = WgradShape<RP>;
     constexpr int NS = S::kStages;
     extern __shared__ unsigned char s_raw[];
-    __shared__ uint64_t s_bar[2 * NS + 1];
+    __shared__ uint64_t s_bar[2 * NS + 4];
     __shared__ int s_abort;
     __shared__ uint32_t s_tmem;
     unsigned char *s_mem = s_raw + (-smem_u32(s_raw) & 1023);
-    const int warp = threadIdx.x / 32;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t ring = smem_u32(s_mem), full = smem_u32(s_bar), empty = full + 8 * NS;
+    const uint32_t dfull = empty + 8 * NS, dempty = dfull + 16;
     if (threadIdx.x == 0) {
-        const uint32_t bar = smem_u32(s_bar);
-        for (int i = 0; i < NS; ++i) mbar_init(bar + 8 * i, kWgradProducers), mbar_init(bar + 8 * (NS + i), 1);
-        mbar_init(bar + 16 * NS, 1);
+        for (int i = 0; i < NS; ++i) mbar_init(full + 8 * i, kWgradProducers), mbar_init(empty + 8 * i, 1);
+        for (int i = 0; i < 2; ++i) mbar_init(dfull + 8 * i, 1), mbar_init(dempty + 8 * i, kWgradStore);
         s_abort = 0;
         fence_barrier_init();
     }
-    if (warp == kWgradWarps) {
+    if (warp == kWgradMma) {
         tc_alloc(smem_u32(&s_tmem), kTmemCols);
         tc_relinquish();
     }
@@ -809,24 +714,261 @@ __global__ void __launch_bounds__(kWgradThreads, 1) lora_wgrad_kernel(const Wgra
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s_tmem;
+    // The kernel before let this one start after what it waited for itself (the
+    // sort, the sums) had ended, and writes nothing that is read here.
     pdl_launch_dependents();
-    pdl_wait();
-    const int slice = blockIdx.x / cluster_size();
-    if (slice < p.slices_x) wgrad_tile<RP, false>(p, slice, blockIdx.y, s_mem, s_bar, &s_abort, tmem);
-    else wgrad_tile<RP, true>(p, slice - p.slices_x, blockIdx.y, s_mem, s_bar, &s_abort, tmem);
+    const long long units = count_units(p);
+    const int ctas = int(units < gridDim.x ? units : gridDim.x), b = blockIdx.x;
+    const long long u0 = b < ctas ? run_start(units, ctas, b) : 0, u1 = b < ctas ? run_start(units, ctas, b + 1) : 0;
+    const int r = p.rank;
+    volatile int *abort_flag = &s_abort;
+    int i = 0, seg = 0;                                          // stages, pairs
+    for (long long u = u0; u < u1; ++seg) {
+        const Pair q = find_pair(p, u);
+        const int block0 = int(u - q.first);
+        const int n_blocks = int(u1 - u < q.blocks - block0 ? u1 - u : q.blocks - block0);
+        u += n_blocks;
+        const bool db = q.slice >= p.slices_x;
+        const int cols = db ? p.N : p.K, col0 = (db ? q.slice - p.slices_x : q.slice) * S::kCols;
+        const int width = min(S::kCols, cols - col0), buf = seg % S::kBufs;
+        if (warp < kWgradProducerWarps) {
+            // Rows row0 + 16 j, column pieces piece + 16 e: their places are 2048 bytes and
+            // 2 blocks apart.  The rows of the next stage are looked up one stage ahead.
+            const uint16_t *src_q = db ? p.dy : p.x;
+            const uint16_t *src_p = (db ? p.th : p.tg) + (long long)q.tile0 * tile_planes(RP);
+            const int vec = db ? p.vec_dy : p.vec_x, *rows = p.order + q.start;
+            const int pt = threadIdx.x, piece = pt % 16, row0 = pt / 16;
+            constexpr int kRows = kWgradProducers / 16, kJ = kStageTokens / kRows, kE = S::kCols / 128;
+            const uint32_t dst = (piece / 8) * S::kQBlock + sw128(row0, piece % 8);
+            int next[kJ];
+            #pragma unroll
+            for (int j = 0; j < kJ; ++j) {
+                const int t = block0 * kStageTokens + row0 + kRows * j;
+                next[j] = t < q.size ? rows[t] : -1;
+            }
+            for (int k = 0; k < n_blocks; ++k, ++i) {
+                const int s = i % NS, tok = (block0 + k) * kStageTokens;
+                int row[kJ];
+                #pragma unroll
+                for (int j = 0; j < kJ; ++j) {
+                    const int t = tok + kStageTokens + row0 + kRows * j;
+                    row[j] = next[j];
+                    next[j] = t < q.size ? rows[t] : -1;
+                }
+                const bool ok = i < NS || mbar_wait(empty + 8 * s, (i / NS - 1) & 1, abort_flag, p.err);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                const uint32_t qs = ring + s * S::kStage, ps = qs + S::kQ;
+                // tokens past the last are zeros on both sides: they are summed over
+                #pragma unroll
+                for (int j = 0; j < kJ; ++j) {
+                    const bool in = row[j] >= 0;
+                    const uint16_t *src = src_q + (long long)max(row[j], 0) * cols + col0 + 8 * piece;
+                    #pragma unroll
+                    for (int e = 0; e < kE; ++e) {
+                        const int left = width - 8 * piece - 128 * e;
+                        const uint32_t at = dst + kRows * 128 * j + 2 * S::kQBlock * e;
+                        if (left <= 0) continue;
+                        if (vec) cp_async16z(qs + at, in ? src + 128 * e : src_q, in);
+                        else *reinterpret_cast<uint4 *>(s_mem + s * S::kStage + at) =
+                                 load_cols8(src + 128 * e, in ? left : 0, 0);
+                    }
+                }
+                // rows of 64 bytes (32 tokens of a plane's rank) in the 64-byte swizzle
+                const uint16_t *src = src_p + (long long)(tok / kTile) * tile_planes(RP) + tok % kTile;
+                #pragma unroll
+                for (int m = pt; m < 2 * RP * 4; m += kWgradProducers) {
+                    const int line = m / 4, e = m % 4;
+                    cp_async16(ps + line * 64 + ((e ^ ((line >> 1) & 3)) << 4), src + line * kTile + 8 * e);
+                }
+                stage_done(full + 8 * s, vec);
+            }
+        } else if (warp == kWgradMma) {
+            constexpr uint32_t idesc = tc_idesc_bf16(128, 2 * RP) | kTcAMajorM;
+            bool ok = seg < S::kBufs || mbar_wait(dempty + 8 * buf, (seg / S::kBufs - 1) & 1, abort_flag, p.err);
+            ok = __all_sync(0xffffffffu, ok);
+            for (int k = 0; k < n_blocks && ok; ++k, ++i) {
+                const int s = i % NS;
+                ok = __all_sync(0xffffffffu, mbar_wait(full + 8 * s, (i / NS) & 1, abort_flag, p.err));
+                if (!ok) break;
+                fence_proxy_async();
+                tc_fence_after();
+                const uint32_t qs = ring + s * S::kStage, ps = qs + S::kQ;
+                if (elect_one()) {
+                    #pragma unroll
+                    for (int m = 0; m < S::kCols / 128; ++m)
+                        #pragma unroll
+                        for (int e = 0; e < kStageTokens / 16; ++e) {
+                            const uint64_t dq = tc_sdesc_sw128_mn(qs + m * 2 * S::kQBlock + e * 2048, S::kQBlock);
+                            const uint64_t dp = tc_sdesc_sw64(ps + e * 32);
+                            tc_mma_ss(tmem + buf * S::kD + m * 2 * RP, dq, dp, idesc, k > 0 || e > 0);
+                        }
+                    tc_commit(empty + 8 * s);
+                }
+                __syncwarp();
+            }
+            if (elect_one()) tc_commit(dfull + 8 * buf);
+            __syncwarp();
+        } else {
+            const int sub = warp % 4;
+            const bool ok = __all_sync(0xffffffffu, mbar_wait(dfull + 8 * buf, (seg / S::kBufs) & 1, abort_flag, p.err));
+            tc_fence_after();
+            const bool whole = n_blocks == q.blocks;
+            float *slot = p.partial + (long long)(2 * b + (block0 == 0)) * S::kTileSums;
+            for (int m = 0; m < S::kCols / 128; ++m) {
+                const int col = 128 * m + 32 * sub + lane;
+                if (128 * m + 32 * sub >= width) break;
+                #pragma unroll 2
+                for (int rank = 0; rank < RP; rank += 8) {
+                    uint32_t v[8], w[8];
+                    const uint32_t at = tmem + (uint32_t(32 * sub) << 16) + buf * S::kD + m * 2 * RP + rank;
+                    tc_ld_32x32b_x8(at, v);
+                    tc_ld_32x32b_x8(at + RP, w);
+                    tc_wait_ld();
+                    float f[8];
+                    #pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        f[e] = ok ? __uint_as_float(v[e]) + __uint_as_float(w[e]) : __int_as_float(0x7fffffff);
+                    if (!whole) {
+                        #pragma unroll
+                        for (int e = 0; e < 8; ++e) __stcg(slot + (rank + e) * S::kCols + col, f[e]);
+                    } else if (col < width && rank < r) {
+                        if (db) {
+                            *reinterpret_cast<uint4 *>(p.db + ((long long)q.adapter * cols + col0 + col) * r + rank) =
+                                make_uint4(pack_bf16x2_rn(f[0], f[1]), pack_bf16x2_rn(f[2], f[3]),
+                                           pack_bf16x2_rn(f[4], f[5]), pack_bf16x2_rn(f[6], f[7]));
+                        } else {
+                            uint16_t *d = p.da + ((long long)q.adapter * r + rank) * cols + col0 + col;
+                            #pragma unroll
+                            for (int e = 0; e < 8; ++e) d[(long long)e * cols] = f32_to_bf16_rn(f[e]);
+                        }
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(dempty + 8 * buf);
+        }
+    }
+    pdl_wait();                                                  // this kernel's end is also the one's before
+    cp_async_wait_all();
+    if (warp == kWgradMma && seg > 0) drain_wait(dfull + 8 * ((seg - 1) % S::kBufs), ((seg - 1) / S::kBufs) & 1);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == kWgradWarps) tc_dealloc(tmem, kTmemCols);
+    if (warp == kWgradMma) tc_dealloc(tmem, kTmemCols);
+}
+
+// The gradients of pairs that several runs share: of a pair that n runs share the
+// n blocks of these CTAs each add a part, in CTA order; so a block has a part of
+// the pair its run began inside of and a part of the pair its run left unfinished.
+// All blocks clear the gradients of adapters without tokens.
+constexpr int kWgradSumThreads = 512;
+
+template <int RP>
+__device__ __forceinline__ void wgrad_sum_part(const WgradArgs &p, const Pair &q, int b0, int slots, int part) {
+    using S = WgradShape<RP>;
+    constexpr int kSlots = 8;
+    const int r = p.rank;
+    const bool db = q.slice >= p.slices_x;
+    const int cols = db ? p.N : p.K, col0 = (db ? q.slice - p.slices_x : q.slice) * S::kCols;
+    const int width = min(S::kCols, cols - col0);
+    // the first CTA's slot 1, then the others' slot 0, which lie two apart
+    const float *sum0 = p.partial + (long long)(2 * b0 + 1) * S::kTileSums, *rest = sum0 + S::kTileSums;
+    const int items = db ? S::kCols * (r / 8) : r * width / 4;
+    const int i0 = int((long long)items * part / slots), i1 = int((long long)items * (part + 1) / slots);
+    for (int i = i0 + threadIdx.x; i < i1; i += kWgradSumThreads) {
+        if (!db) {
+            const int rank = i / (width / 4), col = 4 * (i % (width / 4)), at = rank * S::kCols + col;
+            float4 v = *reinterpret_cast<const float4 *>(sum0 + at);
+            for (int k0 = 1; k0 < slots; k0 += kSlots) {
+                float4 u[kSlots];
+                #pragma unroll
+                for (int k = 0; k < kSlots; ++k)
+                    if (k0 + k < slots)
+                        u[k] = *reinterpret_cast<const float4 *>(rest + (long long)(2 * (k0 + k - 1)) * S::kTileSums + at);
+                #pragma unroll
+                for (int k = 0; k < kSlots; ++k)
+                    if (k0 + k < slots) v.x += u[k].x, v.y += u[k].y, v.z += u[k].z, v.w += u[k].w;
+            }
+            *reinterpret_cast<uint2 *>(p.da + ((long long)q.adapter * r + rank) * cols + col0 + col) =
+                make_uint2(pack_bf16x2_rn(v.x, v.y), pack_bf16x2_rn(v.z, v.w));
+        } else {
+            // one column, eight ranks: neighbouring threads read neighbouring columns
+            const int col = i % S::kCols, rank = 8 * (i / S::kCols);
+            if (col >= width) continue;
+            float v[8];
+            #pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = sum0[(rank + e) * S::kCols + col];
+            for (int k0 = 1; k0 < slots; k0 += 4) {
+                float u[4][8];
+                #pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    #pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (k0 + k < slots)
+                            u[k][e] = rest[(long long)(2 * (k0 + k - 1)) * S::kTileSums + (rank + e) * S::kCols + col];
+                #pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    #pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (k0 + k < slots) v[e] += u[k][e];
+            }
+            *reinterpret_cast<uint4 *>(p.db + ((long long)q.adapter * cols + col0 + col) * r + rank) =
+                make_uint4(pack_bf16x2_rn(v[0], v[1]), pack_bf16x2_rn(v[2], v[3]), pack_bf16x2_rn(v[4], v[5]),
+                           pack_bf16x2_rn(v[6], v[7]));
+        }
+    }
+}
+
+template <int RP>
+__global__ void __launch_bounds__(kWgradSumThreads) wgrad_sum_kernel(const WgradArgs p) {
+    __shared__ Pair s_pair[2];
+    __shared__ int s_b0[2], s_slots[2];                  // 0 slots: no part
+    pdl_launch_dependents();
+    const int r = p.rank, b = blockIdx.x;
+    if (threadIdx.x < 64) {
+        // warp 0: the pair that the run began inside of; warp 1: the one that goes on
+        const int which = threadIdx.x / 32;
+        const long long units = count_units(p);
+        const int ctas = int(units < gridDim.x ? units : gridDim.x);
+        int b0 = 0, slots = 0;
+        Pair q = {};
+        if (b < ctas) {
+            const long long u0 = run_start(units, ctas, b), u1 = run_start(units, ctas, b + 1);
+            q = find_pair(p, which ? u1 - 1 : u0);
+            const long long end = q.first + q.blocks;
+            if (which ? (q.first >= u0 && end > u1) : q.first < u0) {
+                b0 = run_owner(units, ctas, q.first);
+                slots = run_owner(units, ctas, end - 1) - b0 + 1;
+            }
+        }
+        if (threadIdx.x % 32 == 0) s_pair[which] = q, s_b0[which] = b0, s_slots[which] = slots;
+    }
+    __syncthreads();
+    pdl_wait();
+    #pragma unroll 1
+    for (int which = 0; which < 2; ++which)
+        if (s_slots[which]) wgrad_sum_part<RP>(p, s_pair[which], s_b0[which], s_slots[which], b - s_b0[which]);
+    const long long na = (long long)r * p.K / 8, nb = (long long)r * p.N / 8, step = (long long)gridDim.x * kWgradSumThreads;
+    for (int a = 0; a < p.adapters; ++a) {
+        if (p.sizes[a] != 0) continue;
+        uint4 *da = reinterpret_cast<uint4 *>(p.da) + a * na, *db = reinterpret_cast<uint4 *>(p.db) + a * nb;
+        for (long long i = (long long)b * kWgradSumThreads + threadIdx.x; i < na + nb; i += step)
+            (i < na ? da[i] : db[i - na]) = make_uint4(0, 0, 0, 0);
+    }
 }
 
 // ---------------------------------------------------------------- host side
 int ceil_div(long long a, long long b) { return int((a + b - 1) / b); }
 
+}  // namespace
+
 // Tiles at most: the adapters' and the adapterless tokens' last may be part empty.
 int lora_max_tiles(int tokens, int adapters) {
     return ceil_div(tokens, kTile) + (adapters < tokens ? adapters : tokens);
 }
+
+namespace {
 
 template <int RP, bool TRANS>
 cudaError_t launch_tensor_rank(const LoraArgs &p, int sms, cudaStream_t s) {
@@ -845,21 +987,25 @@ cudaError_t launch_tensor_rank(const LoraArgs &p, int sms, cudaStream_t s) {
 }
 
 template <int RP>
-cudaError_t launch_wgrad_rank(WgradArgs p, int adapters, int sms, cudaStream_t s) {
+cudaError_t launch_wgrad_rank(WgradArgs p, int sms, cudaStream_t s) {
     using S = WgradShape<RP>;
-    const cudaError_t e = allow_smem<lora_wgrad_kernel<RP>>(S::kSmem);
+    cudaError_t e = allow_smem<lora_wgrad_kernel<RP>>(S::kSmem);
     if (e != cudaSuccess) return e;
     p.slices_x = ceil_div(p.K, S::kCols);
-    const int slices = p.slices_x + ceil_div(p.N, S::kCols);
-    int cluster = 1;
-    while (cluster < kMaxCluster && 2LL * slices * adapters * cluster <= sms) cluster *= 2;
-    return launch_chained(lora_wgrad_kernel<RP>, dim3(slices * cluster, adapters), kWgradThreads, S::kSmem, cluster, s, p);
+    p.slices = p.slices_x + ceil_div(p.N, S::kCols);
+    const int ctas = sms < kMaxRuns ? sms : kMaxRuns;
+    e = launch_chained(lora_wgrad_kernel<RP>, dim3(ctas), kWgradThreads, S::kSmem, 1, s, p);
+    if (e != cudaSuccess) return e;
+    return launch_chained(wgrad_sum_kernel<RP>, dim3(ctas), kWgradSumThreads, 0, 1, s, p);
 }
 
 }  // namespace
 
-size_t lora_partial_bytes(int tokens, int adapters, int rank) {
-    return (size_t(lora_max_tiles(tokens, adapters)) + kMaxRuns) * kTile * padded_rank(rank) * sizeof(float);
+size_t lora_partial_bytes(int tokens, int adapters, int rank, bool backward) {
+    const int rp = padded_rank(rank);
+    const size_t h = (size_t(lora_max_tiles(tokens, adapters)) + kMaxRuns) * kTile * rp * sizeof(float);
+    const size_t grads = backward ? size_t(2) * kMaxRuns * (rp <= 64 ? 512 : 256) * rp * sizeof(float) : 0;
+    return h > grads ? h : grads;
 }
 
 cudaError_t launch_lora_tensor(const LoraArgs &p, bool trans, int sms, cudaStream_t s) {
@@ -871,12 +1017,12 @@ cudaError_t launch_lora_tensor(const LoraArgs &p, bool trans, int sms, cudaStrea
     }
 }
 
-cudaError_t launch_wgrad(const WgradArgs &p, int adapters, int sms, cudaStream_t s) {
+cudaError_t launch_wgrad(const WgradArgs &p, int sms, cudaStream_t s) {
     switch (padded_rank(p.rank)) {
-        case 16: return launch_wgrad_rank<16>(p, adapters, sms, s);
-        case 32: return launch_wgrad_rank<32>(p, adapters, sms, s);
-        case 64: return launch_wgrad_rank<64>(p, adapters, sms, s);
-        default: return launch_wgrad_rank<128>(p, adapters, sms, s);
+        case 16: return launch_wgrad_rank<16>(p, sms, s);
+        case 32: return launch_wgrad_rank<32>(p, sms, s);
+        case 64: return launch_wgrad_rank<64>(p, sms, s);
+        default: return launch_wgrad_rank<128>(p, sms, s);
     }
 }
 

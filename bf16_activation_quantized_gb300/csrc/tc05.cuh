@@ -41,6 +41,18 @@ __device__ __forceinline__ uint64_t tc_sdesc_sw128(uint32_t smem_addr) {
 constexpr uint32_t kTcAMajorM = 1u << 15;
 constexpr uint32_t kTcBMajorN = 1u << 16;
 
+// The same for rows of 64 bytes (32 elements of K) with the 64-byte swizzle:
+// 8-row atoms of 512 bytes.
+__device__ __forceinline__ uint64_t tc_sdesc_sw64(uint32_t smem_addr) {
+    uint64_t d = 0;
+    d |= uint64_t((smem_addr >> 4) & 0x3FFF);
+    d |= uint64_t(1) << 16;
+    d |= uint64_t(512 >> 4) << 32;
+    d |= uint64_t(1) << 46;
+    d |= uint64_t(4) << 61;                          // layout: 64-byte swizzle
+    return d;
+}
+
 // Shared-memory matrix descriptor for an operand that lies along M or N, with
 // the 128-byte swizzle: each K index is a row of 128 bytes (64 elements of M or
 // N), 8-row atoms of 1024 bytes.  `block_bytes`: from one block of 64 elements
