@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(kFewThreads, RP <= 32 ? 2 : 1) lora_few_kernel
     constexpr int TM = kFewTile, NT = RP / 8, QN = RP >= 32 ? RP / 32 : 1, KS = RP / 16;
     constexpr int PS = RP + 4;                           // floats of a row of h
     constexpr int U = RP <= 32 ? 4 : RP == 64 ? 2 : 1;   // steps of the first product loaded together
-    constexpr int PF = RP <= 32 ? 4 : RP == 64 ? 2 : 1;  // steps of the second
+    constexpr int PF = RP == 16 ? 4 : RP == 32 ? 3 : RP == 64 ? 2 : 1;  // steps of the second
     constexpr int kQuads = RP / 4;
     extern __shared__ float s_mem[];
     float *s_part = s_mem;                               // [kFewWarps][TM][PS]
@@ -400,7 +400,9 @@ w4a16_status w4a16_lora_add(const w4a16_bf16 *X, const w4a16_bf16 *A, const w4a1
     if (e != cudaSuccess) return W4A16_ERR_CUDA;
     p.order = order, p.sizes = sizes;
     place_workspace(&p, ws, w);
-    return from_cuda(launch_lora_tensor(p, false, sms, s));
+    e = launch_lora_tensor(p, false, kLoraDown, sms, s);
+    if (e != cudaSuccess) return W4A16_ERR_CUDA;
+    return from_cuda(launch_lora_tensor(p, false, kLoraUp, sms, s));
 }
 
 w4a16_status w4a16_lora_add_backward(const w4a16_bf16 *dY, const w4a16_bf16 *X, const float *hidden,
@@ -441,13 +443,18 @@ w4a16_status w4a16_lora_add_backward(const w4a16_bf16 *dY, const w4a16_bf16 *X, 
     p.vec_in = N % 8 == 0 && aligned(dY, 16);
     p.vec_out = aligned(dX_base, 16) && aligned(dX, 16);
     place_workspace(&p, ws, w);
-    e = launch_lora_tensor(p, true, sms, s);
+    e = launch_lora_tensor(p, true, kLoraDown, sms, s);
     if (e != cudaSuccess) return W4A16_ERR_CUDA;
     WgradArgs q = {};
     q.x = X, q.dy = dY, q.tg = p.tg, q.th = p.th, q.order = order, q.sizes = sizes, q.partial = p.partial;
     q.da = dA, q.db = dB, q.err = p.err, q.adapters = num_adapters, q.rank = rank, q.K = K, q.N = N;
     q.vec_x = 1, q.vec_dy = p.vec_in;
-    return from_cuda(launch_wgrad(q, sms, s));
+    // The weight gradients' runs come right after g, while dY is still in L2; dX
+    // fills the SMs that they leave, and their sums, which wait for all of them, end.
+    e = launch_wgrad(q, kWgradRuns, sms, s);
+    if (e == cudaSuccess) e = launch_lora_tensor(p, true, kLoraUp, sms, s);
+    if (e != cudaSuccess) return W4A16_ERR_CUDA;
+    return from_cuda(launch_wgrad(q, kWgradSums, sms, s));
 }
 
 }  // extern "C"

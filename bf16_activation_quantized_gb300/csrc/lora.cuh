@@ -269,8 +269,10 @@ cudaError_t allow_smem(size_t bytes) {
 // lora_tensor.cu.  lora_partial_bytes: the workspace of the partial sums.
 size_t lora_partial_bytes(int tokens, int adapters, int rank, bool backward);
 int lora_max_tiles(int tokens, int adapters);
-cudaError_t launch_lora_tensor(const LoraArgs &p, bool trans, int sms, cudaStream_t s);
-cudaError_t launch_wgrad(const WgradArgs &p, int sms, cudaStream_t s);
+enum LoraStep { kLoraDown, kLoraUp };   // h, published in the planes; y
+cudaError_t launch_lora_tensor(const LoraArgs &p, bool trans, LoraStep step, int sms, cudaStream_t s);
+enum WgradStep { kWgradRuns, kWgradSums };
+cudaError_t launch_wgrad(const WgradArgs &p, WgradStep step, int sms, cudaStream_t s);
 
 inline int padded_rank(int r) { return r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128; }
 

@@ -45,6 +45,7 @@ constexpr int kCols = 128;             // columns of a stage: two blocks of 64
 constexpr int kBlock = kTile * 128;    // bytes of 128 rows x 64 columns
 constexpr int kSmemMax = 226 * 1024;
 constexpr int kTmemCols = 512;
+constexpr int kPrefetch = 256 * 1024;  // bytes of X that a CTA prefetches
 constexpr int kMaxRuns = 160;          // CTAs of the two products: one per SM (152)
 
 __device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kEpiThreads) : "memory"); }
@@ -73,18 +74,21 @@ __device__ __forceinline__ Walk make_walk(int tiles, int per, int b, int ctas) {
     return w;
 }
 
-// One warp: tiles of all adapters and, past those, of the tokens without one.
-__device__ void count_tiles(const LoraArgs &p, int *out) {
-    const int lane = threadIdx.x & 31;
+// Tiles of all adapters and, past those, of the tokens without one.  Every warp
+// counts for itself.
+struct TileCount {
+    int with, without;
+};
+__device__ __forceinline__ TileCount count_tiles(const LoraArgs &p) {
     int tiles = 0, rows = 0;
-    for (int a = lane; a < p.adapters; a += 32) {
+    for (int a = threadIdx.x & 31; a < p.adapters; a += 32) {
         const int size = p.sizes[a];
         tiles += (size + kTile - 1) / kTile;
         rows += size;
     }
     tiles = __reduce_add_sync(0xffffffffu, tiles);
     rows = __reduce_add_sync(0xffffffffu, rows);
-    if (lane == 0) out[0] = tiles, out[1] = (p.tokens - rows + kTile - 1) / kTile;
+    return {tiles, (p.tokens - rows + kTile - 1) / kTile};
 }
 
 // Two tiles' tokens, filled by the first producer warp ahead of the others.
@@ -199,7 +203,6 @@ __global__ void __launch_bounds__(kThreads, 1) lora_down_kernel(const LoraArgs p
     extern __shared__ unsigned char s_raw[];
     __shared__ uint64_t s_bar[2 * NS + 8];
     __shared__ TileSlots s_tiles;
-    __shared__ int s_count[2];
     __shared__ int s_abort;
     __shared__ uint32_t s_tmem;
     unsigned char *s_mem = s_raw + (-smem_u32(s_raw) & 1023);
@@ -219,15 +222,23 @@ __global__ void __launch_bounds__(kThreads, 1) lora_down_kernel(const LoraArgs p
         tc_alloc(smem_u32(&s_tmem), kTmemCols);
         tc_relinquish();
     }
-    pdl_wait();
-    if (warp == 0) count_tiles(p, s_count);
+    // While the sort runs (whose CTAs had waited for what came before when they let
+    // this kernel start): this CTA's share of X, the first 256 KB of it, into L2.
+    if (threadIdx.x == 0 && p.vec_in) {
+        const long long t0 = (long long)p.tokens * blockIdx.x / gridDim.x * p.in;
+        const long long t1 = (long long)p.tokens * (blockIdx.x + 1) / gridDim.x * p.in;
+        const long long most = kPrefetch / 2, n = t1 - t0 < most ? t1 - t0 : most;
+        for (long long at = 0; at < n; at += 8192)
+            bulk_prefetch_l2(p.x + t0 + at, uint32_t(n - at < 8192 ? n - at : 8192) * 2);
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    pdl_launch_dependents();
     const uint32_t tmem = s_tmem;
     const int r = p.rank;
-    const Walk w = make_walk(s_count[0], (p.in + kCols - 1) / kCols, blockIdx.x, gridDim.x);
+    pdl_wait();
+    pdl_launch_dependents();
+    const Walk w = make_walk(count_tiles(p).with, (p.in + kCols - 1) / kCols, blockIdx.x, gridDim.x);
     volatile int *abort_flag = &s_abort;
 
     int i = 0, seg = 0;                              // steps and tiles so far
@@ -320,73 +331,86 @@ __global__ void __launch_bounds__(kThreads, 1) lora_down_kernel(const LoraArgs p
 // ranks a thread, all of a tile's slots (5 of them at 4096 tokens) on their way
 // at once.
 constexpr int kSumThreads = 256;
+// Blocks of a tile, four ranks of a row per thread: the kernel is a chain of
+// latencies (a quarter of the blocks with four rows each took 7.6 us, these 3.5).
+constexpr int sum_blocks(int RP) { return kTile * (RP / 4) / kSumThreads; }
 
 template <int RP, bool TRANS>
 __global__ void __launch_bounds__(kSumThreads) lora_sum_kernel(const LoraArgs p, int down_ctas) {
-    constexpr int kPieces = RP / 4, kRows = kSumThreads / kPieces, kBlocks = kTile / kRows, kSlots = 8;
+    constexpr int kPieces = RP / 4, kRows = kTile / sum_blocks(RP), kSlots = 8;
+    static_assert(kRows * kPieces == kSumThreads, "one piece a thread");
     __shared__ int s_rows[kTile];
-    __shared__ int s_info[3], s_count[2];
-    __shared__ uint16_t s_t[TRANS ? 2 : 1][TRANS ? 2 * RP : 1][kRows + 2];   // g, s h: [plane, rank][row]
+    __shared__ int s_info[3];
+    __shared__ long long s_slots[2];                     // first slot, how many
+    __shared__ uint16_t s_t[TRANS ? 2 * RP : 1][kRows + 2];   // g, then s h: [plane, rank][row]
     // The first product's CTAs let this kernel start after the sort had ended.
     pdl_launch_dependents();
-    const int tile = blockIdx.x / kBlocks, row0 = blockIdx.x % kBlocks * kRows;
+    const int tile = blockIdx.x / sum_blocks(RP), row0 = blockIdx.x % sum_blocks(RP) * kRows;
     if (threadIdx.x < 32) {
-        count_tiles(p, s_count);
         find_tile_sorted<kTile>(p, tile, s_rows, s_info);
+        const Walk d = make_walk(count_tiles(p).with, (p.in + kCols - 1) / kCols, 0, down_ctas);
+        __syncwarp();
+        if (threadIdx.x == 0 && s_info[1] > 0 && s_info[0] >= 0) {
+            const long long first = (long long)tile * d.per;
+            const int b0 = run_owner(d.units, d.ctas, first);
+            s_slots[0] = tile + b0;
+            s_slots[1] = run_owner(d.units, d.ctas, first + d.per - 1) - b0 + 1;
+        }
     }
     __syncthreads();
     const int adapter = s_info[0], count = s_info[1], r = p.rank;
-    const int row = row0 + threadIdx.x / kPieces, rank = 4 * (threadIdx.x % kPieces);
-    const bool token = row < count, in = token && rank < r;
-    pdl_wait();
     if (count == 0) return;
-    float4 *hidden = reinterpret_cast<float4 *>(p.hidden + (in ? (long long)s_rows[row] * r + rank : 0));
-    if (adapter < 0) {
-        if (!TRANS && p.hidden && in) *hidden = make_float4(0.f, 0.f, 0.f, 0.f);
-        return;
-    }
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f), w = v;
-    if (in) {
-        const Walk d = make_walk(s_count[0], (p.in + kCols - 1) / kCols, 0, down_ctas);
-        const long long first = (long long)tile * d.per;
-        const int b0 = run_owner(d.units, d.ctas, first), b1 = run_owner(d.units, d.ctas, first + d.per - 1);
-        if (TRANS) w = *hidden;
-        const float *at = p.partial + ((long long)(tile + b0) * kTile + row) * RP + rank;
-        for (int b = b0; b <= b1; b += kSlots) {
-            float4 u[kSlots];
-            #pragma unroll
-            for (int k = 0; k < kSlots; ++k)
-                if (b + k <= b1) u[k] = *reinterpret_cast<const float4 *>(at + (long long)(b - b0 + k) * kTile * RP);
-            #pragma unroll
-            for (int k = 0; k < kSlots; ++k)
-                if (b + k <= b1) v.x += u[k].x, v.y += u[k].y, v.z += u[k].z, v.w += u[k].w;
-        }
-        if (!TRANS && p.hidden) *hidden = v;
-    }
-    // ranks past r are zeros (also where x holds infinities: 0 * inf)
-    const float scale = p.scale[adapter];
-    uint2 hi, lo;
-    split2(scale * v.x, scale * v.y, hi.x, lo.x), split2(scale * v.z, scale * v.w, hi.y, lo.y);
-    if (token) {
-        const long long out = (long long)(s_info[2] + row) * (plane_pitch(RP) / 2) + rank;
-        *reinterpret_cast<uint2 *>(p.planes + out) = hi, *reinterpret_cast<uint2 *>(p.planes + out + RP) = lo;
-    }
-    if (TRANS) {
-        const int mine = threadIdx.x / kPieces;
-        #pragma unroll
-        for (int which = 0; which < 2; ++which) {
-            if (which) split2(scale * w.x, scale * w.y, hi.x, lo.x), split2(scale * w.z, scale * w.w, hi.y, lo.y);
-            #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                s_t[which][rank + e][mine] = uint16_t((e < 2 ? hi.x : hi.y) >> (16 * (e & 1)));
-                s_t[which][RP + rank + e][mine] = uint16_t((e < 2 ? lo.x : lo.y) >> (16 * (e & 1)));
+    const float scale = adapter >= 0 ? p.scale[adapter] : 0.f;
+    const int slots = adapter >= 0 ? int(s_slots[1]) : 0;
+    const int rank = 4 * (threadIdx.x % kPieces);
+    pdl_wait();
+    #pragma unroll
+    for (int which = 0; which < (TRANS ? 2 : 1); ++which) {
+        // first g (forward: h), then s h as it was kept
+        {
+            const int row = row0 + threadIdx.x / kPieces;
+            const bool token = row < count, in = token && rank < r;
+            float4 *hidden = reinterpret_cast<float4 *>(p.hidden + (in ? (long long)s_rows[row] * r + rank : 0));
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (in && which) {
+                v = *hidden;
+            } else if (in) {
+                const float *at = p.partial + (s_slots[0] * kTile + row) * RP + rank;
+                for (int b = 0; b < slots; b += kSlots) {
+                    float4 u[kSlots];
+                    #pragma unroll
+                    for (int k = 0; k < kSlots; ++k)
+                        if (b + k < slots) u[k] = *reinterpret_cast<const float4 *>(at + (long long)(b + k) * kTile * RP);
+                    #pragma unroll
+                    for (int k = 0; k < kSlots; ++k)
+                        if (b + k < slots) v.x += u[k].x, v.y += u[k].y, v.z += u[k].z, v.w += u[k].w;
+                }
+                if (!TRANS && p.hidden) *hidden = v;     // zeros without an adapter
+            }
+            if (adapter < 0) return;
+            // ranks past r are zeros (also where x holds infinities: 0 * inf)
+            uint2 hi, lo;
+            split2(scale * v.x, scale * v.y, hi.x, lo.x), split2(scale * v.z, scale * v.w, hi.y, lo.y);
+            if (token && !which) {
+                const long long out = (long long)(s_info[2] + row) * (plane_pitch(RP) / 2) + rank;
+                *reinterpret_cast<uint2 *>(p.planes + out) = hi, *reinterpret_cast<uint2 *>(p.planes + out + RP) = lo;
+            }
+            if (TRANS) {
+                #pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    s_t[rank + e][row - row0] = uint16_t((e < 2 ? hi.x : hi.y) >> (16 * (e & 1)));
+                    s_t[RP + rank + e][row - row0] = uint16_t((e < 2 ? lo.x : lo.y) >> (16 * (e & 1)));
+                }
             }
         }
-        __syncthreads();
-        for (int i = threadIdx.x; i < 2 * 2 * RP * kRows / 2; i += kSumThreads) {
-            const int pair = i % (kRows / 2), line = i / (kRows / 2) % (2 * RP), which = i / (kRows / 2) / (2 * RP);
-            uint16_t *out = (which ? p.th : p.tg) + (long long)tile * tile_planes(RP) + line * kTile + row0 + 2 * pair;
-            *reinterpret_cast<uint32_t *>(out) = *reinterpret_cast<const uint32_t *>(&s_t[which][line][2 * pair]);
+        if (TRANS) {
+            __syncthreads();
+            uint16_t *out = (which ? p.th : p.tg) + (long long)tile * tile_planes(RP) + row0;
+            for (int i = threadIdx.x; i < 2 * RP * kRows / 2; i += kSumThreads) {
+                const int pair = i % (kRows / 2), line = i / (kRows / 2);
+                *reinterpret_cast<uint32_t *>(out + line * kTile + 2 * pair) = *reinterpret_cast<const uint32_t *>(&s_t[line][2 * pair]);
+            }
+            __syncthreads();
         }
     }
 }
@@ -409,7 +433,6 @@ __global__ void __launch_bounds__(kThreads, 1) lora_up_kernel(const LoraArgs p) 
     extern __shared__ unsigned char s_raw[];
     __shared__ uint64_t s_bar[2 * NS + 13];
     __shared__ TileSlots s_tiles;
-    __shared__ int s_count[2];
     __shared__ int s_abort;
     __shared__ uint32_t s_tmem;
     unsigned char *s_mem = s_raw + (-smem_u32(s_raw) & 1023);
@@ -431,16 +454,17 @@ __global__ void __launch_bounds__(kThreads, 1) lora_up_kernel(const LoraArgs p) 
         tc_alloc(smem_u32(&s_tmem), kTmemCols);
         tc_relinquish();
     }
-    // The first product's CTAs had waited for what came before them when they let
-    // the sums start, and those this kernel: the sort, base and the weights may be
-    // read at once; only h (read by the epilogue) and what overwrites anything wait.
-    if (warp == 0) count_tiles(p, s_count);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s_tmem;
     const int r = p.rank;
-    const Walk w = make_walk(s_count[0] + s_count[1], (p.out + kCols - 1) / kCols, blockIdx.x, gridDim.x);
+    // The first product's CTAs had waited for what came before them when they let
+    // the next kernel start: the sort, base and the weights may be read at once.
+    // h is waited for where the kernel before this one makes it (forward); in the
+    // gradient that is the weight gradients', which had waited for it.
+    const TileCount tiles = count_tiles(p);
+    const Walk w = make_walk(tiles.with + tiles.without, (p.out + kCols - 1) / kCols, blockIdx.x, gridDim.x);
     volatile int *abort_flag = &s_abort;
 
     // steps, tiles, multiplied tiles; step i multiplies into buffer i % 4 of D2
@@ -511,8 +535,8 @@ __global__ void __launch_bounds__(kThreads, 1) lora_up_kernel(const LoraArgs p) 
             // MMAs: 46.4 against 43.2 us for 2858 tokens at 17408 columns); a warp has 32 rows.
             const int sub = warp % 4, group = warp / 4, my_row = 32 * sub + lane;
             bool bad = false;
-            if (seg == 0) pdl_wait();
-            else epi_sync();                         // the MMAs of the tile before have ended
+            if (seg == 0 && !TRANS) pdl_wait();
+            if (seg > 0) epi_sync();                         // the MMAs of the tile before have ended
             if (adapter >= 0) {
                 // h's planes of the tile; rows past its tokens are zeros
                 const int start = s_tiles.info[seg & 1][2];
@@ -714,13 +738,13 @@ __global__ void __launch_bounds__(kWgradThreads, 1) lora_wgrad_kernel(const Wgra
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s_tmem;
-    // The kernel before let this one start after what it waited for itself (the
-    // sort, the sums) had ended, and writes nothing that is read here.
-    pdl_launch_dependents();
+    // The sort had ended when the kernel before let this one start.
     const long long units = count_units(p);
     const int ctas = int(units < gridDim.x ? units : gridDim.x), b = blockIdx.x;
     const long long u0 = b < ctas ? run_start(units, ctas, b) : 0, u1 = b < ctas ? run_start(units, ctas, b + 1) : 0;
     const int r = p.rank;
+    pdl_wait();
+    pdl_launch_dependents();
     volatile int *abort_flag = &s_abort;
     int i = 0, seg = 0;                                          // stages, pairs
     for (long long u = u0; u < u1; ++seg) {
@@ -849,7 +873,6 @@ __global__ void __launch_bounds__(kWgradThreads, 1) lora_wgrad_kernel(const Wgra
             if (lane == 0) mbar_arrive(dempty + 8 * buf);
         }
     }
-    pdl_wait();                                                  // this kernel's end is also the one's before
     cp_async_wait_all();
     if (warp == kWgradMma && seg > 0) drain_wait(dfull + 8 * ((seg - 1) % S::kBufs), ((seg - 1) / S::kBufs) & 1);
     tc_fence_before();
@@ -921,14 +944,13 @@ __device__ __forceinline__ void wgrad_sum_part(const WgradArgs &p, const Pair &q
 }
 
 template <int RP>
-__global__ void __launch_bounds__(kWgradSumThreads) wgrad_sum_kernel(const WgradArgs p) {
-    __shared__ Pair s_pair[2];
-    __shared__ int s_b0[2], s_slots[2];                  // 0 slots: no part
+__global__ void __launch_bounds__(kWgradSumThreads, 2) wgrad_sum_kernel(const WgradArgs p) {
+    __shared__ Pair s_pair;
+    __shared__ int s_b0, s_slots;                        // 0 slots: no part
     pdl_launch_dependents();
-    const int r = p.rank, b = blockIdx.x;
-    if (threadIdx.x < 64) {
-        // warp 0: the pair that the run began inside of; warp 1: the one that goes on
-        const int which = threadIdx.x / 32;
+    // blockIdx.y 0: the pair that the run began inside of; 1: the one that goes on
+    const int r = p.rank, b = blockIdx.x, which = blockIdx.y;
+    if (threadIdx.x < 32) {
         const long long units = count_units(p);
         const int ctas = int(units < gridDim.x ? units : gridDim.x);
         int b0 = 0, slots = 0;
@@ -942,18 +964,16 @@ __global__ void __launch_bounds__(kWgradSumThreads) wgrad_sum_kernel(const Wgrad
                 slots = run_owner(units, ctas, end - 1) - b0 + 1;
             }
         }
-        if (threadIdx.x % 32 == 0) s_pair[which] = q, s_b0[which] = b0, s_slots[which] = slots;
+        if (threadIdx.x == 0) s_pair = q, s_b0 = b0, s_slots = slots;
     }
     __syncthreads();
     pdl_wait();
-    #pragma unroll 1
-    for (int which = 0; which < 2; ++which)
-        if (s_slots[which]) wgrad_sum_part<RP>(p, s_pair[which], s_b0[which], s_slots[which], b - s_b0[which]);
-    const long long na = (long long)r * p.K / 8, nb = (long long)r * p.N / 8, step = (long long)gridDim.x * kWgradSumThreads;
+    if (s_slots) wgrad_sum_part<RP>(p, s_pair, s_b0, s_slots, b - s_b0);
+    const long long na = (long long)r * p.K / 8, nb = (long long)r * p.N / 8, step = 2LL * gridDim.x * kWgradSumThreads;
     for (int a = 0; a < p.adapters; ++a) {
         if (p.sizes[a] != 0) continue;
         uint4 *da = reinterpret_cast<uint4 *>(p.da) + a * na, *db = reinterpret_cast<uint4 *>(p.db) + a * nb;
-        for (long long i = (long long)b * kWgradSumThreads + threadIdx.x; i < na + nb; i += step)
+        for (long long i = (2LL * b + which) * kWgradSumThreads + threadIdx.x; i < na + nb; i += step)
             (i < na ? da[i] : db[i - na]) = make_uint4(0, 0, 0, 0);
     }
 }
@@ -971,32 +991,32 @@ int lora_max_tiles(int tokens, int adapters) {
 namespace {
 
 template <int RP, bool TRANS>
-cudaError_t launch_tensor_rank(const LoraArgs &p, int sms, cudaStream_t s) {
+cudaError_t launch_tensor_rank(const LoraArgs &p, LoraStep step, int sms, cudaStream_t s) {
     using D = DownShape<RP, TRANS>;
     using U = UpShape<RP, TRANS>;
     cudaError_t e = allow_smem<lora_down_kernel<RP, TRANS>>(D::kSmem);
     if (e == cudaSuccess) e = allow_smem<lora_up_kernel<RP, TRANS>>(U::kSmem);
     if (e != cudaSuccess) return e;
     const int ctas = sms < kMaxRuns ? sms : kMaxRuns;
+    if (step == kLoraUp)
+        return launch_chained(lora_up_kernel<RP, TRANS>, dim3(ctas), kThreads, U::kSmem, 1, s, p);
     e = launch_chained(lora_down_kernel<RP, TRANS>, dim3(ctas), kThreads, D::kSmem, 1, s, p);
     if (e != cudaSuccess) return e;
-    const int blocks = lora_max_tiles(p.tokens, p.adapters) * (kTile * (RP / 4) / kSumThreads);
-    e = launch_chained(lora_sum_kernel<RP, TRANS>, dim3(blocks), kSumThreads, 0, 1, s, p, ctas);
-    if (e != cudaSuccess) return e;
-    return launch_chained(lora_up_kernel<RP, TRANS>, dim3(ctas), kThreads, U::kSmem, 1, s, p);
+    const int blocks = lora_max_tiles(p.tokens, p.adapters) * sum_blocks(RP);
+    return launch_chained(lora_sum_kernel<RP, TRANS>, dim3(blocks), kSumThreads, 0, 1, s, p, ctas);
 }
 
 template <int RP>
-cudaError_t launch_wgrad_rank(WgradArgs p, int sms, cudaStream_t s) {
+cudaError_t launch_wgrad_rank(WgradArgs p, WgradStep step, int sms, cudaStream_t s) {
     using S = WgradShape<RP>;
     cudaError_t e = allow_smem<lora_wgrad_kernel<RP>>(S::kSmem);
     if (e != cudaSuccess) return e;
     p.slices_x = ceil_div(p.K, S::kCols);
     p.slices = p.slices_x + ceil_div(p.N, S::kCols);
     const int ctas = sms < kMaxRuns ? sms : kMaxRuns;
-    e = launch_chained(lora_wgrad_kernel<RP>, dim3(ctas), kWgradThreads, S::kSmem, 1, s, p);
-    if (e != cudaSuccess) return e;
-    return launch_chained(wgrad_sum_kernel<RP>, dim3(ctas), kWgradSumThreads, 0, 1, s, p);
+    if (step == kWgradRuns)
+        return launch_chained(lora_wgrad_kernel<RP>, dim3(ctas), kWgradThreads, S::kSmem, 1, s, p);
+    return launch_chained(wgrad_sum_kernel<RP>, dim3(ctas, 2), kWgradSumThreads, 0, 1, s, p);
 }
 
 }  // namespace
@@ -1008,21 +1028,21 @@ size_t lora_partial_bytes(int tokens, int adapters, int rank, bool backward) {
     return h > grads ? h : grads;
 }
 
-cudaError_t launch_lora_tensor(const LoraArgs &p, bool trans, int sms, cudaStream_t s) {
+cudaError_t launch_lora_tensor(const LoraArgs &p, bool trans, LoraStep step, int sms, cudaStream_t s) {
     switch (padded_rank(p.rank)) {
-        case 16: return trans ? launch_tensor_rank<16, true>(p, sms, s) : launch_tensor_rank<16, false>(p, sms, s);
-        case 32: return trans ? launch_tensor_rank<32, true>(p, sms, s) : launch_tensor_rank<32, false>(p, sms, s);
-        case 64: return trans ? launch_tensor_rank<64, true>(p, sms, s) : launch_tensor_rank<64, false>(p, sms, s);
-        default: return trans ? launch_tensor_rank<128, true>(p, sms, s) : launch_tensor_rank<128, false>(p, sms, s);
+        case 16: return trans ? launch_tensor_rank<16, true>(p, step, sms, s) : launch_tensor_rank<16, false>(p, step, sms, s);
+        case 32: return trans ? launch_tensor_rank<32, true>(p, step, sms, s) : launch_tensor_rank<32, false>(p, step, sms, s);
+        case 64: return trans ? launch_tensor_rank<64, true>(p, step, sms, s) : launch_tensor_rank<64, false>(p, step, sms, s);
+        default: return trans ? launch_tensor_rank<128, true>(p, step, sms, s) : launch_tensor_rank<128, false>(p, step, sms, s);
     }
 }
 
-cudaError_t launch_wgrad(const WgradArgs &p, int sms, cudaStream_t s) {
+cudaError_t launch_wgrad(const WgradArgs &p, WgradStep step, int sms, cudaStream_t s) {
     switch (padded_rank(p.rank)) {
-        case 16: return launch_wgrad_rank<16>(p, sms, s);
-        case 32: return launch_wgrad_rank<32>(p, sms, s);
-        case 64: return launch_wgrad_rank<64>(p, sms, s);
-        default: return launch_wgrad_rank<128>(p, sms, s);
+        case 16: return launch_wgrad_rank<16>(p, step, sms, s);
+        case 32: return launch_wgrad_rank<32>(p, step, sms, s);
+        case 64: return launch_wgrad_rank<64>(p, step, sms, s);
+        default: return launch_wgrad_rank<128>(p, step, sms, s);
     }
 }
 

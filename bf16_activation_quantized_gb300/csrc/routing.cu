@@ -28,6 +28,7 @@ constexpr int kRankIds = 256;
 constexpr int kDirectIds = 16384;
 constexpr int kMinChunk = 2048;
 constexpr int kMaxChunks = 64;
+constexpr int kSortThreads = 1024;     // of a CTA of the sort alone: they count, the first kRankIds rank
 constexpr int kMaxTopK = 256;
 // Rows a thread of the combine kernels holds at once.  Four rather than eight
 // lets twice the warps reside: 8192 tokens of 8 rows of 4096 columns took 91.5
@@ -105,23 +106,23 @@ __global__ void __launch_bounds__(4 * kRouteThreads)
 struct RankSmem {
     int total[kMaxGroups + 1];   // ids of each key
     int next[kMaxGroups + 1];    // place of the key's next id
-    int scan[kRouteWarps];
+    int scan[kSortThreads / 32];
     int place[kRankIds];         // ~place for a dropped id
 };
 
-// The CTA (kRouteThreads threads) gets the places of ids f0, f0 + 1, ... ready:
+// The CTA (THREADS threads) gets the places of ids f0, f0 + 1, ... ready:
 // next[key] = ids with a smaller key + ids of this key before f0.  counts (of
 // the counting kernel, or nullptr: all ids are counted here) makes a CTA read
 // only its own chunk's ids.  Block 0 writes the sizes.
-template <bool I64>
+template <bool I64, int THREADS>
 __device__ void rank_prepare(RankSmem &sm, const void *ids, const int *counts, int *sizes, int n, int groups,
                              int f0) {
     const int keys = groups + 1, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    for (int e = threadIdx.x; e < keys; e += kRouteThreads) sm.total[e] = sm.next[e] = 0;
+    for (int e = threadIdx.x; e < keys; e += THREADS) sm.total[e] = sm.next[e] = 0;
     __syncthreads();
     if (counts) {
         const int chunk = chunk_ids(n), chunks = (n + chunk - 1) / chunk, mine = f0 / chunk;
-        for (int e = threadIdx.x; e < keys; e += kRouteThreads) {
+        for (int e = threadIdx.x; e < keys; e += THREADS) {
             int total = 0, before = 0;
             #pragma unroll 16
             for (int c = 0; c < chunks; ++c) {
@@ -134,11 +135,11 @@ __device__ void rank_prepare(RankSmem &sm, const void *ids, const int *counts, i
         }
         __syncthreads();
         #pragma unroll 4
-        for (int f = mine * chunk + threadIdx.x; f < f0; f += kRouteThreads)
+        for (int f = mine * chunk + threadIdx.x; f < f0; f += THREADS)
             atomicAdd(&sm.next[load_key<I64>(ids, f, groups)], 1);
     } else {
         #pragma unroll 4
-        for (int f = threadIdx.x; f < n; f += kRouteThreads) {
+        for (int f = threadIdx.x; f < n; f += THREADS) {
             const int key = load_key<I64>(ids, f, groups);
             atomicAdd(&sm.total[key], 1);
             if (f < f0) atomicAdd(&sm.next[key], 1);
@@ -146,9 +147,9 @@ __device__ void rank_prepare(RankSmem &sm, const void *ids, const int *counts, i
     }
     __syncthreads();
     if (blockIdx.x == 0 && blockIdx.y == 0)
-        for (int e = threadIdx.x; e < groups; e += kRouteThreads) sizes[e] = sm.total[e];
+        for (int e = threadIdx.x; e < groups; e += THREADS) sizes[e] = sm.total[e];
     // exclusive scan over the keys, a run of them per thread
-    const int per = (keys + kRouteThreads - 1) / kRouteThreads;
+    const int per = (keys + THREADS - 1) / THREADS;
     const int e0 = min(keys, int(threadIdx.x) * per), e1 = min(keys, e0 + per);
     int sum = 0;
     for (int e = e0; e < e1; ++e) sum += sm.total[e];
@@ -204,7 +205,7 @@ __device__ void rank_ids(RankSmem &sm, const void *ids, int groups, int f0, int 
 // The sort alone: slots[f] = place (~place for a dropped id), order[place] = f;
 // either may be nullptr.
 template <bool I64>
-__global__ void __launch_bounds__(kRouteThreads)
+__global__ void __launch_bounds__(kSortThreads)
     sort_rank_kernel(const void *__restrict__ ids, const int *__restrict__ counts,
                      int *__restrict__ sizes, int *__restrict__ slots, int *__restrict__ order, int n,
                      int groups) {
@@ -212,7 +213,7 @@ __global__ void __launch_bounds__(kRouteThreads)
     pdl_wait();
     pdl_launch_dependents();
     const int f0 = blockIdx.x * kRankIds, m = min(kRankIds, n - f0);
-    rank_prepare<I64>(sm, ids, counts, sizes, n, groups, f0);
+    rank_prepare<I64, kSortThreads>(sm, ids, counts, sizes, n, groups, f0);
     rank_ids<I64>(sm, ids, groups, f0, m);
     if (int(threadIdx.x) < m) {
         const int place = sm.place[threadIdx.x];
@@ -258,7 +259,7 @@ __global__ void __launch_bounds__(kRouteThreads)
     const int c0 = int((long long)items * blockIdx.y / gridDim.y);
     const int c1 = int((long long)items * (blockIdx.y + 1) / gridDim.y);
     const int f0 = t0 * top_k, m = (t1 - t0) * top_k;
-    rank_prepare<I64>(sm, ids, nullptr, sizes, tokens * top_k, groups, f0);
+    rank_prepare<I64, kRouteThreads>(sm, ids, nullptr, sizes, tokens * top_k, groups, f0);
     rank_ids<I64>(sm, ids, groups, f0, m);
     if (blockIdx.y == 0 && int(threadIdx.x) < m) slots[f0 + threadIdx.x] = sm.place[threadIdx.x];
     int t = t0, c = c0 + threadIdx.x;
@@ -441,7 +442,7 @@ cudaError_t launch_sort_ids(const void *ids, int n, int groups, int *counts, int
                                              4 * kRouteThreads, 0, 1, s, ids, counts, n, groups);
         if (e != cudaSuccess) return e;
     }
-    return launch_chained(sort_rank_kernel<I64>, dim3(ceil_div(n, kRankIds)), kRouteThreads, 0, 1, s, ids,
+    return launch_chained(sort_rank_kernel<I64>, dim3(ceil_div(n, kRankIds)), kSortThreads, 0, 1, s, ids,
                           counts, sizes, slots, order, n, groups);
 }
 
