@@ -270,8 +270,6 @@ __global__ void __launch_bounds__(kFewThreads, RP <= 32 ? 2 : 1) lora_few_kernel
 
 // ---------------------------------------------------------------- host side
 bool aligned(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
-int ceil_div(long long a, long long b) { return int((a + b - 1) / b); }
-
 bool takes_few(int tokens, int adapters) {
     return tokens <= kFewTokens || (tokens <= kFewTokensEach && tokens <= kFewTile * adapters);
 }
@@ -448,7 +446,7 @@ w4a16_status w4a16_lora_add_backward(const w4a16_bf16 *dY, const w4a16_bf16 *X, 
     WgradArgs q = {};
     q.x = X, q.dy = dY, q.tg = p.tg, q.th = p.th, q.order = order, q.sizes = sizes, q.partial = p.partial;
     q.da = dA, q.db = dB, q.err = p.err, q.adapters = num_adapters, q.rank = rank, q.K = K, q.N = N;
-    q.vec_x = 1, q.vec_dy = p.vec_in;
+    q.vec_dy = p.vec_in;
     // The weight gradients' runs come right after g, while dY is still in L2; dX
     // fills the SMs that they leave, and their sums, which wait for all of them, end.
     e = launch_wgrad(q, kWgradRuns, sms, s);

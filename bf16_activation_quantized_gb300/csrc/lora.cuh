@@ -57,47 +57,8 @@ __device__ __forceinline__ float4 ld_cluster4(const void *p, int rank) {
     return v;
 }
 
-__device__ __forceinline__ void st_cluster16(uint32_t addr, int rank, uint4 v) {
-    asm volatile(
-        "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\t"
-        "st.shared::cluster.v4.b32 [a], {%2, %3, %4, %5};\n\t}" ::"r"(addr), "r"(rank), "r"(v.x), "r"(v.y),
-        "r"(v.z), "r"(v.w)
-        : "memory");
-}
 // Makes ordinary writes of shared memory visible to the tensor core and back.
 __device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
-
-// One arrival on CTA `rank`'s barrier at the same shared-memory address.
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar, int rank) {
-    asm volatile(
-        "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\t"
-        "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n\t}" ::"r"(bar), "r"(rank) : "memory");
-}
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-    return ok != 0;
-}
-// The bounded wait of mbar_wait for a barrier that other CTAs arrive on.
-__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, volatile int *abort_flag, int *err) {
-    unsigned long long t0 = 0;
-    for (int spins = 1; !mbar_try_wait_cluster(bar, parity); ++spins) {
-        if (*abort_flag) return false;
-        if (spins % kTimerPollSpins == 0) {
-            if (t0 == 0) {
-                t0 = global_timer_ns();
-            } else if (elapsed_beyond(&t0, kWaitLimitNs)) {
-                *abort_flag = 1;
-                if (err) atomicOr(err, kErrWaitTimeout);
-                return false;
-            }
-        }
-    }
-    return true;
-}
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -144,14 +105,9 @@ __device__ __forceinline__ void store_cols8(uint16_t *p, int left, int vec, uint
     }
 }
 
-// Producer: eight bf16 of a row into the ring.
-__device__ __forceinline__ void stage_piece(unsigned char *dst, const uint16_t *src, int left, int vec) {
-    if (vec) cp_async16(smem_u32(dst), src);
-    else *reinterpret_cast<uint4 *>(dst) = load_cols8(src, left, 0);
-}
 // Producer: its pieces of a stage are under way.
-__device__ __forceinline__ void stage_done(uint32_t bar, int vec) {
-    if (vec) {
+__device__ __forceinline__ void stage_done(uint32_t bar, bool async) {
+    if (async) {
         cp_async_arrive(bar);
     } else {
         cp_async_wait_all();
@@ -244,7 +200,7 @@ struct WgradArgs {
     int *err;
     int adapters, rank, K, N;
     int slices_x, slices;          // column slices of x, of x and dy
-    int vec_x, vec_dy;
+    int vec_dy;                    // rows of dy start on 16 bytes, as x's do
 };
 
 constexpr int kMaxCluster = 8;

@@ -21,9 +21,10 @@
 // the memory's time and left a 64-token mma.sync version waiting on MMA latency
 // (78 us for 4096 tokens, 8192 x 8192); tcgen05 needs a tenth.
 //
-// lora_wgrad_kernel: dA = g^T X and dB = s dY^T h.  The tokens are the MMA's K;
-// rows of X or dY lie along M, rows of g or s h along N, as they come, so nothing
-// is transposed.
+// lora_wgrad_kernel: dA = g^T X and dB = s dY^T h, with the tokens as the MMA's K.
+// Rows of X or dY lie along M as they come; g and s h are kept with the tokens
+// along K (the sums' kernel turns them, a few KB a tile).  wgrad_sum_kernel adds
+// what several runs share.
 #include <atomic>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -54,10 +55,14 @@ __device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, %0;" ::"n
 __device__ __forceinline__ uint32_t sw128(int row, int p) { return uint32_t(row * 128 + ((p ^ (row & 7)) << 4)); }
 
 // The walk: unit u = tile * per + step; CTA b of n takes units [run(b), run(b + 1)).
-__device__ __forceinline__ long long run_start(long long units, int n, int b) { return units * b / n; }
+// (64-bit quotients take a few hundred cycles each: 32-bit ones where they do.)
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+    return ((a | b) >> 32) == 0 ? (long long)(uint32_t(a) / uint32_t(b)) : a / b;
+}
+__device__ __forceinline__ long long run_start(long long units, int n, int b) { return quotient(units * b, n); }
 // The CTA whose run holds unit u.
 __device__ __forceinline__ int run_owner(long long units, int n, long long u) {
-    return int(((u + 1) * n - 1) / units);
+    return int(quotient((u + 1) * n - 1, units));
 }
 struct Walk {
     long long units;
@@ -117,8 +122,8 @@ __device__ __forceinline__ Producer make_producer() {
     return t;
 }
 
-// Rows of x or base: src[j] points at this thread's piece of column 0 of its
-// row; columns past n are zeros.
+// Rows of x or base: src[j] is this thread's piece of column 0 of its row; columns
+// past n are zeros.
 __device__ __forceinline__ void stage_rows(const Producer &t, unsigned char *xs, const uint16_t *const (&src)[kTile / 8],
                                            int rows, long long col, int n, int vec) {
     const uint32_t dst = smem_u32(xs) + t.dst;
@@ -243,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1) lora_down_kernel(const LoraArgs p
 
     int i = 0, seg = 0;                              // steps and tiles so far
     for (long long u = w.u0; u < w.u1; ++seg) {
-        const int tile = int(u / w.per), k0 = int(u - (long long)tile * w.per);
+        const int tile = int(quotient(u, w.per)), k0 = int(u - (long long)tile * w.per);
         const int n_steps = int(w.u1 - u < w.per - k0 ? w.u1 - u : w.per - k0);
         u += n_steps;
         if (!tile_ready(p, s_tiles, seg, tile, tfull, tempty, warp == kEpiWarps, abort_flag)) break;
@@ -472,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1) lora_up_kernel(const LoraArgs p) 
     uint32_t uses = 0;                               // a bit per buffer: the parity of its next use
     uint32_t used = 0;
     for (long long u = w.u0; u < w.u1; ++seg) {
-        const int tile = int(u / w.per), k0 = int(u - (long long)tile * w.per);
+        const int tile = int(quotient(u, w.per)), k0 = int(u - (long long)tile * w.per);
         const int n_steps = int(w.u1 - u < w.per - k0 ? w.u1 - u : w.per - k0);
         u += n_steps;
         if (!tile_ready(p, s_tiles, seg, tile, tfull, tempty, warp == kEpiWarps, abort_flag)) break;
@@ -601,12 +606,27 @@ __global__ void __launch_bounds__(kThreads, 1) lora_up_kernel(const LoraArgs p) 
                             *reinterpret_cast<uint4 *>(bs + sw128(my_row, q)) = make_uint4(fill, fill, fill, fill);
                     }
                     __syncwarp();
-                    #pragma unroll
-                    for (int m = 0; m < 8; ++m) {
-                        const int row = 32 * sub + 4 * m + lane / 8, q = lane % 8;
-                        if (row < count) {
-                            const uint4 v = *reinterpret_cast<const uint4 *>(bs + sw128(row, q));
-                            store_cols8(p.y + (long long)rows[row] * p.out + col + 8 * q, p.out - col - 8 * q, p.vec_out, v);
+                    if (TRANS || p.vec_out) {
+                        #pragma unroll
+                        for (int m = 0; m < 8; ++m) {
+                            const int row = 32 * sub + 4 * m + lane / 8, q = lane % 8;
+                            if (row < count) {
+                                const uint4 v = *reinterpret_cast<const uint4 *>(bs + sw128(row, q));
+                                store_cols8(p.y + (long long)rows[row] * p.out + col + 8 * q, p.out - col - 8 * q, p.vec_out, v);
+                            }
+                        }
+                    } else {
+                        // a row at a time, two columns a lane (N not a multiple of 8)
+                        for (int row = 32 * sub; row < min(32 * sub + 32, count); ++row) {
+                            const int left = p.out - col - 2 * lane;
+                            uint16_t *y = p.y + (long long)rows[row] * p.out + col + 2 * lane;
+                            const uint32_t v = *reinterpret_cast<const uint32_t *>(bs + sw128(row, lane / 4) + 4 * (lane % 4));
+                            if (left > 1 && reinterpret_cast<uintptr_t>(y) % 4 == 0) {
+                                *reinterpret_cast<uint32_t *>(y) = v;
+                            } else {
+                                if (left > 0) y[0] = uint16_t(v);
+                                if (left > 1) y[1] = uint16_t(v >> 16);
+                            }
                         }
                     }
                 }
@@ -686,7 +706,7 @@ __device__ Pair find_pair(const WgradArgs &p, long long u) {
             q.start = __shfl_sync(0xffffffffu, rows + r_end - size, src);
             q.tile0 = __shfl_sync(0xffffffffu, tiles + t_end - my_tiles, src);
             const long long base = __shfl_sync(0xffffffffu, units + u_end - mine, src);
-            q.slice = int((u - base) / q.blocks);
+            q.slice = int(quotient(u - base, q.blocks));
             q.first = base + (long long)q.slice * q.blocks;
             return q;
         }
@@ -760,7 +780,7 @@ __global__ void __launch_bounds__(kWgradThreads, 1) lora_wgrad_kernel(const Wgra
             // 2 blocks apart.  The rows of the next stage are looked up one stage ahead.
             const uint16_t *src_q = db ? p.dy : p.x;
             const uint16_t *src_p = (db ? p.th : p.tg) + (long long)q.tile0 * tile_planes(RP);
-            const int vec = db ? p.vec_dy : p.vec_x, *rows = p.order + q.start;
+            const int vec = db ? p.vec_dy : 1, *rows = p.order + q.start;
             const int pt = threadIdx.x, piece = pt % 16, row0 = pt / 16;
             constexpr int kRows = kWgradProducers / 16, kJ = kStageTokens / kRows, kE = S::kCols / 128;
             const uint32_t dst = (piece / 8) * S::kQBlock + sw128(row0, piece % 8);

@@ -46,9 +46,36 @@ __device__ __forceinline__ int load_key(const void *ids, int f, int groups) {
     return v >= 0 && v < groups ? v : groups;
 }
 
-// VEC consecutive bf16: 8 (one 16-byte access) or 1.
+// VEC consecutive bf16 in one access: 8, 4, 2 or 1, as the rows' starts allow.
 template <int VEC>
-struct Cols;
+struct Cols {                                        // 2 or 4
+    static constexpr int W = VEC / 2;
+    uint32_t v[W];
+    __device__ __forceinline__ void load(const uint16_t *p) {
+        if constexpr (W == 2) {
+            const uint2 u = *reinterpret_cast<const uint2 *>(p);
+            v[0] = u.x, v[1] = u.y;
+        } else {
+            v[0] = *reinterpret_cast<const uint32_t *>(p);
+        }
+    }
+    __device__ __forceinline__ void store(uint16_t *p) const {
+        if constexpr (W == 2) *reinterpret_cast<uint2 *>(p) = make_uint2(v[0], v[1]);
+        else *reinterpret_cast<uint32_t *>(p) = v[0];
+    }
+    __device__ __forceinline__ void zero() {
+        #pragma unroll
+        for (int i = 0; i < W; ++i) v[i] = 0;
+    }
+    __device__ __forceinline__ void unpack(float (&f)[VEC]) const {
+        #pragma unroll
+        for (int i = 0; i < W; ++i) f[2 * i] = bf16_lo_to_f32(v[i]), f[2 * i + 1] = bf16_hi_to_f32(v[i]);
+    }
+    __device__ __forceinline__ void pack(const float (&f)[VEC]) {
+        #pragma unroll
+        for (int i = 0; i < W; ++i) v[i] = pack_bf16x2_rn(f[2 * i], f[2 * i + 1]);
+    }
+};
 template <>
 struct Cols<8> {
     uint4 v;
@@ -415,6 +442,13 @@ ColSplit col_split(int width, int vec) {
     return c;
 }
 
+// Columns that one access of rows of `width` can take.
+int row_vec(int width, const void *a, const void *b, const void *c) {
+    for (int v = 8; v > 1; v /= 2)
+        if (width % v == 0 && aligned(a, 2 * v) && aligned(b, 2 * v) && aligned(c, 2 * v)) return v;
+    return 1;
+}
+
 w4a16_status check_routing(int tokens, int top_k, int width) {
     if (tokens < 0 || top_k < 1 || top_k > kMaxTopK || width < 1 || width > (1 << 20)) return W4A16_ERR_INVALID_ARG;
     if ((long long)tokens * top_k > kMaxSlots) return W4A16_ERR_INVALID_ARG;
@@ -457,23 +491,24 @@ cudaError_t launch_dispatch(const uint16_t *X, const void *ids, uint16_t *Xs, in
                             int tokens, int top_k, int width, int groups, int *counts, int sms,
                             cudaStream_t s) {
     const int n = tokens * top_k;
-    const bool vec = width % 8 == 0;
+    const int vec = row_vec(width, X, Xs, nullptr);
     if (n > kDirectIds) {
         const cudaError_t e = launch_sort_ids<I64>(ids, n, groups, counts, sizes, slots, nullptr, s);
         if (e != cudaSuccess) return e;
-        const ColSplit c = col_split(width, vec ? 8 : 1);
-        return launch_chained(vec ? dispatch_copy_kernel<8> : dispatch_copy_kernel<1>,
-                              dim3(tokens, c.blocks), c.threads, 0, 1, s, X, slots, Xs, top_k, width);
+        const ColSplit c = col_split(width, vec);
+        return launch_chained(vec == 8 ? dispatch_copy_kernel<8> : vec == 4 ? dispatch_copy_kernel<4>
+                              : vec == 2 ? dispatch_copy_kernel<2> : dispatch_copy_kernel<1>, dim3(tokens, c.blocks), c.threads, 0, 1, s, X, slots, Xs, top_k, width);
     }
-    const int items = ceil_div(width, vec ? 8 : 1);
+    const int items = ceil_div(width, vec);
     int per = ceil_div(tokens, 3 * sms);
     if (per * top_k > kRankIds) per = kRankIds / top_k;
     if (per < 1) per = 1;
     const int blocks = tokens > 0 ? ceil_div(tokens, per) : 1;
     int parts = ceil_div(2 * sms, blocks);
     if (parts > ceil_div(items, kRouteThreads)) parts = ceil_div(items, kRouteThreads);
-    return launch_chained(vec ? dispatch_few_kernel<I64, 8> : dispatch_few_kernel<I64, 1>, dim3(blocks, parts),
-                          kRouteThreads, 0, 1, s, X, ids, Xs, sizes, slots, tokens, top_k, width, groups, per);
+    return launch_chained(vec == 8 ? dispatch_few_kernel<I64, 8> : vec == 4 ? dispatch_few_kernel<I64, 4>
+                          : vec == 2 ? dispatch_few_kernel<I64, 2> : dispatch_few_kernel<I64, 1>,
+                          dim3(blocks, parts), kRouteThreads, 0, 1, s, X, ids, Xs, sizes, slots, tokens, top_k, width, groups, per);
 }
 
 }  // namespace
@@ -537,9 +572,11 @@ w4a16_status w4a16_combine(const w4a16_bf16 *Ys, const int32_t *slots_dev, const
     if (!aligned(Ys, 2) || !aligned(Y, 2) || !aligned(slots_dev, 4) ||
         (weights_dev && !aligned(weights_dev, weight_bytes)))
         return W4A16_ERR_INVALID_ARG;
-    const bool vec = width % 8 == 0 && aligned(Ys, 16) && aligned(Y, 16);
-    const ColSplit c = col_split(width, vec ? 8 : 1);
-    return from_cuda(launch_chained(vec ? combine_kernel<8> : combine_kernel<1>, dim3(tokens, c.blocks),
+    const int vec = row_vec(width, Ys, Y, nullptr);
+    const ColSplit c = col_split(width, vec);
+    const auto kernel = vec == 8 ? combine_kernel<8> : vec == 4 ? combine_kernel<4>
+                        : vec == 2 ? combine_kernel<2> : combine_kernel<1>;
+    return from_cuda(launch_chained(kernel, dim3(tokens, c.blocks),
                                     c.threads, 0, 1, static_cast<cudaStream_t>(stream), Ys, slots_dev,
                                     weights_dev, weight_bytes, Y, top_k, tokens * top_k, width));
 }
@@ -555,9 +592,11 @@ w4a16_status w4a16_combine_backward(const w4a16_bf16 *dY, const w4a16_bf16 *Ys, 
     if (!aligned(dY, 2) || !aligned(Ys, 2) || !aligned(dYs, 2) || !aligned(slots_dev, 4) ||
         !aligned(weights_dev, weight_bytes) || !aligned(dweights_dev, weight_bytes))
         return W4A16_ERR_INVALID_ARG;
-    const bool vec = width % 8 == 0 && aligned(dY, 16) && aligned(Ys, 16) && aligned(dYs, 16);
-    const ColSplit c = col_split(width, vec ? 8 : 1);
-    return from_cuda(launch_chained(vec ? combine_backward_kernel<8> : combine_backward_kernel<1>, dim3(tokens), c.threads, 0, 1, static_cast<cudaStream_t>(stream), dY, Ys,
+    const int vec = row_vec(width, dY, Ys, dYs);
+    const ColSplit c = col_split(width, vec);
+    const auto kernel = vec == 8 ? combine_backward_kernel<8> : vec == 4 ? combine_backward_kernel<4>
+                        : vec == 2 ? combine_backward_kernel<2> : combine_backward_kernel<1>;
+    return from_cuda(launch_chained(kernel, dim3(tokens), c.threads, 0, 1, static_cast<cudaStream_t>(stream), dY, Ys,
                                     slots_dev, weights_dev, weight_bytes, dYs, dweights_dev, top_k,
                                     tokens * top_k, width));
 }

@@ -398,8 +398,8 @@ w4a16_status w4a16_dispatch(const w4a16_bf16 *X, const void *ids_dev, int id_byt
  *               for weights of one, which makes the call the gradient of
  *               w4a16_dispatch (dX from dXs).
  *  Y:           device bf16 [tokens][width]; must not overlap Ys.
- * Element alignment is enough; 16-byte aligned Ys and Y with width a multiple
- * of 8 take the wide path.  Limits as for w4a16_dispatch. */
+ * Element alignment is enough; the widest access (16 bytes down to 2) that
+ * width and the addresses allow is taken.  Limits as for w4a16_dispatch. */
 w4a16_status w4a16_combine(const w4a16_bf16 *Ys, const int32_t *slots_dev, const void *weights_dev,
                            int weight_bytes, w4a16_bf16 *Y, int tokens, int top_k, int width,
                            void *stream);
@@ -434,7 +434,7 @@ w4a16_status w4a16_combine_backward(const w4a16_bf16 *dY, const w4a16_bf16 *Ys, 
  * with zeros by the caller.  1 <= num_adapters <= 1024, K a positive multiple
  * of 128, N >= 1, 0 <= tokens <= 2^24.  X, A, B, hidden and workspace 16-byte
  * aligned, base and Y 2-byte; with N a multiple of 8 and 16-byte aligned base
- * and Y the rows move 16 bytes at a time.  Nothing is read on the host, so the
+ * and Y the rows move 16 bytes at a time, which is fastest.  Nothing is read on the host, so the
  * call is capturable; the result does not depend on timing. */
 w4a16_status w4a16_lora_workspace_bytes(int tokens, int num_adapters, int rank, int backward,
                                         size_t *bytes);
