@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(kFewThreads, RP <= 32 ? 2 : 1) lora_few_kernel
     constexpr int TM = kFewTile, NT = RP / 8, QN = RP >= 32 ? RP / 32 : 1, KS = RP / 16;
     constexpr int PS = RP + 4;                           // floats of a row of h
     constexpr int U = RP <= 32 ? 4 : RP == 64 ? 2 : 1;   // steps of the first product loaded together
-    constexpr int PF = RP == 16 ? 4 : RP == 32 ? 3 : RP == 64 ? 2 : 1;  // steps of the second
+    constexpr int PF = RP == 16 ? 4 : RP <= 64 ? 2 : 1;   // steps of the second: three at RP 32 spilled (6.4 against 6.2 us)
     constexpr int kQuads = RP / 4;
     extern __shared__ float s_mem[];
     float *s_part = s_mem;                               // [kFewWarps][TM][PS]
