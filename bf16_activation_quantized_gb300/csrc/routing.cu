@@ -111,7 +111,8 @@ __host__ __device__ __forceinline__ int chunk_ids(int n) {
     return even > kMinChunk ? even : kMinChunk;
 }
 
-// counts[c][key] over the ids of chunk c.
+// counts[c][key] over the ids of chunk c: a histogram in shared memory.  Bound by
+// latency (one chunk's ids in a few loads a thread): 65536 ids of 128 keys 3.6 us.
 template <bool I64>
 __global__ void __launch_bounds__(4 * kRouteThreads)
     sort_count_kernel(const void *__restrict__ ids, int *__restrict__ counts, int n, int groups) {
@@ -149,18 +150,13 @@ __device__ void rank_prepare(RankSmem &sm, const void *ids, const int *counts, i
     __syncthreads();
     if (counts) {
         const int chunk = chunk_ids(n), chunks = (n + chunk - 1) / chunk, mine = f0 / chunk;
-        for (int e = threadIdx.x; e < keys; e += THREADS) {
-            int total = 0, before = 0;
-            #pragma unroll 16
-            for (int c = 0; c < chunks; ++c) {
-                const int v = counts[c * keys + e];
-                total += v;
-                before += c < mine ? v : 0;
-            }
-            sm.total[e] = total;
-            sm.next[e] = before;
+        #pragma unroll 4
+        for (int i = threadIdx.x; i < chunks * keys; i += THREADS) {
+            const int v = counts[i], c = i / keys, e = i - c * keys;
+            if (v == 0) continue;
+            atomicAdd(&sm.total[e], v);
+            if (c < mine) atomicAdd(&sm.next[e], v);
         }
-        __syncthreads();
         #pragma unroll 4
         for (int f = mine * chunk + threadIdx.x; f < f0; f += THREADS)
             atomicAdd(&sm.next[load_key<I64>(ids, f, groups)], 1);
@@ -189,7 +185,8 @@ __device__ void rank_prepare(RankSmem &sm, const void *ids, const int *counts, i
     if (lane == 31) sm.scan[warp] = scan;
     __syncthreads();
     int start = scan - sum;
-    for (int w = 0; w < warp; ++w) start += sm.scan[w];
+    if (e0 < e1)
+        for (int w = 0; w < warp; ++w) start += sm.scan[w];
     for (int e = e0; e < e1; ++e) {
         sm.next[e] += start;
         start += sm.total[e];
@@ -230,7 +227,9 @@ __device__ void rank_ids(RankSmem &sm, const void *ids, int groups, int f0, int 
 }
 
 // The sort alone: slots[f] = place (~place for a dropped id), order[place] = f;
-// either may be nullptr.
+// either may be nullptr.  Bound by latency (ids, counts, scan, ranks, one after the
+// other), so a CTA of 1024 threads counts and its first 256 rank: 65536 ids of 128
+// keys 10 us after the counts, 4096 ids of one key 5 us by itself.
 template <bool I64>
 __global__ void __launch_bounds__(kSortThreads)
     sort_rank_kernel(const void *__restrict__ ids, const int *__restrict__ counts,
@@ -249,18 +248,24 @@ __global__ void __launch_bounds__(kSortThreads)
     }
 }
 
-// Token t's columns to the rows of its slots.
+// Token t's columns to the rows of its slots: xs[row(f)] = x[t], read once and
+// written top_k times; no arithmetic.  Bound by HBM's writes.  A thread holds one
+// access of a token: blocks in token order keep each group's writes together, and
+// thousands of small CTAs leave enough stores in flight.  8192 tokens of 8 rows of
+// 4096 columns: 89 us, 6.8 TB/s (99.8 with the sort before it).
 template <int VEC>
 __global__ void __launch_bounds__(kRouteThreads)
     dispatch_copy_kernel(const uint16_t *__restrict__ X, const int *__restrict__ slots,
                          uint16_t *__restrict__ Xs, int top_k, int width) {
-    pdl_wait();
-    pdl_launch_dependents();
     const int t = blockIdx.x;
     const int col = (blockIdx.y * blockDim.x + threadIdx.x) * VEC;
-    if (col >= width) return;
+    // The sort's CTAs had waited for what came before them when they let this
+    // kernel start: X may be read before the sort has ended.
     Cols<VEC> x;
-    x.load(X + (long long)t * width + col);
+    if (col < width) x.load(X + (long long)t * width + col);
+    pdl_wait();
+    pdl_launch_dependents();
+    if (col >= width) return;
     const int *mine = slots + (long long)t * top_k;
     #pragma unroll 8
     for (int j = 0; j < top_k; ++j) {
@@ -272,7 +277,11 @@ __global__ void __launch_bounds__(kRouteThreads)
 }
 
 // CTA (b, c) ranks the slots of tokens [b * per, ...) and copies their columns
-// of part c: each row is read once and written top_k times.
+// of part c: each row is read once and written top_k times.  Bound by latency: the
+// ids, the counts and the scan come before the first store.  One launch instead of
+// three: one token of 8 rows of 8192 columns 2.9 us, 1322 tokens of 2 rows of 2560
+// columns 5.5 us (3.7 TB/s).  Loading X before the ranking, four pieces a thread,
+// took 3.2 and 7.4 us.
 template <bool I64, int VEC>
 __global__ void __launch_bounds__(kRouteThreads)
     dispatch_few_kernel(const uint16_t *__restrict__ X, const void *__restrict__ ids,
@@ -315,7 +324,10 @@ __device__ __forceinline__ float load_weight(const void *w, int bytes, long long
 
 // y[t] = sum over the kept slots of w * ys[row], in fp32, j ascending, rounded
 // once.  w == nullptr: weights of one (the gradient of dispatch).  A slot at
-// or past `rows` is skipped.
+// or past `rows` is skipped.  Bound by HBM's reads, one VEC of a token's columns
+// per thread with kSlotsAtOnce rows in flight; gathering by token leaves no atomics
+// and a fixed order.  8192 tokens of 8 rows of 4096 columns: 91.4 us, 6.6 TB/s; as
+// dispatch's gradient 4096 tokens of 4 rows of 5120 columns: 32.7 us, 6.4 TB/s.
 template <int VEC>
 __global__ void __launch_bounds__(kRouteThreads)
     combine_kernel(const uint16_t *__restrict__ Ys, const int *__restrict__ slots,
@@ -356,7 +368,10 @@ __global__ void __launch_bounds__(kRouteThreads)
 }
 
 // One CTA per token: dys[row] = w * dy (zeros for a dropped slot's own row),
-// dw[t][j] = <dy[t], ys[row]> in fp32.  kSlotsAtOnce slots a pass.
+// dw[t][j] = <dy[t], ys[row]> in fp32.  kSlotsAtOnce slots a pass.  Bound by HBM:
+// dy is read once per pass, ys once, dys written once, and the dot products need the
+// token's whole row in one CTA.  4096 tokens of 4 rows of 5120 columns: 59.9 us,
+// 6.3 TB/s.
 template <int VEC>
 __global__ void __launch_bounds__(kRouteThreads)
     combine_backward_kernel(const uint16_t *__restrict__ dY, const uint16_t *__restrict__ Ys,
@@ -481,10 +496,10 @@ cudaError_t launch_sort_ids(const void *ids, int n, int groups, int *counts, int
 }
 
 // Few ids: one launch, whose CTAs each count all ids, so there are only about
-// three per SM (1322 tokens of 2 ids and 2560 columns: 5.7 us, with six per SM
+// three per SM (1322 tokens of 2 ids and 2560 columns: 5.5 us, with six per SM
 // 8.0), each with at most kRankIds ids; few tokens also split their columns.
 // Many ids: the sort, then a copy in token order, whose writes advance through
-// every group together (8192 tokens of 8 ids and 4096 columns: 100 us; 911
+// every group together (8192 tokens of 8 ids and 4096 columns: 99.8 us; 911
 // CTAs that rank and copy nine tokens each took 111).
 template <bool I64>
 cudaError_t launch_dispatch(const uint16_t *X, const void *ids, uint16_t *Xs, int *sizes, int *slots,
