@@ -606,27 +606,12 @@ __global__ void __launch_bounds__(kThreads, 1) lora_up_kernel(const LoraArgs p) 
                             *reinterpret_cast<uint4 *>(bs + sw128(my_row, q)) = make_uint4(fill, fill, fill, fill);
                     }
                     __syncwarp();
-                    if (TRANS || p.vec_out) {
-                        #pragma unroll
-                        for (int m = 0; m < 8; ++m) {
-                            const int row = 32 * sub + 4 * m + lane / 8, q = lane % 8;
-                            if (row < count) {
-                                const uint4 v = *reinterpret_cast<const uint4 *>(bs + sw128(row, q));
-                                store_cols8(p.y + (long long)rows[row] * p.out + col + 8 * q, p.out - col - 8 * q, p.vec_out, v);
-                            }
-                        }
-                    } else {
-                        // a row at a time, two columns a lane (N not a multiple of 8)
-                        for (int row = 32 * sub; row < min(32 * sub + 32, count); ++row) {
-                            const int left = p.out - col - 2 * lane;
-                            uint16_t *y = p.y + (long long)rows[row] * p.out + col + 2 * lane;
-                            const uint32_t v = *reinterpret_cast<const uint32_t *>(bs + sw128(row, lane / 4) + 4 * (lane % 4));
-                            if (left > 1 && reinterpret_cast<uintptr_t>(y) % 4 == 0) {
-                                *reinterpret_cast<uint32_t *>(y) = v;
-                            } else {
-                                if (left > 0) y[0] = uint16_t(v);
-                                if (left > 1) y[1] = uint16_t(v >> 16);
-                            }
+                    #pragma unroll
+                    for (int m = 0; m < 8; ++m) {
+                        const int row = 32 * sub + 4 * m + lane / 8, q = lane % 8;
+                        if (row < count) {
+                            const uint4 v = *reinterpret_cast<const uint4 *>(bs + sw128(row, q));
+                            store_cols8(p.y + (long long)rows[row] * p.out + col + 8 * q, p.out - col - 8 * q, p.vec_out, v);
                         }
                     }
                 }
