@@ -581,23 +581,31 @@ __global__ void __launch_bounds__(kThreads, 1) lora_up_kernel(const LoraArgs p) 
                     const int col = (k0 + k) * kCols + 64 * half;
                     if (col >= p.out || 32 * sub >= count) break;
                     unsigned char *bs = s_mem + s * S::kStage + half * kBlock;
+                    // Four pieces of 16 bytes at once: the compiler cannot tell that a store of
+                    // one leaves the next one's load alone.
                     if (adapter >= 0 && !bad) {
                         uint32_t acc[2][32];
                         tc_ld_32x32b_x32(lanes + 64 * half, acc[0]);
                         tc_ld_32x32b_x32(lanes + 64 * half + 32, acc[1]);
-                        tc_wait_ld();
+                        uint4 v[4];
                         #pragma unroll
-                        for (int q = 0; q < 8; ++q) {
-                            uint4 *at = reinterpret_cast<uint4 *>(bs + sw128(my_row, q));
-                            uint4 b = make_uint4(0, 0, 0, 0);
-                            if (p.base) b = *at;
-                            const uint32_t *d = &acc[q / 4][8 * (q % 4)];
-                            uint4 v;
-                            v.x = pack_bf16x2_rn(bf16_lo_to_f32(b.x) + __uint_as_float(d[0]), bf16_hi_to_f32(b.x) + __uint_as_float(d[1]));
-                            v.y = pack_bf16x2_rn(bf16_lo_to_f32(b.y) + __uint_as_float(d[2]), bf16_hi_to_f32(b.y) + __uint_as_float(d[3]));
-                            v.z = pack_bf16x2_rn(bf16_lo_to_f32(b.z) + __uint_as_float(d[4]), bf16_hi_to_f32(b.z) + __uint_as_float(d[5]));
-                            v.w = pack_bf16x2_rn(bf16_lo_to_f32(b.w) + __uint_as_float(d[6]), bf16_hi_to_f32(b.w) + __uint_as_float(d[7]));
-                            *at = v;
+                        for (int h = 0; h < 2; ++h) {
+                            #pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                v[q] = make_uint4(0, 0, 0, 0);
+                                if (p.base) v[q] = *reinterpret_cast<const uint4 *>(bs + sw128(my_row, 4 * h + q));
+                            }
+                            if (h == 0) tc_wait_ld();
+                            #pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                const uint32_t *d = &acc[h][8 * q];
+                                const uint4 b = v[q];
+                                v[q].x = pack_bf16x2_rn(bf16_lo_to_f32(b.x) + __uint_as_float(d[0]), bf16_hi_to_f32(b.x) + __uint_as_float(d[1]));
+                                v[q].y = pack_bf16x2_rn(bf16_lo_to_f32(b.y) + __uint_as_float(d[2]), bf16_hi_to_f32(b.y) + __uint_as_float(d[3]));
+                                v[q].z = pack_bf16x2_rn(bf16_lo_to_f32(b.z) + __uint_as_float(d[4]), bf16_hi_to_f32(b.z) + __uint_as_float(d[5]));
+                                v[q].w = pack_bf16x2_rn(bf16_lo_to_f32(b.w) + __uint_as_float(d[6]), bf16_hi_to_f32(b.w) + __uint_as_float(d[7]));
+                                *reinterpret_cast<uint4 *>(bs + sw128(my_row, 4 * h + q)) = v[q];
+                            }
                         }
                     } else if (bad || !p.base) {
                         const uint32_t fill = bad ? 0x7fff7fffu : 0u;
@@ -606,13 +614,20 @@ __global__ void __launch_bounds__(kThreads, 1) lora_up_kernel(const LoraArgs p) 
                             *reinterpret_cast<uint4 *>(bs + sw128(my_row, q)) = make_uint4(fill, fill, fill, fill);
                     }
                     __syncwarp();
+                    const int q = lane % 8, left = p.out - col - 8 * q;
                     #pragma unroll
-                    for (int m = 0; m < 8; ++m) {
-                        const int row = 32 * sub + 4 * m + lane / 8, q = lane % 8;
-                        if (row < count) {
-                            const uint4 v = *reinterpret_cast<const uint4 *>(bs + sw128(row, q));
-                            store_cols8(p.y + (long long)rows[row] * p.out + col + 8 * q, p.out - col - 8 * q, p.vec_out, v);
+                    for (int h = 0; h < 2; ++h) {
+                        uint4 v[4];
+                        uint16_t *y[4];
+                        #pragma unroll
+                        for (int m = 0; m < 4; ++m) {
+                            const int row = 32 * sub + 16 * h + 4 * m + lane / 8;
+                            v[m] = *reinterpret_cast<const uint4 *>(bs + sw128(row, q));
+                            y[m] = p.y + (long long)rows[row < count ? row : 0] * p.out + col + 8 * q;
                         }
+                        #pragma unroll
+                        for (int m = 0; m < 4; ++m)
+                            if (32 * sub + 16 * h + 4 * m + lane / 8 < count) store_cols8(y[m], left, p.vec_out, v[m]);
                     }
                 }
                 tc_fence_before();
