@@ -12,6 +12,7 @@
 // Precision: products of bf16 are exact in the MMA and summed in fp32; h (and g)
 // stay in fp32 and enter the second product as a sum of two bf16 terms, which
 // holds them to 2^-17.  The outputs are rounded once.
+#include <atomic>
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -27,21 +28,28 @@ constexpr int kFewThreads = 256;
 constexpr int kFewWarps = kFewThreads / 32;
 constexpr int kStepCols = 32;          // columns of a step: 16 bytes per lane of a quad
 constexpr int kFewTile = 16;
-// Up to kFewTokens tokens take this kernel, and up to kFewTokensEach while the
-// adapters have at most 16 each on average.  Measured at 8192 x 8192 and rank 16
-// (64), this kernel / the tensor core kernels: 192 tokens of 1 adapter 13.6 / 19.1
-// us (27.4 / 21.6), of 16 13.4 / 26.2 (23.0 / 30.5); 384 tokens of 16 19.2 / 27.6
-// (40.3 / 32.1); 512 tokens of 1 36.4 / 25.7, of 128 32.0 / 108 (78 / 118).
-constexpr int kFewTokens = 192, kFewTokensEach = 512;
+// Up to `tokens` tokens take this kernel, and up to `most` while the adapters have at
+// most `each` on average (many adapters leave the tensor core kernels' tiles of 128
+// tokens mostly empty).  Measured at 8192 x 8192, this kernel / the tensor core kernels,
+// in us.  Rank 16: 384 tokens of 1 adapter 26.8 / 30.8, 448 33.9 / 29.3; 512 of 16 26.5 /
+// 27.0, 640 34.8 / 27.3; 768 of 64 33.8 / 61.4.  Rank 32: 192 tokens of 1 adapter 17.4 /
+// 19.8, 384 of 4 29.8 / 28.8, 768 of 64 41.5 / 64.2.  Rank 64: 128 tokens of 1 adapter
+// 19.3 / 19.8, 160 24.4 / 21.0; 256 of 16 26.3 / 30.0, 320 34.5 / 30.3; 512 of 64 59.6 /
+// 67.6, 640 73.3 / 68.0.  Rank 128: 128 of 4 23.4 / 24.7, 512 of 64 69.2 / 95.4.
+struct FewLimits {
+    int tokens, most, each;
+};
+constexpr FewLimits few_limits(int rank) { return rank <= 32 ? FewLimits{384, 768, 32} : FewLimits{128, 512, 16}; }
 constexpr int kMaxRank = 128;
 
 __device__ __forceinline__ void mma_acc(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     mma_16816_c(c, a, b0, b1, c);
 }
 
-// Few tokens: one launch.  A cluster of eight CTAs owns up to 16 tokens of one
+// Few tokens: one launch.  A cluster of eight CTAs (fewer where not all clusters would
+// be resident, few_cluster) owns up to 16 tokens of one
 // adapter (cluster i starts at token i, or leaves if an earlier one has it),
-// found in the ids without a sort.  Its 64 warps split the columns of the first
+// found in the ids without a sort.  Its warps split the columns of the first
 // product, add their sums of h in shared and then distributed shared memory in
 // a fixed order, and split the columns of the second.  Everything goes from
 // global memory straight into MMA fragments: the order of k inside an MMA is
@@ -51,13 +59,18 @@ __device__ __forceinline__ void mma_acc(float (&c)[4], const uint32_t (&a)[4], u
 //
 // What bounds it: latency.  One token at rank 16 and 8192 x 8192 needs 0.5 MB;
 // the chain is ids -> rows and A -> sums over warps and CTAs -> y, so the first
-// B and base of each warp are on their way before the sums are.
+// B and base of each warp are on their way before the sums are.  Measured at 8192 x
+// 8192 and rank 16: one token 5.1 us, 32 tokens of 32 adapters 6.6 (2.8 TB/s, of which
+// much from L2); 61 tokens of 64 adapters at rank 32, 2560 to 19456 columns: 19.5
+// us (57 MB, 2.9 TB/s), bound by how many loads the 8 warps of a CTA hold in registers.
 template <int RP>
 __global__ void __launch_bounds__(kFewThreads, RP <= 32 ? 2 : 1) lora_few_kernel(const LoraArgs p) {
     constexpr int TM = kFewTile, NT = RP / 8, QN = RP >= 32 ? RP / 32 : 1, KS = RP / 16;
     constexpr int PS = RP + 4;                           // floats of a row of h
-    constexpr int U = RP <= 32 ? 4 : RP == 64 ? 2 : 1;   // steps of the first product loaded together
-    constexpr int PF = RP == 16 ? 4 : RP <= 64 ? 2 : 1;   // steps of the second: three at RP 32 spilled (6.4 against 6.2 us)
+    // Steps of the first and of the second product whose operands a lane loads together,
+    // as many as its registers hold (128 up to rank 32, else 255): three of the first at
+    // rank 64 or two at 128 gained nothing, one more of the second spilled.
+    constexpr int U = RP <= 32 ? 2 : 1, PF = RP == 16 || RP == 64 ? 4 : RP == 32 ? 3 : 2;
     constexpr int kQuads = RP / 4;
     extern __shared__ float s_mem[];
     float *s_part = s_mem;                               // [kFewWarps][TM][PS]
@@ -270,38 +283,61 @@ __global__ void __launch_bounds__(kFewThreads, RP <= 32 ? 2 : 1) lora_few_kernel
 
 // ---------------------------------------------------------------- host side
 bool aligned(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
-bool takes_few(int tokens, int adapters) {
-    return tokens <= kFewTokens || (tokens <= kFewTokensEach && tokens <= kFewTile * adapters);
+bool takes_few(int tokens, int adapters, int rank) {
+    const FewLimits m = few_limits(rank);
+    return tokens <= m.tokens || (tokens <= m.most && tokens <= m.each * adapters);
 }
 
-// CTAs of a cluster: eight where all clusters can be resident at once (two CTAs
-// per SM up to rank 32, else one), counting a cluster per adapter in use and one
-// per 16 tokens.  Measured at 8192 x 8192 with 64 adapters, 8 / 4 / 2 CTAs: rank
-// 16, 32 tokens 6.8 / 7.7 / 12.1 us, 64 tokens 12.6 / 10.2 / 12.8; rank 64, 16
-// tokens 10.7 / 15.6 / 26.6, 64 tokens 34.9 / 34.9 / 30.4.
-int few_cluster(int tokens, int adapters, int padded, int sms) {
+// Clusters of c CTAs of the kernel that can be resident at once on the current device.
+template <int RP>
+int resident_clusters(int c, size_t smem) {
+    static std::atomic<int> known[64][kMaxCluster + 1];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    if (dev < 64 && (n = known[dev][c].load(std::memory_order_relaxed)) > 0) return n;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(c);
+    cfg.blockDim = dim3(kFewThreads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = c;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, lora_few_kernel<RP>, &cfg) != cudaSuccess) return 0;
+    if (dev < 64) known[dev][c].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+// CTAs of a cluster: eight where all clusters can be resident at once, counting one
+// per adapter in use and one per 16 tokens.  Measured at 8192 x 8192 with 64
+// adapters, 8 / 4 / 2 CTAs: rank 16, 32 tokens 6.6 / 7.6 / 11.8 us, 64 tokens 13.2 /
+// 9.8 / 12.4; rank 64, 16 tokens (one cluster of eight too many) 15.9 / 12.2 / 20.5,
+// 64 tokens 51.8 / 36.7 / 32.2.
+template <int RP>
+int few_cluster(int tokens, int adapters, size_t smem) {
     const int used = adapters + tokens / kFewTile, clusters = tokens < used ? tokens : used;
-    const int slots = (padded <= 32 ? 2 : 1) * sms;
     int c = kMaxCluster;
-    while (c > 2 && clusters * c > slots) c /= 2;
+    while (c > 2 && clusters > resident_clusters<RP>(c, smem)) c /= 2;
     return c;
 }
 
 template <int RP>
-cudaError_t launch_few(const LoraArgs &p, int sms, cudaStream_t s) {
+cudaError_t launch_few(const LoraArgs &p, cudaStream_t s) {
     constexpr size_t smem = size_t(kFewWarps + 1) * kFewTile * (RP + 4) * 4;
     const cudaError_t e = allow_smem<lora_few_kernel<RP>>(smem);
     if (e != cudaSuccess) return e;
-    const int cluster = few_cluster(p.tokens, p.adapters, RP, sms);
+    const int cluster = few_cluster<RP>(p.tokens, p.adapters, smem);
     return launch_chained(lora_few_kernel<RP>, dim3(unsigned(p.tokens) * cluster), kFewThreads, smem, cluster, s, p);
 }
 
-cudaError_t launch_lora_few(const LoraArgs &p, int sms, cudaStream_t s) {
+cudaError_t launch_lora_few(const LoraArgs &p, cudaStream_t s) {
     switch (padded_rank(p.rank)) {
-        case 16: return launch_few<16>(p, sms, s);
-        case 32: return launch_few<32>(p, sms, s);
-        case 64: return launch_few<64>(p, sms, s);
-        default: return launch_few<128>(p, sms, s);
+        case 16: return launch_few<16>(p, s);
+        case 32: return launch_few<32>(p, s);
+        case 64: return launch_few<64>(p, s);
+        default: return launch_few<128>(p, s);
     }
 }
 
@@ -324,7 +360,7 @@ LoraWorkspace lora_workspace(int tokens, int adapters, int rank, bool backward) 
     const size_t by_tile = backward ? size_t(lora_max_tiles(tokens, adapters)) * tile_planes(padded_rank(rank)) * 2 : 0;
     w.th = w.tg + by_tile;
     w.total = w.th + by_tile;
-    if (!backward && takes_few(tokens, adapters)) w.total = 0;
+    if (!backward && takes_few(tokens, adapters, rank)) w.total = 0;
     return w;
 }
 
@@ -390,7 +426,7 @@ w4a16_status w4a16_lora_add(const w4a16_bf16 *X, const w4a16_bf16 *A, const w4a1
     p.tokens = tokens, p.adapters = num_adapters, p.rank = rank, p.in = K, p.out = N;
     p.vec_in = 1;
     p.vec_out = N % 8 == 0 && aligned(base, 16) && aligned(Y, 16);
-    if (takes_few(tokens, num_adapters)) return from_cuda(launch_lora_few(p, sms, s));
+    if (takes_few(tokens, num_adapters, rank)) return from_cuda(launch_lora_few(p, s));
     char *ws = static_cast<char *>(workspace);
     int *order = reinterpret_cast<int *>(ws + w.order), *sizes = reinterpret_cast<int *>(ws + w.sizes);
     cudaError_t e = launch_sort(adapters_dev, id_bytes, tokens, num_adapters,

@@ -192,6 +192,12 @@ __device__ __forceinline__ void tile_done(int seg, uint32_t tempty) {
 }
 
 // ------------------------------------------------------------ first product
+// h[t][rank] = sum over columns of x[t][col] A[rank][col] (g: of dy and B, whose
+// columns lie along the weight's rows: an MN-major operand).  Tokens are the MMA's M,
+// ranks its N.  Bound by HBM, the rows of X: a stage is 32 KB of them, six stages
+// keep up to 216 KB per SM in flight.  4096 tokens of 8192 columns at rank 64 (67 MB):
+// 11.5 us from the first data to the last sum, 5.8 TB/s; 17 us with the start and the
+// walk's set-up (sizes -> tile -> rows -> X, one load after the other).
 template <int RP, bool TRANS>
 struct DownShape {
     static constexpr int kW = weight_bytes(RP, !TRANS);
@@ -337,7 +343,8 @@ __global__ void __launch_bounds__(kThreads, 1) lora_down_kernel(const LoraArgs p
 // at once.
 constexpr int kSumThreads = 256;
 // Blocks of a tile, four ranks of a row per thread: the kernel is a chain of
-// latencies (a quarter of the blocks with four rows each took 7.6 us, these 3.5).
+// latencies (a quarter of the blocks with four rows each took 7.6 us, these 3.5 when
+// the sums are in L2: 4096 tokens at rank 64).
 constexpr int sum_blocks(int RP) { return kTile * (RP / 4) / kSumThreads; }
 
 template <int RP, bool TRANS>
@@ -421,6 +428,13 @@ __global__ void __launch_bounds__(kSumThreads) lora_sum_kernel(const LoraArgs p,
 }
 
 // ----------------------------------------------------------- second product
+// y[t][col] = base[t][col] + sum over ranks of (hi + lo)[t][rank] B[col][rank] (dx: A,
+// the weight's ranks along its rows, an MN-major operand).  Tokens are the MMA's M, the
+// stage's 128 columns its N; the low plane first, both into one accumulator in TMEM.
+// Bound by HBM: base in, y out.  The accumulators meet base in its swizzled place, and
+// a warp stores four rows' 128 bytes in one instruction; pieces four at a time (one at a
+// time the shared-memory round trips took 2 of 57.5 us below).  2858 tokens of 12 adapters,
+// 17408 columns, rank 16: 42 of the call's 55.6 us, 4.8 TB/s with 200 MB of base and y.
 template <int RP, bool TRANS>
 struct UpShape {
     static constexpr int kW = weight_bytes(RP, TRANS);
@@ -536,8 +550,8 @@ __global__ void __launch_bounds__(kThreads, 1) lora_up_kernel(const LoraArgs p) 
             }
         } else {
             // Two groups of four warps take the steps in turn, two buffers of D2 each (with
-            // one, 1100 to 1700 of a group's 5300 cycles a step went by waiting for the
-            // MMAs: 46.4 against 43.2 us for 2858 tokens at 17408 columns); a warp has 32 rows.
+            // one buffer 1100 to 1700 of a group's 5300 cycles a step went by waiting for
+            // the MMAs); a warp has 32 rows.
             const int sub = warp % 4, group = warp / 4, my_row = 32 * sub + lane;
             bool bad = false;
             if (seg == 0 && !TRANS) pdl_wait();
@@ -731,7 +745,8 @@ __device__ __forceinline__ long long count_units(const WgradArgs &p) {
 // What bounds it: the MMAs, at 142 cycles for 128 x 128 x 16 with the rows along M
 // (a stage of 32 tokens and 512 columns at rank 64: 1150 of the 1750 cycles that
 // its copies and they take together).  Two MMAs for the planes took 90 each, x or dy
-// as the MMA's 256 columns 375.
+// as the MMA's 256 columns 375.  4096 tokens of 8192 and 8192 columns at rank 64: 33 us,
+// 4.1 TB/s of x and dy (dy from L2) besides a quarter of that in planes.
 template <int RP>
 __global__ void __launch_bounds__(kWgradThreads, 1) lora_wgrad_kernel(const WgradArgs p) {
     using S = WgradShape<RP>;
@@ -904,7 +919,9 @@ __global__ void __launch_bounds__(kWgradThreads, 1) lora_wgrad_kernel(const Wgra
 // The gradients of pairs that several runs share: of a pair that n runs share the
 // n blocks of these CTAs each add a part, in CTA order; so a block has a part of
 // the pair its run began inside of and a part of the pair its run left unfinished.
-// All blocks clear the gradients of adapters without tokens.
+// All blocks clear the gradients of adapters without tokens.  Bound by latency and
+// L2: two tiles of sums per run at most (40 MB at rank 64), 5 us for 4096 tokens of
+// one adapter with 8192 and 8192 columns.
 constexpr int kWgradSumThreads = 512;
 
 template <int RP>

@@ -110,14 +110,16 @@ def assert_within(got, want, bound, what):
     assert not bool(bad.any()), f"{what}: {int(bad.sum())} of {bad.numel()} off, worst {float((err - bound).nan_to_num(1e9).max())}"
 
 
-# T, L, r, N, K: one token; a tile and one more; the most tokens of the few-token form
-# and one more, by their number and by their number per adapter; every rank block;
-# odd output widths; more adapters than tokens; past the ids one CTA counts.
+# T, L, r, N, K: one token; a tile and one more; both forms at every rank block; odd
+# output widths; more adapters than tokens; past the ids one CTA counts.
 SHAPES = [(1, 1, 8, 8, 128), (1, 8, 16, 8192, 1024), (2, 3, 24, 1, 128), (16, 1, 16, 264, 256), (17, 1, 32, 72, 384),
           (61, 64, 48, 1000, 640), (128, 4, 64, 136, 256), (128, 2, 128, 200, 256), (129, 2, 128, 200, 256),
           (129, 40, 16, 7, 128), (64, 1, 40, 2561, 1152), (193, 3, 64, 2561, 1152), (500, 16, 8, 33, 2560),
           (192, 1, 16, 72, 128), (193, 12, 16, 72, 128), (400, 25, 64, 136, 256), (401, 25, 64, 136, 256),
-          (512, 32, 32, 40, 128), (513, 40, 32, 40, 128), (1000, 5, 32, 640, 256), (777, 300, 16, 96, 128), (2051, 2, 56, 300, 128), (17000, 9, 16, 24, 128)]
+          (512, 32, 32, 40, 128), (513, 40, 32, 40, 128), (1000, 5, 32, 640, 256), (777, 300, 16, 96, 128), (2051, 2, 56, 300, 128), (17000, 9, 16, 24, 128),
+          # the most tokens of the few-token form and one more, to rank 32 and past it
+          (384, 1, 16, 72, 128), (385, 1, 16, 72, 128), (768, 24, 32, 40, 128), (769, 24, 32, 40, 128),
+          (512, 32, 40, 40, 128), (513, 32, 40, 40, 128), (512, 31, 64, 40, 128)]
 
 
 @pytest.mark.parametrize("kind", ["plain", "wild", "segments", "one", "none"])
