@@ -3,7 +3,9 @@
 ``Y[M, N] = X[M, K] . dequant(W)[N, K]^T`` with bf16 X and Y, int4 W packed two
 codes per byte (low nibble = even k), one bf16 scale per G weights along K
 (G = 128, 64 or 32, read off the scales' shape [N, K/G]),
-``dequant = scale * (code - 8)``, fp32 accumulation.
+``dequant = scale * (code - 8)``, fp32 accumulation.  Beside the products: rows to the
+groups of the grouped product and back (``dispatch``, ``combine``) and low-rank
+adapters (``lora_add``), with their gradients.
 
 Every function here only checks tensor metadata, allocates outputs and
 workspaces with torch, and calls the C ABI on the current torch stream: all

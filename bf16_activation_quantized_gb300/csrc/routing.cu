@@ -48,7 +48,7 @@ __device__ __forceinline__ int load_key(const void *ids, int f, int groups) {
 
 // VEC consecutive bf16 in one access: 8, 4, 2 or 1, as the rows' starts allow.
 template <int VEC>
-struct Cols {                                        // 2 or 4
+struct Cols {                                        // of 4 or 2
     static constexpr int W = VEC / 2;
     uint32_t v[W];
     __device__ __forceinline__ void load(const uint16_t *p) {
@@ -512,7 +512,8 @@ cudaError_t launch_dispatch(const uint16_t *X, const void *ids, uint16_t *Xs, in
         if (e != cudaSuccess) return e;
         const ColSplit c = col_split(width, vec);
         return launch_chained(vec == 8 ? dispatch_copy_kernel<8> : vec == 4 ? dispatch_copy_kernel<4>
-                              : vec == 2 ? dispatch_copy_kernel<2> : dispatch_copy_kernel<1>, dim3(tokens, c.blocks), c.threads, 0, 1, s, X, slots, Xs, top_k, width);
+                              : vec == 2 ? dispatch_copy_kernel<2> : dispatch_copy_kernel<1>,
+                              dim3(tokens, c.blocks), c.threads, 0, 1, s, X, slots, Xs, top_k, width);
     }
     const int items = ceil_div(width, vec);
     int per = ceil_div(tokens, 3 * sms);
@@ -523,7 +524,8 @@ cudaError_t launch_dispatch(const uint16_t *X, const void *ids, uint16_t *Xs, in
     if (parts > ceil_div(items, kRouteThreads)) parts = ceil_div(items, kRouteThreads);
     return launch_chained(vec == 8 ? dispatch_few_kernel<I64, 8> : vec == 4 ? dispatch_few_kernel<I64, 4>
                           : vec == 2 ? dispatch_few_kernel<I64, 2> : dispatch_few_kernel<I64, 1>,
-                          dim3(blocks, parts), kRouteThreads, 0, 1, s, X, ids, Xs, sizes, slots, tokens, top_k, width, groups, per);
+                          dim3(blocks, parts), kRouteThreads, 0, 1, s, X, ids, Xs, sizes, slots, tokens, top_k,
+                          width, groups, per);
 }
 
 }  // namespace
@@ -558,7 +560,7 @@ w4a16_status w4a16_dispatch(const w4a16_bf16 *X, const void *ids_dev, int id_byt
     if (!M_sizes_dev || !aligned(M_sizes_dev, 4)) return W4A16_ERR_INVALID_ARG;
     if (tokens > 0) {
         if (!X || !ids_dev || !Xs || !slots_dev) return W4A16_ERR_INVALID_ARG;
-        if (!aligned(X, 16) || !aligned(Xs, 16) || !aligned(ids_dev, id_bytes) || !aligned(slots_dev, 4))
+        if (!aligned(X, 2) || !aligned(Xs, 2) || !aligned(ids_dev, id_bytes) || !aligned(slots_dev, 4))
             return W4A16_ERR_INVALID_ARG;
     }
     const size_t need = sort_bytes(tokens * top_k, num_groups);

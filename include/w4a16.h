@@ -379,8 +379,8 @@ w4a16_status w4a16_gemm_noalloc(const w4a16_bf16 *X, const uint8_t *W_packed,
  *               negative number) for a dropped slot.
  *  workspace:   at least w4a16_dispatch_workspace_bytes (may be NULL when that
  *               is 0); contents need no initialisation.
- * X, Xs and workspace 16-byte aligned, ids and the int32 outputs to their
- * element.  1 <= num_groups <= 1024, 1 <= top_k <= 256, tokens * top_k <= 2^24,
+ * workspace 16-byte aligned, the others to their element (the widest access, 16
+ * bytes down to 2, that width and the addresses allow is taken).  1 <= num_groups <= 1024, 1 <= top_k <= 256, tokens * top_k <= 2^24,
  * 1 <= width <= 2^20; tokens == 0 only writes the sizes.  id_bytes other than
  * 4 and 8 is W4A16_ERR_UNSUPPORTED. */
 w4a16_status w4a16_dispatch_workspace_bytes(int tokens, int top_k, int num_groups, size_t *bytes);

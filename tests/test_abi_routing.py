@@ -24,7 +24,7 @@ def dispatch(L, X=FAKE, ids=FAKE, ib=4, Xs=FAKE, sizes=FAKE, slots=FAKE, T=4, k=
 
 @pytest.mark.parametrize("bad", [dict(X=None), dict(ids=None), dict(Xs=None), dict(sizes=None),
                                  dict(slots=None), dict(T=-1), dict(k=0), dict(W=0), dict(E=0),
-                                 dict(E=1025), dict(X=FAKE + 8), dict(Xs=FAKE + 2), dict(ids=FAKE + 2),
+                                 dict(E=1025), dict(X=FAKE + 1), dict(Xs=FAKE + 1), dict(ids=FAKE + 2),
                                  dict(ib=8, ids=FAKE + 4), dict(T=1 << 20, k=17), dict(W=(1 << 20) + 1)])
 def test_dispatch_refuses(L, bad):
     assert dispatch(L, **bad) == INVALID

@@ -207,6 +207,18 @@ def test_unaligned_rows_take_the_narrow_path():
     assert torch.allclose(got[1], want[1], rtol=0, atol=72 * 2.0**-24 * 64 * 9)
 
 
+@pytest.mark.parametrize("tokens,top_k,width", [(9, 2, 41), (9, 2, 42), (9, 2, 44), (9, 2, 64), (4200, 4, 42)])
+def test_dispatch_of_a_view(tokens, top_k, width):
+    # rows that start on 2, 4 or 8 bytes: both forms take the widest access that fits
+    flat = torch.randn(tokens * width + 1, device="cuda").bfloat16()
+    ids = torch.randint(-1, 5, (tokens, top_k), device="cuda")
+    for x in (flat[1:].view(tokens, width), flat[:-1].view(tokens, width)):
+        xs, _, slots = w4.dispatch(x, ids, 5)
+        rows = torch.where(slots >= 0, slots, ~slots).long()
+        want = torch.where((slots >= 0)[:, :, None], x[:, None, :], torch.zeros_like(x[:, None, :]))
+        assert torch.equal(xs[rows], want)
+
+
 def test_rows_feed_the_grouped_product_and_replay_in_a_graph():
     rng = np.random.default_rng(7)
     T, k, E, K, N = 24, 2, 4, 256, 384
