@@ -432,6 +432,10 @@ _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
 
 
+def _empty(shape, dtype, index: int) -> torch.Tensor:
+    return torch.empty(shape, dtype=dtype, device=index)
+
+
 def _launch(name: str, index: int, *args) -> None:
     """One library call on the current torch stream of device ``index``."""
     fn = getattr(_lib._lib or _lib.lib(), name)
@@ -491,10 +495,10 @@ def dispatch(x: torch.Tensor, ids: torch.Tensor, num_groups: int):
     T, K = x.shape
     k = ids.shape[1]
     need = _sort_bytes(T, k, num_groups)
-    ws = x.new_empty(need, dtype=torch.uint8) if need else None
-    xs = x.new_empty((T * k, K))
-    m_sizes = x.new_empty(num_groups, dtype=torch.int32)
-    slots = x.new_empty((T, k), dtype=torch.int32)
+    ws = _empty(need, torch.uint8, dev) if need else None
+    xs = _empty((T * k, K), torch.bfloat16, dev)
+    m_sizes = _empty(num_groups, torch.int32, dev)
+    slots = _empty((T, k), torch.int32, dev)
     _launch("w4a16_dispatch", dev, x.data_ptr(), ids.data_ptr(), ids.element_size(), xs.data_ptr(),
             m_sizes.data_ptr(), slots.data_ptr(), T, k, K, num_groups,
             ws.data_ptr() if need else None, need)
@@ -521,7 +525,7 @@ def _combine(ys, slots, weights, name) -> torch.Tensor:
     dev = _need_slots(ys, slots, weights, name)
     T, k = slots.shape
     N = ys.shape[1]
-    y = ys.new_empty((T, N))
+    y = _empty((T, N), torch.bfloat16, dev)
     _launch("w4a16_combine", dev, ys.data_ptr(), slots.data_ptr(),
             None if weights is None else weights.data_ptr(),
             0 if weights is None else weights.element_size(), y.data_ptr(), T, k, N)
@@ -569,7 +573,7 @@ def combine_backward(dy: torch.Tensor, ys: torch.Tensor, slots: torch.Tensor, we
 _lora_bytes_cache: dict = {}
 
 
-def _lora_workspace(x, tokens: int, adapters: int, rank: int, backward: int):
+def _lora_workspace(index: int, tokens: int, adapters: int, rank: int, backward: int):
     key = (tokens, adapters, rank, backward)
     need = _lora_bytes_cache.get(key)
     if need is None:
@@ -577,8 +581,7 @@ def _lora_workspace(x, tokens: int, adapters: int, rank: int, backward: int):
         _lib.check(_lib.lib().w4a16_lora_workspace_bytes(tokens, adapters, rank, backward, ctypes.byref(nb)),
                    "w4a16_lora_workspace_bytes")
         need = _lora_bytes_cache[key] = int(nb.value)
-    ws = x.new_empty(need, dtype=torch.uint8) if need else None
-    return ws, need
+    return (_empty(need, torch.uint8, index) if need else None), need
 
 
 def _need_lora(x, lora_a, lora_b, adapters, lora_scales):
@@ -624,11 +627,11 @@ def lora_add(x: torch.Tensor, lora_a: torch.Tensor, lora_b: torch.Tensor, adapte
     if base is not None:
         _need_rows(dev, base, "base", (T, N))
     if out is None:
-        out = x.new_empty((T, N))
+        out = _empty((T, N), torch.bfloat16, dev)
     else:
         _need_rows(dev, out, "out", (T, N))
-    hidden = x.new_empty((T, r), dtype=torch.float32) if return_hidden else None
-    ws, need = _lora_workspace(x, T, L, r, 0)
+    hidden = _empty((T, r), torch.float32, dev) if return_hidden else None
+    ws, need = _lora_workspace(dev, T, L, r, 0)
     _launch("w4a16_lora_add", dev, x.data_ptr(), lora_a.data_ptr(), lora_b.data_ptr(), adapters.data_ptr(),
             adapters.element_size(), lora_scales.data_ptr(), None if base is None else base.data_ptr(),
             out.data_ptr(), hidden.data_ptr() if return_hidden else None, T, L, r, N, K,
@@ -652,7 +655,7 @@ def lora_add_backward(dy: torch.Tensor, x: torch.Tensor, hidden: torch.Tensor, l
         _need_rows(dev, dx_base, "dx_base", (T, K))
     dx = torch.empty_like(x)
     da, db = torch.empty_like(lora_a), torch.empty_like(lora_b)
-    ws, need = _lora_workspace(x, T, L, r, 1)
+    ws, need = _lora_workspace(dev, T, L, r, 1)
     _launch("w4a16_lora_add_backward", dev, dy.data_ptr(), x.data_ptr(), hidden.data_ptr(), lora_a.data_ptr(),
             lora_b.data_ptr(), adapters.data_ptr(), adapters.element_size(), lora_scales.data_ptr(),
             None if dx_base is None else dx_base.data_ptr(), dx.data_ptr(), da.data_ptr(), db.data_ptr(),

@@ -46,12 +46,12 @@ __device__ __forceinline__ void mma_acc(float (&c)[4], const uint32_t (&a)[4], u
     mma_16816_c(c, a, b0, b1, c);
 }
 
-// Few tokens: one launch.  A cluster of eight CTAs (fewer where not all clusters would
-// be resident, few_cluster) owns up to 16 tokens of one
-// adapter (cluster i starts at token i, or leaves if an earlier one has it),
-// found in the ids without a sort.  Its warps split the columns of the first
-// product, add their sums of h in shared and then distributed shared memory in
-// a fixed order, and split the columns of the second.  Everything goes from
+// Few tokens: one launch.  A cluster of eight CTAs (fewer where not all clusters
+// would be resident, few_cluster) owns up to 16 tokens of one adapter (cluster i
+// starts at token i, or leaves if an earlier one has it), found in the ids without a
+// sort.  Its warps split the columns of the first product, add their sums of h in
+// shared and then distributed shared memory in a fixed order, and split the columns
+// of the second.  Everything goes from
 // global memory straight into MMA fragments: the order of k inside an MMA is
 // free as long as both operands agree, so a lane takes 16 bytes of a row and 32
 // columns feed two MMAs; and the columns of the second product are dealt to the
