@@ -277,7 +277,6 @@ __global__ void __launch_bounds__(kFewThreads, RP <= 32 ? 2 : 1) lora_few_kernel
             }
         }
     }
-    __syncwarp();
     cluster_wait();                                      // no CTA leaves while its sums are read
 }
 

@@ -49,7 +49,10 @@ constexpr int kTmemCols = 512;
 constexpr int kPrefetch = 256 * 1024;  // bytes of X that a CTA prefetches
 constexpr int kMaxRuns = 160;          // CTAs of the two products: one per SM (152)
 
-__device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kEpiThreads) : "memory"); }
+__device__ __forceinline__ void epi_sync() {
+    __syncwarp();                                    // bar.sync takes whole warps
+    asm volatile("bar.sync 1, %0;" ::"n"(kEpiThreads) : "memory");
+}
 
 // Byte of piece p (16 bytes) of row `row` in a block of 128-byte rows.
 __device__ __forceinline__ uint32_t sw128(int row, int p) { return uint32_t(row * 128 + ((p ^ (row & 7)) << 4)); }
@@ -321,6 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1) lora_down_kernel(const LoraArgs p
                     *reinterpret_cast<uint4 *>(out + 8 * k) = make_uint4(v[0], v[1], v[2], v[3]);
                     *reinterpret_cast<uint4 *>(out + 8 * k + 4) = make_uint4(v[4], v[5], v[6], v[7]);
                 }
+                __syncwarp();                        // tcgen05.ld takes the whole warp
             }
             tc_fence_before();
             __syncwarp();
@@ -643,6 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1) lora_up_kernel(const LoraArgs p) 
                         for (int m = 0; m < 4; ++m)
                             if (32 * sub + 16 * h + 4 * m + lane / 8 < count) store_cols8(y[m], left, p.vec_out, v[m]);
                     }
+                    __syncwarp();                            // tcgen05.ld takes the whole warp
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -901,6 +906,7 @@ __global__ void __launch_bounds__(kWgradThreads, 1) lora_wgrad_kernel(const Wgra
                             for (int e = 0; e < 8; ++e) d[(long long)e * cols] = f32_to_bf16_rn(f[e]);
                         }
                     }
+                    __syncwarp();                                // tcgen05.ld takes the whole warp
                 }
             }
             tc_fence_before();
