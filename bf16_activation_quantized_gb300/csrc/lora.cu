@@ -10,8 +10,8 @@
 // output, with the weights read along the other axis.
 //
 // Precision: products of bf16 are exact in the MMA and summed in fp32; h (and g)
-// stay in fp32 and enter the second product as a sum of two bf16 terms, which
-// holds them to 2^-17.  The outputs are rounded once.
+// stay in fp32 and enter the second product as a sum of three bf16 terms, which is
+// their value itself.  The outputs are rounded once.
 #include <atomic>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -74,7 +74,8 @@ __global__ void __launch_bounds__(kFewThreads, RP <= 32 ? 2 : 1) lora_few_kernel
     constexpr int kQuads = RP / 4;
     extern __shared__ float s_mem[];
     float *s_part = s_mem;                               // [kFewWarps][TM][PS]
-    float *s_h = s_mem + kFewWarps * TM * PS;            // [TM][PS]
+    // s h: fragments of the second product, [plane][KS][lane]
+    uint4 *s_h = reinterpret_cast<uint4 *>(s_mem + kFewWarps * TM * PS);
     __shared__ int s_rows[TM];
     __shared__ int s_tile[3];
 
@@ -194,6 +195,7 @@ __global__ void __launch_bounds__(kFewThreads, RP <= 32 ? 2 : 1) lora_few_kernel
     }
     __syncthreads();
     const float scale = p.scale[adapter];
+    const bool packed = count <= 8;                      // see s_h below
     for (int i = threadIdx.x; i < count * kQuads; i += kFewThreads) {
         float *d = s_part + (i / kQuads) * PS + 4 * (i % kQuads);
         float4 v = *reinterpret_cast<const float4 *>(d);
@@ -206,6 +208,7 @@ __global__ void __launch_bounds__(kFewThreads, RP <= 32 ? 2 : 1) lora_few_kernel
     }
     cluster_arrive();
     cluster_wait();
+    #pragma unroll 1
     for (int i = threadIdx.x; i < count * kQuads; i += kFewThreads) {
         const int row = i / kQuads, rank = 4 * (i % kQuads);
         float4 part[kMaxCluster], v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -219,25 +222,37 @@ __global__ void __launch_bounds__(kFewThreads, RP <= 32 ? 2 : 1) lora_few_kernel
         if (rank >= r) v = make_float4(0.f, 0.f, 0.f, 0.f);
         if (p.hidden && c == 0 && rank < r)
             *reinterpret_cast<float4 *>(p.hidden + (long long)s_rows[row] * r + rank) = v;
-        *reinterpret_cast<float4 *>(s_h + row * PS + rank) =
-            make_float4(scale * v.x, scale * v.y, scale * v.z, scale * v.w);
+        // the MMA's slots (2t, 2t + 1) and (2t + 8, 2t + 9) of row g (or g + 8) hold ranks
+        // 4 t + 0..3 of a rank block of 16, 8 t + 4 (k % 2) + 0..3 of two
+        uint32_t lo2[kPlanes], hi2[kPlanes];
+        split3(scale * v.x, scale * v.y, lo2);
+        split3(scale * v.z, scale * v.w, hi2);
+        const int k = RP >= 32 ? 2 * (rank / 32) + (rank / 4) % 2 : 0;
+        const int slot = RP >= 32 ? rank % 32 / 8 : rank / 4;
+        uint32_t *d = reinterpret_cast<uint32_t *>(s_h + k * 32 + 4 * (row % 8) + slot) + row / 8;
+        if (packed) {
+            // rows g + 8 have no tokens: the high plane in rows g, the middle one there,
+            // then the low one, so that two MMAs take the three
+            d[0] = lo2[0], d[1] = lo2[1], d[2] = hi2[0], d[3] = hi2[1];
+            d += KS * 32 * 4;
+            d[0] = 0, d[1] = lo2[2], d[2] = 0, d[3] = hi2[2];
+        } else {
+            #pragma unroll
+            for (int e = 0; e < kPlanes; ++e, d += KS * 32 * 4) d[0] = lo2[e], d[2] = hi2[e];
+        }
     }
     __syncthreads();
     cluster_arrive();                                    // this CTA has read the others' sums
 
     // ---- y
     {
-        uint32_t hi[KS][4], lo[KS][4];
+        // s h's upper fragments stay in registers (read anew for every step they cost 1 of
+        // 20 us at 61 tokens)
+        uint4 held[2][KS];
         #pragma unroll
-        for (int k = 0; k < KS; ++k)
+        for (int e = 0; e < 2; ++e)
             #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                // slots (2t, 2t+1) for i < 2, (2t+8, 2t+9) for i >= 2; rows past the
-                // tokens hold anything and are not stored
-                const int rank = RP >= 32 ? 32 * (k / 2) + 8 * t + 4 * (k % 2) + 2 * (i / 2) : 4 * t + 2 * (i / 2);
-                const float2 v = *reinterpret_cast<const float2 *>(s_h + (g + 8 * (i % 2)) * PS + rank);
-                split2(v.x, v.y, hi[k][i], lo[k][i]);
-            }
+            for (int k = 0; k < KS; ++k) held[e][k] = s_h[(e * KS + k) * 32 + lane];
         for (int nb = n0; nb < n1; nb += PF) {
             if (nb > n0) load_up(nb);
             #pragma unroll
@@ -249,15 +264,25 @@ __global__ void __launch_bounds__(kFewThreads, RP <= 32 ? 2 : 1) lora_few_kernel
                 for (int j = 0; j < 4; ++j)
                     #pragma unroll
                     for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
+                // the low plane first; rows past the tokens hold anything and are not stored
                 #pragma unroll
-                for (int k = 0; k < KS; ++k)
+                for (int e = kPlanes - 1; e >= 0; --e)
                     #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint32_t f0 = RP >= 32 ? w[f][(j * QN + k / 2) * 4 + 2 * (k % 2)] : w[f][2 * j];
-                        const uint32_t f1 = RP >= 32 ? w[f][(j * QN + k / 2) * 4 + 2 * (k % 2) + 1] : w[f][2 * j + 1];
-                        mma_acc(acc[j], lo[k], f0, f1);
-                        mma_acc(acc[j], hi[k], f0, f1);
+                    for (int k = 0; k < KS; ++k) {
+                        if (e == 2 && packed) break;
+                        const uint4 v = e == 2 ? s_h[(e * KS + k) * 32 + lane] : held[e][k];
+                        const uint32_t h[4] = {v.x, v.y, v.z, v.w};
+                        #pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t f0 = RP >= 32 ? w[f][(j * QN + k / 2) * 4 + 2 * (k % 2)] : w[f][2 * j];
+                            const uint32_t f1 = RP >= 32 ? w[f][(j * QN + k / 2) * 4 + 2 * (k % 2) + 1] : w[f][2 * j + 1];
+                            mma_acc(acc[j], h, f0, f1);
+                        }
                     }
+                if (packed) {
+                    #pragma unroll
+                    for (int j = 0; j < 4; ++j) acc[j][0] += acc[j][2], acc[j][1] += acc[j][3];
+                }
                 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const long long row = h ? row1 : row0;
@@ -324,7 +349,7 @@ int few_cluster(int tokens, int adapters, size_t smem) {
 
 template <int RP>
 cudaError_t launch_few(const LoraArgs &p, cudaStream_t s) {
-    constexpr size_t smem = size_t(kFewWarps + 1) * kFewTile * (RP + 4) * 4;
+    constexpr size_t smem = size_t(kFewWarps) * kFewTile * (RP + 4) * 4 + kPlanes * (RP / 16) * 32 * sizeof(uint4);
     const cudaError_t e = allow_smem<lora_few_kernel<RP>>(smem);
     if (e != cudaSuccess) return e;
     const int cluster = few_cluster<RP>(p.tokens, p.adapters, smem);

@@ -11,11 +11,13 @@
 
 namespace w4a16 {
 
-// Bytes of a sorted token's row of h or g: two bf16 planes (hi, lo) of RP ranks.
-__host__ __device__ constexpr int plane_pitch(int RP) { return 4 * RP; }
+// h and g enter their second product as a sum of bf16 terms, one plane each (split3).
+constexpr int kPlanes = 3;
+// Bytes of a sorted token's row of h or g: the planes, high to low, of RP ranks.
+__host__ __device__ constexpr int plane_pitch(int RP) { return 2 * kPlanes * RP; }
 // The same by tile of 128 tokens of an adapter, for the weight gradients: rows of
-// 128 tokens, RP of hi and RP of lo, zeros past the last token.  In elements.
-__host__ __device__ constexpr int tile_planes(int RP) { return 2 * RP * 128; }
+// 128 tokens, RP of each plane, zeros past the last token.  In elements.
+__host__ __device__ constexpr int tile_planes(int RP) { return kPlanes * RP * 128; }
 
 struct LoraArgs {
     const uint16_t *x;       // [tokens][in]
@@ -123,11 +125,18 @@ __device__ __forceinline__ void stage_done(uint32_t bar, bool async) {
     }
 }
 
-// hi + lo = v to 2^-17 of it; an infinity stays in hi alone.
-__device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo) {
-    hi = pack_bf16x2_rn(a, b);
-    const float ha = bf16_lo_to_f32(hi), hb = bf16_hi_to_f32(hi);
-    lo = pack_bf16x2_rn(isinf(ha) ? 0.f : a - ha, isinf(hb) ? 0.f : b - hb);
+// The values a, b as sums of three bf16 terms: the upper 8 bits of the 24, the next 8
+// and the rest, cut off, so that the sum is the value itself; an infinity stays in the
+// first term alone.  Two terms hold 17 bits: a sum that cancels shows the rest.
+__device__ __forceinline__ float upper8(float a) { return __uint_as_float(__float_as_uint(a) & 0xffff0000u); }
+__device__ __forceinline__ uint32_t upper8x2(float a, float b) {
+    return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+}
+__device__ __forceinline__ void split3(float a, float b, uint32_t (&v)[kPlanes]) {
+    v[0] = upper8x2(a, b);
+    a = isinf(a) ? 0.f : a - upper8(a), b = isinf(b) ? 0.f : b - upper8(b);
+    v[1] = upper8x2(a, b);
+    v[2] = upper8x2(a - upper8(a), b - upper8(b));
 }
 
 __device__ __forceinline__ int adapter_of(const LoraArgs &p, int t) {

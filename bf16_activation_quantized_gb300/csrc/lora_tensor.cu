@@ -15,7 +15,7 @@
 // with 16-byte asynchronous copies into a ring of stages, in the 128-byte
 // swizzle that tcgen05.mma reads; one warp issues the MMAs; the other warps
 // empty TMEM, and in the second kernel add base in shared memory and store
-// whole 128-byte pieces of rows.  h enters the second product as two bf16 planes.
+// whole 128-byte pieces of rows.  h enters the second product as three bf16 planes.
 //
 // What bounds them: HBM.  At rank 64 the legacy MMA pipe would need two thirds of
 // the memory's time and left a 64-token mma.sync version waiting on MMA latency
@@ -108,7 +108,8 @@ struct TileSlots {
 // Bytes of a stage's weights: along, rows of RP ranks x 128 columns; across, rows
 // of 128 columns x RP ranks (in blocks of 64 elements either way).
 constexpr int weight_bytes(int RP, bool along) { return along ? 2 * RP * 128 : (RP + 63) / 64 * kBlock; }
-constexpr int plane_bytes(int RP) { return (RP + 63) / 64 * kBlock; }
+// Of a tile's planes side by side, in blocks of 64 elements.
+constexpr int planes_bytes(int RP) { return (kPlanes * RP + 63) / 64 * kBlock; }
 
 // A producer thread's part of a stage: column piece `piece` of rows row0 + 8 j,
 // whose swizzled places are 1024 bytes apart.
@@ -358,7 +359,7 @@ __global__ void __launch_bounds__(kSumThreads) lora_sum_kernel(const LoraArgs p,
     __shared__ int s_rows[kTile];
     __shared__ int s_info[3];
     __shared__ long long s_slots[2];                     // first slot, how many
-    __shared__ uint16_t s_t[TRANS ? 2 * RP : 1][kRows + 2];   // g, then s h: [plane, rank][row]
+    __shared__ uint16_t s_t[TRANS ? kPlanes * RP : 1][kRows + 2];   // g, then s h: [plane, rank][row]
     // The first product's CTAs let this kernel start after the sort had ended.
     pdl_launch_dependents();
     const int tile = blockIdx.x / sum_blocks(RP), row0 = blockIdx.x % sum_blocks(RP) * kRows;
@@ -405,24 +406,26 @@ __global__ void __launch_bounds__(kSumThreads) lora_sum_kernel(const LoraArgs p,
             }
             if (adapter < 0) return;
             // ranks past r are zeros (also where x holds infinities: 0 * inf)
-            uint2 hi, lo;
-            split2(scale * v.x, scale * v.y, hi.x, lo.x), split2(scale * v.z, scale * v.w, hi.y, lo.y);
+            uint32_t v01[kPlanes], v23[kPlanes];
+            split3(scale * v.x, scale * v.y, v01), split3(scale * v.z, scale * v.w, v23);
             if (token && !which) {
                 const long long out = (long long)(s_info[2] + row) * (plane_pitch(RP) / 2) + rank;
-                *reinterpret_cast<uint2 *>(p.planes + out) = hi, *reinterpret_cast<uint2 *>(p.planes + out + RP) = lo;
+                #pragma unroll
+                for (int k = 0; k < kPlanes; ++k)
+                    *reinterpret_cast<uint2 *>(p.planes + out + k * RP) = make_uint2(v01[k], v23[k]);
             }
             if (TRANS) {
                 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    s_t[rank + e][row - row0] = uint16_t((e < 2 ? hi.x : hi.y) >> (16 * (e & 1)));
-                    s_t[RP + rank + e][row - row0] = uint16_t((e < 2 ? lo.x : lo.y) >> (16 * (e & 1)));
-                }
+                for (int k = 0; k < kPlanes; ++k)
+                    #pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        s_t[k * RP + rank + e][row - row0] = uint16_t((e < 2 ? v01[k] : v23[k]) >> (16 * (e & 1)));
             }
         }
         if (TRANS) {
             __syncthreads();
             uint16_t *out = (which ? p.th : p.tg) + (long long)tile * tile_planes(RP) + row0;
-            for (int i = threadIdx.x; i < 2 * RP * kRows / 2; i += kSumThreads) {
+            for (int i = threadIdx.x; i < kPlanes * RP * kRows / 2; i += kSumThreads) {
                 const int pair = i % (kRows / 2), line = i / (kRows / 2);
                 *reinterpret_cast<uint32_t *>(out + line * kTile + 2 * pair) = *reinterpret_cast<const uint32_t *>(&s_t[line][2 * pair]);
             }
@@ -432,9 +435,9 @@ __global__ void __launch_bounds__(kSumThreads) lora_sum_kernel(const LoraArgs p,
 }
 
 // ----------------------------------------------------------- second product
-// y[t][col] = base[t][col] + sum over ranks of (hi + lo)[t][rank] B[col][rank] (dx: A,
+// y[t][col] = base[t][col] + sum over ranks and planes of h[t][rank] B[col][rank] (dx: A,
 // the weight's ranks along its rows, an MN-major operand).  Tokens are the MMA's M, the
-// stage's 128 columns its N; the low plane first, both into one accumulator in TMEM.
+// stage's 128 columns its N; the low plane first, all into one accumulator in TMEM.
 // Bound by HBM: base in, y out.  The accumulators meet base in its swizzled place, and
 // a warp stores four rows' 128 bytes in one instruction; pieces four at a time (one at a
 // time the shared-memory round trips took 2 of 57.5 us below).  2858 tokens of 12 adapters,
@@ -443,7 +446,7 @@ template <int RP, bool TRANS>
 struct UpShape {
     static constexpr int kW = weight_bytes(RP, TRANS);
     static constexpr int kStage = 2 * kBlock + kW;
-    static constexpr int kH = 2 * plane_bytes(RP);
+    static constexpr int kH = planes_bytes(RP);
     static constexpr int kStages = (kSmemMax - 1024 - kH) / kStage < 5 ? (kSmemMax - 1024 - kH) / kStage : 5;
     static constexpr int kSmem = kStages * kStage + kH + 1024;
     static_assert(kStages >= 2, "the ring does not fit");
@@ -459,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1) lora_up_kernel(const LoraArgs p) 
     __shared__ int s_abort;
     __shared__ uint32_t s_tmem;
     unsigned char *s_mem = s_raw + (-smem_u32(s_raw) & 1023);
-    unsigned char *s_hi = s_mem + NS * S::kStage, *s_lo = s_hi + plane_bytes(RP);
+    unsigned char *s_h = s_mem + NS * S::kStage;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t full = smem_u32(s_bar), empty = full + 8 * NS, tfull = empty + 8 * NS, tempty = tfull + 16;
     const uint32_t dfull = tempty + 16, dempty = dfull + 32, hready = dempty + 32;
@@ -536,14 +539,14 @@ __global__ void __launch_bounds__(kThreads, 1) lora_up_kernel(const LoraArgs p) 
                     const uint32_t ws = smem_u32(s_mem) + s * S::kStage + 2 * kBlock;
                     if (elect_one()) {
                         #pragma unroll
-                        for (int part = 0; part < 2; ++part)     // the low plane first
+                        for (int part = kPlanes - 1; part >= 0; --part)     // the low plane first
                             #pragma unroll
                             for (int m = 0; m < KS; ++m) {
-                                const uint32_t at = (m / 4) * kBlock + (m % 4) * 32;
-                                const uint64_t a = tc_sdesc_sw128(smem_u32(part ? s_hi : s_lo) + at);
+                                const int k = part * KS + m;                 // 16 columns of the planes
+                                const uint64_t a = tc_sdesc_sw128(smem_u32(s_h) + (k / 4) * kBlock + (k % 4) * 32);
                                 const uint64_t b = TRANS ? tc_sdesc_sw128_mn(ws + m * 2048, RP * 128)
-                                                         : tc_sdesc_sw128(ws + at);
-                                tc_mma_ss(tmem + buf * kCols, a, b, idesc, part > 0 || m > 0);
+                                                         : tc_sdesc_sw128(ws + (m / 4) * kBlock + (m % 4) * 32);
+                                tc_mma_ss(tmem + buf * kCols, a, b, idesc, part < kPlanes - 1 || m > 0);
                             }
                         tc_commit(dfull + 8 * buf);
                     }
@@ -563,7 +566,8 @@ __global__ void __launch_bounds__(kThreads, 1) lora_up_kernel(const LoraArgs p) 
             if (adapter >= 0) {
                 // h's planes of the tile; rows past its tokens are zeros
                 const int start = s_tiles.info[seg & 1][2];
-                constexpr int kPieces = RP / 4, kOnce = RP >= 64 ? 8 : RP / 8;
+                constexpr int kPieces = kPlanes * RP / 8, kOnce = RP >= 64 ? 6 : kPlanes * RP / 16;
+                static_assert(kTile * kPieces % (kOnce * kEpiThreads) == 0, "whole rounds");
                 #pragma unroll 1
                 for (int m0 = threadIdx.x; m0 < kTile * kPieces; m0 += kOnce * kEpiThreads) {
                     uint4 v[kOnce];
@@ -576,8 +580,8 @@ __global__ void __launch_bounds__(kThreads, 1) lora_up_kernel(const LoraArgs p) 
                     }
                     #pragma unroll
                     for (int e = 0; e < kOnce; ++e) {
-                        const int m = m0 + e * kEpiThreads, row = m / kPieces, b = m % kPieces, q = b % (RP / 8);
-                        *reinterpret_cast<uint4 *>((b < RP / 8 ? s_hi : s_lo) + (q / 8) * kBlock + sw128(row, q % 8)) = v[e];
+                        const int m = m0 + e * kEpiThreads, row = m / kPieces, b = m % kPieces;
+                        *reinterpret_cast<uint4 *>(s_h + (b / 8) * kBlock + sw128(row, b % 8)) = v[e];
                     }
                 }
                 fence_proxy_async();
@@ -682,11 +686,11 @@ struct WgradShape {
     static constexpr int kCols = RP <= 64 ? 512 : 256;      // columns of a pair
     static constexpr int kQBlock = kStageTokens * 128;      // bytes of 32 tokens x 64 columns
     static constexpr int kQ = kCols / 64 * kQBlock;
-    static constexpr int kP = 2 * RP * 64;                  // both planes: rows of 32 tokens
+    static constexpr int kP = kPlanes * RP * 64;            // the planes: rows of 32 tokens
     static constexpr int kStage = kQ + kP;
     static constexpr int kStages = (kSmemMax - 1024) / kStage < 6 ? (kSmemMax - 1024) / kStage : 6;
     static constexpr int kSmem = kStages * kStage + 1024;
-    static constexpr int kD = kCols / 128 * 2 * RP;         // TMEM columns of a pair's sums
+    static constexpr int kD = kCols / 128 * 2 * RP;         // TMEM columns of a pair's sums: of the high plane, of the others
     static constexpr int kBufs = 2 * kD <= kTmemCols ? 2 : 1;
     static constexpr int kTileSums = kCols * RP;            // floats of a pair's sums
     static_assert(kStages >= 3 && kD <= kTmemCols, "the ring does not fit");
@@ -742,7 +746,8 @@ __device__ __forceinline__ long long count_units(const WgradArgs &p) {
 }
 
 // D[column][plane, rank] of a pair is summed in TMEM in blocks of 128 columns: x or
-// dy lies along M as it comes, both planes of g or s h along N, one MMA for the two.
+// dy lies along M as it comes, the planes of g or s h along N: one MMA for the upper
+// two, one that adds the lowest to the middle's sums (TMEM holds no third).
 // A run that covers all of a pair's tokens stores the gradient, the others their
 // sums ([rank][column], slot 0: the pair began before the run, slot 1: it goes on
 // after it) for wgrad_sum_kernel.
@@ -839,15 +844,15 @@ __global__ void __launch_bounds__(kWgradThreads, 1) lora_wgrad_kernel(const Wgra
                 }
                 // rows of 64 bytes (32 tokens of a plane's rank) in the 64-byte swizzle
                 const uint16_t *src = src_p + (long long)(tok / kTile) * tile_planes(RP) + tok % kTile;
-                #pragma unroll
-                for (int m = pt; m < 2 * RP * 4; m += kWgradProducers) {
+                #pragma unroll 1
+                for (int m = pt; m < kPlanes * RP * 4; m += kWgradProducers) {
                     const int line = m / 4, e = m % 4;
                     cp_async16(ps + line * 64 + ((e ^ ((line >> 1) & 3)) << 4), src + line * kTile + 8 * e);
                 }
                 stage_done(full + 8 * s, vec);
             }
         } else if (warp == kWgradMma) {
-            constexpr uint32_t idesc = tc_idesc_bf16(128, 2 * RP) | kTcAMajorM;
+            constexpr uint32_t idesc = tc_idesc_bf16(128, 2 * RP) | kTcAMajorM, idesc1 = tc_idesc_bf16(128, RP) | kTcAMajorM;
             bool ok = seg < S::kBufs || mbar_wait(dempty + 8 * buf, (seg / S::kBufs - 1) & 1, abort_flag, p.err);
             ok = __all_sync(0xffffffffu, ok);
             for (int k = 0; k < n_blocks && ok; ++k, ++i) {
@@ -863,8 +868,9 @@ __global__ void __launch_bounds__(kWgradThreads, 1) lora_wgrad_kernel(const Wgra
                         #pragma unroll
                         for (int e = 0; e < kStageTokens / 16; ++e) {
                             const uint64_t dq = tc_sdesc_sw128_mn(qs + m * 2 * S::kQBlock + e * 2048, S::kQBlock);
-                            const uint64_t dp = tc_sdesc_sw64(ps + e * 32);
-                            tc_mma_ss(tmem + buf * S::kD + m * 2 * RP, dq, dp, idesc, k > 0 || e > 0);
+                            const uint32_t d = tmem + buf * S::kD + m * 2 * RP;
+                            tc_mma_ss(d, dq, tc_sdesc_sw64(ps + e * 32), idesc, k > 0 || e > 0);
+                            tc_mma_ss(d + RP, dq, tc_sdesc_sw64(ps + 2 * RP * 64 + e * 32), idesc1, 1);
                         }
                     tc_commit(empty + 8 * s);
                 }

@@ -1,0 +1,68 @@
+"""GPU: adapters where a kernel can go wrong without a random problem showing it --
+sums that cancel, infinities, each form of lora_add by itself.
+
+lora_add has two forms, by rank and tokens; FEW and MANY are on their sides of the
+border for one adapter at every rank that is used here (up to rank 32 the few-token
+form ends at 384 tokens, past it at 128; the gradient has one form)."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+import bf16_activation_quantized_gb300 as w4
+
+from gpu_util import require_gpu
+
+pytestmark = pytest.mark.gpu
+
+FEW, MANY = 5, 450
+INF = float("inf")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    require_gpu()
+
+
+def zeros(*shape):
+    return torch.zeros(*shape, device="cuda", dtype=torch.bfloat16)
+
+
+@pytest.mark.parametrize("T", [FEW, MANY])
+@pytest.mark.parametrize("r", [8, 16, 24, 48, 64, 128])
+def test_h_and_g_keep_all_bits_of_32(T, r):
+    """h (and g) of 1 + 2^-10 + 2^-20 beside 1 + 2^-10: 21 bits, all but the last of
+    which cancel in the second product and in the weight gradients.  Every product and
+    sum is exact in 24 bits, so the outputs have to be 2^-20 and nothing else."""
+    N = K = 256
+    ids, one = torch.zeros(T, device="cuda", dtype=torch.int32), torch.ones(1, device="cuda")
+    long, short = torch.tensor([1, 2.0**-10, 2.0**-20], device="cuda"), torch.tensor([1, 2.0**-10, 0], device="cuda")
+    p, q = r - 1, r - 2                                  # the two ranks
+    # forward, and dB over two tokens: x = long and short (negated) under A = ones
+    x, a, b = zeros(T, K), zeros(1, r, K), zeros(1, N, r)
+    x[:, 130:133] = long.bfloat16()
+    a[0, p, 130:133], a[0, q, 130:132] = 1, 1
+    b[0, :, p], b[0, :, q] = 1, -1
+    y, hidden = w4.lora_add(x, a, b, ids, one, return_hidden=True)
+    assert hidden[:, p].tolist() == [1 + 2.0**-10 + 2.0**-20] * T and hidden[:, q].tolist() == [1 + 2.0**-10] * T
+    assert bool((y == 2.0**-20).all())
+    # dx: g from dy, the weights' parts exchanged
+    dy, a, b = zeros(T, N), zeros(1, r, K), zeros(1, N, r)
+    dy[:, 130:133] = long.bfloat16()
+    b[0, 130:133, p], b[0, 130:132, q] = 1, 1
+    a[0, p], a[0, q] = 1, -1
+    dx = w4.lora_add_backward(dy, zeros(T, K), torch.zeros(T, r, device="cuda"), a, b, ids, one)[0]
+    assert bool((dx == 2.0**-20).all())
+    # dA: two tokens' g cancel; dB: two tokens' h
+    dy[1:] = 0
+    dy[T - 1, 130:133] = -short.bfloat16()
+    x, hidden, b = zeros(T, K), torch.zeros(T, r, device="cuda"), zeros(1, N, r)
+    x[0], x[T - 1] = 1, 1
+    b[0, 130:133, p] = 1
+    da = w4.lora_add_backward(dy, x, hidden, a, b, ids, one)[1]
+    assert bool((da[0, p] == 2.0**-20).all()) and not bool(da[0, :p].any())
+    dy.zero_()
+    dy[0], dy[T - 1] = 1, 1
+    hidden[0, p], hidden[T - 1, p] = 1 + 2.0**-10 + 2.0**-20, -(1 + 2.0**-10)
+    db = w4.lora_add_backward(dy, x, hidden, a, b, ids, one)[2]
+    assert bool((db[0, :, p] == 2.0**-20).all()) and not bool(db[0, :, :p].any())
