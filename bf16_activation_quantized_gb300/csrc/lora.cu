@@ -218,15 +218,14 @@ __global__ void __launch_bounds__(kFewThreads, RP <= 32 ? 2 : 1) lora_few_kernel
         #pragma unroll
         for (int k = 0; k < kMaxCluster; ++k)
             if (k < C) v.x += part[k].x, v.y += part[k].y, v.z += part[k].z, v.w += part[k].w;
-        // a rank past r is 0 also where x holds infinities (0 * inf)
-        if (rank >= r) v = make_float4(0.f, 0.f, 0.f, 0.f);
         if (p.hidden && c == 0 && rank < r)
             *reinterpret_cast<float4 *>(p.hidden + (long long)s_rows[row] * r + rank) = v;
         // the MMA's slots (2t, 2t + 1) and (2t + 8, 2t + 9) of row g (or g + 8) hold ranks
         // 4 t + 0..3 of a rank block of 16, 8 t + 4 (k % 2) + 0..3 of two
         uint32_t lo2[kPlanes], hi2[kPlanes];
-        split3(scale * v.x, scale * v.y, lo2);
-        split3(scale * v.z, scale * v.w, hi2);
+        // a rank past r is 0 also where x or the scale is infinite (0 * inf)
+        v = rank < r ? make_float4(scale * v.x, scale * v.y, scale * v.z, scale * v.w) : make_float4(0.f, 0.f, 0.f, 0.f);
+        split3(v.x, v.y, lo2), split3(v.z, v.w, hi2);
         const int k = RP >= 32 ? 2 * (rank / 32) + (rank / 4) % 2 : 0;
         const int slot = RP >= 32 ? rank % 32 / 8 : rank / 4;
         uint32_t *d = reinterpret_cast<uint32_t *>(s_h + k * 32 + 4 * (row % 8) + slot) + row / 8;

@@ -420,9 +420,11 @@ __global__ void __launch_bounds__(kSumThreads) lora_sum_kernel(const LoraArgs p,
                 if (!TRANS && p.hidden) *hidden = v;     // zeros without an adapter
             }
             if (adapter < 0) return;
-            // ranks past r are zeros (also where x holds infinities: 0 * inf)
+            // ranks past r and rows past the tokens are zeros, also where x or the scale is
+            // infinite (0 * inf)
+            if (in) v = make_float4(scale * v.x, scale * v.y, scale * v.z, scale * v.w);
             uint32_t v01[kPlanes], v23[kPlanes];
-            split3(scale * v.x, scale * v.y, v01), split3(scale * v.z, scale * v.w, v23);
+            split3(v.x, v.y, v01), split3(v.z, v.w, v23);
             if (token && !which) {
                 const long long out = (long long)(s_info[2] + row) * (plane_pitch(RP) / 2) + rank;
                 #pragma unroll

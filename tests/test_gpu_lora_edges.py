@@ -66,3 +66,28 @@ def test_h_and_g_keep_all_bits_of_32(T, r):
     hidden[0, p], hidden[T - 1, p] = 1 + 2.0**-10 + 2.0**-20, -(1 + 2.0**-10)
     db = w4.lora_add_backward(dy, x, hidden, a, b, ids, one)[2]
     assert bool((db[0, :, p] == 2.0**-20).all()) and not bool(db[0, :, :p].any())
+
+
+def positive(g, *shape):
+    return (torch.rand(*shape, device="cuda", generator=g) + 0.25).bfloat16()
+
+
+@pytest.mark.parametrize("T", [FEW, MANY])
+@pytest.mark.parametrize("r", [8, 16, 24, 40, 64, 72])
+def test_an_infinite_scale_gives_infinities(T, r):
+    """Every operand positive: s h, g and all that follows are +inf, also at ranks that
+    the kernels pad and in tiles whose last rows hold no token; the other adapter's
+    tokens and gradients stay finite."""
+    g = torch.Generator(device="cuda").manual_seed(r)
+    N, K = 136, 128
+    x, dy, base = positive(g, T, K), positive(g, T, N), positive(g, T, N)
+    a, b = positive(g, 2, r, K), positive(g, 2, N, r)
+    ids = (torch.arange(T, device="cuda") % 2).to(torch.int32)
+    scale = torch.tensor([INF, 1.0], device="cuda")
+    y, hidden = w4.lora_add(x, a, b, ids, scale, base, return_hidden=True)
+    dx, da, db = w4.lora_add_backward(dy, x, hidden, a, b, ids, scale)
+    assert bool(torch.isfinite(hidden).all())
+    for name, v in (("y", y), ("dx", dx)):
+        assert bool((v[ids == 0] == INF).all()) and bool(torch.isfinite(v[ids == 1]).all()), name
+    for name, v in (("dA", da), ("dB", db)):
+        assert bool((v[0] == INF).all()) and bool(torch.isfinite(v[1]).all()), name
