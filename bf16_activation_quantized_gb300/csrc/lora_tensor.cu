@@ -904,17 +904,22 @@ __global__ void __launch_bounds__(kWgradThreads, 1) lora_wgrad_kernel(const Wgra
             for (int m = 0; m < S::kCols / 128; ++m) {
                 const int col = 128 * m + 32 * sub + lane;
                 if (128 * m + 32 * sub >= width) break;
-                #pragma unroll 2
+                #pragma unroll 1
                 for (int rank = 0; rank < RP; rank += 8) {
                     uint32_t v[8], w[8];
                     const uint32_t at = tmem + (uint32_t(32 * sub) << 16) + buf * S::kD + m * 2 * RP + rank;
                     tc_ld_32x32b_x8(at, v);
                     tc_ld_32x32b_x8(at + RP, w);
                     tc_wait_ld();
+                    // an infinity of x or dy: in the upper plane's sum alone, the lower planes
+                    // have zeros (0 * inf) and either sign
                     float f[8];
                     #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        f[e] = ok ? __uint_as_float(v[e]) + __uint_as_float(w[e]) : __int_as_float(0x7fffffff);
+                    for (int e = 0; e < 8; ++e) {
+                        f[e] = __uint_as_float(v[e]);
+                        if (!isinf(f[e])) f[e] += __uint_as_float(w[e]);
+                        if (!ok) f[e] = __int_as_float(0x7fffffff);
+                    }
                     if (!whole) {
                         #pragma unroll
                         for (int e = 0; e < 8; ++e) __stcg(slot + (rank + e) * S::kCols + col, f[e]);

@@ -91,3 +91,33 @@ def test_an_infinite_scale_gives_infinities(T, r):
         assert bool((v[ids == 0] == INF).all()) and bool(torch.isfinite(v[ids == 1]).all()), name
     for name, v in (("dA", da), ("dB", db)):
         assert bool((v[0] == INF).all()) and bool(torch.isfinite(v[1]).all()), name
+
+
+@pytest.mark.parametrize("r", [8, 24, 64, 128])
+def test_an_infinity_of_a_row_reaches_its_column_of_the_weight_gradients(r):
+    """x[t, c] = inf makes dA[:, c] = g[t] * inf, dy[t, n] = inf makes dB[n] = s h[t] *
+    inf: infinities of g's and h's signs, whether these fill 24 bits or one."""
+    T, N, K = 200, 136, 256
+    g = torch.Generator(device="cuda").manual_seed(r)
+    x, dy = positive(g, T, K), positive(g, T, N)
+    a, b = positive(g, 1, r, K), positive(g, 1, N, r)
+    sign = torch.where(torch.arange(r, device="cuda") % 2 == 0, 1.0, -1.0)
+    b *= sign.bfloat16()
+    ids, one = torch.zeros(T, device="cuda", dtype=torch.int32), torch.ones(1, device="cuda")
+    hidden = (torch.rand(T, r, device="cuda", generator=g) + 0.25) * sign
+    hidden[3] = 0.5 * sign                               # one bit: nothing in the lower planes
+    finite_x, finite_dy = x.clone(), dy.clone()
+    x[2, 5], x[3, 130], x[150, 255] = INF, -INF, INF
+    da = w4.lora_add_backward(finite_dy, x, hidden, a, b, ids, one)[1][0]
+    for c, s in ((5, 1), (130, -1), (255, 1)):
+        assert da[:, c].tolist() == (INF * s * sign).tolist(), c
+    rest = torch.ones(K, dtype=torch.bool, device="cuda")
+    rest[[5, 130, 255]] = False
+    assert bool(torch.isfinite(da[:, rest]).all())
+    dy[2, 7], dy[3, 8], dy[150, 135] = INF, -INF, INF
+    db = w4.lora_add_backward(dy, finite_x, hidden, a, b, ids, one)[2][0]
+    for n, s in ((7, 1), (8, -1), (135, 1)):
+        assert db[n].tolist() == (INF * s * sign).tolist(), n
+    rest = torch.ones(N, dtype=torch.bool, device="cuda")
+    rest[[7, 8, 135]] = False
+    assert bool(torch.isfinite(db[rest]).all())
