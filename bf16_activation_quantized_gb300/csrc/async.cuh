@@ -13,7 +13,10 @@
 
 namespace w4a16 {
 
-constexpr unsigned long long kWaitLimitNs = 2000000000ull;  // 2 s
+#ifndef W4A16_WAIT_LIMIT_NS                                 // a test's build sets a shorter one
+#define W4A16_WAIT_LIMIT_NS 2000000000ull                   // 2 s
+#endif
+constexpr unsigned long long kWaitLimitNs = W4A16_WAIT_LIMIT_NS;
 
 // Error bits a kernel may record in the library's device error word (read
 // back, and cleared, with w4a16_read_error_word).

@@ -171,9 +171,13 @@ __device__ void find_tile_few(const LoraArgs &p, int tile, int *rows, int *out) 
     }
 }
 
-// Sorted tokens: adapters' tiles in order, those without an adapter last.
+// Sorted tokens: adapters' tiles in order, those without an adapter last.  All lanes
+// get the tile's adapter, its tokens and their first place in the sort.
+struct Tile {
+    int adapter, count, start;
+};
 template <int TM>
-__device__ void find_tile_sorted(const LoraArgs &p, int tile, int *rows, int *out) {
+__device__ Tile locate_tile(const LoraArgs &p, int tile) {
     const int lane = threadIdx.x & 31;
     int tiles = 0, row = 0, adapter = -1, start = 0, count = 0;
     bool found = false;
@@ -204,8 +208,14 @@ __device__ void find_tile_sorted(const LoraArgs &p, int tile, int *rows, int *ou
         start = row + (tile - tiles) * TM;
         count = max(0, min(TM, p.tokens - start));
     }
-    for (int i = lane; i < count; i += 32) rows[i] = p.order[start + i];
-    if (lane == 0) out[0] = adapter, out[1] = count, out[2] = start;
+    return {adapter, count, start};
+}
+template <int TM>
+__device__ void find_tile_sorted(const LoraArgs &p, int tile, int *rows, int *out) {
+    const int lane = threadIdx.x & 31;
+    const Tile t = locate_tile<TM>(p, tile);
+    for (int i = lane; i < t.count; i += 32) rows[i] = p.order[t.start + i];
+    if (lane == 0) out[0] = t.adapter, out[1] = t.count, out[2] = t.start;
 }
 
 struct WgradArgs {

@@ -49,9 +49,28 @@ constexpr int kTmemCols = 512;
 constexpr int kPrefetch = 256 * 1024;  // bytes of X that a CTA prefetches
 constexpr int kMaxRuns = 160;          // CTAs of the two products: one per SM (152)
 
-__device__ __forceinline__ void epi_sync() {
-    __syncwarp();                                    // bar.sync takes whole warps
-    asm volatile("bar.sync 1, %0;" ::"n"(kEpiThreads) : "memory");
+// A wait that runs out ends the pipeline of its CTA: the abort flag is set, no warp
+// takes a step after a wait of its own has failed (`lost`; a later phase's parity
+// would no longer say anything), and the warps that store leave NaN in all that is
+// left of the CTA's run.
+//
+// A test's build makes waits run out: from stage (or tile) g_stall_at of kernel
+// g_stall_kernel on, the producers of every other CTA do not report theirs.
+enum Stall { kStallDown = 1, kStallUp, kStallWgrad, kStallDownTile, kStallUpTile };
+#ifdef W4A16_TEST_STALL
+__device__ int g_stall_kernel, g_stall_at;
+__device__ __forceinline__ bool stalled(int kernel, int at) {
+    return kernel == g_stall_kernel && at >= g_stall_at && blockIdx.x % 2 == 0;
+}
+#else
+__device__ __forceinline__ constexpr bool stalled(int, int) { return false; }
+#endif
+
+// All MMAs have ended: no CTA leaves, or gives its TMEM back, before.
+__device__ __forceinline__ void drain_mmas(uint32_t bar) {
+    if (elect_one()) tc_commit(bar);
+    __syncwarp();
+    drain_wait(bar, 0);
 }
 
 // Byte of piece p (16 bytes) of row `row` in a block of 128-byte rows.
@@ -176,12 +195,12 @@ __device__ __forceinline__ void stage_weights(const Producer &t, uint32_t ws, co
 
 // The first producer warp fills segment seg's slot; everyone waits for it.
 __device__ __forceinline__ bool tile_ready(const LoraArgs &p, TileSlots &ts, int seg, int tile, uint32_t tfull,
-                                           uint32_t tempty, bool writer, volatile int *abort_flag) {
+                                           uint32_t tempty, bool writer, int stall, volatile int *abort_flag) {
     const int slot = seg & 1;
     bool ok = true;
     if (writer) {
         if (seg >= 2) ok = mbar_wait(tempty + 8 * slot, ((seg >> 1) - 1) & 1, abort_flag, p.err);
-        if (__all_sync(0xffffffffu, ok)) {
+        if (__all_sync(0xffffffffu, ok) && !stalled(stall, seg)) {
             find_tile_sorted<kTile>(p, tile, ts.rows[slot], ts.info[slot]);
             __syncwarp();
             if ((threadIdx.x & 31) == 0) mbar_arrive(tfull + 8 * slot);
@@ -220,15 +239,16 @@ __global__ void __launch_bounds__(kThreads, 1) lora_down_kernel(const LoraArgs p
     using S = DownShape<RP, TRANS>;
     constexpr int NS = S::kStages;
     extern __shared__ unsigned char s_raw[];
-    __shared__ uint64_t s_bar[2 * NS + 8];
+    __shared__ uint64_t s_bar[2 * NS + 9];
     __shared__ TileSlots s_tiles;
     __shared__ int s_abort;
     __shared__ uint32_t s_tmem;
     unsigned char *s_mem = s_raw + (-smem_u32(s_raw) & 1023);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t full = smem_u32(s_bar), empty = full + 8 * NS, tfull = empty + 8 * NS, tempty = tfull + 16;
-    const uint32_t dfull = tempty + 16, dempty = dfull + 16;
+    const uint32_t dfull = tempty + 16, dempty = dfull + 16, drained = dempty + 16;
     if (threadIdx.x == 0) {
+        mbar_init(drained, 1);
         for (int i = 0; i < NS; ++i) mbar_init(full + 8 * i, kProducers), mbar_init(empty + 8 * i, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(tfull + 8 * i, 1), mbar_init(tempty + 8 * i, kThreads / 32);
@@ -261,11 +281,13 @@ __global__ void __launch_bounds__(kThreads, 1) lora_down_kernel(const LoraArgs p
     volatile int *abort_flag = &s_abort;
 
     int i = 0, seg = 0;                              // steps and tiles so far
-    for (long long u = w.u0; u < w.u1; ++seg) {
+    bool lost = false;                               // a wait of this warp's has run out
+    long long u = w.u0;                              // the first unit that is not done
+    for (int n_steps; u < w.u1; ++seg, u += n_steps) {
         const int tile = int(quotient(u, w.per)), k0 = int(u - (long long)tile * w.per);
-        const int n_steps = int(w.u1 - u < w.per - k0 ? w.u1 - u : w.per - k0);
-        u += n_steps;
-        if (!tile_ready(p, s_tiles, seg, tile, tfull, tempty, warp == kEpiWarps, abort_flag)) break;
+        n_steps = int(w.u1 - u < w.per - k0 ? w.u1 - u : w.per - k0);
+        lost = !tile_ready(p, s_tiles, seg, tile, tfull, tempty, warp == kEpiWarps, kStallDownTile, abort_flag);
+        if (lost) break;
         const int *rows = s_tiles.rows[seg & 1];
         const int adapter = s_tiles.info[seg & 1][0], count = s_tiles.info[seg & 1][1];
         if (warp >= kEpiWarps && warp < kMmaWarp) {
@@ -278,12 +300,14 @@ __global__ void __launch_bounds__(kThreads, 1) lora_down_kernel(const LoraArgs p
             for (int k = 0; k < n_steps; ++k, ++i) {
                 const int s = i % NS, col = (k0 + k) * kCols, n = min(kCols, p.in - col);
                 const bool ok = i < NS || mbar_wait(empty + 8 * s, (i / NS - 1) & 1, abort_flag, p.err);
-                if (!__all_sync(0xffffffffu, ok)) break;
+                lost = !__all_sync(0xffffffffu, ok);
+                if (lost) break;
                 unsigned char *xs = s_mem + s * S::kStage;
                 stage_rows(t, xs, src, mine, col, n, p.vec_in);
                 stage_weights<RP, !TRANS>(t, smem_u32(xs) + 2 * kBlock, wt, r, p.in, col, n);
-                stage_done(full + 8 * s, p.vec_in);
+                if (!stalled(kStallDown, i)) stage_done(full + 8 * s, p.vec_in);
             }
+            if (lost) break;
         } else if (warp == kMmaWarp) {
             constexpr uint32_t idesc = tc_idesc_bf16(kTile, RP) | (TRANS ? kTcBMajorN : 0);
             const uint32_t d = tmem + (seg & 1) * (S::kAcc * RP);
@@ -308,12 +332,15 @@ __global__ void __launch_bounds__(kThreads, 1) lora_down_kernel(const LoraArgs p
                 }
                 __syncwarp();
             }
+            lost = !ok;
+            if (lost) break;
             if (elect_one()) tc_commit(dfull + 8 * (seg & 1));
             __syncwarp();
         } else {
             // this run's sum over the tile's columns, to its slot
             const int sub = warp % 4, half = warp / 4, row = 32 * sub + lane;
-            const bool ok = __all_sync(0xffffffffu, mbar_wait(dfull + 8 * (seg & 1), (seg >> 1) & 1, abort_flag, p.err));
+            lost = !__all_sync(0xffffffffu, mbar_wait(dfull + 8 * (seg & 1), (seg >> 1) & 1, abort_flag, p.err));
+            if (lost) break;
             tc_fence_after();
             float *out = p.partial + ((long long)(tile + blockIdx.x) * kTile + row) * RP + half * (RP / 2);
             #pragma unroll
@@ -332,10 +359,6 @@ __global__ void __launch_bounds__(kThreads, 1) lora_down_kernel(const LoraArgs p
                     #pragma unroll
                     for (int e = 0; e < 8; ++e)
                         v[e] = __float_as_uint(__uint_as_float(v[e]) + __uint_as_float(w[n - 1][e]));
-                if (!ok || *abort_flag) {
-                    #pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] = 0x7fffffffu;
-                }
                 if (row < count) {
                     *reinterpret_cast<uint4 *>(out + 8 * k) = make_uint4(v[0], v[1], v[2], v[3]);
                     *reinterpret_cast<uint4 *>(out + 8 * k + 4) = make_uint4(v[4], v[5], v[6], v[7]);
@@ -348,8 +371,16 @@ __global__ void __launch_bounds__(kThreads, 1) lora_down_kernel(const LoraArgs p
         }
         tile_done(seg, tempty);
     }
+    if (warp < kEpiWarps)                            // the tiles that a wait lost, this thread's part
+        for (; u < w.u1; u += w.per - u % w.per) {
+            const int tile = int(u / w.per), row = 32 * (warp % 4) + lane;
+            float *out = p.partial + ((long long)(tile + blockIdx.x) * kTile + row) * RP + warp / 4 * (RP / 2);
+            if (row < locate_tile<kTile>(p, tile).count)
+                for (int k = 0; k < RP / 2; ++k) out[k] = __int_as_float(0x7fffffff);
+            __syncwarp();
+        }
     cp_async_wait_all();
-    if (warp == kMmaWarp && seg > 0) drain_wait(dfull + 8 * ((seg - 1) & 1), ((seg - 1) >> 1) & 1);
+    if (warp == kMmaWarp) drain_mmas(drained);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -474,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1) lora_up_kernel(const LoraArgs p) 
     using S = UpShape<RP, TRANS>;
     constexpr int NS = S::kStages, KS = RP / 16;
     extern __shared__ unsigned char s_raw[];
-    __shared__ uint64_t s_bar[2 * NS + 13];
+    __shared__ uint64_t s_bar[2 * NS + 15];
     __shared__ TileSlots s_tiles;
     __shared__ int s_abort;
     __shared__ uint32_t s_tmem;
@@ -483,7 +514,9 @@ __global__ void __launch_bounds__(kThreads, 1) lora_up_kernel(const LoraArgs p) 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t full = smem_u32(s_bar), empty = full + 8 * NS, tfull = empty + 8 * NS, tempty = tfull + 16;
     const uint32_t dfull = tempty + 16, dempty = dfull + 32, hready = dempty + 32;
+    const uint32_t multiplied = hready + 8, drained = multiplied + 8;
     if (threadIdx.x == 0) {
+        mbar_init(multiplied, kEpiWarps), mbar_init(drained, 1);
         for (int i = 0; i < NS; ++i) mbar_init(full + 8 * i, kProducers), mbar_init(empty + 8 * i, kEpiWarps / 2);
         for (int i = 0; i < 2; ++i) {
             mbar_init(tfull + 8 * i, 1), mbar_init(tempty + 8 * i, kThreads / 32);
@@ -514,11 +547,13 @@ __global__ void __launch_bounds__(kThreads, 1) lora_up_kernel(const LoraArgs p) 
     int i = 0, seg = 0, h_seg = 0;
     uint32_t uses = 0;                               // a bit per buffer: the parity of its next use
     uint32_t used = 0;
-    for (long long u = w.u0; u < w.u1; ++seg) {
+    bool lost = false;                               // a wait of this warp's has run out
+    long long u = w.u0;                              // the first unit that is not done
+    for (int n_steps; u < w.u1; ++seg, u += n_steps) {
         const int tile = int(quotient(u, w.per)), k0 = int(u - (long long)tile * w.per);
-        const int n_steps = int(w.u1 - u < w.per - k0 ? w.u1 - u : w.per - k0);
-        u += n_steps;
-        if (!tile_ready(p, s_tiles, seg, tile, tfull, tempty, warp == kEpiWarps, abort_flag)) break;
+        n_steps = int(w.u1 - u < w.per - k0 ? w.u1 - u : w.per - k0);
+        lost = !tile_ready(p, s_tiles, seg, tile, tfull, tempty, warp == kEpiWarps, kStallUpTile, abort_flag);
+        if (lost) break;
         const int *rows = s_tiles.rows[seg & 1];
         const int adapter = s_tiles.info[seg & 1][0], count = s_tiles.info[seg & 1][1];
         const bool in_place = adapter < 0 && p.y == p.base;      // nothing to do
@@ -532,12 +567,14 @@ __global__ void __launch_bounds__(kThreads, 1) lora_up_kernel(const LoraArgs p) 
             for (int k = 0; k < n_steps && !in_place; ++k, ++i) {
                 const int s = i % NS, col = (k0 + k) * kCols, n = min(kCols, p.out - col);
                 const bool ok = i < NS || mbar_wait(empty + 8 * s, (i / NS - 1) & 1, abort_flag, p.err);
-                if (!__all_sync(0xffffffffu, ok)) break;
+                lost = !__all_sync(0xffffffffu, ok);
+                if (lost) break;
                 unsigned char *xs = s_mem + s * S::kStage;
                 stage_rows(t, xs, src, mine, col, n, p.vec_out);
                 if (adapter >= 0) stage_weights<RP, TRANS>(t, smem_u32(xs) + 2 * kBlock, wt, r, p.out, col, n);
-                stage_done(full + 8 * s, p.vec_out);
+                if (!stalled(kStallUp, i)) stage_done(full + 8 * s, p.vec_out);
             }
+            if (lost) break;
         } else if (warp == kMmaWarp) {
             constexpr uint32_t idesc = tc_idesc_bf16(kTile, kCols) | (TRANS ? kTcBMajorN : 0);
             if (adapter >= 0) {
@@ -569,6 +606,8 @@ __global__ void __launch_bounds__(kThreads, 1) lora_up_kernel(const LoraArgs p) 
                     }
                     __syncwarp();
                 }
+                lost = !ok;
+                if (lost) break;
             } else if (!in_place) {
                 i += n_steps;
             }
@@ -577,9 +616,14 @@ __global__ void __launch_bounds__(kThreads, 1) lora_up_kernel(const LoraArgs p) 
             // one buffer 1100 to 1700 of a group's 5300 cycles a step went by waiting for
             // the MMAs); a warp has 32 rows.
             const int sub = warp % 4, group = warp / 4, my_row = 32 * sub + lane;
-            bool bad = false;
             if (seg == 0 && !TRANS) pdl_wait();
-            if (seg > 0) epi_sync();                         // the MMAs of the tile before have ended
+            if (seg > 0) {
+                // the MMAs of the tile before have ended: every warp of these has waited for its own
+                __syncwarp();
+                if (lane == 0) mbar_arrive(multiplied);
+                lost = !__all_sync(0xffffffffu, mbar_wait(multiplied, (seg - 1) & 1, abort_flag, p.err));
+                if (lost) break;
+            }
             if (adapter >= 0) {
                 // h's planes of the tile; rows past its tokens are zeros
                 const int start = s_tiles.info[seg & 1][2];
@@ -614,7 +658,11 @@ __global__ void __launch_bounds__(kThreads, 1) lora_up_kernel(const LoraArgs p) 
                     uses ^= 1u << (i & 3);
                     tc_fence_after();
                 }
-                bad |= !__all_sync(0xffffffffu, ok);
+                lost = !__all_sync(0xffffffffu, ok);
+                if (lost) {
+                    u += k;
+                    break;
+                }
                 #pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
                     const int col = (k0 + k) * kCols + 64 * half;
@@ -622,7 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1) lora_up_kernel(const LoraArgs p) 
                     unsigned char *bs = s_mem + s * S::kStage + half * kBlock;
                     // Four pieces of 16 bytes at once: the compiler cannot tell that a store of
                     // one leaves the next one's load alone.
-                    if (adapter >= 0 && !bad) {
+                    if (adapter >= 0) {
                         uint32_t acc[2][32];
                         tc_ld_32x32b_x32(lanes + 64 * half, acc[0]);
                         tc_ld_32x32b_x32(lanes + 64 * half + 32, acc[1]);
@@ -646,11 +694,10 @@ __global__ void __launch_bounds__(kThreads, 1) lora_up_kernel(const LoraArgs p) 
                                 *reinterpret_cast<uint4 *>(bs + sw128(my_row, 4 * h + q)) = v[q];
                             }
                         }
-                    } else if (bad || !p.base) {
-                        const uint32_t fill = bad ? 0x7fff7fffu : 0u;
+                    } else if (!p.base) {
                         #pragma unroll
                         for (int q = 0; q < 8; ++q)
-                            *reinterpret_cast<uint4 *>(bs + sw128(my_row, q)) = make_uint4(fill, fill, fill, fill);
+                            *reinterpret_cast<uint4 *>(bs + sw128(my_row, q)) = make_uint4(0, 0, 0, 0);
                     }
                     __syncwarp();
                     const int q = lane % 8, left = p.out - col - 8 * q;
@@ -677,15 +724,24 @@ __global__ void __launch_bounds__(kThreads, 1) lora_up_kernel(const LoraArgs p) 
                     mbar_arrive(empty + 8 * s);
                 }
             }
+            if (lost) break;
         }
         tile_done(seg, tempty);
     }
     pdl_wait();
     pdl_launch_dependents();
+    if (warp < kEpiWarps)                            // the steps that a wait lost, this warp's rows
+        for (; u < w.u1; ++u) {
+            const int tile = int(u / w.per), col = int(u % w.per) * kCols, n = min(kCols, p.out - col);
+            const Tile t = locate_tile<kTile>(p, tile);
+            if (t.adapter < 0 && p.y == p.base) continue;
+            if ((i++ & 1) != warp / 4) continue;
+            for (int row = 32 * (warp % 4); row < min(t.count, 32 * (warp % 4) + 32); ++row)
+                for (int c = lane; c < n; c += 32)
+                    p.y[(long long)p.order[t.start + row] * p.out + col + c] = 0x7fffu;
+        }
     cp_async_wait_all();
-    if (warp == kMmaWarp)
-        for (int buf = 0; buf < 4; ++buf)
-            if ((used >> buf) & 1) drain_wait(dfull + 8 * buf, (~uses >> buf) & 1);
+    if (warp == kMmaWarp) drain_mmas(drained);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -779,14 +835,15 @@ __global__ void __launch_bounds__(kWgradThreads, 1) lora_wgrad_kernel(const Wgra
     using S = WgradShape<RP>;
     constexpr int NS = S::kStages;
     extern __shared__ unsigned char s_raw[];
-    __shared__ uint64_t s_bar[2 * NS + 4];
+    __shared__ uint64_t s_bar[2 * NS + 5];
     __shared__ int s_abort;
     __shared__ uint32_t s_tmem;
     unsigned char *s_mem = s_raw + (-smem_u32(s_raw) & 1023);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t ring = smem_u32(s_mem), full = smem_u32(s_bar), empty = full + 8 * NS;
-    const uint32_t dfull = empty + 8 * NS, dempty = dfull + 16;
+    const uint32_t dfull = empty + 8 * NS, dempty = dfull + 16, drained = dempty + 16;
     if (threadIdx.x == 0) {
+        mbar_init(drained, 1);
         for (int i = 0; i < NS; ++i) mbar_init(full + 8 * i, kWgradProducers), mbar_init(empty + 8 * i, 1);
         for (int i = 0; i < 2; ++i) mbar_init(dfull + 8 * i, 1), mbar_init(dempty + 8 * i, kWgradStore);
         s_abort = 0;
@@ -809,6 +866,7 @@ __global__ void __launch_bounds__(kWgradThreads, 1) lora_wgrad_kernel(const Wgra
     pdl_launch_dependents();
     volatile int *abort_flag = &s_abort;
     int i = 0, seg = 0;                                          // stages, pairs
+    bool lost = false;                                           // a wait of this warp's has run out
     for (long long u = u0; u < u1; ++seg) {
         const Pair q = find_pair(p, u);
         const int block0 = int(u - q.first);
@@ -842,7 +900,8 @@ __global__ void __launch_bounds__(kWgradThreads, 1) lora_wgrad_kernel(const Wgra
                     next[j] = t < q.size ? rows[t] : -1;
                 }
                 const bool ok = i < NS || mbar_wait(empty + 8 * s, (i / NS - 1) & 1, abort_flag, p.err);
-                if (!__all_sync(0xffffffffu, ok)) break;
+                lost = !__all_sync(0xffffffffu, ok);
+                if (lost) break;
                 const uint32_t qs = ring + s * S::kStage, ps = qs + S::kQ;
                 // tokens past the last are zeros on both sides: they are summed over
                 #pragma unroll
@@ -866,8 +925,9 @@ __global__ void __launch_bounds__(kWgradThreads, 1) lora_wgrad_kernel(const Wgra
                     const int line = m / 4, e = m % 4;
                     cp_async16(ps + line * 64 + ((e ^ ((line >> 1) & 3)) << 4), src + line * kTile + 8 * e);
                 }
-                stage_done(full + 8 * s, vec);
+                if (!stalled(kStallWgrad, i)) stage_done(full + 8 * s, vec);
             }
+            if (lost) break;
         } else if (warp == kWgradMma) {
             constexpr uint32_t idesc = tc_idesc_bf16(128, 2 * RP) | kTcAMajorM, idesc1 = tc_idesc_bf16(128, RP) | kTcAMajorM;
             bool ok = seg < S::kBufs || mbar_wait(dempty + 8 * buf, (seg / S::kBufs - 1) & 1, abort_flag, p.err);
@@ -893,11 +953,14 @@ __global__ void __launch_bounds__(kWgradThreads, 1) lora_wgrad_kernel(const Wgra
                 }
                 __syncwarp();
             }
+            lost = !ok;
+            if (lost) break;
             if (elect_one()) tc_commit(dfull + 8 * buf);
             __syncwarp();
         } else {
             const int sub = warp % 4;
-            const bool ok = __all_sync(0xffffffffu, mbar_wait(dfull + 8 * buf, (seg / S::kBufs) & 1, abort_flag, p.err));
+            const bool ok = !lost && mbar_wait(dfull + 8 * buf, (seg / S::kBufs) & 1, abort_flag, p.err);
+            lost = !__all_sync(0xffffffffu, ok);
             tc_fence_after();
             const bool whole = n_blocks == q.blocks;
             float *slot = p.partial + (long long)(2 * b + (block0 == 0)) * S::kTileSums;
@@ -918,7 +981,7 @@ __global__ void __launch_bounds__(kWgradThreads, 1) lora_wgrad_kernel(const Wgra
                     for (int e = 0; e < 8; ++e) {
                         f[e] = __uint_as_float(v[e]);
                         if (!isinf(f[e])) f[e] += __uint_as_float(w[e]);
-                        if (!ok) f[e] = __int_as_float(0x7fffffff);
+                        if (lost) f[e] = __int_as_float(0x7fffffff);
                     }
                     if (!whole) {
                         #pragma unroll
@@ -939,11 +1002,11 @@ __global__ void __launch_bounds__(kWgradThreads, 1) lora_wgrad_kernel(const Wgra
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(dempty + 8 * buf);
+            if (lane == 0 && !lost) mbar_arrive(dempty + 8 * buf);
         }
     }
     cp_async_wait_all();
-    if (warp == kWgradMma && seg > 0) drain_wait(dfull + 8 * ((seg - 1) % S::kBufs), ((seg - 1) / S::kBufs) & 1);
+    if (warp == kWgradMma) drain_mmas(drained);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -1118,3 +1181,10 @@ cudaError_t launch_wgrad(const WgradArgs &p, WgradStep step, int sms, cudaStream
 }
 
 }  // namespace w4a16
+
+#ifdef W4A16_TEST_STALL
+extern "C" int w4a16_test_stall(int kernel, int at) {
+    const cudaError_t e = cudaMemcpyToSymbol(w4a16::g_stall_kernel, &kernel, sizeof kernel);
+    return e != cudaSuccess ? int(e) : int(cudaMemcpyToSymbol(w4a16::g_stall_at, &at, sizeof at));
+}
+#endif

@@ -47,11 +47,6 @@ def test_lanes_meet_before_a_cluster_barrier(name):
     assert body.index("__syncwarp();") < body.index("barrier.cluster.")
 
 
-def test_lanes_meet_before_the_barrier_of_the_storing_warps():
-    body = re.search(r"void epi_sync\(\) \{(.*?)\n\}", source("lora_tensor.cu"), re.S).group(1)
-    assert body.index("__syncwarp();") < body.index("bar.sync")
-
-
 def test_lanes_meet_before_the_next_load_from_tensor_memory():
     text = source("lora_tensor.cu")
     calls = [m.start() for m in re.finditer(r"\btc_ld_\w+\(", text)]
