@@ -6,11 +6,13 @@ cluster barriers, which follow loops whose trip counts differ between lanes, and
 loads from tensor memory in loops whose bodies store under lane-dependent conditions."""
 from __future__ import annotations
 
+import ctypes
 import os
 import re
 
 import pytest
 
+from bf16_activation_quantized_gb300 import _lib
 from bf16_activation_quantized_gb300 import build as build_mod
 
 
@@ -53,3 +55,19 @@ def test_lanes_meet_before_the_next_load_from_tensor_memory():
     assert len(calls) >= 5
     for at in calls:
         assert enclosing_loop(text, at).rstrip().endswith("__syncwarp();"), text[at:at + 60]
+
+
+def test_smoke_takes_both_forms_of_the_adapters():
+    """The few-token form takes no workspace, the many-token form does."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    text = open(os.path.join(root, "__graft_entry__.py")).read()
+    sizes = [int(v) for v in re.search(r"for tokens in \((\d+), (\d+)\)", text).groups()]
+    rank, adapters = 16, 3
+    assert f"normal({adapters}, {rank}, 256" in text
+    build_mod.build()
+    need = ctypes.c_size_t(0)
+    forms = []
+    for tokens in sizes:
+        assert _lib.lib().w4a16_lora_workspace_bytes(tokens, adapters, rank, 0, ctypes.byref(need)) == 0
+        forms.append(need.value > 0)
+    assert forms == [False, True]
