@@ -428,8 +428,9 @@ def splitk_reduce(ws: torch.Tensor, out: torch.Tensor | None = None) -> torch.Te
 
 # The current stream's handle and the current device without the objects around
 # them: a call of a few microseconds spends a third of its time there otherwise.
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+# (A torch without CUDA has neither; its tensors never get past the checks.)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
 def _empty(shape, dtype, index: int) -> torch.Tensor:

@@ -1,0 +1,23 @@
+"""The Python binding of dispatch, combine and the adapters, on the host (no GPU)."""
+from __future__ import annotations
+
+import os
+import subprocess
+import sys
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+def test_imports_with_a_torch_that_has_no_cuda():
+    """Such a torch lacks the two calls; pack sizes, plans and host checks need neither."""
+    code = ("import torch\n"
+            "for name in ('_cuda_getCurrentRawStream', '_cuda_getDevice'):\n"
+            "    if hasattr(torch._C, name): delattr(torch._C, name)\n"
+            "import bf16_activation_quantized_gb300 as w4\n"
+            "x = torch.zeros(2, 8, dtype=torch.bfloat16)\n"
+            "try:\n"
+            "    w4.dispatch(x, torch.zeros(2, 1, dtype=torch.int32), 2)\n"
+            "except ValueError:\n"
+            "    print('refused')\n")
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "refused", r.stdout + r.stderr
