@@ -15,6 +15,7 @@ with CPU tensors or without the built library raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import threading
 
 import torch
@@ -464,18 +465,14 @@ def _index_of(t: torch.Tensor, name: str, dtype) -> int:
     return t.get_device()
 
 
-_sort_bytes_cache: dict = {}
-
-
+# The workspaces' sizes are kept for the sizes used last: a call then costs one library
+# call, and a server that meets every token count holds no entry for each.
+@functools.lru_cache(maxsize=1024)
 def _sort_bytes(tokens: int, top_k: int, num_groups: int) -> int:
-    key = (tokens, top_k, num_groups)
-    need = _sort_bytes_cache.get(key)
-    if need is None:
-        nb = ctypes.c_size_t(0)
-        _lib.check(_lib.lib().w4a16_dispatch_workspace_bytes(tokens, top_k, num_groups, ctypes.byref(nb)),
-                   "w4a16_dispatch_workspace_bytes")
-        need = _sort_bytes_cache[key] = int(nb.value)
-    return need
+    nb = ctypes.c_size_t(0)
+    _lib.check(_lib.lib().w4a16_dispatch_workspace_bytes(tokens, top_k, num_groups, ctypes.byref(nb)),
+               "w4a16_dispatch_workspace_bytes")
+    return int(nb.value)
 
 
 def dispatch(x: torch.Tensor, ids: torch.Tensor, num_groups: int):
@@ -571,17 +568,16 @@ def combine_backward(dy: torch.Tensor, ys: torch.Tensor, slots: torch.Tensor, we
     return dys, dweights
 
 
-_lora_bytes_cache: dict = {}
+@functools.lru_cache(maxsize=1024)
+def _lora_bytes(tokens: int, adapters: int, rank: int, backward: int) -> int:
+    nb = ctypes.c_size_t(0)
+    _lib.check(_lib.lib().w4a16_lora_workspace_bytes(tokens, adapters, rank, backward, ctypes.byref(nb)),
+               "w4a16_lora_workspace_bytes")
+    return int(nb.value)
 
 
 def _lora_workspace(index: int, tokens: int, adapters: int, rank: int, backward: int):
-    key = (tokens, adapters, rank, backward)
-    need = _lora_bytes_cache.get(key)
-    if need is None:
-        nb = ctypes.c_size_t(0)
-        _lib.check(_lib.lib().w4a16_lora_workspace_bytes(tokens, adapters, rank, backward, ctypes.byref(nb)),
-                   "w4a16_lora_workspace_bytes")
-        need = _lora_bytes_cache[key] = int(nb.value)
+    need = _lora_bytes(tokens, adapters, rank, backward)
     return (_empty(need, torch.uint8, index) if need else None), need
 
 

@@ -5,6 +5,9 @@ import os
 import subprocess
 import sys
 
+import bf16_activation_quantized_gb300 as w4
+from bf16_activation_quantized_gb300 import build as build_mod
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
@@ -21,3 +24,13 @@ def test_imports_with_a_torch_that_has_no_cuda():
             "    print('refused')\n")
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.strip() == "refused", r.stdout + r.stderr
+
+
+def test_sizes_kept_for_calls_are_bounded():
+    """A server that meets every token count keeps no entry for each of them."""
+    build_mod.build()
+    for tokens in range(1, 5001):
+        w4._sort_bytes(tokens, 8, 64)
+        w4._lora_bytes(tokens, 4, 16, 1)
+    for cached in (w4._sort_bytes, w4._lora_bytes):
+        assert cached.cache_info().currsize <= 1024
