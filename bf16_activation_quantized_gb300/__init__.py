@@ -450,6 +450,12 @@ def _launch(name: str, index: int, *args) -> None:
         _lib.check(status, name)
 
 
+def _need_int32(*sizes: int) -> None:
+    """The C ABI takes sizes as 32-bit integers; ctypes would drop the upper bits."""
+    if max(sizes) > 0x7fffffff:
+        raise ValueError(f"a size is past 32 bits: {sizes}")
+
+
 def _need_on(index: int, t: torch.Tensor, name: str, dtype=None) -> None:
     """``t`` is a contiguous tensor of ``dtype`` on CUDA device ``index``."""
     if (isinstance(t, torch.Tensor) and (dtype is None or t.dtype == dtype) and t.is_contiguous()
@@ -492,6 +498,7 @@ def dispatch(x: torch.Tensor, ids: torch.Tensor, num_groups: int):
         raise ValueError(f"ids must be int32 or int64, got {ids.dtype}")
     T, K = x.shape
     k = ids.shape[1]
+    _need_int32(T, k, K, num_groups)
     need = _sort_bytes(T, k, num_groups)
     ws = _empty(need, torch.uint8, dev) if need else None
     xs = _empty((T * k, K), torch.bfloat16, dev)
@@ -512,6 +519,7 @@ def _need_slots(rows: torch.Tensor, slots: torch.Tensor, weights, name: str) -> 
     _need_on(dev, slots, "slots", torch.int32)
     if rows.dim() != 2 or slots.dim() != 2 or rows.shape[0] != slots.numel():
         raise ValueError(f"{name} must be [T*k, N] for slots [T, k]")
+    _need_int32(*slots.shape, rows.shape[1])
     if weights is not None:
         _need_on(dev, weights, "weights")
         if weights.dtype not in _WEIGHT_DTYPES or weights.shape != slots.shape:
@@ -599,6 +607,7 @@ def _need_lora(x, lora_a, lora_b, adapters, lora_scales):
         raise ValueError("adapters must be int32 or int64 [T]")
     if lora_scales.shape != (L,):
         raise ValueError("lora_scales must be float32 [L]")
+    _need_int32(T, L, r, N, K)
     return dev, T, L, r, N, K
 
 
