@@ -31,11 +31,16 @@ constexpr int kFewTile = 16;
 // Up to `tokens` tokens take this kernel, and up to `most` while the adapters have at
 // most `each` on average (many adapters leave the tensor core kernels' tiles of 128
 // tokens mostly empty).  Measured at 8192 x 8192, this kernel / the tensor core kernels,
-// in us.  Rank 16: 384 tokens of 1 adapter 26.8 / 30.8, 448 33.9 / 29.3; 512 of 16 26.5 /
-// 27.0, 640 34.8 / 27.3; 768 of 64 33.8 / 61.4.  Rank 32: 192 tokens of 1 adapter 17.4 /
-// 19.8, 384 of 4 29.8 / 28.8, 768 of 64 41.5 / 64.2.  Rank 64: 128 tokens of 1 adapter
-// 19.3 / 19.8, 160 24.4 / 21.0; 256 of 16 26.3 / 30.0, 320 34.5 / 30.3; 512 of 64 59.6 /
-// 67.6, 640 73.3 / 68.0.  Rank 128: 128 of 4 23.4 / 24.7, 512 of 64 69.2 / 95.4.
+// in us.  Rank 16: 384 tokens of 1 adapter 24.7 / 30.3, 512 35.8 / 29.9; 512 of 16 24.5 /
+// 27.6, 768 40.3 / 28.5; 768 of 64 31.3 / 61.2.  Rank 32: 192 tokens of 1 adapter 15.4 /
+// 26.6, 384 of 4 26.7 / 28.4, 768 of 64 37.1 / 63.6.  Rank 64: 128 tokens of 1 adapter
+// 17.5 / 22.6, 192 27.3 / 25.5; 256 of 16 25.1 / 31.8, 384 36.7 / 32.3; 512 of 64 62.0 /
+// 73.8, 768 78.2 / 74.3.  Rank 128: 128 of 4 20.5 / 23.2, 512 of 64 80.5 / 96.8.
+// The border is 8192 x 8192's; other shapes have another, at rank 16: 1024 x 1024, 256 of
+// 1 13.0 / 16.1, 384 20.3 / 15.9; 2560 to 19456 columns, 192 of 1 17.3 / 19.0, 384 32.6 /
+// 21.7.  And the adapters counted are the table's, not those in use, which only the
+// device knows: 768 tokens that all use one of 64 take 37.2 / 29.3 (2560 to 19456: 56.1 /
+// 26.9), against 31.3 / 61.2 (48.5 / 78.8) where they are spread.
 struct FewLimits {
     int tokens, most, each;
 };
@@ -60,9 +65,11 @@ __device__ __forceinline__ void mma_acc(float (&c)[4], const uint32_t (&a)[4], u
 // What bounds it: latency.  One token at rank 16 and 8192 x 8192 needs 0.5 MB;
 // the chain is ids -> rows and A -> sums over warps and CTAs -> y, so the first
 // B and base of each warp are on their way before the sums are.  Measured at 8192 x
-// 8192 and rank 16: one token 5.1 us, 32 tokens of 32 adapters 6.6 (2.8 TB/s, of which
-// much from L2); 61 tokens of 64 adapters at rank 32, 2560 to 19456 columns: 19.5
-// us (57 MB, 2.9 TB/s), bound by how many loads the 8 warps of a CTA hold in registers.
+// 8192 and rank 16: one token 5.5 us, 32 tokens of 64 adapters 6.8 (2.7 TB/s, of which
+// much from L2); 61 tokens of 64 adapters at rank 32, 2560 to 19456 columns: 20.2
+// us (57 MB, 2.8 TB/s), bound by how many loads the 8 warps of a CTA hold in registers.
+// h's third term costs 0.4 us of one token's and 0.6 of 61 tokens' (two terms in an MMA
+// that has no tokens in half its rows; three MMAs instead: 23.1).
 template <int RP>
 __global__ void __launch_bounds__(kFewThreads, RP <= 32 ? 2 : 1) lora_few_kernel(const LoraArgs p) {
     constexpr int TM = kFewTile, NT = RP / 8, QN = RP >= 32 ? RP / 32 : 1, KS = RP / 16;
@@ -335,9 +342,9 @@ int resident_clusters(int c, size_t smem) {
 
 // CTAs of a cluster: eight where all clusters can be resident at once, counting one
 // per adapter in use and one per 16 tokens.  Measured at 8192 x 8192 with 64
-// adapters, 8 / 4 / 2 CTAs: rank 16, 32 tokens 6.6 / 7.6 / 11.8 us, 64 tokens 13.2 /
-// 9.8 / 12.4; rank 64, 16 tokens (one cluster of eight too many) 15.9 / 12.2 / 20.5,
-// 64 tokens 51.8 / 36.7 / 32.2.
+// adapters, 8 / 4 / 2 CTAs: rank 16, 32 tokens 6.8 / 8.0 / 11.9 us, 64 tokens 13.4 /
+// 9.8 / 12.3; rank 64, 16 tokens (one cluster of eight too many) 15.6 / 12.4 / 20.0,
+// 64 tokens 51.2 / 37.0 / 32.8.
 template <int RP>
 int few_cluster(int tokens, int adapters, size_t smem) {
     const int used = adapters + tokens / kFewTile, clusters = tokens < used ? tokens : used;

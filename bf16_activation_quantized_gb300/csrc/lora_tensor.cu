@@ -217,10 +217,11 @@ __device__ __forceinline__ void tile_done(int seg, uint32_t tempty) {
 // ------------------------------------------------------------ first product
 // h[t][rank] = sum over columns of x[t][col] A[rank][col] (g: of dy and B, whose
 // columns lie along the weight's rows: an MN-major operand).  Tokens are the MMA's M,
-// ranks its N.  Bound by HBM, the rows of X: a stage is 32 KB of them, six stages
-// keep up to 216 KB per SM in flight.  4096 tokens of 8192 columns at rank 64 (67 MB):
-// 11.5 us from the first data to the last sum, 5.8 TB/s; 17 us with the start and the
-// walk's set-up (sizes -> tile -> rows -> X, one load after the other).
+// ranks its N.  Bound by HBM, the rows of X: a stage is 32 KB of them and its weights;
+// six stages fit at padded rank 16, five at 32, four at 64, three at 128 (in the gradient
+// four up to 64).  4096 tokens of 8192 columns at rank 64 (67 MB): 21 us behind the sort,
+// of which time stamps put 11.5 from the first data to the last sum (5.8 TB/s); the rest
+// is the start and the walk's set-up (sizes -> tile -> rows -> X, one load after the other).
 template <int RP, bool TRANS>
 struct DownShape {
     static constexpr int kW = weight_bytes(RP, !TRANS);
@@ -489,7 +490,7 @@ __global__ void __launch_bounds__(kSumThreads) lora_sum_kernel(const LoraArgs p,
 // Bound by HBM: base in, y out.  The accumulators meet base in its swizzled place, and
 // a warp stores four rows' 128 bytes in one instruction; pieces four at a time (one at a
 // time the shared-memory round trips took 2 of 57.5 us below).  2858 tokens of 12 adapters,
-// 17408 columns, rank 16: 35 of the call's 55.6 us, 5.7 TB/s with 200 MB of base and y.
+// 17408 columns, rank 16: 38 of the call's 56 us, 5.2 TB/s with 200 MB of base and y.
 template <int RP, bool TRANS>
 struct UpShape {
     static constexpr int kW = weight_bytes(RP, TRANS);
@@ -825,11 +826,12 @@ __device__ __forceinline__ long long count_units(const WgradArgs &p) {
 // sums ([rank][column], slot 0: the pair began before the run, slot 1: it goes on
 // after it) for wgrad_sum_kernel.
 //
-// What bounds it: the MMAs, at 142 cycles for 128 x 128 x 16 with the rows along M
-// (a stage of 32 tokens and 512 columns at rank 64: 1150 of the 1750 cycles that
-// its copies and they take together).  Two MMAs for the planes took 90 each, x or dy
-// as the MMA's 256 columns 375.  4096 tokens of 8192 and 8192 columns at rank 64: 33 us,
-// 4.1 TB/s of x and dy (dy from L2) besides a quarter of that in planes.
+// What bounds it: the MMAs, with the rows along M: 142 cycles for 128 x 128 x 16 (the
+// upper two planes at rank 64), 90 for 128 x 64 x 16 (the lowest plane; its MMAs are 6 of
+// the 42 us below).  x or dy as the MMA's 256 columns took 375; one MMA for all three
+// planes, whose sums leave room for slices of 256 columns only, 2 us more.  4096 tokens
+// of 8192 and 8192 columns at rank 64: 42 us behind g, 3.2 TB/s of x and dy (dy from L2)
+// besides three eighths of that in planes.
 template <int RP>
 __global__ void __launch_bounds__(kWgradThreads, 1) lora_wgrad_kernel(const WgradArgs p) {
     using S = WgradShape<RP>;
@@ -1017,8 +1019,8 @@ __global__ void __launch_bounds__(kWgradThreads, 1) lora_wgrad_kernel(const Wgra
 // n blocks of these CTAs each add a part, in CTA order; so a block has a part of
 // the pair its run began inside of and a part of the pair its run left unfinished.
 // All blocks clear the gradients of adapters without tokens.  Bound by latency and
-// L2: two tiles of sums per run at most (40 MB at rank 64), 5 us for 4096 tokens of
-// one adapter with 8192 and 8192 columns.
+// L2: two tiles of sums per run at most (40 MB at rank 64), 9 us behind dX for 4096
+// tokens of one adapter with 8192 and 8192 columns.
 constexpr int kWgradSumThreads = 512;
 
 template <int RP>

@@ -71,3 +71,47 @@ def test_smoke_takes_both_forms_of_the_adapters():
         assert _lib.lib().w4a16_lora_workspace_bytes(tokens, adapters, rank, 0, ctypes.byref(need)) == 0
         forms.append(need.value > 0)
     assert forms == [False, True]
+
+
+def kernel_parts(text, name):
+    """The names of the kernel's parameters, and its body."""
+    at = re.search(r"\b%s\(([^)]*)\)" % name, text[text.index("__global__"):])
+    names = [v.split()[-1].lstrip("*") for v in at.group(1).split(",")]
+    start = text.index("{", text.index("__global__") + at.end()) + 1
+    depth = 1
+    for j in range(start, len(text)):
+        depth += {"{": 1, "}": -1}.get(text[j], 0)
+        if depth == 0:
+            return names, text[start:j]
+    raise AssertionError("unbalanced braces")
+
+
+# kernel -> the kernel that may run right before it in a call (None: it comes first)
+CHAIN = {
+    "routing.cu": {"sort_count_kernel": None, "sort_rank_kernel": None, "dispatch_copy_kernel": "sort_rank_kernel",
+                   "dispatch_few_kernel": None, "combine_kernel": None, "combine_backward_kernel": None},
+    "lora.cu": {"lora_few_kernel": None},
+    "lora_tensor.cu": {"lora_down_kernel": "sort_rank_kernel", "lora_sum_kernel": "lora_down_kernel",
+                       "lora_up_kernel": "lora_sum_kernel", "lora_wgrad_kernel": "lora_sum_kernel",
+                       "wgrad_sum_kernel": "lora_up_kernel"}}
+
+
+def test_chained_kernels_wait_before_they_let_the_next_one_start():
+    """What a kernel reads before its own wait rests on its predecessor having waited
+    before letting it start; the two that let it start first are followed by kernels
+    that rely on the launch before those alone, which has to have waited."""
+    waits_first = {}
+    for name, kernels in CHAIN.items():
+        text = source(name)
+        assert len(re.findall(r"__global__", text)) == len(kernels)
+        for kernel, before in kernels.items():
+            names, body = kernel_parts(text, kernel)
+            wait, trigger = body.index("pdl_wait();"), body.index("pdl_launch_dependents();")
+            waits_first[kernel] = wait < trigger
+            if before is None:                           # no argument is looked at before the wait
+                assert not re.search(r"\b(%s)\b" % "|".join(names), body[:wait]), kernel
+    assert {k for k, first in waits_first.items() if not first} == {"lora_sum_kernel", "wgrad_sum_kernel"}
+    # the launch before the early one waits first
+    for early in ("lora_sum_kernel", "wgrad_sum_kernel"):
+        before = next(v[early] for v in CHAIN.values() if early in v)
+        assert waits_first[before]
