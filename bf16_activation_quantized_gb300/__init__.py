@@ -10,7 +10,9 @@ adapters (``lora_add``), with their gradients.
 Every function here only checks tensor metadata, allocates outputs and
 workspaces with torch, and calls the C ABI on the current torch stream: all
 arithmetic runs in the library's CUDA kernels.  There is no CPU path; a call
-with CPU tensors or without the built library raises.
+with CPU tensors or without the built library raises.  Nothing is recorded for
+autograd: results have no gradient function, whatever their inputs require, and a
+gradient is what the ``*_backward`` call of an operator returns.
 """
 from __future__ import annotations
 
@@ -489,7 +491,8 @@ def dispatch(x: torch.Tensor, ids: torch.Tensor, num_groups: int):
     slots int32 [T, k]): xs and m_sizes are what gemm_grouped takes; slots[t, j]
     is the row of xs that holds the copy, or ~row (negative) for a dropped slot,
     whose row lies past the groups and holds zeros.  The order is stable: inside
-    a group rows stand by token, then slot."""
+    a group rows stand by token, then slot.  Not recorded for autograd: xs's
+    gradient goes through dispatch_backward."""
     dev = _index_of(x, "x", torch.bfloat16)
     _need_on(dev, ids, "ids")
     if x.dim() != 2 or ids.dim() != 2 or ids.shape[0] != x.shape[0]:
@@ -543,7 +546,8 @@ def combine(ys: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor) -> tor
 
     ys: bf16 [T*k, N], rows in group order (the grouped product of dispatch's
     rows); slots: from dispatch; weights: float32 or bfloat16 [T, k].  fp32 sums,
-    rounded once; returns bf16 [T, N]."""
+    rounded once; returns bf16 [T, N].  Not recorded for autograd: the gradients are
+    combine_backward's."""
     if weights is None:
         raise ValueError("weights must be a CUDA tensor")
     return _combine(ys, slots, weights, "ys")
@@ -628,7 +632,8 @@ def lora_add(x: torch.Tensor, lora_a: torch.Tensor, lora_b: torch.Tensor, adapte
     the token as it is; lora_scales: float32 [L]; base: bf16 [T, N] (gemm's
     result) or None for zeros.  ``out`` may be base itself.  Returns y bf16
     [T, N], with ``return_hidden`` also A . x (float32 [T, r]), which
-    lora_add_backward takes."""
+    lora_add_backward takes.  Not recorded for autograd: the gradients are
+    lora_add_backward's."""
     dev, T, L, r, N, K = _need_lora(x, lora_a, lora_b, adapters, lora_scales)
     if base is not None:
         _need_rows(dev, base, "base", (T, N))

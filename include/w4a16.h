@@ -429,7 +429,9 @@ w4a16_status w4a16_combine_backward(const w4a16_bf16 *dY, const w4a16_bf16 *Ys, 
  *                (zeros without an adapter), kept for the gradient.
  *  workspace:    at least w4a16_lora_workspace_bytes(..., backward 0) bytes;
  *                contents need no initialisation.
- * The inner A . X stays in fp32; Y is rounded once.  rank: a multiple of 8, 8 to
+ * The inner A . X stays in fp32 and enters the second product with all of its bits; Y
+ * is rounded once.  An infinite element of X or lora_scales gives what the formula does;
+ * one of B (of A, in the gradient's dX) gives infinity or NaN.  rank: a multiple of 8, 8 to
  * 128 (W4A16_ERR_UNSUPPORTED otherwise); adapters of a smaller rank are padded
  * with zeros by the caller.  1 <= num_adapters <= 1024, K a positive multiple
  * of 128, N >= 1, 0 <= tokens <= 2^24.  X, A, B, hidden and workspace 16-byte

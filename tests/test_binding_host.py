@@ -34,3 +34,10 @@ def test_sizes_kept_for_calls_are_bounded():
         w4._lora_bytes(tokens, 4, 16, 1)
     for cached in (w4._sort_bytes, w4._lora_bytes):
         assert cached.cache_info().currsize <= 1024
+
+
+def test_the_operators_say_that_autograd_does_not_see_them():
+    for op, gradient in ((w4.dispatch, "dispatch_backward"), (w4.combine, "combine_backward"),
+                         (w4.lora_add, "lora_add_backward")):
+        assert "Not recorded for autograd" in op.__doc__ and gradient in op.__doc__
+    assert "autograd" in w4.__doc__
