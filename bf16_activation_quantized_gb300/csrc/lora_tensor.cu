@@ -976,8 +976,8 @@ __global__ void __launch_bounds__(kWgradThreads, 1) lora_wgrad_kernel(const Wgra
                     tc_ld_32x32b_x8(at, v);
                     tc_ld_32x32b_x8(at + RP, w);
                     tc_wait_ld();
-                    // an infinity of x or dy: in the upper plane's sum alone, the lower planes
-                    // have zeros (0 * inf) and either sign
+                    // an infinity of x or dy: the upper plane's sum has it, the lower planes may
+                    // hold zeros (0 * inf)
                     float f[8];
                     #pragma unroll
                     for (int e = 0; e < 8; ++e) {
