@@ -4,8 +4,9 @@
 codes per byte (low nibble = even k), one bf16 scale per G weights along K
 (G = 128, 64 or 32, read off the scales' shape [N, K/G]),
 ``dequant = scale * (code - 8)``, fp32 accumulation.  Beside the products: rows to the
-groups of the grouped product and back (``dispatch``, ``combine``) and low-rank
-adapters (``lora_add``), with their gradients.
+groups of the grouped product and back (``dispatch``, ``combine``), low-rank
+adapters (``lora_add``), and products with rows and weights in 8-bit floating point
+(``quantize_fp8``, ``gemm_fp8``, ``gemm_fp8_grouped``), with their gradients.
 
 Every function here only checks tensor metadata, allocates outputs and
 workspaces with torch, and calls the C ABI on the current torch stream: all
@@ -32,7 +33,7 @@ _ARMS = {None: ARM_AUTO, "auto": ARM_AUTO, "decode": ARM_DECODE, "tensor": ARM_T
 
 __all__ = ["GROUP", "pack", "gemm", "gemm_partials", "gemm_grouped", "gemm_batched", "plan_batched", "dequant_fp32", "dequant_bf16",
            "splitk_reduce", "dispatch", "dispatch_backward", "combine", "combine_backward",
-           "lora_add", "lora_add_backward", "plan", "packed_weight_bytes", "layout_version", "read_error_word",
+           "lora_add", "lora_add_backward", "quantize_fp8", "gemm_fp8", "gemm_fp8_grouped", "gemm_grouped_wgrad", "plan", "packed_weight_bytes", "layout_version", "read_error_word",
            "ERROR_WAIT_TIMEOUT", "W4A16Error"]
 
 
@@ -672,3 +673,146 @@ def lora_add_backward(dy: torch.Tensor, x: torch.Tensor, hidden: torch.Tensor, l
             None if dx_base is None else dx_base.data_ptr(), dx.data_ptr(), da.data_ptr(), db.data_ptr(),
             T, L, r, N, K, ws.data_ptr() if need else None, need)
     return dx, da, db
+
+
+FP8_BLOCK = 128              # elements of a row per scale; of weights 128 x 128
+_FP8 = torch.float8_e4m3fn
+
+
+def quantize_fp8(x: torch.Tensor, *, blocks: bool = False):
+    """(codes, scales): x in e4m3 with a float32 scale for 128 elements of a row, or,
+    with ``blocks``, for a block of 128 x 128: what the 8-bit products take as their
+    rows and as their weights.
+
+    x: bf16 [M, K], any K; codes float8_e4m3fn [M, Kp] with Kp = K rounded up to a
+    multiple of 128 and zeros past K; scales [Kp/128, M].  With ``blocks`` x is bf16
+    [N, K] or [G, N, K] (K a multiple of 128); codes have its shape and scales are
+    [N/128 rounded up, K/128], a leading G kept.  A scale is max |x| / 448, a code the
+    nearest e4m3 to 448 x / max |x| (ties to even); a block of zeros has scale 0."""
+    dev = _index_of(x, "x", torch.bfloat16)
+    if not blocks:
+        if x.dim() != 2 or x.shape[1] < 1:
+            raise ValueError("x must be [M, K]")
+        M, K = x.shape
+        _need_int32(M, K)
+        n = -(-K // FP8_BLOCK)
+        codes, scales = _empty((M, n * FP8_BLOCK), _FP8, dev), _empty((n, M), torch.float32, dev)
+        _launch("w4a16_quantize_fp8", dev, x.data_ptr(), codes.data_ptr(), scales.data_ptr(), M, K)
+        return codes, scales
+    if x.dim() not in (2, 3) or x.shape[-1] % FP8_BLOCK or 0 in x.shape:
+        raise ValueError("x must be [N, K] or [G, N, K], K a multiple of 128")
+    N, K = x.shape[-2:]
+    G = x.shape[0] if x.dim() == 3 else 1
+    _need_int32(G, N, K)
+    codes = _empty(x.shape, _FP8, dev)
+    scales = _empty((*x.shape[:-2], -(-N // FP8_BLOCK), K // FP8_BLOCK), torch.float32, dev)
+    _launch("w4a16_quantize_fp8_blocks", dev, x.data_ptr(), codes.data_ptr(), scales.data_ptr(), G, N, K)
+    return codes, scales
+
+
+def _need_fp8(x, x_scales, w, w_scales, dims, transposed):
+    """Checks of what the 8-bit products share: (device, M, N, K, output columns)."""
+    dev = _index_of(x, "x", _FP8)
+    _need_on(dev, x_scales, "x_scales", torch.float32)
+    _need_on(dev, w, "w", _FP8)
+    _need_on(dev, w_scales, "w_scales", torch.float32)
+    if x.dim() != 2 or w.dim() != dims:
+        raise ValueError(f"x must be [M, C] and w {'[N, K]' if dims == 2 else '[num_groups, N, K]'}")
+    N, K = w.shape[-2:]
+    M, C = x.shape
+    n = -(-N // FP8_BLOCK)
+    if K % FP8_BLOCK or C != (n * FP8_BLOCK if transposed else K):
+        raise ValueError("K must be a multiple of 128, and x [M, K] or, transposed, [M, N rounded up to one]")
+    if x_scales.shape != (C // FP8_BLOCK, M):
+        raise ValueError("x_scales must be float32 [C/128, M] for x [M, C]")
+    if w_scales.shape != (*w.shape[:-2], n, K // FP8_BLOCK):
+        raise ValueError("w_scales must be float32 [N/128 rounded up, K/128], by group as w is")
+    _need_int32(M, N, K)
+    return dev, M, N, K, K if transposed else N
+
+
+def gemm_fp8(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor, *,
+             transposed: bool = False, out: torch.Tensor | None = None,
+             resident_weights: bool = False) -> torch.Tensor:
+    """Y = X . W^T (bf16 [M, N]) of rows and weights in 8 bits, as quantize_fp8 gives
+    them: x [M, K] with x_scales [K/128, M], w [N, K] with w_scales of its blocks.
+
+    ``transposed=True`` multiplies by W instead, from the same weights: x is [M, N]
+    (N rounded up to a multiple of 128, the columns past N finite), the result bf16
+    [M, K]; with the quantised gradient of Y that is the gradient of X.  Sums over a
+    block of 128 are the tensor core's, over the blocks fp32; one rounding.
+    ``resident_weights`` as for gemm.  Not recorded for autograd."""
+    dev, M, N, K, cols = _need_fp8(x, x_scales, w, w_scales, 2, transposed)
+    if out is None:
+        out = _empty((M, cols), torch.bfloat16, dev)
+    else:
+        _need_rows(dev, out, "out", (M, cols))
+    _launch("w4a16_gemm_fp8", dev, x.data_ptr(), x_scales.data_ptr(), w.data_ptr(), w_scales.data_ptr(),
+            out.data_ptr(), M, N, K, 1 if transposed else 0, FLAG_RESIDENT_WEIGHTS if resident_weights else 0)
+    return out
+
+
+def _need_groups(dev, m_sizes, groups, status):
+    _need_on(dev, m_sizes, "m_sizes", torch.int32)
+    if m_sizes.shape != (groups,):
+        raise ValueError("m_sizes must be int32 [num_groups]")
+    if status is None:
+        return _empty(4, torch.int32, dev)
+    _need_on(dev, status, "status", torch.int32)
+    if status.numel() < 1:
+        raise ValueError("status must hold an int32")
+    return status
+
+
+def gemm_fp8_grouped(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
+                     m_sizes: torch.Tensor, *, transposed: bool = False, out: torch.Tensor | None = None,
+                     status: torch.Tensor | None = None):
+    """gemm_fp8 by group in one launch: group g owns m_sizes[g] rows of x, in order, and
+    w[g] of w [num_groups, N, K].
+
+    m_sizes: int32 [num_groups] on the device (dispatch's), never read on the host.  Rows
+    no group covers are left unwritten.  Returns (Y, status), status as gemm_grouped's.
+    ``transposed=True``: the gradient of the rows.  Not recorded for autograd."""
+    dev, M, N, K, cols = _need_fp8(x, x_scales, w, w_scales, 3, transposed)
+    status = _need_groups(dev, m_sizes, w.shape[0], status)
+    if out is None:
+        out = _empty((M, cols), torch.bfloat16, dev)
+    else:
+        _need_rows(dev, out, "out", (M, cols))
+    _launch("w4a16_gemm_fp8_grouped", dev, x.data_ptr(), x_scales.data_ptr(), w.data_ptr(), w_scales.data_ptr(),
+            m_sizes.data_ptr(), out.data_ptr(), w.shape[0], M, N, K, 1 if transposed else 0, status.data_ptr())
+    return out, status
+
+
+def gemm_grouped_wgrad(dy: torch.Tensor, x: torch.Tensor, m_sizes: torch.Tensor, *,
+                       dtype: torch.dtype = torch.float32, out: torch.Tensor | None = None,
+                       status: torch.Tensor | None = None):
+    """The gradients of the weights of a product by group: dw[g] = dy_g^T . x_g over the
+    rows of group g, zeros for a group without rows.
+
+    dy: bf16 [M, N]; x: bf16 [M, K]; m_sizes: int32 [num_groups] on the device; N and K
+    multiples of 8.  Returns (dw [num_groups, N, K] in ``dtype`` (float32 or bfloat16),
+    status as gemm_grouped's).  fp32 sums, rounded once; rows no group covers are not
+    summed."""
+    dev = _index_of(dy, "dy", torch.bfloat16)
+    _need_on(dev, x, "x", torch.bfloat16)
+    if dy.dim() != 2 or x.dim() != 2 or dy.shape[0] != x.shape[0]:
+        raise ValueError("dy must be [M, N] and x [M, K]")
+    M, N = dy.shape
+    K = x.shape[1]
+    if m_sizes is None or not isinstance(m_sizes, torch.Tensor) or m_sizes.dim() != 1:
+        raise ValueError("m_sizes must be int32 [num_groups]")
+    G = m_sizes.shape[0]
+    status = _need_groups(dev, m_sizes, G, status)
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"dtype must be float32 or bfloat16, got {dtype}")
+    if N % 8 or K % 8:
+        raise ValueError("N and K must be multiples of 8")
+    _need_int32(M, N, K, G)
+    if out is None:
+        out = _empty((G, N, K), dtype, dev)
+    else:
+        _need_rows(dev, out, "out", (G, N, K), dtype)
+    _launch("w4a16_gemm_grouped_wgrad", dev, dy.data_ptr(), x.data_ptr(), m_sizes.data_ptr(), out.data_ptr(),
+            out.element_size(), G, M, N, K, status.data_ptr())
+    return out, status

@@ -58,6 +58,11 @@ SIGNATURES = {
     "w4a16_combine_backward": (I, [P, P, P, P, I, P, P, I, I, I, P]),
     "w4a16_lora_workspace_bytes": (I, [I, I, I, I, ctypes.POINTER(SZ)]),
     "w4a16_lora_add": (I, [P, P, P, P, I, P, P, P, P, I, I, I, I, I, P, SZ, P]),
+    "w4a16_quantize_fp8": (I, [P, P, P, I, I, P]),
+    "w4a16_quantize_fp8_blocks": (I, [P, P, P, I, I, I, P]),
+    "w4a16_gemm_fp8": (I, [P, P, P, P, P, I, I, I, I, I, P]),
+    "w4a16_gemm_fp8_grouped": (I, [P, P, P, P, P, P, I, I, I, I, I, P, P]),
+    "w4a16_gemm_grouped_wgrad": (I, [P, P, P, P, I, I, I, I, I, P, P]),
     "w4a16_lora_add_backward": (I, [P, P, P, P, P, P, I, P, P, P, P, P, I, I, I, I, I, P, SZ, P]),
 }
 

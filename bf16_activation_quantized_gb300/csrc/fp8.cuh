@@ -1,0 +1,41 @@
+// fp8.cuh -- what the products in 8-bit floating point share: arguments and launchers.
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+namespace w4a16 {
+
+constexpr int kFp8Block = 128;       // elements of a row per scale; weights: 128 x 128
+
+struct Fp8Args {
+    const float *xs;         // [blocks][M]
+    const float *ws;         // [groups][ceil(N / 128)][K / 128]
+    uint16_t *y;             // [M][out]
+    const int32_t *m_sizes;  // nullptr: one group of M rows
+    int *status, *err;
+    long long ws_group;      // scales of a group's weights
+    int ws_tile, ws_block;   // from one output tile's scale to the next one's, from one summed block's
+    int M, out, blocks;      // rows, output columns, blocks of 128 that are summed over
+    int out_tiles, groups;
+    int bt;                  // rows of x per tile at most (a multiple of 16)
+    int stages;              // ring depth
+    int vec;                 // rows of y start on 16 bytes and hold a multiple of 8 columns
+    int resident;            // the weights may be read before the stream's previous kernel has ended
+};
+
+// How a product is cut: template size, rows of x per tile, CTAs that share a tile's sum
+// (a cluster), CTAs launched and per SM.
+struct Fp8Plan {
+    int size, bt, split, ctas, occupancy;
+};
+Fp8Plan fp8_plan(int M, int out, int blocks, int groups, bool grouped, int sms);
+
+cudaError_t launch_fp8_gemm(const Fp8Plan &p, Fp8Args a, const uint8_t *x, const uint8_t *w, int N, int K,
+                            bool trans, cudaStream_t s);
+cudaError_t launch_quantize_rows(const uint16_t *x, uint8_t *codes, float *scales, int rows, int width,
+                                 cudaStream_t s);
+cudaError_t launch_quantize_blocks(const uint16_t *w, uint8_t *codes, float *scales, int groups, int rows,
+                                   int width, cudaStream_t s);
+
+}  // namespace w4a16

@@ -1,0 +1,463 @@
+// fp8_gemm.cu -- products of e4m3 rows with e4m3 weights, a scale for 128 elements of a
+// row and for a block of 128 x 128 of the weights:
+//
+//   Y[m][n]  = sum_b xs[b][m] ws[n / 128][b] sum_{k in block b} X[m][k] W[n][k]
+//   dX[m][k] = sum_b ds[b][m] ws[b][k / 128] sum_{n in block b} dY[m][n] W[n][k]
+//
+// plain and by group, the second (TRANS) from the weights as they lie: a tile of W is
+// the same box of 128 x 128 bytes in both, whose rows are the tensor core's M in the
+// first and its K in the second.
+//
+// The weights are the MMA's A (M = 128 output columns), rows of x its N: any number of
+// them down to 16 makes a tile, so one kernel serves a single token and a long prefill
+// and a group's last tile multiplies what it holds.  A block's sum (4 MMAs of K = 32)
+// lands in one of several buffers of tensor memory; eight warps read it, multiply by
+// both scales and add in registers, in fp32, while the next block's MMAs run.
+//
+// Warps: 0 copies (TMA) the tiles, 1 issues the MMAs, 2 and 3 form the products of the
+// scales, 4 to 11 add.
+#include "async.cuh"
+#include "common.cuh"
+#include "fp8.cuh"
+#include "groups.cuh"
+#include "internal.h"
+#include "launch.cuh"
+#include "lora.cuh"
+#include "tc05.cuh"
+
+namespace w4a16 {
+
+namespace {
+
+constexpr int kFp8Threads = 384, kAddWarp0 = 4, kAddWarps = 8;
+constexpr int kWTile = kFp8Block * kFp8Block;      // bytes of a tile of W
+constexpr int kScaleSlots = 4;
+
+template <int BT>
+struct Fp8Shape {
+    static constexpr int kBufs = BT == 256 ? 2 : 4;            // blocks' sums in tensor memory
+    static constexpr int kTmem = kBufs * BT < 32 ? 32 : kBufs * BT;
+    static constexpr int kChunk = BT == 16 ? 8 : 16;           // columns a load from tensor memory brings
+    static constexpr int kChunks = BT / 2 / kChunk;            // per warp
+    static constexpr int kOccupancy = BT <= 64 ? 2 : 1;
+};
+// Registers a thread of the first four warps and of the adding ones with 256 rows of x:
+// the launch's (168 x 384) are what the two shares draw on.
+constexpr int kRegsIn = 72, kRegsAdd = 216;
+static_assert(128 * kRegsIn + 256 * kRegsAdd <= 168 * kFp8Threads, "registers");
+
+struct Fp8Smem {
+    int stage, off_scale, off_store, off_join, off_bar, off_tab, total;
+};
+// join: fp32 sums of a tile, from the CTAs that share it.
+__host__ __device__ inline Fp8Smem fp8_smem(int size, int bt, int stages, int split, int groups) {
+    Fp8Smem L;
+    L.stage = kWTile + bt * kFp8Block;
+    L.off_scale = stages * L.stage;
+    L.off_store = L.off_scale + kScaleSlots * size * 4;
+    L.off_join = L.off_store + kAddWarps * 32 * 16 * 2;
+    L.off_bar = L.off_join + (split > 1 ? size * kFp8Block * 4 : 0);
+    L.off_tab = L.off_bar + (2 * stages + 2 * 4 + 2 * kScaleSlots + 1) * 8 + 16;
+    L.total = (L.off_tab + 2 * (groups + 1) * 4 + 15) & ~15;
+    return L;
+}
+
+struct Fp8Tile {
+    int group, tile, row0, rows;      // output tile, first row of x, rows
+};
+
+// Output tiles fastest, so that CTAs that run together share rows of x.  A group's rows
+// are cut evenly, in steps of 16.
+__device__ __forceinline__ bool fp8_tile(const Fp8Args &a, const int *tab_rows, const int *tab_tiles, int id,
+                                         Fp8Tile &t) {
+    int first_row = 0, rows = a.M, r = id;
+    t.group = 0;
+    if (a.m_sizes) {
+        if (id >= tab_tiles[a.groups]) return false;
+        int lo = 0, hi = a.groups;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (tab_tiles[mid] <= id) lo = mid; else hi = mid;
+        }
+        t.group = lo;
+        r = id - tab_tiles[lo];
+        first_row = tab_rows[lo], rows = tab_rows[lo + 1] - first_row;
+    }
+    const int n = row_tiles(rows, a.bt), tt = r / a.out_tiles;
+    if (tt >= n) return false;
+    const int each = ((rows + n - 1) / n + 15) & ~15;
+    t.tile = r - tt * a.out_tiles;
+    t.row0 = first_row + tt * each;
+    t.rows = min(each, rows - tt * each);
+    return true;
+}
+
+// acc += v * s on two floats at once.
+__device__ __forceinline__ void fma2(unsigned long long &acc, uint32_t v0, uint32_t v1, float s0, float s1) {
+    asm("{\n\t.reg .b64 v, s;\n\tmov.b64 v, {%1, %2};\n\tmov.b64 s, {%3, %4};\n\t"
+        "fma.rn.f32x2 %0, v, s, %0;\n\t}"
+        : "+l"(acc) : "r"(v0), "r"(v1), "f"(s0), "f"(s1));
+}
+__device__ __forceinline__ float lower(unsigned long long v) { return __uint_as_float(uint32_t(v)); }
+__device__ __forceinline__ float upper(unsigned long long v) { return __uint_as_float(uint32_t(v >> 32)); }
+
+__device__ __forceinline__ void st_cluster(uint32_t addr, int rank, float v) {
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void load_sums(uint32_t addr, uint32_t (&v)[N]) {
+    if constexpr (N == 8) tc_ld_32x32b_x8(addr, v); else tc_ld_32x32b_x16(addr, v);
+}
+
+template <int BT, bool TRANS>
+__global__ void __launch_bounds__(kFp8Threads, Fp8Shape<BT>::kOccupancy)
+fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w,
+                const Fp8Args a) {
+    using S = Fp8Shape<BT>;
+    extern __shared__ unsigned char s_raw[];
+    unsigned char *smem = s_raw + (-smem_u32(s_raw) & 1023);
+    const int split = cluster_size(), part = cluster_rank();
+    const int NS = a.stages;
+    const Fp8Smem L = fp8_smem(BT, a.bt, NS, split, a.groups);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t ring = smem_u32(smem), full = smem_u32(smem + L.off_bar), empty = full + 8 * NS;
+    const uint32_t dfull = empty + 8 * NS, dempty = dfull + 8 * 4;
+    const uint32_t sfull = dempty + 8 * 4, sempty = sfull + 8 * kScaleSlots, drained = sempty + 8 * kScaleSlots;
+    float *scales = reinterpret_cast<float *>(smem + L.off_scale);
+    float *join = reinterpret_cast<float *>(smem + L.off_join);
+    int *tab_rows = reinterpret_cast<int *>(smem + L.off_tab), *tab_tiles = tab_rows + a.groups + 1;
+    __shared__ int s_abort;
+    __shared__ uint32_t s_tmem;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NS; ++i) mbar_init(full + 8 * i, 1), mbar_init(empty + 8 * i, 1);
+        for (int i = 0; i < 4; ++i) mbar_init(dfull + 8 * i, 1), mbar_init(dempty + 8 * i, kAddWarps);
+        for (int i = 0; i < kScaleSlots; ++i) mbar_init(sfull + 8 * i, 1), mbar_init(sempty + 8 * i, kAddWarps);
+        mbar_init(drained, 1);
+        s_abort = 0;
+        fence_barrier_init();
+    }
+    if (warp == 0 && lane == 0) tma_prefetch_desc(&tmap_x), tma_prefetch_desc(&tmap_w);
+    if (warp == 1) {
+        tc_alloc(smem_u32(&s_tmem), S::kTmem);
+        tc_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    volatile int *abort_flag = &s_abort;
+    if (split > 1) cluster_arrive();                     // this CTA runs: its shared memory may be written
+    const int b0 = int((long long)a.blocks * part / split), b1 = int((long long)a.blocks * (part + 1) / split);
+    const uint32_t stage_bytes = kWTile + a.bt * kFp8Block;
+
+    // Weights that nothing on the stream still writes: the first stages start at once.
+    int early = 0;
+    if (warp == 0 && a.resident && !a.m_sizes) {
+        const int tile = (int(blockIdx.x) / split) % a.out_tiles;
+        early = min(NS, b1 - b0);
+        if (elect_one())
+            for (int i = 0; i < early; ++i) {
+                const int b = (b0 + i) * kFp8Block, o = tile * kFp8Block;
+                mbar_arrive_expect_tx(full + 8 * i, stage_bytes);
+                tma_load_3d(ring + i * L.stage, &tmap_w, TRANS ? o : b, TRANS ? b : o, 0, full + 8 * i);
+            }
+        __syncwarp();
+    }
+    pdl_wait();
+    pdl_launch_dependents();
+    if (split > 1) cluster_wait();
+    if (a.m_sizes) {
+        if (warp == 1)
+            scan_groups(a.m_sizes, a.groups, a.M, a.bt, a.out_tiles, tab_rows, tab_tiles, blockIdx.x == 0 ? a.status : nullptr);
+        __syncthreads();
+    }
+    const int id0 = int(blockIdx.x) / split, step = int(gridDim.x) / split;
+    Fp8Tile t;
+
+    if (warp < kAddWarp0) {
+    if constexpr (BT == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIn));
+    if (warp == 0) {
+        int i = 0;
+        bool lost = false;
+        for (int id = id0; !lost && fp8_tile(a, tab_rows, tab_tiles, id, t); id += step)
+            for (int b = b0; b < b1; ++b, ++i) {
+                const int s = i % NS;
+                const bool ok = i < NS || mbar_wait(empty + 8 * s, (i / NS - 1) & 1, abort_flag, a.err);
+                lost = !__all_sync(0xffffffffu, ok);
+                if (lost) break;
+                if (elect_one()) {
+                    const uint32_t dst = ring + s * L.stage;
+                    if (i >= early) {
+                        mbar_arrive_expect_tx(full + 8 * s, stage_bytes);
+                        tma_load_3d(dst, &tmap_w, (TRANS ? t.tile : b) * kFp8Block, (TRANS ? b : t.tile) * kFp8Block,
+                                    t.group, full + 8 * s);
+                    }
+                    tma_load_2d(dst + kWTile, &tmap_x, b * kFp8Block, t.row0, full + 8 * s);
+                }
+                __syncwarp();
+            }
+        // Every copy lands before the CTA ends.
+        if (*abort_flag)
+            for (int u = i > NS ? i - NS : 0; u < i; ++u) drain_wait(full + 8 * (u % NS), (u / NS) & 1);
+    } else if (warp == 1) {
+        int i = 0;
+        bool lost = false;
+        for (int id = id0; !lost && fp8_tile(a, tab_rows, tab_tiles, id, t); id += step) {
+            const uint32_t idesc = tc_idesc_e4m3(kFp8Block, (t.rows + 15) & ~15) | (TRANS ? kTcAMajorM : 0u);
+            for (int b = b0; b < b1; ++b, ++i) {
+                const int s = i % NS, d = i % S::kBufs;
+                bool ok = mbar_wait(full + 8 * s, (i / NS) & 1, abort_flag, a.err);
+                ok = ok && (i < S::kBufs || mbar_wait(dempty + 8 * d, (i / S::kBufs - 1) & 1, abort_flag, a.err));
+                lost = !__all_sync(0xffffffffu, ok);
+                if (lost) break;
+                tc_fence_after();
+                const uint32_t ws = ring + s * L.stage;
+                const uint64_t dx = tc_sdesc_sw128(ws + kWTile);
+                const uint64_t dw = TRANS ? tc_sdesc_sw128_mn(ws, 1024) : tc_sdesc_sw128(ws);
+                if (elect_one()) {
+                    #pragma unroll
+                    for (int e = 0; e < 4; ++e)       // 32 of the block's 128: 32 bytes along rows, 4096 down them
+                        tc_mma_f8_ss(tmem + d * BT, dw + (TRANS ? 256 : 2) * e, dx + 2 * e, idesc, e > 0);
+                    tc_commit(empty + 8 * s);
+                    tc_commit(dfull + 8 * d);
+                }
+                __syncwarp();
+            }
+        }
+        if (elect_one()) tc_commit(drained);
+        __syncwarp();
+        drain_wait(drained, 0);
+    } else {
+        // Products of the scales, one block after the other: this warp every second one.  The
+        // values of its next block are loaded before it waits for the slot.
+        constexpr int kEach = BT < 32 ? 1 : BT / 32;
+        int i = 0;
+        bool lost = false;
+        for (int id = id0; !lost && fp8_tile(a, tab_rows, tab_tiles, id, t); id += step) {
+            const float *ws = a.ws + t.group * a.ws_group + (long long)t.tile * a.ws_tile;
+            auto load = [&](int b, float (&v)[kEach], float &w) {
+                w = b < b1 ? ws[(long long)b * a.ws_block] : 0.f;
+                #pragma unroll
+                for (int j = 0; j < kEach; ++j) {
+                    const int r = lane + 32 * j;
+                    v[j] = b < b1 && r < t.rows ? a.xs[(long long)b * a.M + t.row0 + r] : 0.f;
+                }
+            };
+            float v[kEach], w;
+            int b = b0 + ((warp ^ i) & 1);
+            load(b, v, w);
+            for (; b < b1; b += 2) {
+                float next[kEach], w_next;
+                load(b + 2, next, w_next);
+                const int k = i + b - b0, s = k % kScaleSlots;
+                const bool ok = k < kScaleSlots ||
+                                mbar_wait(sempty + 8 * s, (k / kScaleSlots - 1) & 1, abort_flag, a.err);
+                lost = !__all_sync(0xffffffffu, ok);
+                if (lost) break;
+                #pragma unroll
+                for (int j = 0; j < kEach; ++j)
+                    if (BT >= 32 || lane < BT) scales[s * BT + lane + 32 * j] = v[j] * w;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sfull + 8 * s);
+                #pragma unroll
+                for (int j = 0; j < kEach; ++j) v[j] = next[j];
+                w = w_next;
+            }
+            i += b1 - b0;
+        }
+    }
+    } else {
+        if constexpr (BT == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsAdd));
+        // Lane l of a warp holds output column 32 (warp % 4) + l of the tile, for half of
+        // its rows of x.
+        const int sub = warp % 4, half = (warp - kAddWarp0) / 4;
+        const uint32_t lanes = tmem + (uint32_t(32 * sub) << 16);
+        uint16_t *store = reinterpret_cast<uint16_t *>(smem + L.off_store) + (warp - kAddWarp0) * 32 * 16;
+        int i = 0;
+        bool lost = false;
+        for (int id = id0; fp8_tile(a, tab_rows, tab_tiles, id, t); id += step) {
+            const int c0 = half * ((((t.rows + 1) / 2) + S::kChunk - 1) / S::kChunk * S::kChunk);
+            const int left = (half ? t.rows : min(t.rows, (((t.rows + 1) / 2) + S::kChunk - 1) / S::kChunk * S::kChunk)) - c0;
+            unsigned long long acc[BT / 4];
+            #pragma unroll
+            for (int j = 0; j < BT / 4; ++j) acc[j] = 0;
+            for (int b = b0; b < b1 && !lost; ++b, ++i) {
+                const int s = i % kScaleSlots, d = i % S::kBufs;
+                const bool ok = mbar_wait(sfull + 8 * s, (i / kScaleSlots) & 1, abort_flag, a.err) &&
+                                mbar_wait(dfull + 8 * d, (i / S::kBufs) & 1, abort_flag, a.err);
+                lost = !__all_sync(0xffffffffu, ok);
+                if (lost) break;
+                tc_fence_after();
+                const float *sc = scales + s * BT + c0;
+                #pragma unroll
+                for (int c = 0; c < S::kChunks; ++c) {
+                    if (c * S::kChunk < left) {
+                        uint32_t v[S::kChunk];
+                        load_sums(lanes + d * BT + c0 + c * S::kChunk, v);
+                        tc_wait_ld_of(v);
+                        #pragma unroll
+                        for (int e = 0; e < S::kChunk; e += 4) {
+                            const float4 f = *reinterpret_cast<const float4 *>(sc + c * S::kChunk + e);
+                            fma2(acc[(c * S::kChunk + e) / 2], v[e], v[e + 1], f.x, f.y);
+                            fma2(acc[(c * S::kChunk + e) / 2 + 1], v[e + 2], v[e + 3], f.z, f.w);
+                        }
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(dempty + 8 * d), mbar_arrive(sempty + 8 * s);
+            }
+            // A wait that ran out: this tile and the CTA's later ones are NaN.
+            if (lost) {
+                #pragma unroll
+                for (int j = 0; j < BT / 4; ++j) acc[j] = 0x7fffffff7fffffffull;
+            }
+            if (BT <= 128 && split > 1) {
+                // The tile's rows of x are shared out: CTA r adds those from r * BT / split on.
+                const int each = BT / split;
+                #pragma unroll
+                for (int j = 0; j < BT / 2; ++j)
+                    if (j < left) {
+                        const int c = c0 + j, r = c / each;
+                        const float v = j & 1 ? upper(acc[j / 2]) : lower(acc[j / 2]);
+                        st_cluster(smem_u32(join + (part * each + c - r * each) * kFp8Block + 32 * sub + lane), r, v);
+                    }
+                break;                                   // a cluster has one tile
+            }
+            const int col = t.tile * kFp8Block + 32 * sub;
+            #pragma unroll
+            for (int c = 0; c < BT / 2; c += S::kChunk) {
+                if (c < left) {
+                    uint16_t *y = a.y + (long long)(t.row0 + c0 + c) * a.out + col;
+                    if (a.vec) {
+                        #pragma unroll
+                        for (int e = 0; e < S::kChunk; e += 2) {
+                            const uint32_t p = pack_bf16x2_rn(lower(acc[(c + e) / 2]), upper(acc[(c + e) / 2]));
+                            store[e * 32 + lane] = uint16_t(p);
+                            store[(e + 1) * 32 + lane] = uint16_t(p >> 16);
+                        }
+                        __syncwarp();
+                        #pragma unroll
+                        for (int k = 0; k < S::kChunk; k += 8) {
+                            const int e = k + lane / 4, q = 8 * (lane % 4);
+                            if (c + e < left && col + q < a.out)
+                                *reinterpret_cast<uint4 *>(y + (long long)e * a.out + q) =
+                                    *reinterpret_cast<const uint4 *>(store + e * 32 + q);
+                        }
+                    } else {
+                        #pragma unroll
+                        for (int e = 0; e < S::kChunk; ++e)
+                            if (c + e < left && col + lane < a.out)
+                                y[(long long)e * a.out + lane] =
+                                    f32_to_bf16_rn(e & 1 ? upper(acc[(c + e) / 2]) : lower(acc[(c + e) / 2]));
+                    }
+                }
+                __syncwarp();                            // tcgen05.ld takes the whole warp
+            }
+        }
+    }
+    if (split > 1) {
+        cluster_arrive();
+        cluster_wait();
+        if (warp >= kAddWarp0 && fp8_tile(a, tab_rows, tab_tiles, id0, t)) {
+            const int each = BT / split, c0 = part * each, n = min(each, t.rows - c0);
+            const int col0 = t.tile * kFp8Block, cols = min(kFp8Block, a.out - col0);
+            for (int i = threadIdx.x - 32 * kAddWarp0; i < n * (kFp8Block / 2); i += 32 * kAddWarps) {
+                const int r = i / (kFp8Block / 2), c = 2 * (i % (kFp8Block / 2));
+                float2 v = make_float2(0.f, 0.f);
+                for (int k = 0; k < split; ++k) {
+                    const float2 u = *reinterpret_cast<const float2 *>(join + (k * each + r) * kFp8Block + c);
+                    v.x += u.x, v.y += u.y;
+                }
+                uint16_t *y = a.y + (long long)(t.row0 + c0 + r) * a.out + col0 + c;
+                if (a.vec) {
+                    if (c < cols) *reinterpret_cast<uint32_t *>(y) = pack_bf16x2_rn(v.x, v.y);
+                } else {
+                    if (c < cols) y[0] = f32_to_bf16_rn(v.x);
+                    if (c + 1 < cols) y[1] = f32_to_bf16_rn(v.y);
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tc_dealloc(tmem, S::kTmem);
+}
+
+int ceil_div(long long x, long long y) { return int((x + y - 1) / y); }
+
+template <int BT, bool TRANS>
+cudaError_t launch_size(const Fp8Plan &p, const Fp8Args &a, const CUtensorMap &tx, const CUtensorMap &tw, size_t smem,
+                        cudaStream_t s) {
+    cudaError_t e = allow_smem<fp8_gemm_kernel<BT, TRANS>>(kTensorMaxSmem - 256);
+    if (e != cudaSuccess) return e;
+    return launch_chained(fp8_gemm_kernel<BT, TRANS>, dim3(p.ctas), kFp8Threads, smem, p.split, s, tx, tw, a);
+}
+
+template <int BT>
+cudaError_t launch_trans(const Fp8Plan &p, const Fp8Args &a, const CUtensorMap &tx, const CUtensorMap &tw, size_t smem,
+                         bool trans, cudaStream_t s) {
+    return trans ? launch_size<BT, true>(p, a, tx, tw, smem, s) : launch_size<BT, false>(p, a, tx, tw, smem, s);
+}
+
+}  // namespace
+
+Fp8Plan fp8_plan(int M, int out, int blocks, int groups, bool grouped, int sms) {
+    Fp8Plan p;
+    const int out_tiles = ceil_div(out, kFp8Block);
+    // Rows a group is expected to hold.
+    const int rows = grouped ? ceil_div(M, groups < M ? groups : M) : M;
+    p.size = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256;
+    p.occupancy = p.size <= 64 ? 2 : 1;
+    const int slots = p.occupancy * sms;
+    p.split = 1;
+    if (grouped) {
+        p.bt = p.size;
+        const long long tiles = (long long)out_tiles * (ceil_div(M, p.bt) + (groups < M ? groups : M));
+        p.ctas = int(tiles < slots ? tiles : slots);
+        return p;
+    }
+    const int n = ceil_div(rows, p.size);
+    p.bt = (ceil_div(rows, n) + 15) & ~15;
+    const long long tiles = (long long)out_tiles * n;
+    if (p.size <= 128)
+        while (p.split < 8 && tiles * p.split * 2 <= slots && blocks >= 4 * p.split) p.split *= 2;
+    p.ctas = int(p.split > 1 ? tiles * p.split : tiles < slots ? tiles : slots);
+    return p;
+}
+
+cudaError_t launch_fp8_gemm(const Fp8Plan &p, Fp8Args a, const uint8_t *x, const uint8_t *w, int N, int K, bool trans,
+                            cudaStream_t s) {
+    CUtensorMap tx, tw;
+    const cuuint64_t xdim[2] = {cuuint64_t(a.blocks) * kFp8Block, cuuint64_t(a.M)};
+    const cuuint64_t xstride[1] = {xdim[0]};
+    const cuuint32_t xbox[2] = {kFp8Block, cuuint32_t(p.bt)};
+    cudaError_t e = encode_tensor_map(&tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, x, xdim, xstride, xbox,
+                                      CU_TENSOR_MAP_SWIZZLE_128B);
+    if (e != cudaSuccess) return e;
+    const cuuint64_t wdim[3] = {cuuint64_t(K), cuuint64_t(N), cuuint64_t(a.groups)};
+    const cuuint64_t wstride[2] = {cuuint64_t(K), cuuint64_t(N) * K};
+    const cuuint32_t wbox[3] = {kFp8Block, kFp8Block, 1};
+    e = encode_tensor_map(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, w, wdim, wstride, wbox, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (e != cudaSuccess) return e;
+    a.bt = p.bt;
+    const int budget = (p.occupancy == 2 ? kSmemPerSm / 2 - kSmemReservedPerCta : kTensorMaxSmem) - 1024 - 256;
+    const int rest = fp8_smem(p.size, p.bt, 0, p.split, a.groups).total + 64 * 16;
+    a.stages = (budget - rest) / (kWTile + p.bt * kFp8Block);
+    if (a.stages > 16) a.stages = 16;
+    if (a.stages < 2) return cudaErrorInvalidValue;
+    const size_t smem = fp8_smem(p.size, p.bt, a.stages, p.split, a.groups).total + 1024;
+    switch (p.size) {
+        case 16: return launch_trans<16>(p, a, tx, tw, smem, trans, s);
+        case 32: return launch_trans<32>(p, a, tx, tw, smem, trans, s);
+        case 64: return launch_trans<64>(p, a, tx, tw, smem, trans, s);
+        case 128: return launch_trans<128>(p, a, tx, tw, smem, trans, s);
+        default: return launch_trans<256>(p, a, tx, tw, smem, trans, s);
+    }
+}
+
+}  // namespace w4a16

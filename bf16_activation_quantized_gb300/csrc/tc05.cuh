@@ -22,6 +22,12 @@ __host__ __device__ constexpr uint32_t tc_idesc_bf16(int M, int N) {
            | (uint32_t(M >> 4) << 24);     // M / 16
 }
 
+// Instruction descriptor of tcgen05.mma .kind::f8f6f4: fp32 accumulate, e4m3 A and
+// B (format 0), both K-major, shape M x N.
+__host__ __device__ constexpr uint32_t tc_idesc_e4m3(int M, int N) {
+    return (1u << 4) | (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
+}
+
 // Shared-memory matrix descriptor for a K-major operand stored with the
 // 128-byte swizzle: rows of 128 bytes, 8-row atoms of 1024 bytes (the layout a
 // SWIZZLE_128B TMA load of a 64-element bf16 box writes).  The tile must start
@@ -110,6 +116,16 @@ __device__ __forceinline__ void tc_mma_ss(uint32_t d_tmem, uint64_t a_desc, uint
         : "memory");
 }
 
+// The same on 8-bit operands: one step sums over 32 elements of K.
+__device__ __forceinline__ void tc_mma_f8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                             uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
 // Arrive once on an mbarrier when every tcgen05 operation this thread issued
 // before has completed.
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
@@ -148,6 +164,36 @@ __device__ __forceinline__ void tc_ld_32x32b_x32(uint32_t taddr, uint32_t (&v)[3
           "=r"(v[31])
         : "r"(taddr)
         : "memory");
+}
+
+// 32 lanes x 32 bits, 16 repetitions: thread i gets columns c .. c+15 of lane i.
+__device__ __forceinline__ void tc_ld_32x32b_x16(uint32_t taddr, uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+          "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]),
+          "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(taddr)
+        : "memory");
+}
+
+// tcgen05.wait::ld that the loaded registers pass through, so that no use of them is
+// scheduled before it.
+template <int N>
+__device__ __forceinline__ void tc_wait_ld_of(uint32_t (&v)[N]) {
+    static_assert(N == 8 || N == 16, "8 or 16 registers");
+    if constexpr (N == 8)
+        asm volatile("tcgen05.wait::ld.sync.aligned;"
+                     : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]),
+                       "+r"(v[6]), "+r"(v[7])
+                     :: "memory");
+    else
+        asm volatile("tcgen05.wait::ld.sync.aligned;"
+                     : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]),
+                       "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]),
+                       "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
+                     :: "memory");
 }
 
 // 32 lanes x 32 bits, 8 repetitions: thread i gets columns c .. c+7 of lane i.

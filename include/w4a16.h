@@ -464,6 +464,78 @@ w4a16_status w4a16_lora_add_backward(const w4a16_bf16 *dY, const w4a16_bf16 *X, 
                                      int num_adapters, int rank, int N, int K, void *workspace,
                                      size_t workspace_bytes, void *stream);
 
+/* Products in 8-bit floating point beside the 4-bit ones: rows and weights in e4m3
+ * with fp32 scales, one for 128 elements of a row of X and one for a block of
+ * 128 x 128 of W.  The pages have none; the calls are the library's own.
+ *
+ * w4a16_quantize_fp8: rows of X.  Block b of a row holds columns 128 b .. 128 b + 127:
+ *   scales[b][m] = max |x| / 448,   codes[m][c] = e4m3(448 x / max |x|),
+ * the nearest code of the exact quotient, ties to even.  A block of zeros has scale 0
+ * and codes 0; in one that holds a NaN all codes and the scale are NaN; an infinity
+ * gives scale infinity and the code NaN, finite elements beside it 0.  (Below about
+ * 2^-110 the scale is subnormal and holds fewer bits.)
+ *  X:      device bf16 [rows][width], any width >= 1 (at most 2^20).
+ *  codes:  device e4m3 [rows][Wp], Wp = width rounded up to a multiple of 128; the
+ *          columns past width are written as zeros.
+ *  scales: device fp32 [Wp / 128][rows]: the scales of a block of all rows stand
+ *          together.
+ * w4a16_quantize_fp8_blocks: num_groups weights [N][K] at once (K a multiple of 128):
+ * codes [num_groups][N][K], scales [num_groups][ceil(N / 128)][K / 128], a block's
+ * maximum taken over the rows it has.
+ * X 2-byte aligned (16-byte with a width that is a multiple of 8 is fastest), W and
+ * codes 16-byte, scales 4-byte.  0 <= rows <= 2^24. */
+w4a16_status w4a16_quantize_fp8(const w4a16_bf16 *X, uint8_t *codes, float *scales, int rows, int width,
+                                void *stream);
+w4a16_status w4a16_quantize_fp8_blocks(const w4a16_bf16 *W, uint8_t *codes, float *scales, int num_groups, int N,
+                                       int K, void *stream);
+
+/* transposed == 0:  Y[m][n] = sum_b x_scales[b][m] w_scales[n / 128][b] P_b,
+ *                   P_b = sum of X[m][k] W[n][k] over k in block b of K.
+ * transposed == 1:  Y[m][k] = sum_b x_scales[b][m] w_scales[b][k / 128] P_b,
+ *                   P_b = sum of X[m][n] W[n][k] over n in block b of N:
+ *                   with X the quantised gradient of the product's result, the
+ *                   gradient of its rows, from the weights as they lie.
+ * P_b is summed by the tensor core, the blocks in fp32 in a fixed order; Y is rounded
+ * once.
+ *  X:        device e4m3 [M][C], C = K, transposed: N rounded up to a multiple of 128
+ *            (the columns past N have to be finite: they meet zeros).
+ *  x_scales: device fp32 [C / 128][M].
+ *  W:        device e4m3 [N][K].   w_scales: device fp32 [ceil(N / 128)][K / 128].
+ *  Y:        device bf16 [M][N], transposed: [M][K]; overlaps nothing else.
+ *  flags:    0 or W4A16_FLAG_RESIDENT_WEIGHTS.
+ * K a positive multiple of 128, at most 2^20; 1 <= N <= 2^24 (transposed: 2^20),
+ * 0 <= M <= 2^24, M times the columns of Y at most 2^40.  X and W 16-byte aligned, the
+ * scales 4-byte, Y 2-byte; rows of Y that start on 16 bytes are written fastest. */
+w4a16_status w4a16_gemm_fp8(const uint8_t *X, const float *x_scales, const uint8_t *W, const float *w_scales,
+                            w4a16_bf16 *Y, int M, int N, int K, int transposed, int flags, void *stream);
+
+/* The same by group: group g owns M_sizes[g] rows of X and Y behind those of the groups
+ * before it, and block g of W [num_groups][N][K] and of w_scales.
+ *  M_sizes_dev: device int32 [num_groups], read only by the kernel.
+ *  status_dev:  device int32: as w4a16_gemm_grouped's status word (0: consistent; bit 0:
+ *               a negative size, which counts as 0; bit 1: the sizes sum past M_total,
+ *               rows at or past which are not computed).  Rows no group covers are left
+ *               unwritten.
+ * 1 <= num_groups <= 1024. */
+w4a16_status w4a16_gemm_fp8_grouped(const uint8_t *X, const float *x_scales, const uint8_t *W,
+                                    const float *w_scales, const int32_t *M_sizes_dev, w4a16_bf16 *Y,
+                                    int num_groups, int M_total, int N, int K, int transposed, int32_t *status_dev,
+                                    void *stream);
+
+/* The gradients of the weights of a product by group, from bf16 rows:
+ *   dW[g][n][k] = sum over g's rows t of dY[t][n] X[t][k],
+ * fp32 sums in a fixed order, rounded once; zeros for a group without rows.  Rows no
+ * group covers are never summed, whatever they hold.
+ *  dY: device bf16 [M_total][N].   X: device bf16 [M_total][K].
+ *  dW: device [num_groups][N][K], fp32 (dw_bytes 4) or bf16 (2), written fully.
+ *  M_sizes_dev, status_dev: as for w4a16_gemm_fp8_grouped.
+ * N and K multiples of 8 and dw_bytes 4 or 2 (W4A16_ERR_UNSUPPORTED otherwise);
+ * num_groups * N * K at most 2^40, N <= 2^24, K <= 2^20, 0 <= M_total <= 2^24.  dY, X and
+ * dW 16-byte aligned. */
+w4a16_status w4a16_gemm_grouped_wgrad(const w4a16_bf16 *dY, const w4a16_bf16 *X, const int32_t *M_sizes_dev,
+                                      void *dW, int dw_bytes, int num_groups, int M_total, int N, int K,
+                                      int32_t *status_dev, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,162 @@
+"""Argument checks of the 8-bit entry points and of the weights' gradients, on the host
+(no GPU), and what their sources and resources have to keep."""
+from __future__ import annotations
+
+import os
+import re
+
+import pytest
+
+from bf16_activation_quantized_gb300 import _lib
+from bf16_activation_quantized_gb300 import build as build_mod
+
+OK, INVALID, UNSUPPORTED = 0, 1, 2
+FAKE = 1 << 20    # aligned, never dereferenced on these paths
+
+
+@pytest.fixture(scope="module")
+def L():
+    build_mod.build()
+    return _lib.lib()
+
+
+def quantize(L, X=FAKE, c=FAKE, s=FAKE, rows=4, width=128):
+    return L.w4a16_quantize_fp8(X, c, s, rows, width, None)
+
+
+def quantize_blocks(L, W=FAKE, c=FAKE, s=FAKE, G=1, N=4, K=128):
+    return L.w4a16_quantize_fp8_blocks(W, c, s, G, N, K, None)
+
+
+def gemm(L, X=FAKE, xs=FAKE, W=FAKE, ws=FAKE, Y=FAKE, M=4, N=64, K=128, t=0, flags=0):
+    return L.w4a16_gemm_fp8(X, xs, W, ws, Y, M, N, K, t, flags, None)
+
+
+def grouped(L, X=FAKE, xs=FAKE, W=FAKE, ws=FAKE, sizes=FAKE, Y=FAKE, G=2, M=4, N=64, K=128, t=0, status=FAKE):
+    return L.w4a16_gemm_fp8_grouped(X, xs, W, ws, sizes, Y, G, M, N, K, t, status, None)
+
+
+def wgrad(L, dY=FAKE, X=FAKE, sizes=FAKE, dW=FAKE, b=4, G=2, M=4, N=64, K=128, status=FAKE):
+    return L.w4a16_gemm_grouped_wgrad(dY, X, sizes, dW, b, G, M, N, K, status, None)
+
+
+@pytest.mark.parametrize("bad", [dict(X=None), dict(c=None), dict(s=None), dict(X=FAKE + 1), dict(c=FAKE + 8),
+                                 dict(s=FAKE + 2), dict(rows=-1), dict(rows=(1 << 24) + 1), dict(width=0),
+                                 dict(width=(1 << 20) + 1)])
+def test_quantize_refuses(L, bad):
+    assert quantize(L, **bad) == INVALID
+
+
+@pytest.mark.parametrize("bad", [dict(W=None), dict(c=None), dict(s=None), dict(W=FAKE + 8), dict(c=FAKE + 8),
+                                 dict(s=FAKE + 2), dict(G=0), dict(G=1025), dict(N=0), dict(N=(1 << 24) + 1),
+                                 dict(K=0), dict(K=64), dict(K=200), dict(K=(1 << 20) + 128)])
+def test_quantize_blocks_refuses(L, bad):
+    assert quantize_blocks(L, **bad) == INVALID
+
+
+PRODUCT = [dict(X=None), dict(xs=None), dict(W=None), dict(ws=None), dict(Y=None), dict(X=FAKE + 8), dict(W=FAKE + 8),
+           dict(xs=FAKE + 2), dict(ws=FAKE + 2), dict(Y=FAKE + 1), dict(M=-1), dict(M=(1 << 24) + 1), dict(N=0),
+           dict(N=(1 << 24) + 1), dict(K=0), dict(K=64), dict(K=192), dict(K=(1 << 20) + 128),
+           dict(N=(1 << 20) + 1, t=1), dict(M=1 << 24, N=1 << 17)]
+
+
+@pytest.mark.parametrize("bad", PRODUCT + [dict(flags=2), dict(flags=-1)])
+def test_gemm_refuses(L, bad):
+    assert gemm(L, **bad) == INVALID
+
+
+@pytest.mark.parametrize("bad", PRODUCT + [dict(sizes=None), dict(status=None), dict(sizes=FAKE + 2),
+                                           dict(status=FAKE + 2), dict(G=0), dict(G=1025)])
+def test_grouped_refuses(L, bad):
+    assert grouped(L, **bad) == INVALID
+
+
+@pytest.mark.parametrize("bad", [dict(dY=None), dict(X=None), dict(sizes=None), dict(dW=None), dict(status=None),
+                                 dict(dY=FAKE + 8), dict(X=FAKE + 8), dict(dW=FAKE + 8), dict(sizes=FAKE + 2),
+                                 dict(status=FAKE + 2), dict(G=0), dict(G=1025), dict(M=-1), dict(M=(1 << 24) + 1),
+                                 dict(N=0), dict(K=0), dict(N=1 << 24, K=1 << 18)])
+def test_wgrad_refuses(L, bad):
+    assert wgrad(L, **bad) == INVALID
+
+
+@pytest.mark.parametrize("bad", [dict(b=8), dict(b=1), dict(N=68), dict(K=4)])
+def test_wgrad_unsupported(L, bad):
+    assert wgrad(L, **bad) == UNSUPPORTED
+
+
+def test_no_rows(L):
+    assert quantize(L, rows=0, X=None, c=None, s=None) == OK
+    assert gemm(L, M=0, X=None, xs=None, W=None, ws=None, Y=None) == OK
+
+
+def test_python_refuses():
+    import torch
+    import bf16_activation_quantized_gb300 as w4
+    f8 = torch.float8_e4m3fn
+    x, w = torch.zeros(2, 128).to(f8), torch.zeros(4, 128).to(f8)
+    xs, ws = torch.zeros(1, 2), torch.zeros(1, 1)
+    sizes = torch.zeros(1, dtype=torch.int32)
+    rows = torch.zeros(2, 128, dtype=torch.bfloat16)
+    for call in (lambda: w4.quantize_fp8(rows), lambda: w4.quantize_fp8(rows, blocks=True),
+                 lambda: w4.gemm_fp8(x, xs, w, ws), lambda: w4.gemm_fp8_grouped(x, xs, w[None], ws[None], sizes),
+                 lambda: w4.gemm_grouped_wgrad(rows, rows, sizes)):
+        with pytest.raises(ValueError):
+            call()
+    for op in (w4.gemm_fp8, w4.gemm_fp8_grouped):
+        assert "Not recorded for autograd" in op.__doc__
+
+
+# ------------------------------------------------------- sources and resources
+def source(name):
+    return re.sub(r"//[^\n]*", "", open(os.path.join(build_mod.CSRC, name)).read())
+
+
+@pytest.fixture(scope="module")
+def report():
+    build_mod.build()
+    path = os.path.join(build_mod.BUILD, "ptxas.log")
+    if not os.path.exists(path):
+        build_mod.build(force=True)
+    out, name = {}, None
+    for line in open(path).read().splitlines():
+        m = re.search(r"Compiling entry function '(\S+)'", line)
+        if m:
+            name = m.group(1)
+        elif name and "spill stores" in line:
+            out.setdefault(name, {})["spill"] = int(re.search(r"(\d+) bytes spill stores", line).group(1))
+        elif name and re.search(r"Used \d+ registers", line):
+            out.setdefault(name, {})["regs"] = int(re.search(r"Used (\d+) registers", line).group(1))
+            name = None
+    return out
+
+
+@pytest.mark.parametrize("kernel", ["quantize_rows_kernel", "quantize_blocks_kernel", "fp8_gemm_kernel",
+                                    "grouped_wgrad_kernel"])
+def test_no_spills(report, kernel):
+    hits = {k: v for k, v in report.items() if kernel in k}
+    assert hits
+    for name, r in hits.items():
+        assert r["spill"] == 0, name
+
+
+def test_register_shares_fit_the_launch(report):
+    """setmaxnreg waits until the block's registers at launch cover what it asks for: a share
+    above them would wait forever."""
+    text = source("fp8_gemm.cu")
+    threads = int(re.search(r"kFp8Threads = (\d+)", text).group(1))
+    few, more = (int(v) for v in re.search(r"kRegsIn = (\d+), kRegsAdd = (\d+)", text).groups())
+    hits = {k: v["regs"] for k, v in report.items() if "fp8_gemm_kernelILi256" in k}
+    assert hits
+    for name, regs in hits.items():
+        assert regs == 168, name
+        assert 128 * few + (threads - 128) * more <= regs * threads
+    assert text.count("setmaxnreg") == 2
+
+
+@pytest.mark.parametrize("name,kernels", [("fp8.cu", 2), ("fp8_gemm.cu", 1), ("wgrad.cu", 1)])
+def test_kernels_wait_before_they_let_the_next_one_start(name, kernels):
+    text = source(name)
+    starts = [m.start() for m in re.finditer(r"__global__", text)]
+    assert len(starts) == kernels
+    for at in starts:
+        assert 0 < text.index("pdl_wait();", at) < text.index("pdl_launch_dependents();", at)
