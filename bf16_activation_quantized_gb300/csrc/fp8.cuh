@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 namespace w4a16 {
@@ -17,21 +18,24 @@ struct Fp8Args {
     long long ws_group;      // scales of a group's weights
     int ws_tile, ws_block;   // from one output tile's scale to the next one's, from one summed block's
     int M, out, blocks;      // rows, output columns, blocks of 128 that are summed over
-    int out_tiles, groups;
+    int out_tiles, groups;   // tiles of 128 output columns (many rows: of 256)
     int bt;                  // rows of x per tile at most (a multiple of 16)
     int stages;              // ring depth
     int vec;                 // rows of y start on 16 bytes and hold a multiple of 8 columns
     int resident;            // the weights may be read before the stream's previous kernel has ended
 };
 
-// How a product is cut: template size, rows of x per tile, CTAs that share a tile's sum
-// (a cluster), CTAs launched and per SM.
+// How a product is cut.  size 16 to 128: the kernel for few rows, of that template size,
+// with bt rows of x per tile and `split` CTAs (a cluster) that share a tile's sum; 0: the
+// kernel for many rows, split 2: pairs of CTAs.  CTAs launched and per SM.
 struct Fp8Plan {
     int size, bt, split, ctas, occupancy;
 };
 Fp8Plan fp8_plan(int M, int out, int blocks, int groups, bool grouped, int sms);
 
 cudaError_t launch_fp8_gemm(const Fp8Plan &p, Fp8Args a, const uint8_t *x, const uint8_t *w, int N, int K,
+                            bool trans, cudaStream_t s);
+cudaError_t launch_fp8_many(const Fp8Plan &p, const Fp8Args &a, const CUtensorMap &tx, const CUtensorMap &tw,
                             bool trans, cudaStream_t s);
 cudaError_t launch_quantize_rows(const uint16_t *x, uint8_t *codes, float *scales, int rows, int width,
                                  cudaStream_t s);

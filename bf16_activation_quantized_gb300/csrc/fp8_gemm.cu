@@ -1,4 +1,4 @@
-// fp8_gemm.cu -- products of e4m3 rows with e4m3 weights, a scale for 128 elements of a
+// fp8_gemm.cu -- few rows: products of e4m3 rows with e4m3 weights, a scale for 128 elements of a
 // row and for a block of 128 x 128 of the weights:
 //
 //   Y[m][n]  = sum_b xs[b][m] ws[n / 128][b] sum_{k in block b} X[m][k] W[n][k]
@@ -35,16 +35,13 @@ constexpr int kScaleSlots = 4;
 
 template <int BT>
 struct Fp8Shape {
-    static constexpr int kBufs = BT == 256 ? 2 : 4;            // blocks' sums in tensor memory
+    static constexpr int kBufs = 4;            // blocks' sums in tensor memory
     static constexpr int kTmem = kBufs * BT < 32 ? 32 : kBufs * BT;
-    static constexpr int kChunk = BT == 16 ? 8 : 16;           // columns a load from tensor memory brings
+    static constexpr int kChunk = BT >= 128 ? 32 : BT >= 32 ? 16 : 8;    // columns a load from tensor memory brings
     static constexpr int kChunks = BT / 2 / kChunk;            // per warp
+    static constexpr int kLoads = 1;           // chunks in registers
     static constexpr int kOccupancy = BT <= 64 ? 2 : 1;
 };
-// Registers a thread of the first four warps and of the adding ones with 256 rows of x:
-// the launch's (168 x 384) are what the two shares draw on.
-constexpr int kRegsIn = 72, kRegsAdd = 216;
-static_assert(128 * kRegsIn + 256 * kRegsAdd <= 168 * kFp8Threads, "registers");
 
 struct Fp8Smem {
     int stage, off_scale, off_store, off_join, off_bar, off_tab, total;
@@ -109,7 +106,9 @@ __device__ __forceinline__ void st_cluster(uint32_t addr, int rank, float v) {
 
 template <int N>
 __device__ __forceinline__ void load_sums(uint32_t addr, uint32_t (&v)[N]) {
-    if constexpr (N == 8) tc_ld_32x32b_x8(addr, v); else tc_ld_32x32b_x16(addr, v);
+    if constexpr (N == 8) tc_ld_32x32b_x8(addr, v);
+    else if constexpr (N == 16) tc_ld_32x32b_x16(addr, v);
+    else tc_ld_32x32b_x32(addr, v);
 }
 
 template <int BT, bool TRANS>
@@ -177,8 +176,6 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
     const int id0 = int(blockIdx.x) / split, step = int(gridDim.x) / split;
     Fp8Tile t;
 
-    if (warp < kAddWarp0) {
-    if constexpr (BT == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIn));
     if (warp == 0) {
         int i = 0;
         bool lost = false;
@@ -230,7 +227,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
         if (elect_one()) tc_commit(drained);
         __syncwarp();
         drain_wait(drained, 0);
-    } else {
+    } else if (warp < kAddWarp0) {
         // Products of the scales, one block after the other: this warp every second one.  The
         // values of its next block are loaded before it waits for the slot.
         constexpr int kEach = BT < 32 ? 1 : BT / 32;
@@ -268,9 +265,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
             }
             i += b1 - b0;
         }
-    }
     } else {
-        if constexpr (BT == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsAdd));
         // Lane l of a warp holds output column 32 (warp % 4) + l of the tile, for half of
         // its rows of x.
         const int sub = warp % 4, half = (warp - kAddWarp0) / 4;
@@ -291,18 +286,23 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
                 lost = !__all_sync(0xffffffffu, ok);
                 if (lost) break;
                 tc_fence_after();
+                // A chunk's load is under way while the one before it is added.
                 const float *sc = scales + s * BT + c0;
+                uint32_t v[S::kLoads][S::kChunk];
+                if (S::kLoads == 2 && left > 0) load_sums(lanes + d * BT + c0, v[0]);
                 #pragma unroll
                 for (int c = 0; c < S::kChunks; ++c) {
                     if (c * S::kChunk < left) {
-                        uint32_t v[S::kChunk];
-                        load_sums(lanes + d * BT + c0 + c * S::kChunk, v);
-                        tc_wait_ld_of(v);
+                        uint32_t (&now)[S::kChunk] = v[c % S::kLoads];
+                        if (S::kLoads == 1) load_sums(lanes + d * BT + c0 + c * S::kChunk, now);
+                        tc_wait_ld_of(now);
+                        if (S::kLoads == 2 && c + 1 < S::kChunks && (c + 1) * S::kChunk < left)
+                            load_sums(lanes + d * BT + c0 + (c + 1) * S::kChunk, v[(c + 1) % S::kLoads]);
                         #pragma unroll
                         for (int e = 0; e < S::kChunk; e += 4) {
                             const float4 f = *reinterpret_cast<const float4 *>(sc + c * S::kChunk + e);
-                            fma2(acc[(c * S::kChunk + e) / 2], v[e], v[e + 1], f.x, f.y);
-                            fma2(acc[(c * S::kChunk + e) / 2 + 1], v[e + 2], v[e + 3], f.z, f.w);
+                            fma2(acc[(c * S::kChunk + e) / 2], now[e], now[e + 1], f.x, f.y);
+                            fma2(acc[(c * S::kChunk + e) / 2 + 1], now[e + 2], now[e + 3], f.z, f.w);
                         }
                     }
                 }
@@ -315,7 +315,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
                 #pragma unroll
                 for (int j = 0; j < BT / 4; ++j) acc[j] = 0x7fffffff7fffffffull;
             }
-            if (BT <= 128 && split > 1) {
+            if (split > 1) {
                 // The tile's rows of x are shared out: CTA r adds those from r * BT / split on.
                 const int each = BT / split;
                 #pragma unroll
@@ -328,20 +328,21 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
                 break;                                   // a cluster has one tile
             }
             const int col = t.tile * kFp8Block + 32 * sub;
+            constexpr int kStoreCols = BT == 16 ? 8 : 16;
             #pragma unroll
-            for (int c = 0; c < BT / 2; c += S::kChunk) {
+            for (int c = 0; c < BT / 2; c += kStoreCols) {
                 if (c < left) {
                     uint16_t *y = a.y + (long long)(t.row0 + c0 + c) * a.out + col;
                     if (a.vec) {
                         #pragma unroll
-                        for (int e = 0; e < S::kChunk; e += 2) {
+                        for (int e = 0; e < kStoreCols; e += 2) {
                             const uint32_t p = pack_bf16x2_rn(lower(acc[(c + e) / 2]), upper(acc[(c + e) / 2]));
                             store[e * 32 + lane] = uint16_t(p);
                             store[(e + 1) * 32 + lane] = uint16_t(p >> 16);
                         }
                         __syncwarp();
                         #pragma unroll
-                        for (int k = 0; k < S::kChunk; k += 8) {
+                        for (int k = 0; k < kStoreCols; k += 8) {
                             const int e = k + lane / 4, q = 8 * (lane % 4);
                             if (c + e < left && col + q < a.out)
                                 *reinterpret_cast<uint4 *>(y + (long long)e * a.out + q) =
@@ -349,7 +350,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
                         }
                     } else {
                         #pragma unroll
-                        for (int e = 0; e < S::kChunk; ++e)
+                        for (int e = 0; e < kStoreCols; ++e)
                             if (c + e < left && col + lane < a.out)
                                 y[(long long)e * a.out + lane] =
                                     f32_to_bf16_rn(e & 1 ? upper(acc[(c + e) / 2]) : lower(acc[(c + e) / 2]));
@@ -408,25 +409,32 @@ cudaError_t launch_trans(const Fp8Plan &p, const Fp8Args &a, const CUtensorMap &
 
 Fp8Plan fp8_plan(int M, int out, int blocks, int groups, bool grouped, int sms) {
     Fp8Plan p;
+    const int used = grouped && groups < M ? groups : grouped ? M : 1;      // groups with rows at most
+    const int rows = ceil_div(M, used);                                     // a group's, if they are even
+    p.split = 1;
+    if (rows > 128) {
+#ifdef V_SPLIT
+        p.split = V_SPLIT;
+#endif
+        const int out_tiles = ceil_div(out, 2 * kFp8Block);
+        p.size = 0, p.bt = 128, p.occupancy = 1;
+        const long long tiles = (long long)out_tiles * (ceil_div(M, 128 * p.split) + (grouped ? used : 0));
+        p.ctas = p.split * int(tiles < sms / p.split ? tiles : sms / p.split);
+        return p;
+    }
     const int out_tiles = ceil_div(out, kFp8Block);
-    // Rows a group is expected to hold.
-    const int rows = grouped ? ceil_div(M, groups < M ? groups : M) : M;
-    p.size = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256;
+    p.size = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
     p.occupancy = p.size <= 64 ? 2 : 1;
     const int slots = p.occupancy * sms;
-    p.split = 1;
     if (grouped) {
         p.bt = p.size;
-        const long long tiles = (long long)out_tiles * (ceil_div(M, p.bt) + (groups < M ? groups : M));
+        const long long tiles = (long long)out_tiles * (ceil_div(M, p.bt) + used);
         p.ctas = int(tiles < slots ? tiles : slots);
         return p;
     }
-    const int n = ceil_div(rows, p.size);
-    p.bt = (ceil_div(rows, n) + 15) & ~15;
-    const long long tiles = (long long)out_tiles * n;
-    if (p.size <= 128)
-        while (p.split < 8 && tiles * p.split * 2 <= slots && blocks >= 4 * p.split) p.split *= 2;
-    p.ctas = int(p.split > 1 ? tiles * p.split : tiles < slots ? tiles : slots);
+    p.bt = (rows + 15) & ~15;
+    while (p.split < 8 && out_tiles * p.split * 2 <= slots && blocks >= 4 * p.split) p.split *= 2;
+    p.ctas = p.split > 1 || out_tiles < slots ? out_tiles * p.split : slots;
     return p;
 }
 
@@ -445,6 +453,10 @@ cudaError_t launch_fp8_gemm(const Fp8Plan &p, Fp8Args a, const uint8_t *x, const
     e = encode_tensor_map(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, w, wdim, wstride, wbox, CU_TENSOR_MAP_SWIZZLE_128B);
     if (e != cudaSuccess) return e;
     a.bt = p.bt;
+    if (p.size == 0) {
+        a.out_tiles = ceil_div(a.out, 2 * kFp8Block);
+        return launch_fp8_many(p, a, tx, tw, trans, s);
+    }
     const int budget = (p.occupancy == 2 ? kSmemPerSm / 2 - kSmemReservedPerCta : kTensorMaxSmem) - 1024 - 256;
     const int rest = fp8_smem(p.size, p.bt, 0, p.split, a.groups).total + 64 * 16;
     a.stages = (budget - rest) / (kWTile + p.bt * kFp8Block);
@@ -455,8 +467,7 @@ cudaError_t launch_fp8_gemm(const Fp8Plan &p, Fp8Args a, const uint8_t *x, const
         case 16: return launch_trans<16>(p, a, tx, tw, smem, trans, s);
         case 32: return launch_trans<32>(p, a, tx, tw, smem, trans, s);
         case 64: return launch_trans<64>(p, a, tx, tw, smem, trans, s);
-        case 128: return launch_trans<128>(p, a, tx, tw, smem, trans, s);
-        default: return launch_trans<256>(p, a, tx, tw, smem, trans, s);
+        default: return launch_trans<128>(p, a, tx, tw, smem, trans, s);
     }
 }
 

@@ -1,0 +1,322 @@
+// fp8_many.cu -- many rows: the products of fp8_gemm.cu with the rows of x along M.
+//
+// A tile is 128 rows of x by 256 output columns.  A block's sum (4 MMAs of K = 32)
+// lands in one of two buffers of tensor memory; eight warps read it and add it to their
+// sums in registers, in fp32, while the next block's MMAs run.  A lane holds one row of
+// x and 128 columns of one block of the weights, so a block's scale is one number a
+// lane, the product of its row's and the weights'.
+//
+// PAIR: two CTAs share a tile of 256 rows; each loads its rows of x and half of the
+// weights, which the pair's MMAs (cta_group::2) read from both.  That halves what an SM
+// has to fetch of the weights.
+//
+// Warps: 0 copies (TMA) the tiles, 1 issues the MMAs, 4 to 11 add.
+#include "async.cuh"
+#include "common.cuh"
+#include "fp8.cuh"
+#include "groups.cuh"
+#include "internal.h"
+#include "launch.cuh"
+#include "lora.cuh"
+#include "tc05.cuh"
+
+namespace w4a16 {
+
+namespace {
+
+constexpr int kManyThreads = 384, kAddWarp0 = 4, kAddWarps = 8;
+// Registers a thread of the first four warps and of the adding ones: the launch's
+// (168 x 384) are what the two shares draw on.
+constexpr int kRegsIn = 72, kRegsAdd = 216;
+static_assert(128 * kRegsIn + 256 * kRegsAdd <= 168 * kManyThreads, "registers");
+
+constexpr int kRows = 128, kCols = 256;
+constexpr int kTile = kFp8Block * kFp8Block;       // bytes of 128 rows of x, of 128 columns' weights
+constexpr int kAhead = 4;                          // blocks whose scales are under way
+
+template <bool PAIR>
+struct ManyShape {
+    static constexpr int kStage = PAIR ? 2 * kTile : 3 * kTile;
+    static constexpr int kStages = PAIR ? 6 : 4;
+    static constexpr int kOffScale = kStages * kStage;
+    static constexpr int kOffStore = kOffScale + kAddWarps * kAhead * 32 * 8;
+    static constexpr int kOffBar = kOffStore + kAddWarps * 32 * 64;
+    static constexpr int kOffTab = kOffBar + (2 * kStages + 5) * 8 + 8;
+    static size_t smem(int groups, bool grouped) { return kOffTab + (grouped ? 2 * (groups + 1) * 4 : 0) + 1024; }
+};
+
+struct ManyTile {
+    int group, tile, row0, rows;                   // rows: of this CTA, none or negative past the group's end
+};
+template <bool PAIR>
+__device__ __forceinline__ bool many_tile(const Fp8Args &a, const int *tab_rows, const int *tab_tiles, int id, int part,
+                                          ManyTile &t) {
+    int first_row = 0, rows = a.M, r = id;
+    t.group = 0;
+    if (a.m_sizes) {
+        if (id >= tab_tiles[a.groups]) return false;
+        int lo = 0, hi = a.groups;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (tab_tiles[mid] <= id) lo = mid; else hi = mid;
+        }
+        t.group = lo;
+        r = id - tab_tiles[lo];
+        first_row = tab_rows[lo], rows = tab_rows[lo + 1] - first_row;
+    }
+    const int tt = r / a.out_tiles, at = tt * (PAIR ? 2 : 1) * kRows;
+    if (at >= rows) return false;
+    t.tile = r - tt * a.out_tiles;
+    t.row0 = first_row + at + part * kRows;
+    t.rows = min(kRows, rows - at - part * kRows);
+    return true;
+}
+
+template <int N>
+__device__ __forceinline__ void load_sums(uint32_t addr, uint32_t (&v)[N]) {
+    if constexpr (N == 16) tc_ld_32x32b_x16(addr, v); else tc_ld_32x32b_x32(addr, v);
+}
+
+// 4 bytes, or zero where !in (src is not read then).
+__device__ __forceinline__ void cp_async4z(uint32_t dst, const void *src, bool in) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+template <bool TRANS, bool PAIR>
+__global__ void __launch_bounds__(kManyThreads, 1)
+fp8_many_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w,
+                const Fp8Args a) {
+    using S = ManyShape<PAIR>;
+    constexpr int NS = S::kStages;
+    extern __shared__ unsigned char s_raw[];
+    unsigned char *smem = s_raw + (-smem_u32(s_raw) & 1023);
+    __shared__ int s_abort;
+    __shared__ uint32_t s_tmem;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, part = PAIR ? cluster_rank() : 0;
+    const uint32_t ring = smem_u32(smem), full = ring + S::kOffBar, empty = full + 8 * NS;
+    const uint32_t dfull = empty + 8 * NS, dempty = dfull + 16, drained = dempty + 16;
+    int *tab_rows = reinterpret_cast<int *>(smem + S::kOffTab), *tab_tiles = tab_rows + a.groups + 1;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NS; ++i) mbar_init(full + 8 * i, 1), mbar_init(empty + 8 * i, 1);
+        for (int i = 0; i < 2; ++i) mbar_init(dfull + 8 * i, 1), mbar_init(dempty + 8 * i, (PAIR ? 2 : 1) * kAddWarps);
+        mbar_init(drained, 1);
+        s_abort = 0;
+        fence_barrier_init();
+    }
+    if (warp == 0 && lane == 0) tma_prefetch_desc(&tmap_x), tma_prefetch_desc(&tmap_w);
+    if (warp == 1) {
+        if (PAIR) {
+            tc_alloc_pair(smem_u32(&s_tmem), 2 * kCols);
+        } else {
+            tc_alloc(smem_u32(&s_tmem), 2 * kCols);
+            tc_relinquish();
+        }
+    }
+    pdl_wait();
+    pdl_launch_dependents();
+    if (a.m_sizes && warp == 0)
+        scan_groups(a.m_sizes, a.groups, a.M, (PAIR ? 2 : 1) * kRows, a.out_tiles, tab_rows, tab_tiles,
+                    blockIdx.x == 0 ? a.status : nullptr);
+    tc_fence_before();
+    __syncthreads();
+    if (PAIR) cluster_arrive(), cluster_wait();          // the other CTA's barriers stand
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    volatile int *abort_flag = &s_abort;
+    const int id0 = PAIR ? blockIdx.x / 2 : blockIdx.x, step = PAIR ? gridDim.x / 2 : gridDim.x;
+    ManyTile t;
+    if (warp < kAddWarp0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIn));
+        bool lost = false;
+        int i = 0;
+        if (warp == 0) {
+            for (int id = id0; !lost && many_tile<PAIR>(a, tab_rows, tab_tiles, id, part, t); id += step)
+                for (int b = 0; b < a.blocks; ++b, ++i) {
+                    const int s = i % NS;
+                    const bool ok = i < NS || mbar_wait(empty + 8 * s, (i / NS - 1) & 1, abort_flag, a.err);
+                    lost = !__all_sync(0xffffffffu, ok);
+                    if (lost) break;
+                    if (elect_one()) {
+                        const uint32_t dst = ring + s * S::kStage;
+                        const int at = b * kFp8Block, col = t.tile * kCols + part * kFp8Block;
+                        if (PAIR) {
+                            const uint32_t bar = cluster_address(full + 8 * s, 0);
+                            if (part == 0) mbar_arrive_expect_tx(full + 8 * s, 2 * S::kStage);
+                            tma_load_2d_pair(dst, &tmap_x, at, t.row0, bar);
+                            tma_load_3d_pair(dst + kTile, &tmap_w, TRANS ? col : at, TRANS ? at : col, t.group, bar);
+                        } else {
+                            mbar_arrive_expect_tx(full + 8 * s, S::kStage);
+                            tma_load_2d(dst, &tmap_x, at, t.row0, full + 8 * s);
+                            for (int h = 0; h < 2; ++h) {
+                                const int c = col + h * kFp8Block;
+                                tma_load_3d(dst + (1 + h) * kTile, &tmap_w, TRANS ? c : at, TRANS ? at : c, t.group, full + 8 * s);
+                            }
+                        }
+                    }
+                    __syncwarp();
+                }
+            // Every copy lands before the CTA ends (a pair's are counted in its even CTA).
+            if (*abort_flag && part == 0)
+                for (int u = i > NS ? i - NS : 0; u < i; ++u) drain_wait(full + 8 * (u % NS), (u / NS) & 1);
+        } else if (warp == 1 && part == 0) {
+            constexpr uint32_t idesc = tc_idesc_e4m3((PAIR ? 2 : 1) * kRows, kCols) | (TRANS ? kTcBMajorN : 0u);
+            for (int id = id0; !lost && many_tile<PAIR>(a, tab_rows, tab_tiles, id, part, t); id += step)
+                for (int b = 0; b < a.blocks; ++b, ++i) {
+                    const int s = i % NS, d = i & 1;
+                    const bool ok = mbar_wait(full + 8 * s, (i / NS) & 1, abort_flag, a.err) &&
+                                    (i < 2 || mbar_wait(dempty + 8 * d, (i / 2 - 1) & 1, abort_flag, a.err));
+                    lost = !__all_sync(0xffffffffu, ok);
+                    if (lost) break;
+                    tc_fence_after();
+                    const uint32_t xs = ring + s * S::kStage;
+                    const uint64_t dx = tc_sdesc_sw128(xs);
+                    const uint64_t dw = TRANS ? tc_sdesc_sw128_mn(xs + kTile, kTile) : tc_sdesc_sw128(xs + kTile);
+                    if (elect_one()) {
+                        #pragma unroll
+                        for (int e = 0; e < 4; ++e) {     // 32 of the block's 128: 32 bytes along rows, 4096 down them
+                            const uint64_t de = dw + (TRANS ? 256 : 2) * e;
+                            if (PAIR) tc_mma_f8_ss_pair(tmem + d * kCols, dx + 2 * e, de, idesc, e > 0);
+                            else tc_mma_f8_ss(tmem + d * kCols, dx + 2 * e, de, idesc, e > 0);
+                        }
+                        if (PAIR) tc_commit_pair(empty + 8 * s), tc_commit_pair(dfull + 8 * d);
+                        else tc_commit(empty + 8 * s), tc_commit(dfull + 8 * d);
+                    }
+                    __syncwarp();
+                }
+            if (elect_one()) {
+                if (PAIR) tc_commit_pair(drained);
+                else tc_commit(drained);
+            }
+            __syncwarp();
+            drain_wait(drained, 0);
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsAdd));
+        const int sub = warp % 4, half = (warp - kAddWarp0) / 4;
+        const uint32_t from = tmem + (uint32_t(32 * sub) << 16) + half * kFp8Block;
+        const uint32_t done = PAIR ? cluster_address(dempty, 0) : dempty;
+        // This lane's scales of kAhead blocks: x's and the weights'.
+        float2 *scales = reinterpret_cast<float2 *>(smem + S::kOffScale) + (warp - kAddWarp0) * kAhead * 32 + lane;
+        unsigned char *store = smem + S::kOffStore + (warp - kAddWarp0) * 32 * 64;
+        int i = 0;
+        bool lost = false;
+        for (int id = id0; many_tile<PAIR>(a, tab_rows, tab_tiles, id, part, t); id += step) {
+            const int row = 32 * sub + lane, wt = 2 * t.tile + half, col0 = wt * kFp8Block;
+            const float *xs = a.xs + t.row0 + row;
+            const float *ws = a.ws + t.group * a.ws_group + (long long)wt * a.ws_tile;
+            const bool in = row < t.rows, in_w = col0 < a.out;
+            auto fetch = [&](int b) {
+                if (b < a.blocks) {
+                    const uint32_t dst = smem_u32(scales + (b % kAhead) * 32);
+                    cp_async4z(dst, in ? xs + (long long)b * a.M : a.xs, in);
+                    cp_async4z(dst + 4, in_w ? ws + (long long)b * a.ws_block : a.ws, in_w);
+                }
+                cp_async_commit();
+            };
+            #pragma unroll
+            for (int b = 0; b < kAhead - 1; ++b) fetch(b);
+            float acc[kFp8Block];
+            #pragma unroll
+            for (int j = 0; j < kFp8Block; ++j) acc[j] = 0.f;
+            for (int b = 0; b < a.blocks && !lost; ++b, ++i) {
+                const int d = i & 1;
+                fetch(b + kAhead - 1);
+                cp_async_wait<kAhead - 1>();
+                const float2 f = scales[(b % kAhead) * 32];
+                const float scale = f.x * f.y;
+                lost = !__all_sync(0xffffffffu, mbar_wait(dfull + 8 * d, (i / 2) & 1, abort_flag, a.err));
+                if (lost) break;
+                tc_fence_after();
+                // A chunk's load is under way while the one before it is added.
+                constexpr int kChunk = 16, kChunks = kFp8Block / kChunk;
+                uint32_t v[2][kChunk];
+                load_sums(from + d * kCols, v[0]);
+                #pragma unroll
+                for (int c = 0; c < kChunks; ++c) {
+                    tc_wait_ld_of(v[c & 1]);
+                    if (c + 1 < kChunks) {
+                        load_sums(from + d * kCols + kChunk * (c + 1), v[(c + 1) & 1]);
+                    } else {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (PAIR) mbar_arrive_cluster(done + 8 * d);
+                            else mbar_arrive(done + 8 * d);
+                        }
+                    }
+                    #pragma unroll
+                    for (int e = 0; e < kChunk; ++e)
+                        acc[kChunk * c + e] = fmaf(__uint_as_float(v[c & 1][e]), scale, acc[kChunk * c + e]);
+                }
+            }
+            // A wait that ran out: this tile and the CTA's later ones are NaN.
+            if (lost) {
+                #pragma unroll
+                for (int j = 0; j < kFp8Block; ++j) acc[j] = __int_as_float(0x7fffffff);
+            }
+            // 32 rows and 32 columns at a time through shared memory (16-byte pieces placed so
+            // that eight rows' meet in no bank).
+            #pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int col = col0 + 32 * c;
+                #pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t p[4];
+                    #pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        p[j] = pack_bf16x2_rn(acc[32 * c + 8 * q + 2 * j], acc[32 * c + 8 * q + 2 * j + 1]);
+                    *reinterpret_cast<uint4 *>(store + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) =
+                        make_uint4(p[0], p[1], p[2], p[3]);
+                }
+                __syncwarp();
+                uint16_t *y = a.y + (long long)(t.row0 + 32 * sub) * a.out + col;
+                const int left = t.rows - 32 * sub;
+                if (a.vec) {
+                    #pragma unroll
+                    for (int k = 0; k < 32; k += 8) {
+                        const int r = k + lane / 4, q = lane % 4;
+                        if (r < left && col + 8 * q < a.out)
+                            *reinterpret_cast<uint4 *>(y + (long long)r * a.out + 8 * q) =
+                                *reinterpret_cast<const uint4 *>(store + r * 64 + ((q ^ ((r >> 1) & 3)) << 4));
+                    }
+                } else if (col + lane < a.out) {
+                    for (int r = 0; r < min(left, 32); ++r)
+                        y[(long long)r * a.out + lane] = *reinterpret_cast<const uint16_t *>(
+                            store + r * 64 + (((lane / 8) ^ ((r >> 1) & 3)) << 4) + 2 * (lane % 8));
+                }
+                __syncwarp();                            // tcgen05.ld takes the whole warp
+            }
+        }
+        cp_async_wait<0>();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (PAIR) cluster_arrive(), cluster_wait();          // the pair's MMAs have read both CTAs' memory
+    tc_fence_after();
+    if (warp == 1) {
+        if (PAIR) tc_dealloc_pair(tmem, 2 * kCols);
+        else tc_dealloc(tmem, 2 * kCols);
+    }
+}
+
+template <bool TRANS, bool PAIR>
+cudaError_t launch_many_form(const Fp8Plan &p, const Fp8Args &a, const CUtensorMap &tx, const CUtensorMap &tw,
+                             cudaStream_t s) {
+    const cudaError_t e = allow_smem<fp8_many_kernel<TRANS, PAIR>>(kTensorMaxSmem - 256);
+    if (e != cudaSuccess) return e;
+    return launch_chained(fp8_many_kernel<TRANS, PAIR>, dim3(p.ctas), kManyThreads,
+                          ManyShape<PAIR>::smem(a.groups, a.m_sizes != nullptr), PAIR ? 2 : 1, s, tx, tw, a);
+}
+
+}  // namespace
+
+cudaError_t launch_fp8_many(const Fp8Plan &p, const Fp8Args &a, const CUtensorMap &tx, const CUtensorMap &tw,
+                            bool trans, cudaStream_t s) {
+    if (p.split == 2) return trans ? launch_many_form<true, true>(p, a, tx, tw, s) : launch_many_form<false, true>(p, a, tx, tw, s);
+    return trans ? launch_many_form<true, false>(p, a, tx, tw, s) : launch_many_form<false, false>(p, a, tx, tw, s);
+}
+
+}  // namespace w4a16

@@ -130,7 +130,7 @@ def report():
     return out
 
 
-@pytest.mark.parametrize("kernel", ["quantize_rows_kernel", "quantize_blocks_kernel", "fp8_gemm_kernel",
+@pytest.mark.parametrize("kernel", ["quantize_rows_kernel", "quantize_blocks_kernel", "fp8_gemm_kernel", "fp8_many_kernel",
                                     "grouped_wgrad_kernel"])
 def test_no_spills(report, kernel):
     hits = {k: v for k, v in report.items() if kernel in k}
@@ -142,10 +142,10 @@ def test_no_spills(report, kernel):
 def test_register_shares_fit_the_launch(report):
     """setmaxnreg waits until the block's registers at launch cover what it asks for: a share
     above them would wait forever."""
-    text = source("fp8_gemm.cu")
-    threads = int(re.search(r"kFp8Threads = (\d+)", text).group(1))
+    text = source("fp8_many.cu")
+    threads = int(re.search(r"kManyThreads = (\d+)", text).group(1))
     few, more = (int(v) for v in re.search(r"kRegsIn = (\d+), kRegsAdd = (\d+)", text).groups())
-    hits = {k: v["regs"] for k, v in report.items() if "fp8_gemm_kernelILi256" in k}
+    hits = {k: v["regs"] for k, v in report.items() if "fp8_many_kernel" in k}
     assert hits
     for name, regs in hits.items():
         assert regs == 168, name
@@ -153,7 +153,7 @@ def test_register_shares_fit_the_launch(report):
     assert text.count("setmaxnreg") == 2
 
 
-@pytest.mark.parametrize("name,kernels", [("fp8.cu", 2), ("fp8_gemm.cu", 1), ("wgrad.cu", 1)])
+@pytest.mark.parametrize("name,kernels", [("fp8.cu", 2), ("fp8_gemm.cu", 1), ("fp8_many.cu", 1), ("wgrad.cu", 1)])
 def test_kernels_wait_before_they_let_the_next_one_start(name, kernels):
     text = source(name)
     starts = [m.start() for m in re.finditer(r"__global__", text)]
