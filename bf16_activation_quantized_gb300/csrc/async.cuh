@@ -191,6 +191,12 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *tmap, int 
         : "memory");
 }
 
+// Bring the box to L2 (see bulk_prefetch_l2).
+__device__ __forceinline__ void tma_prefetch_3d(const void *tmap, int x, int y, int z) {
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global [%0, {%1, %2, %3}];" ::"l"(tmap), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+
 // The same loads into this CTA's shared memory, counted on a barrier of either CTA of
 // its pair (`bar`: an address of the cluster's shared memory).
 __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void *tmap, int x, int y, uint32_t bar) {
@@ -214,9 +220,11 @@ __device__ __forceinline__ uint32_t cluster_address(uint32_t a, int rank) {
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
     return r;
 }
-// Arrive on a barrier of another CTA (`bar` from cluster_address).
+// Arrive on a barrier of another CTA (`bar` from cluster_address).  Orders no writes of
+// this thread to memory for the other CTA (that takes a release at the cluster's scope,
+// a fence of about a microsecond): what it hands over is tensor memory it has read.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // 3-D tiled TMA store of a box (parts past the tensor's ends are left out); the issuing

@@ -31,30 +31,27 @@ namespace {
 
 constexpr int kFp8Threads = 384, kAddWarp0 = 4, kAddWarps = 8;
 constexpr int kWTile = kFp8Block * kFp8Block;      // bytes of a tile of W
-constexpr int kScaleSlots = 4;
+constexpr int kSlots = 4;                          // blocks whose sums and scales are held
+constexpr int kAhead = 4;                          // blocks whose scales a warp fetches ahead
 
 template <int BT>
 struct Fp8Shape {
-    static constexpr int kBufs = 4;            // blocks' sums in tensor memory
-    static constexpr int kTmem = kBufs * BT < 32 ? 32 : kBufs * BT;
-    static constexpr int kChunk = BT >= 128 ? 32 : BT >= 32 ? 16 : 8;    // columns a load from tensor memory brings
+    static constexpr int kTmem = kSlots * BT;
+    static constexpr int kChunk = BT >= 32 ? 16 : 8;    // columns a load from tensor memory brings
     static constexpr int kChunks = BT / 2 / kChunk;            // per warp
-    static constexpr int kLoads = 1;           // chunks in registers
     static constexpr int kOccupancy = BT <= 64 ? 2 : 1;
 };
 
 struct Fp8Smem {
-    int stage, off_scale, off_store, off_join, off_bar, off_tab, total;
+    int stage, off_scale, off_store, off_bar, off_tab, total;
 };
-// join: fp32 sums of a tile, from the CTAs that share it.
-__host__ __device__ inline Fp8Smem fp8_smem(int size, int bt, int stages, int split, int groups) {
+__host__ __device__ inline Fp8Smem fp8_smem(int size, int bt, int stages, int groups) {
     Fp8Smem L;
     L.stage = kWTile + bt * kFp8Block;
     L.off_scale = stages * L.stage;
-    L.off_store = L.off_scale + kScaleSlots * size * 4;
-    L.off_join = L.off_store + kAddWarps * 32 * 16 * 2;
-    L.off_bar = L.off_join + (split > 1 ? size * kFp8Block * 4 : 0);
-    L.off_tab = L.off_bar + (2 * stages + 2 * 4 + 2 * kScaleSlots + 1) * 8 + 16;
+    L.off_store = L.off_scale + kSlots * size * 4;
+    L.off_bar = L.off_store + kAddWarps * 32 * 16 * 2;
+    L.off_tab = L.off_bar + (2 * stages + 2 * kSlots + 1) * 8 + 16;
     L.total = (L.off_tab + 2 * (groups + 1) * 4 + 15) & ~15;
     return L;
 }
@@ -89,19 +86,18 @@ __device__ __forceinline__ bool fp8_tile(const Fp8Args &a, const int *tab_rows, 
     return true;
 }
 
-// acc += v * s on two floats at once.
-__device__ __forceinline__ void fma2(unsigned long long &acc, uint32_t v0, uint32_t v1, float s0, float s1) {
-    asm("{\n\t.reg .b64 v, s;\n\tmov.b64 v, {%1, %2};\n\tmov.b64 s, {%3, %4};\n\t"
-        "fma.rn.f32x2 %0, v, s, %0;\n\t}"
-        : "+l"(acc) : "r"(v0), "r"(v1), "f"(s0), "f"(s1));
+// volatile: issued where it is written, so that a value fetched ahead is not fetched next
+// to its use.
+__device__ __forceinline__ float fetch(const float *p) {
+    float v;
+    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+    return v;
 }
-__device__ __forceinline__ float lower(unsigned long long v) { return __uint_as_float(uint32_t(v)); }
-__device__ __forceinline__ float upper(unsigned long long v) { return __uint_as_float(uint32_t(v >> 32)); }
 
-__device__ __forceinline__ void st_cluster(uint32_t addr, int rank, float v) {
-    uint32_t a;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
+__device__ __forceinline__ int ld_cluster1(const int *p, int rank) {
+    int v;
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(cluster_address(smem_u32(p), rank)) : "memory");
+    return v;
 }
 
 template <int N>
@@ -120,20 +116,21 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
     unsigned char *smem = s_raw + (-smem_u32(s_raw) & 1023);
     const int split = cluster_size(), part = cluster_rank();
     const int NS = a.stages;
-    const Fp8Smem L = fp8_smem(BT, a.bt, NS, split, a.groups);
+    const Fp8Smem L = fp8_smem(BT, a.bt, NS, a.groups);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t ring = smem_u32(smem), full = smem_u32(smem + L.off_bar), empty = full + 8 * NS;
-    const uint32_t dfull = empty + 8 * NS, dempty = dfull + 8 * 4;
-    const uint32_t sfull = dempty + 8 * 4, sempty = sfull + 8 * kScaleSlots, drained = sempty + 8 * kScaleSlots;
+    const uint32_t dfull = empty + 8 * NS, dempty = dfull + 8 * kSlots, drained = dempty + 8 * kSlots;
     float *scales = reinterpret_cast<float *>(smem + L.off_scale);
-    float *join = reinterpret_cast<float *>(smem + L.off_join);
+    // fp32 sums of a tile that several CTAs share, over the ring: whoever has waited for a
+    // tile's last MMAs finds its copies landed and read.
+    float *join = reinterpret_cast<float *>(smem);
     int *tab_rows = reinterpret_cast<int *>(smem + L.off_tab), *tab_tiles = tab_rows + a.groups + 1;
     __shared__ int s_abort;
     __shared__ uint32_t s_tmem;
     if (threadIdx.x == 0) {
         for (int i = 0; i < NS; ++i) mbar_init(full + 8 * i, 1), mbar_init(empty + 8 * i, 1);
-        for (int i = 0; i < 4; ++i) mbar_init(dfull + 8 * i, 1), mbar_init(dempty + 8 * i, kAddWarps);
-        for (int i = 0; i < kScaleSlots; ++i) mbar_init(sfull + 8 * i, 1), mbar_init(sempty + 8 * i, kAddWarps);
+        for (int i = 0; i < kSlots; ++i)                   // full: the MMAs' end and the scales
+            mbar_init(dfull + 8 * i, 2), mbar_init(dempty + 8 * i, kAddWarps);
         mbar_init(drained, 1);
         s_abort = 0;
         fence_barrier_init();
@@ -148,26 +145,29 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
     tc_fence_after();
     const uint32_t tmem = s_tmem;
     volatile int *abort_flag = &s_abort;
-    if (split > 1) cluster_arrive();                     // this CTA runs: its shared memory may be written
     const int b0 = int((long long)a.blocks * part / split), b1 = int((long long)a.blocks * (part + 1) / split);
     const uint32_t stage_bytes = kWTile + a.bt * kFp8Block;
 
-    // Weights that nothing on the stream still writes: the first stages start at once.
+    // The first stages of weights that nothing on the stream still writes start at once;
+    // others are brought to L2, where a later write replaces them.
     int early = 0;
-    if (warp == 0 && a.resident && !a.m_sizes) {
-        const int tile = (int(blockIdx.x) / split) % a.out_tiles;
-        early = min(NS, b1 - b0);
+    if (warp == 0 && !a.m_sizes) {
+        const int tile = (int(blockIdx.x) / split) % a.out_tiles, n = min(NS, b1 - b0);
+        early = a.resident ? n : 0;
         if (elect_one())
-            for (int i = 0; i < early; ++i) {
-                const int b = (b0 + i) * kFp8Block, o = tile * kFp8Block;
-                mbar_arrive_expect_tx(full + 8 * i, stage_bytes);
-                tma_load_3d(ring + i * L.stage, &tmap_w, TRANS ? o : b, TRANS ? b : o, 0, full + 8 * i);
+            for (int i = 0; i < n; ++i) {
+                const int b = (b0 + i) * kFp8Block, o = tile * kFp8Block, x = TRANS ? o : b, y = TRANS ? b : o;
+                if (a.resident) {
+                    mbar_arrive_expect_tx(full + 8 * i, stage_bytes);
+                    tma_load_3d(ring + i * L.stage, &tmap_w, x, y, 0, full + 8 * i);
+                } else {
+                    tma_prefetch_3d(&tmap_w, x, y, 0);
+                }
             }
         __syncwarp();
     }
     pdl_wait();
     pdl_launch_dependents();
-    if (split > 1) cluster_wait();
     if (a.m_sizes) {
         if (warp == 1)
             scan_groups(a.m_sizes, a.groups, a.M, a.bt, a.out_tiles, tab_rows, tab_tiles, blockIdx.x == 0 ? a.status : nullptr);
@@ -177,12 +177,12 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
     Fp8Tile t;
 
     if (warp == 0) {
-        int i = 0;
+        int i = 0, s = 0;
+        uint32_t phase = 1;                              // of the slot's release (first lap: none)
         bool lost = false;
         for (int id = id0; !lost && fp8_tile(a, tab_rows, tab_tiles, id, t); id += step)
             for (int b = b0; b < b1; ++b, ++i) {
-                const int s = i % NS;
-                const bool ok = i < NS || mbar_wait(empty + 8 * s, (i / NS - 1) & 1, abort_flag, a.err);
+                const bool ok = i < NS || mbar_wait(empty + 8 * s, phase, abort_flag, a.err);
                 lost = !__all_sync(0xffffffffu, ok);
                 if (lost) break;
                 if (elect_one()) {
@@ -195,19 +195,22 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
                     tma_load_2d(dst + kWTile, &tmap_x, b * kFp8Block, t.row0, full + 8 * s);
                 }
                 __syncwarp();
+                if (++s == NS) s = 0, phase ^= 1;
             }
         // Every copy lands before the CTA ends.
         if (*abort_flag)
             for (int u = i > NS ? i - NS : 0; u < i; ++u) drain_wait(full + 8 * (u % NS), (u / NS) & 1);
     } else if (warp == 1) {
-        int i = 0;
+        // The slot is a counter: a division by the ring's depth would cost more than a block's MMAs.
+        int i = 0, s = 0;
+        uint32_t phase = 0;
         bool lost = false;
         for (int id = id0; !lost && fp8_tile(a, tab_rows, tab_tiles, id, t); id += step) {
             const uint32_t idesc = tc_idesc_e4m3(kFp8Block, (t.rows + 15) & ~15) | (TRANS ? kTcAMajorM : 0u);
             for (int b = b0; b < b1; ++b, ++i) {
-                const int s = i % NS, d = i % S::kBufs;
-                bool ok = mbar_wait(full + 8 * s, (i / NS) & 1, abort_flag, a.err);
-                ok = ok && (i < S::kBufs || mbar_wait(dempty + 8 * d, (i / S::kBufs - 1) & 1, abort_flag, a.err));
+                const int d = i % kSlots;
+                bool ok = mbar_wait(full + 8 * s, phase, abort_flag, a.err);
+                ok = ok && (i < kSlots || mbar_wait(dempty + 8 * d, (i / kSlots - 1) & 1, abort_flag, a.err));
                 lost = !__all_sync(0xffffffffu, ok);
                 if (lost) break;
                 tc_fence_after();
@@ -222,46 +225,52 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
                     tc_commit(dfull + 8 * d);
                 }
                 __syncwarp();
+                if (++s == NS) s = 0, phase ^= 1;
             }
         }
         if (elect_one()) tc_commit(drained);
         __syncwarp();
         drain_wait(drained, 0);
     } else if (warp < kAddWarp0) {
-        // Products of the scales, one block after the other: this warp every second one.  The
-        // values of its next block are loaded before it waits for the slot.
+        // Products of the scales, one block after the other: this warp every second one, fetched
+        // kAhead of its blocks before their use.
         constexpr int kEach = BT < 32 ? 1 : BT / 32;
         int i = 0;
         bool lost = false;
         for (int id = id0; !lost && fp8_tile(a, tab_rows, tab_tiles, id, t); id += step) {
-            const float *ws = a.ws + t.group * a.ws_group + (long long)t.tile * a.ws_tile;
-            auto load = [&](int b, float (&v)[kEach], float &w) {
-                w = b < b1 ? ws[(long long)b * a.ws_block] : 0.f;
+            const int first = b0 + ((warp ^ i) & 1);
+            const float *ws = a.ws + t.group * a.ws_group + (long long)t.tile * a.ws_tile + (long long)first * a.ws_block;
+            const float *xs = a.xs + (long long)first * a.M + t.row0;
+            int r[kEach];
+            #pragma unroll
+            for (int j = 0; j < kEach; ++j) r[j] = min(lane + 32 * j, t.rows - 1);   // no row's scale: never used
+            float v[kAhead][kEach], w[kAhead];
+            auto load = [&](int u) {
+                w[u] = fetch(ws);
                 #pragma unroll
-                for (int j = 0; j < kEach; ++j) {
-                    const int r = lane + 32 * j;
-                    v[j] = b < b1 && r < t.rows ? a.xs[(long long)b * a.M + t.row0 + r] : 0.f;
-                }
+                for (int j = 0; j < kEach; ++j) v[u][j] = fetch(xs + r[j]);
             };
-            float v[kEach], w;
-            int b = b0 + ((warp ^ i) & 1);
-            load(b, v, w);
-            for (; b < b1; b += 2) {
-                float next[kEach], w_next;
-                load(b + 2, next, w_next);
-                const int k = i + b - b0, s = k % kScaleSlots;
-                const bool ok = k < kScaleSlots ||
-                                mbar_wait(sempty + 8 * s, (k / kScaleSlots - 1) & 1, abort_flag, a.err);
-                lost = !__all_sync(0xffffffffu, ok);
-                if (lost) break;
+            #pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                if (first + 2 * u < b1) load(u);
+                ws += 2 * a.ws_block, xs += 2LL * a.M;
+            }
+            for (int b = first; b < b1 && !lost; b += 2 * kAhead) {
                 #pragma unroll
-                for (int j = 0; j < kEach; ++j)
-                    if (BT >= 32 || lane < BT) scales[s * BT + lane + 32 * j] = v[j] * w;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(sfull + 8 * s);
-                #pragma unroll
-                for (int j = 0; j < kEach; ++j) v[j] = next[j];
-                w = w_next;
+                for (int u = 0; u < kAhead; ++u) {
+                    if (b + 2 * u >= b1) break;
+                    const int k = i + b + 2 * u - b0, s = k % kSlots;
+                    const bool ok = k < kSlots || mbar_wait(dempty + 8 * s, (k / kSlots - 1) & 1, abort_flag, a.err);
+                    lost = !__all_sync(0xffffffffu, ok);
+                    if (lost) break;
+                    #pragma unroll
+                    for (int j = 0; j < kEach; ++j)
+                        if (BT >= 32 || lane < BT) scales[s * BT + lane + 32 * j] = v[u][j] * w[u];
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(dfull + 8 * s);
+                    if (b + 2 * (u + kAhead) < b1) load(u);
+                    ws += 2 * a.ws_block, xs += 2LL * a.M;
+                }
             }
             i += b1 - b0;
         }
@@ -276,56 +285,46 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
         for (int id = id0; fp8_tile(a, tab_rows, tab_tiles, id, t); id += step) {
             const int c0 = half * ((((t.rows + 1) / 2) + S::kChunk - 1) / S::kChunk * S::kChunk);
             const int left = (half ? t.rows : min(t.rows, (((t.rows + 1) / 2) + S::kChunk - 1) / S::kChunk * S::kChunk)) - c0;
-            unsigned long long acc[BT / 4];
+            float acc[BT / 2];
             #pragma unroll
-            for (int j = 0; j < BT / 4; ++j) acc[j] = 0;
+            for (int j = 0; j < BT / 2; ++j) acc[j] = 0.f;
             for (int b = b0; b < b1 && !lost; ++b, ++i) {
-                const int s = i % kScaleSlots, d = i % S::kBufs;
-                const bool ok = mbar_wait(sfull + 8 * s, (i / kScaleSlots) & 1, abort_flag, a.err) &&
-                                mbar_wait(dfull + 8 * d, (i / S::kBufs) & 1, abort_flag, a.err);
-                lost = !__all_sync(0xffffffffu, ok);
+                const int d = i % kSlots;
+                lost = !__all_sync(0xffffffffu, mbar_wait(dfull + 8 * d, (i / kSlots) & 1, abort_flag, a.err));
                 if (lost) break;
                 tc_fence_after();
-                // A chunk's load is under way while the one before it is added.
-                const float *sc = scales + s * BT + c0;
-                uint32_t v[S::kLoads][S::kChunk];
-                if (S::kLoads == 2 && left > 0) load_sums(lanes + d * BT + c0, v[0]);
+                const float *sc = scales + d * BT + c0;
                 #pragma unroll
                 for (int c = 0; c < S::kChunks; ++c) {
                     if (c * S::kChunk < left) {
-                        uint32_t (&now)[S::kChunk] = v[c % S::kLoads];
-                        if (S::kLoads == 1) load_sums(lanes + d * BT + c0 + c * S::kChunk, now);
-                        tc_wait_ld_of(now);
-                        if (S::kLoads == 2 && c + 1 < S::kChunks && (c + 1) * S::kChunk < left)
-                            load_sums(lanes + d * BT + c0 + (c + 1) * S::kChunk, v[(c + 1) % S::kLoads]);
+                        uint32_t v[S::kChunk];
+                        load_sums(lanes + d * BT + c0 + c * S::kChunk, v);
+                        tc_wait_ld_of(v);
                         #pragma unroll
                         for (int e = 0; e < S::kChunk; e += 4) {
                             const float4 f = *reinterpret_cast<const float4 *>(sc + c * S::kChunk + e);
-                            fma2(acc[(c * S::kChunk + e) / 2], now[e], now[e + 1], f.x, f.y);
-                            fma2(acc[(c * S::kChunk + e) / 2 + 1], now[e + 2], now[e + 3], f.z, f.w);
+                            float *s = acc + c * S::kChunk + e;
+                            s[0] = fmaf(__uint_as_float(v[e]), f.x, s[0]);
+                            s[1] = fmaf(__uint_as_float(v[e + 1]), f.y, s[1]);
+                            s[2] = fmaf(__uint_as_float(v[e + 2]), f.z, s[2]);
+                            s[3] = fmaf(__uint_as_float(v[e + 3]), f.w, s[3]);
                         }
                     }
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(dempty + 8 * d), mbar_arrive(sempty + 8 * s);
+                if (lane == 0) mbar_arrive(dempty + 8 * d);
             }
             // A wait that ran out: this tile and the CTA's later ones are NaN.
             if (lost) {
                 #pragma unroll
-                for (int j = 0; j < BT / 4; ++j) acc[j] = 0x7fffffff7fffffffull;
+                for (int j = 0; j < BT / 2; ++j) acc[j] = __int_as_float(0x7fffffff);
             }
-            if (split > 1) {
-                // The tile's rows of x are shared out: CTA r adds those from r * BT / split on.
-                const int each = BT / split;
+            if (split > 1) {                             // a cluster has one tile
                 #pragma unroll
                 for (int j = 0; j < BT / 2; ++j)
-                    if (j < left) {
-                        const int c = c0 + j, r = c / each;
-                        const float v = j & 1 ? upper(acc[j / 2]) : lower(acc[j / 2]);
-                        st_cluster(smem_u32(join + (part * each + c - r * each) * kFp8Block + 32 * sub + lane), r, v);
-                    }
-                break;                                   // a cluster has one tile
+                    if (j < left) join[(c0 + j) * kFp8Block + 32 * sub + lane] = acc[j];
+                break;
             }
             const int col = t.tile * kFp8Block + 32 * sub;
             constexpr int kStoreCols = BT == 16 ? 8 : 16;
@@ -336,7 +335,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
                     if (a.vec) {
                         #pragma unroll
                         for (int e = 0; e < kStoreCols; e += 2) {
-                            const uint32_t p = pack_bf16x2_rn(lower(acc[(c + e) / 2]), upper(acc[(c + e) / 2]));
+                            const uint32_t p = pack_bf16x2_rn(acc[c + e], acc[c + e + 1]);
                             store[e * 32 + lane] = uint16_t(p);
                             store[(e + 1) * 32 + lane] = uint16_t(p >> 16);
                         }
@@ -353,7 +352,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
                         for (int e = 0; e < kStoreCols; ++e)
                             if (c + e < left && col + lane < a.out)
                                 y[(long long)e * a.out + lane] =
-                                    f32_to_bf16_rn(e & 1 ? upper(acc[(c + e) / 2]) : lower(acc[(c + e) / 2]));
+                                    f32_to_bf16_rn(acc[c + e]);
                     }
                 }
                 __syncwarp();                            // tcgen05.ld takes the whole warp
@@ -361,27 +360,38 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
         }
     }
     if (split > 1) {
+        // The tile's rows of x are shared out: this CTA adds the parts of rows part, part +
+        // split, ..., a warp a row, four columns a lane, in the order of the CTAs.
         cluster_arrive();
         cluster_wait();
-        if (warp >= kAddWarp0 && fp8_tile(a, tab_rows, tab_tiles, id0, t)) {
-            const int each = BT / split, c0 = part * each, n = min(each, t.rows - c0);
-            const int col0 = t.tile * kFp8Block, cols = min(kFp8Block, a.out - col0);
-            for (int i = threadIdx.x - 32 * kAddWarp0; i < n * (kFp8Block / 2); i += 32 * kAddWarps) {
-                const int r = i / (kFp8Block / 2), c = 2 * (i % (kFp8Block / 2));
-                float2 v = make_float2(0.f, 0.f);
-                for (int k = 0; k < split; ++k) {
-                    const float2 u = *reinterpret_cast<const float2 *>(join + (k * each + r) * kFp8Block + c);
-                    v.x += u.x, v.y += u.y;
-                }
-                uint16_t *y = a.y + (long long)(t.row0 + c0 + r) * a.out + col0 + c;
+        if (fp8_tile(a, tab_rows, tab_tiles, id0, t)) {
+            // Where a wait ran out, copies may have landed on the sums.
+            bool lost = false;
+            for (int k = 0; k < split; ++k) lost = lost || ld_cluster1(&s_abort, k) != 0;
+            const int col0 = t.tile * kFp8Block + 4 * lane, cols = a.out - col0;
+            for (int r = part + split * warp; r < t.rows; r += split * (kFp8Threads / 32)) {
+                float4 v[kMaxCluster];
+                #pragma unroll
+                for (int k = 0; k < kMaxCluster; ++k)
+                    if (k < split) v[k] = ld_cluster4(join + r * kFp8Block + 4 * lane, k);
+                #pragma unroll
+                for (int k = 1; k < kMaxCluster; ++k)
+                    if (k < split) v[0].x += v[k].x, v[0].y += v[k].y, v[0].z += v[k].z, v[0].w += v[k].w;
+                if (lost) v[0].x = v[0].y = v[0].z = v[0].w = __int_as_float(0x7fffffff);
+                uint16_t *y = a.y + (long long)(t.row0 + r) * a.out + col0;
+                const uint32_t lo = pack_bf16x2_rn(v[0].x, v[0].y), hi = pack_bf16x2_rn(v[0].z, v[0].w);
                 if (a.vec) {
-                    if (c < cols) *reinterpret_cast<uint32_t *>(y) = pack_bf16x2_rn(v.x, v.y);
+                    if (cols > 0) *reinterpret_cast<uint2 *>(y) = make_uint2(lo, hi);
                 } else {
-                    if (c < cols) y[0] = f32_to_bf16_rn(v.x);
-                    if (c + 1 < cols) y[1] = f32_to_bf16_rn(v.y);
+                    if (cols > 0) y[0] = uint16_t(lo);
+                    if (cols > 1) y[1] = uint16_t(lo >> 16);
+                    if (cols > 2) y[2] = uint16_t(hi);
+                    if (cols > 3) y[3] = uint16_t(hi >> 16);
                 }
             }
         }
+        cluster_arrive();                                // the others have read this CTA's part
+        cluster_wait();
     }
     tc_fence_before();
     __syncthreads();
@@ -413,28 +423,29 @@ Fp8Plan fp8_plan(int M, int out, int blocks, int groups, bool grouped, int sms) 
     const int rows = ceil_div(M, used);                                     // a group's, if they are even
     p.split = 1;
     if (rows > 128) {
-#ifdef V_SPLIT
-        p.split = V_SPLIT;
-#endif
         const int out_tiles = ceil_div(out, 2 * kFp8Block);
+        // A pair fetches less of the weights and runs a tile in 0.84 to 0.9 of the time (198
+        // against 236 us for 4096 x 8192 x 8192, 142 against 129 us where 64 groups of 256 rows
+        // on average have 1000 summed columns), but its tiles hold 256 rows: a group's last is
+        // half empty on average.
+        auto waves = [&](int tile_rows, int places) {
+            const long long tiles = (long long)ceil_div(M, tile_rows) * out_tiles;
+            return ceil_div(tiles + (grouped ? (long long)used * out_tiles / 2 : 0), places);
+        };
+        if (0.88 * waves(256, sms / 2) < waves(128, sms)) p.split = 2;
         p.size = 0, p.bt = 128, p.occupancy = 1;
-        const long long tiles = (long long)out_tiles * (ceil_div(M, 128 * p.split) + (grouped ? used : 0));
+        const long long tiles = (long long)out_tiles * (grouped ? M / (128 * p.split) + used : ceil_div(M, 128 * p.split));
         p.ctas = p.split * int(tiles < sms / p.split ? tiles : sms / p.split);
         return p;
     }
     const int out_tiles = ceil_div(out, kFp8Block);
     p.size = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
     p.occupancy = p.size <= 64 ? 2 : 1;
+    p.bt = grouped ? p.size : (rows + 15) & ~15;
     const int slots = p.occupancy * sms;
-    if (grouped) {
-        p.bt = p.size;
-        const long long tiles = (long long)out_tiles * (ceil_div(M, p.bt) + used);
-        p.ctas = int(tiles < slots ? tiles : slots);
-        return p;
-    }
-    p.bt = (rows + 15) & ~15;
-    while (p.split < 8 && out_tiles * p.split * 2 <= slots && blocks >= 4 * p.split) p.split *= 2;
-    p.ctas = p.split > 1 || out_tiles < slots ? out_tiles * p.split : slots;
+    const long long tiles = (long long)out_tiles * (grouped ? M / p.bt + used : 1);      // at most
+    while (p.split < kMaxCluster && tiles * p.split * 2 <= slots && blocks >= 4 * p.split) p.split *= 2;
+    p.ctas = int(p.split > 1 ? tiles * p.split : tiles < slots ? tiles : slots);
     return p;
 }
 
@@ -458,11 +469,11 @@ cudaError_t launch_fp8_gemm(const Fp8Plan &p, Fp8Args a, const uint8_t *x, const
         return launch_fp8_many(p, a, tx, tw, trans, s);
     }
     const int budget = (p.occupancy == 2 ? kSmemPerSm / 2 - kSmemReservedPerCta : kTensorMaxSmem) - 1024 - 256;
-    const int rest = fp8_smem(p.size, p.bt, 0, p.split, a.groups).total + 64 * 16;
+    const int rest = fp8_smem(p.size, p.bt, 0, a.groups).total + 64 * 16;
     a.stages = (budget - rest) / (kWTile + p.bt * kFp8Block);
     if (a.stages > 16) a.stages = 16;
     if (a.stages < 2) return cudaErrorInvalidValue;
-    const size_t smem = fp8_smem(p.size, p.bt, a.stages, p.split, a.groups).total + 1024;
+    const size_t smem = fp8_smem(p.size, p.bt, a.stages, a.groups).total + 1024;
     switch (p.size) {
         case 16: return launch_trans<16>(p, a, tx, tw, smem, trans, s);
         case 32: return launch_trans<32>(p, a, tx, tw, smem, trans, s);

@@ -32,14 +32,13 @@ static_assert(128 * kRegsIn + 256 * kRegsAdd <= 168 * kManyThreads, "registers")
 
 constexpr int kRows = 128, kCols = 256;
 constexpr int kTile = kFp8Block * kFp8Block;       // bytes of 128 rows of x, of 128 columns' weights
-constexpr int kAhead = 4;                          // blocks whose scales are under way
+constexpr int kAhead = 4;                          // blocks whose scales are fetched ahead
 
 template <bool PAIR>
 struct ManyShape {
     static constexpr int kStage = PAIR ? 2 * kTile : 3 * kTile;
     static constexpr int kStages = PAIR ? 6 : 4;
-    static constexpr int kOffScale = kStages * kStage;
-    static constexpr int kOffStore = kOffScale + kAddWarps * kAhead * 32 * 8;
+    static constexpr int kOffStore = kStages * kStage;
     static constexpr int kOffBar = kOffStore + kAddWarps * 32 * 64;
     static constexpr int kOffTab = kOffBar + (2 * kStages + 5) * 8 + 8;
     static size_t smem(int groups, bool grouped) { return kOffTab + (grouped ? 2 * (groups + 1) * 4 : 0) + 1024; }
@@ -77,13 +76,13 @@ __device__ __forceinline__ void load_sums(uint32_t addr, uint32_t (&v)[N]) {
     if constexpr (N == 16) tc_ld_32x32b_x16(addr, v); else tc_ld_32x32b_x32(addr, v);
 }
 
-// 4 bytes, or zero where !in (src is not read then).
-__device__ __forceinline__ void cp_async4z(uint32_t dst, const void *src, bool in) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
+// volatile: issued where it is written, so that a value fetched ahead is not fetched next
+// to its use.
+__device__ __forceinline__ float fetch(const float *p) {
+    float v;
+    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+    return v;
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 template <bool TRANS, bool PAIR>
 __global__ void __launch_bounds__(kManyThreads, 1)
@@ -198,60 +197,69 @@ fp8_many_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
         const int sub = warp % 4, half = (warp - kAddWarp0) / 4;
         const uint32_t from = tmem + (uint32_t(32 * sub) << 16) + half * kFp8Block;
         const uint32_t done = PAIR ? cluster_address(dempty, 0) : dempty;
-        // This lane's scales of kAhead blocks: x's and the weights'.
-        float2 *scales = reinterpret_cast<float2 *>(smem + S::kOffScale) + (warp - kAddWarp0) * kAhead * 32 + lane;
         unsigned char *store = smem + S::kOffStore + (warp - kAddWarp0) * 32 * 64;
-        int i = 0;
-        bool lost = false;
-        for (int id = id0; many_tile<PAIR>(a, tab_rows, tab_tiles, id, part, t); id += step) {
-            const int row = 32 * sub + lane, wt = 2 * t.tile + half, col0 = wt * kFp8Block;
-            const float *xs = a.xs + t.row0 + row;
-            const float *ws = a.ws + t.group * a.ws_group + (long long)wt * a.ws_tile;
-            const bool in = row < t.rows, in_w = col0 < a.out;
-            auto fetch = [&](int b) {
-                if (b < a.blocks) {
-                    const uint32_t dst = smem_u32(scales + (b % kAhead) * 32);
-                    cp_async4z(dst, in ? xs + (long long)b * a.M : a.xs, in);
-                    cp_async4z(dst + 4, in_w ? ws + (long long)b * a.ws_block : a.ws, in_w);
-                }
-                cp_async_commit();
-            };
+        const int row = 32 * sub + lane;
+        // This lane's scales of x and of the weights, fetched kAhead blocks before their use.
+        float fx[kAhead], fw[kAhead];
+        const float *xs = nullptr, *ws = nullptr;
+        // Rows past the tile's and columns past the last are not stored: any scale does.
+        auto enter = [&]() {
+            const int wt = min(2 * t.tile + half, (a.out - 1) / kFp8Block);
+            xs = a.xs + min(t.row0 + row, a.M - 1);
+            ws = a.ws + t.group * a.ws_group + (long long)wt * a.ws_tile;
             #pragma unroll
-            for (int b = 0; b < kAhead - 1; ++b) fetch(b);
+            for (int u = 0; u < kAhead; ++u) {
+                if (u < a.blocks) fx[u] = fetch(xs), fw[u] = fetch(ws);
+                xs += a.M, ws += a.ws_block;
+            }
+        };
+        int i = 0;
+        bool lost = false, more = many_tile<PAIR>(a, tab_rows, tab_tiles, id0, part, t);
+        if (more) enter();
+        for (int id = id0; more; ) {
+            const ManyTile at = t;
             float acc[kFp8Block];
             #pragma unroll
             for (int j = 0; j < kFp8Block; ++j) acc[j] = 0.f;
-            for (int b = 0; b < a.blocks && !lost; ++b, ++i) {
-                const int d = i & 1;
-                fetch(b + kAhead - 1);
-                cp_async_wait<kAhead - 1>();
-                const float2 f = scales[(b % kAhead) * 32];
-                const float scale = f.x * f.y;
-                lost = !__all_sync(0xffffffffu, mbar_wait(dfull + 8 * d, (i / 2) & 1, abort_flag, a.err));
-                if (lost) break;
-                tc_fence_after();
-                // A chunk's load is under way while the one before it is added.
-                constexpr int kChunk = 16, kChunks = kFp8Block / kChunk;
-                uint32_t v[2][kChunk];
-                load_sums(from + d * kCols, v[0]);
+            for (int b = 0; b < a.blocks && !lost; b += kAhead) {
                 #pragma unroll
-                for (int c = 0; c < kChunks; ++c) {
-                    tc_wait_ld_of(v[c & 1]);
-                    if (c + 1 < kChunks) {
-                        load_sums(from + d * kCols + kChunk * (c + 1), v[(c + 1) & 1]);
-                    } else {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) {
-                            if (PAIR) mbar_arrive_cluster(done + 8 * d);
-                            else mbar_arrive(done + 8 * d);
-                        }
-                    }
+                for (int u = 0; u < kAhead; ++u) {
+                    if (b + u >= a.blocks || lost) break;
+                    const int d = i & 1;
+                    const float scale = fx[u] * fw[u];
+                    if (b + u + kAhead < a.blocks) fx[u] = fetch(xs), fw[u] = fetch(ws);
+                    xs += a.M, ws += a.ws_block;
+                    lost = !__all_sync(0xffffffffu, mbar_wait(dfull + 8 * d, (i / 2) & 1, abort_flag, a.err));
+                    if (lost) break;
+                    ++i;
+                    tc_fence_after();
+                    // A chunk's load is under way while the one before it is added.
+                    constexpr int kChunk = 16, kChunks = kFp8Block / kChunk;
+                    uint32_t v[2][kChunk];
+                    load_sums(from + d * kCols, v[0]);
                     #pragma unroll
-                    for (int e = 0; e < kChunk; ++e)
-                        acc[kChunk * c + e] = fmaf(__uint_as_float(v[c & 1][e]), scale, acc[kChunk * c + e]);
+                    for (int c = 0; c < kChunks; ++c) {
+                        tc_wait_ld_of(v[c & 1]);
+                        if (c + 1 < kChunks) {
+                            load_sums(from + d * kCols + kChunk * (c + 1), v[(c + 1) & 1]);
+                        } else {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) {
+                                if (PAIR) mbar_arrive_cluster(done + 8 * d);
+                                else mbar_arrive(done + 8 * d);
+                            }
+                        }
+                        #pragma unroll
+                        for (int e = 0; e < kChunk; ++e)
+                            acc[kChunk * c + e] = fmaf(__uint_as_float(v[c & 1][e]), scale, acc[kChunk * c + e]);
+                    }
                 }
             }
+            // The next tile's first scales come while this one is stored.
+            id += step;
+            more = many_tile<PAIR>(a, tab_rows, tab_tiles, id, part, t);
+            if (more) enter();
             // A wait that ran out: this tile and the CTA's later ones are NaN.
             if (lost) {
                 #pragma unroll
@@ -261,7 +269,7 @@ fp8_many_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
             // that eight rows' meet in no bank).
             #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                const int col = col0 + 32 * c;
+                const int col = at.tile * kCols + half * kFp8Block + 32 * c;
                 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     uint32_t p[4];
@@ -272,8 +280,8 @@ fp8_many_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
                         make_uint4(p[0], p[1], p[2], p[3]);
                 }
                 __syncwarp();
-                uint16_t *y = a.y + (long long)(t.row0 + 32 * sub) * a.out + col;
-                const int left = t.rows - 32 * sub;
+                uint16_t *y = a.y + (long long)(at.row0 + 32 * sub) * a.out + col;
+                const int left = at.rows - 32 * sub;
                 if (a.vec) {
                     #pragma unroll
                     for (int k = 0; k < 32; k += 8) {
@@ -290,7 +298,6 @@ fp8_many_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
                 __syncwarp();                            // tcgen05.ld takes the whole warp
             }
         }
-        cp_async_wait<0>();
     }
     tc_fence_before();
     __syncthreads();

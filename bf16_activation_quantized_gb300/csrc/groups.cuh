@@ -16,8 +16,16 @@ __device__ __forceinline__ void scan_groups(const int32_t *m_sizes, int groups, 
     const int lane = threadIdx.x & 31;
     int status = 0, tiles = 0;
     long long rows = 0;
+    // The sizes of 128 groups are fetched at once.
+    int ahead[4];
     for (int g0 = 0; g0 < groups; g0 += 32) {
-        const int g = g0 + lane, given = g < groups ? m_sizes[g] : 0, size = given < 0 ? 0 : given;
+        const int g = g0 + lane;
+        if (g0 % 128 == 0) {
+            #pragma unroll
+            for (int j = 0; j < 4; ++j) ahead[j] = g + 32 * j < groups ? m_sizes[g + 32 * j] : 0;
+        }
+        const int given = ahead[0], size = given < 0 ? 0 : given;
+        ahead[0] = ahead[1], ahead[1] = ahead[2], ahead[2] = ahead[3];
         if (given < 0) status |= 1;
         long long end = size;
         #pragma unroll
