@@ -220,27 +220,14 @@ __device__ __forceinline__ uint32_t cluster_address(uint32_t a, int rank) {
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
     return r;
 }
-// Arrive on a barrier of another CTA (`bar` from cluster_address).  Orders no writes of
-// this thread to memory for the other CTA (that takes a release at the cluster's scope,
-// a fence of about a microsecond): what it hands over is tensor memory it has read.
+// Arrive on a barrier of a CTA of the cluster (`bar` from cluster_address).  Orders no
+// writes of this thread to memory for the other CTA (that takes a release at the
+// cluster's scope, a fence of about a microsecond): what it hands over is tensor memory
+// that has been read, or shared memory written before a proxy fence that only the tensor
+// core reads.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-
-// 3-D tiled TMA store of a box (parts past the tensor's ends are left out); the issuing
-// thread's bulk groups.
-__device__ __forceinline__ void tma_store_3d(const void *tmap, int x, int y, int z, uint32_t src) {
-    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(tmap),
-                 "r"(x), "r"(y), "r"(z), "r"(src)
-                 : "memory");
-}
-__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-// All but the N newest groups have read their source.
-template <int N>
-__device__ __forceinline__ void bulk_wait_read() {
-    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 __device__ __forceinline__ void tma_prefetch_desc(const void *tmap) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(tmap) : "memory");

@@ -32,13 +32,14 @@ namespace {
 constexpr int kFp8Threads = 384, kAddWarp0 = 4, kAddWarps = 8;
 constexpr int kWTile = kFp8Block * kFp8Block;      // bytes of a tile of W
 constexpr int kSlots = 4;                          // blocks whose sums and scales are held
-constexpr int kAhead = 4;                          // blocks whose scales a warp fetches ahead
 
 template <int BT>
 struct Fp8Shape {
     static constexpr int kTmem = kSlots * BT;
     static constexpr int kChunk = BT >= 32 ? 16 : 8;    // columns a load from tensor memory brings
     static constexpr int kChunks = BT / 2 / kChunk;            // per warp
+    static constexpr int kAhead = 4;            // blocks whose scales a warp fetches ahead
+    static constexpr int kLoads = BT == 128 ? 2 : 1;           // chunks in registers
     static constexpr int kOccupancy = BT <= 64 ? 2 : 1;
 };
 
@@ -94,17 +95,45 @@ __device__ __forceinline__ float fetch(const float *p) {
     return v;
 }
 
-__device__ __forceinline__ int ld_cluster1(const int *p, int rank) {
-    int v;
-    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(cluster_address(smem_u32(p), rank)) : "memory");
-    return v;
-}
-
 template <int N>
 __device__ __forceinline__ void load_sums(uint32_t addr, uint32_t (&v)[N]) {
     if constexpr (N == 8) tc_ld_32x32b_x8(addr, v);
     else if constexpr (N == 16) tc_ld_32x32b_x16(addr, v);
     else tc_ld_32x32b_x32(addr, v);
+}
+
+// One warp: rows first, first + SPLIT * warps, ... of a tile that SPLIT CTAs share, four
+// columns a lane; 8 parts are under way at once, a row's are added in the order of the CTAs.
+template <int SPLIT>
+__device__ __forceinline__ void join_rows(const Fp8Args &a, const Fp8Tile &t, const float *join, int first, int lost) {
+    constexpr int kAtOnce = 8 / SPLIT, kStep = SPLIT * (kFp8Threads / 32);
+    const int lane = threadIdx.x % 32, col0 = t.tile * kFp8Block + 4 * lane, cols = a.out - col0;
+    for (int r0 = first; r0 < t.rows; r0 += kAtOnce * kStep) {
+        float4 v[kAtOnce][SPLIT];
+        #pragma unroll
+        for (int j = 0; j < kAtOnce; ++j)
+            #pragma unroll
+            for (int k = 0; k < SPLIT; ++k)
+                if (r0 + j * kStep < t.rows) v[j][k] = ld_cluster4(join + (r0 + j * kStep) * kFp8Block + 4 * lane, k);
+        #pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+            if (r0 + j * kStep >= t.rows) break;
+            float4 s = v[j][0];
+            #pragma unroll
+            for (int k = 1; k < SPLIT; ++k) s.x += v[j][k].x, s.y += v[j][k].y, s.z += v[j][k].z, s.w += v[j][k].w;
+            if (lost) s.x = s.y = s.z = s.w = __int_as_float(0x7fffffff);
+            uint16_t *y = a.y + (long long)(t.row0 + r0 + j * kStep) * a.out + col0;
+            const uint32_t lo = pack_bf16x2_rn(s.x, s.y), hi = pack_bf16x2_rn(s.z, s.w);
+            if (a.vec) {
+                if (cols > 0) *reinterpret_cast<uint2 *>(y) = make_uint2(lo, hi);
+            } else {
+                if (cols > 0) y[0] = uint16_t(lo);
+                if (cols > 1) y[1] = uint16_t(lo >> 16);
+                if (cols > 2) y[2] = uint16_t(hi);
+                if (cols > 3) y[3] = uint16_t(hi >> 16);
+            }
+        }
+    }
 }
 
 template <int BT, bool TRANS>
@@ -234,7 +263,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
     } else if (warp < kAddWarp0) {
         // Products of the scales, one block after the other: this warp every second one, fetched
         // kAhead of its blocks before their use.
-        constexpr int kEach = BT < 32 ? 1 : BT / 32;
+        constexpr int kEach = BT < 32 ? 1 : BT / 32, kAhead = S::kAhead;
         int i = 0;
         bool lost = false;
         for (int id = id0; !lost && fp8_tile(a, tab_rows, tab_tiles, id, t); id += step) {
@@ -294,20 +323,25 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
                 if (lost) break;
                 tc_fence_after();
                 const float *sc = scales + d * BT + c0;
+                // With registers to spare a chunk's load is under way while the one before is added.
+                uint32_t v[S::kLoads][S::kChunk];
+                if (S::kLoads == 2 && left > 0) load_sums(lanes + d * BT + c0, v[0]);
                 #pragma unroll
                 for (int c = 0; c < S::kChunks; ++c) {
                     if (c * S::kChunk < left) {
-                        uint32_t v[S::kChunk];
-                        load_sums(lanes + d * BT + c0 + c * S::kChunk, v);
-                        tc_wait_ld_of(v);
+                        uint32_t (&now)[S::kChunk] = v[c % S::kLoads];
+                        if (S::kLoads == 1) load_sums(lanes + d * BT + c0 + c * S::kChunk, now);
+                        tc_wait_ld_of(now);
+                        if (S::kLoads == 2 && c + 1 < S::kChunks && (c + 1) * S::kChunk < left)
+                            load_sums(lanes + d * BT + c0 + (c + 1) * S::kChunk, v[(c + 1) % S::kLoads]);
                         #pragma unroll
                         for (int e = 0; e < S::kChunk; e += 4) {
                             const float4 f = *reinterpret_cast<const float4 *>(sc + c * S::kChunk + e);
                             float *s = acc + c * S::kChunk + e;
-                            s[0] = fmaf(__uint_as_float(v[e]), f.x, s[0]);
-                            s[1] = fmaf(__uint_as_float(v[e + 1]), f.y, s[1]);
-                            s[2] = fmaf(__uint_as_float(v[e + 2]), f.z, s[2]);
-                            s[3] = fmaf(__uint_as_float(v[e + 3]), f.w, s[3]);
+                            s[0] = fmaf(__uint_as_float(now[e]), f.x, s[0]);
+                            s[1] = fmaf(__uint_as_float(now[e + 1]), f.y, s[1]);
+                            s[2] = fmaf(__uint_as_float(now[e + 2]), f.z, s[2]);
+                            s[3] = fmaf(__uint_as_float(now[e + 3]), f.w, s[3]);
                         }
                     }
                 }
@@ -366,29 +400,14 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
         cluster_wait();
         if (fp8_tile(a, tab_rows, tab_tiles, id0, t)) {
             // Where a wait ran out, copies may have landed on the sums.
-            bool lost = false;
-            for (int k = 0; k < split; ++k) lost = lost || ld_cluster1(&s_abort, k) != 0;
-            const int col0 = t.tile * kFp8Block + 4 * lane, cols = a.out - col0;
-            for (int r = part + split * warp; r < t.rows; r += split * (kFp8Threads / 32)) {
-                float4 v[kMaxCluster];
-                #pragma unroll
-                for (int k = 0; k < kMaxCluster; ++k)
-                    if (k < split) v[k] = ld_cluster4(join + r * kFp8Block + 4 * lane, k);
-                #pragma unroll
-                for (int k = 1; k < kMaxCluster; ++k)
-                    if (k < split) v[0].x += v[k].x, v[0].y += v[k].y, v[0].z += v[k].z, v[0].w += v[k].w;
-                if (lost) v[0].x = v[0].y = v[0].z = v[0].w = __int_as_float(0x7fffffff);
-                uint16_t *y = a.y + (long long)(t.row0 + r) * a.out + col0;
-                const uint32_t lo = pack_bf16x2_rn(v[0].x, v[0].y), hi = pack_bf16x2_rn(v[0].z, v[0].w);
-                if (a.vec) {
-                    if (cols > 0) *reinterpret_cast<uint2 *>(y) = make_uint2(lo, hi);
-                } else {
-                    if (cols > 0) y[0] = uint16_t(lo);
-                    if (cols > 1) y[1] = uint16_t(lo >> 16);
-                    if (cols > 2) y[2] = uint16_t(hi);
-                    if (cols > 3) y[3] = uint16_t(hi >> 16);
-                }
-            }
+            int lost = 0;
+            #pragma unroll
+            for (int k = 0; k < kMaxCluster; ++k)
+                if (k < split) lost |= ld_cluster1(&s_abort, k);
+            const int first = part + split * warp;
+            if (split == 2) join_rows<2>(a, t, join, first, lost);
+            else if (split == 4) join_rows<4>(a, t, join, first, lost);
+            else join_rows<8>(a, t, join, first, lost);
         }
         cluster_arrive();                                // the others have read this CTA's part
         cluster_wait();

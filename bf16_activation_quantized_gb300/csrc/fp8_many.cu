@@ -180,13 +180,13 @@ fp8_many_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
                             if (PAIR) tc_mma_f8_ss_pair(tmem + d * kCols, dx + 2 * e, de, idesc, e > 0);
                             else tc_mma_f8_ss(tmem + d * kCols, dx + 2 * e, de, idesc, e > 0);
                         }
-                        if (PAIR) tc_commit_pair(empty + 8 * s), tc_commit_pair(dfull + 8 * d);
+                        if (PAIR) tc_commit_pair(empty + 8 * s, 3), tc_commit_pair(dfull + 8 * d, 3);
                         else tc_commit(empty + 8 * s), tc_commit(dfull + 8 * d);
                     }
                     __syncwarp();
                 }
             if (elect_one()) {
-                if (PAIR) tc_commit_pair(drained);
+                if (PAIR) tc_commit_pair(drained, 3);
                 else tc_commit(drained);
             }
             __syncwarp();

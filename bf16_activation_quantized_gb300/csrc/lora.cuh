@@ -66,6 +66,11 @@ __device__ __forceinline__ float4 ld_cluster4(const void *p, int rank) {
                  : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
     return v;
 }
+__device__ __forceinline__ int ld_cluster1(const int *p, int rank) {
+    int v;
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(cluster_address(smem_u32(p), rank)) : "memory");
+    return v;
+}
 
 // Makes ordinary writes of shared memory visible to the tensor core and back.
 __device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async;" ::: "memory"); }

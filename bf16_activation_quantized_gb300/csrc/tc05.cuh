@@ -161,11 +161,11 @@ __device__ __forceinline__ void tc_mma_ss_pair(uint32_t d_tmem, uint64_t a_desc,
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(acc)
         : "memory");
 }
-// Arrive on this barrier's place in both CTAs of the pair.
-__device__ __forceinline__ void tc_commit_pair(uint32_t bar) {
+// Arrive on this barrier's place in the CTAs of the cluster that `ctas` names (a bit each).
+__device__ __forceinline__ void tc_commit_pair(uint32_t bar, uint16_t ctas) {
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-        "h"(uint16_t(3))
+        "h"(ctas)
         : "memory");
 }
 

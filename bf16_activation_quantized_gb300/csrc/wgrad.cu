@@ -4,12 +4,18 @@
 //
 // Rows are summed over as they lie: a TMA box of 64 rows and 64 columns (128 bytes) is
 // an operand along M (dY) or N (X) of the tensor core, whose K runs down the rows; no
-// transpose.  A tile is 128 columns of dY by 256 of X.  A group may end anywhere: the
-// rows of a box past the last are the next group's, and those that share an MMA's step
-// of 16 with it are overwritten with zeros in shared memory, on both sides.
+// transpose.  Two CTAs share a tile of 256 columns of each (cta_group::2): a CTA loads
+// 128 columns of dY and 128 of X and holds the sums of its 128 rows of dW.
 //
-// Warps: 0 copies (TMA) the boxes, 1 issues the MMAs (and clears the rows past the
-// last), 2 to 5 empty one of two accumulators while the next tile is summed into the other.
+// A group may end anywhere: the rows of a box past the last are the next group's, and
+// those that share an MMA's step of 16 with it are overwritten with zeros in shared
+// memory, on both sides of the product and in both CTAs.
+//
+// With few tiles and many rows `split` pairs (a cluster of 2 split CTAs) share a tile's
+// rows; the parts stand in shared memory and are added in the order of the pairs.
+//
+// Warps: 0 copies (TMA) the boxes, 1 issues the MMAs, 2 to 5 empty one of two
+// accumulators while the next tile is summed into the other, 6 clears rows past the last.
 #include "async.cuh"
 #include "common.cuh"
 #include "groups.cuh"
@@ -24,150 +30,203 @@ namespace w4a16 {
 namespace {
 
 constexpr int kRowStep = 64;                       // rows of a stage
-constexpr int kTileN = 128, kTileK = 256;
+constexpr int kSide = 256, kHalf = 128;            // columns of dY and of X of a tile, of a CTA
 constexpr int kBox = kRowStep * 128;               // bytes of 64 rows x 64 columns
-constexpr int kWgStage = (kTileN + kTileK) / 64 * kBox, kWgStages = 4;
-constexpr int kWgThreads = 192, kWgStore0 = 2, kWgStoreWarps = 4;
+constexpr int kWgStage = 4 * kBox, kWgStages = 5;
+constexpr int kWgThreads = 224, kWgStore0 = 2, kWgStoreWarps = 4;
 constexpr int kStoreBox = 32 * 128;                // bytes of 32 rows of dW, 128 bytes of each
 
 struct GroupWgradArgs {
     const int32_t *m_sizes;
     int *status, *err;
+    void *dw;
     int M, N, K, groups, n_tiles, k_tiles;
 };
 
 constexpr int kWgOffStore = kWgStages * kWgStage, kWgOffBar = kWgOffStore + kWgStoreWarps * kStoreBox;
-constexpr int kWgOffTab = kWgOffBar + (2 * kWgStages + 5) * 8 + 8;
-inline size_t wgrad_smem(int groups) { return kWgOffTab + 2 * (groups + 1) * sizeof(int) + 1024; }
+constexpr int kWgOffTab = kWgOffBar + (4 * kWgStages + 5) * 8 + 8;
+inline size_t wgrad_smem(int groups) { return kWgOffTab + (groups + 1) * sizeof(int) + 1024; }
+static_assert(kWgOffTab + (kMaxGroups + 1) * 4 + 1024 <= kTensorMaxSmem - 256, "shared memory");
+static_assert(kHalf * kSide * 4 <= kWgOffStore, "a tile's sums lie over the ring");
 
 struct WgTile {
-    int group, n0, k0, row0, rows;
+    int group, n0, k0, row0, rows;                 // the tile's columns, the rows of this pair's part
 };
-__device__ __forceinline__ WgTile wg_tile(const GroupWgradArgs &a, const int *tab_rows, int id) {
+__device__ __forceinline__ WgTile wg_tile(const GroupWgradArgs &a, const int *tab_rows, int id, int part, int split) {
     WgTile t;
     const int per = a.n_tiles * a.k_tiles;
     t.group = id / per;
     const int r = id - t.group * per;
-    t.k0 = r / a.n_tiles * kTileK;
-    t.n0 = r % a.n_tiles * kTileN;
-    t.row0 = tab_rows[t.group];
-    t.rows = tab_rows[t.group + 1] - t.row0;
+    t.k0 = r / a.n_tiles * kSide;
+    t.n0 = r % a.n_tiles * kSide;
+    const int first = tab_rows[t.group], rows = tab_rows[t.group + 1] - first;
+    if (split == 1) {
+        t.row0 = first, t.rows = rows;
+    } else {
+        const int steps = (rows + kRowStep - 1) / kRowStep;
+        const int s0 = steps * part / split * kRowStep, s1 = steps * (part + 1) / split * kRowStep;
+        t.row0 = first + s0, t.rows = min(rows, s1) - s0;
+    }
     return t;
+}
+
+// One warp: zeros in rows `rows` to the end of the last step of 16, in the stage's boxes.
+__device__ __forceinline__ void clear_rows(unsigned char *stage, int rows) {
+    const int lane = threadIdx.x % 32;
+    for (int r = rows + lane / 8; r < ((rows + 15) & ~15); r += 4)
+        #pragma unroll
+        for (int box = 0; box < 4; ++box)
+            *reinterpret_cast<uint4 *>(stage + box * kBox + r * 128 + lane % 8 * 16) = make_uint4(0, 0, 0, 0);
+    fence_proxy_async();
+    __syncwarp();
 }
 
 template <bool F32>
 __global__ void __launch_bounds__(kWgThreads, 1)
 grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmap_dy, const __grid_constant__ CUtensorMap tmap_x,
-                     const __grid_constant__ CUtensorMap tmap_dw, const GroupWgradArgs a) {
+                     const GroupWgradArgs a) {
     extern __shared__ unsigned char s_raw[];
     unsigned char *smem = s_raw + (-smem_u32(s_raw) & 1023);
     __shared__ int s_abort;
     __shared__ uint32_t s_tmem;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int rank = cluster_rank(), split = cluster_size() / 2, half = rank & 1, part = rank / 2;
     const uint32_t ring = smem_u32(smem), full = ring + kWgOffBar, empty = full + 8 * kWgStages;
-    const uint32_t dfull = empty + 8 * kWgStages, dempty = dfull + 16, drained = dempty + 16;
-    int *tab_rows = reinterpret_cast<int *>(smem + kWgOffTab), *tab_tiles = tab_rows + a.groups + 1;
+    // full: both CTAs' boxes have landed (counted in the even one).  The last boxes of a part
+    // that ends inside a step: tail, this CTA's have landed; ready (in the even one), both
+    // CTAs' rows past the last are cleared.
+    const uint32_t tail = empty + 8 * kWgStages, ready = tail + 8 * kWgStages;
+    const uint32_t dfull = ready + 8 * kWgStages, dempty = dfull + 16, drained = dempty + 16;
+    int *tab_rows = reinterpret_cast<int *>(smem + kWgOffTab);
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kWgStages; ++i) mbar_init(full + 8 * i, 1), mbar_init(empty + 8 * i, 1);
-        for (int i = 0; i < 2; ++i) mbar_init(dfull + 8 * i, 1), mbar_init(dempty + 8 * i, kWgStoreWarps);
+        for (int i = 0; i < kWgStages; ++i) {
+            mbar_init(full + 8 * i, 1), mbar_init(empty + 8 * i, 1);
+            mbar_init(tail + 8 * i, 1), mbar_init(ready + 8 * i, 2);
+        }
+        for (int i = 0; i < 2; ++i) mbar_init(dfull + 8 * i, 1), mbar_init(dempty + 8 * i, 2 * kWgStoreWarps);
         mbar_init(drained, 1);
         s_abort = 0;
         fence_barrier_init();
     }
-    if (warp == 1) {
-        tc_alloc(smem_u32(&s_tmem), 2 * kTileK);
-        tc_relinquish();
-    }
-    if (warp == 0 && lane == 0) tma_prefetch_desc(&tmap_dy), tma_prefetch_desc(&tmap_x), tma_prefetch_desc(&tmap_dw);
+    if (warp == 1) tc_alloc_pair(smem_u32(&s_tmem), 2 * kSide);
+    if (warp == 0 && lane == 0) tma_prefetch_desc(&tmap_dy), tma_prefetch_desc(&tmap_x);
     pdl_wait();
     pdl_launch_dependents();
     if (warp == 0)
-        scan_groups(a.m_sizes, a.groups, a.M, 1, 0, tab_rows, tab_tiles, blockIdx.x == 0 ? a.status : nullptr);
+        scan_groups(a.m_sizes, a.groups, a.M, 1, 0, tab_rows, nullptr, blockIdx.x == 0 ? a.status : nullptr);
     tc_fence_before();
     __syncthreads();
+    cluster_arrive();                                    // the others' barriers stand
+    cluster_wait();
     tc_fence_after();
     const uint32_t tmem = s_tmem;
     volatile int *abort_flag = &s_abort;
-    const int tiles = a.groups * a.n_tiles * a.k_tiles;
+    const int tiles = a.groups * a.n_tiles * a.k_tiles, id0 = int(blockIdx.x) / (2 * split);
+    const int step = int(gridDim.x) / (2 * split);
+    const uint16_t both = uint16_t(3u << (rank & ~1));
     bool lost = false;
     if (warp == 0) {
         int i = 0;
-        for (int id = blockIdx.x; id < tiles && !lost; id += gridDim.x) {
-            const WgTile t = wg_tile(a, tab_rows, id);
-            const int boxes_n = min(kTileN, a.N - t.n0) > 64 ? 2 : 1, boxes_k = (min(kTileK, a.K - t.k0) + 63) / 64;
+        uint32_t uses = 0, tails = 0;                    // parities of the slots' full and tail barriers
+        const uint32_t even = cluster_address(full, rank & ~1), own = cluster_address(tail, rank);
+        for (int id = id0; id < tiles && !lost; id += step) {
+            const WgTile t = wg_tile(a, tab_rows, id, part, split);
             for (int r = 0; r < t.rows; r += kRowStep, ++i) {
                 const int s = i % kWgStages;
                 const bool ok = i < kWgStages || mbar_wait(empty + 8 * s, (i / kWgStages - 1) & 1, abort_flag, a.err);
                 lost = !__all_sync(0xffffffffu, ok);
                 if (lost) break;
+                const bool last = (t.rows - r < kRowStep) && t.rows % 16;
                 if (elect_one()) {
-                    const uint32_t dst = ring + s * kWgStage, bar = full + 8 * s;
-                    mbar_arrive_expect_tx(bar, (boxes_n + boxes_k) * kBox);
-                    for (int c = 0; c < boxes_n; ++c)
-                        tma_load_2d(dst + c * kBox, &tmap_dy, t.n0 + 64 * c, t.row0 + r, bar);
-                    for (int c = 0; c < boxes_k; ++c)
-                        tma_load_2d(dst + (kTileN / 64 + c) * kBox, &tmap_x, t.k0 + 64 * c, t.row0 + r, bar);
+                    const uint32_t dst = ring + s * kWgStage, bar = (last ? own : even) + 8 * s;
+                    if (last) mbar_arrive_expect_tx(tail + 8 * s, kWgStage);
+                    else if (half == 0) mbar_arrive_expect_tx(full + 8 * s, 2 * kWgStage);
+                    #pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        tma_load_2d_pair(dst + c * kBox, &tmap_dy, t.n0 + half * kHalf + 64 * c, t.row0 + r, bar);
+                        tma_load_2d_pair(dst + (2 + c) * kBox, &tmap_x, t.k0 + half * kHalf + 64 * c, t.row0 + r, bar);
+                    }
                 }
                 __syncwarp();
+                if (last) tails ^= 1u << s;
+                else uses ^= 1u << s;
             }
         }
+        // Every copy lands before the CTA ends (the pair's are counted in the even one).
         if (*abort_flag)
-            for (int u = i > kWgStages ? i - kWgStages : 0; u < i; ++u)
-                drain_wait(full + 8 * (u % kWgStages), (u / kWgStages) & 1);
-    } else if (warp == 1) {
+            for (int s = 0; s < kWgStages; ++s) {
+                if (half == 0) drain_wait(full + 8 * s, ~(uses >> s) & 1);
+                drain_wait(tail + 8 * s, ~(tails >> s) & 1);
+            }
+    } else if (warp == 1 && half == 0) {
+        constexpr uint32_t idesc = tc_idesc_bf16(kSide, kSide) | kTcAMajorM | kTcBMajorN;
         int i = 0, n = 0;
-        for (int id = blockIdx.x; id < tiles && !lost; id += gridDim.x) {
-            const WgTile t = wg_tile(a, tab_rows, id);
+        uint32_t uses = 0, tails = 0;                    // parities of the slots' full and ready barriers
+        for (int id = id0; id < tiles && !lost; id += step) {
+            const WgTile t = wg_tile(a, tab_rows, id, part, split);
             if (t.rows == 0) continue;
-            const uint32_t idesc = tc_idesc_bf16(kTileN, (min(kTileK, a.K - t.k0) + 15) & ~15) | kTcAMajorM | kTcBMajorN;
             const int d = n & 1;
             const bool free = n < 2 || mbar_wait(dempty + 8 * d, (n / 2 - 1) & 1, abort_flag, a.err);
             lost = !__all_sync(0xffffffffu, free);
             if (lost) break;
             for (int r = 0; r < t.rows; r += kRowStep, ++i) {
-                const int s = i % kWgStages;
-                lost = !__all_sync(0xffffffffu, mbar_wait(full + 8 * s, (i / kWgStages) & 1, abort_flag, a.err));
+                const int s = i % kWgStages, rows = min(kRowStep, t.rows - r), steps = (rows + 15) / 16;
+                const bool last = rows % 16;
+                const bool ok = last ? mbar_wait(ready + 8 * s, (tails >> s) & 1, abort_flag, a.err)
+                                     : mbar_wait(full + 8 * s, (uses >> s) & 1, abort_flag, a.err);
+                lost = !__all_sync(0xffffffffu, ok);
                 if (lost) break;
-                const int rows = min(kRowStep, t.rows - r), steps = (rows + 15) / 16;
-                if (rows % 16) {
-                    // rows to the end of the last step, 128 bytes in each box
-                    const int pad = 16 * steps - rows;
-                    for (int m = lane; m < pad * 8 * (kTileN + kTileK) / 64; m += 32) {
-                        const int box = m / (pad * 8), at = m % (pad * 8);
-                        *reinterpret_cast<uint4 *>(smem + s * kWgStage + box * kBox + rows * 128 + at * 16) =
-                            make_uint4(0, 0, 0, 0);
-                    }
-                    fence_proxy_async();
-                    __syncwarp();
-                }
+                if (last) tails ^= 1u << s;
+                else uses ^= 1u << s;
                 tc_fence_after();
                 const uint32_t st = ring + s * kWgStage;
-                const uint64_t dn = tc_sdesc_sw128_mn(st, kBox), dk = tc_sdesc_sw128_mn(st + kTileN / 64 * kBox, kBox);
+                const uint64_t dn = tc_sdesc_sw128_mn(st, kBox), dk = tc_sdesc_sw128_mn(st + 2 * kBox, kBox);
                 if (elect_one()) {
-                    for (int e = 0; e < steps; ++e)
-                        tc_mma_ss(tmem + d * kTileK, dn + 128 * e, dk + 128 * e, idesc, r > 0 || e > 0);
-                    tc_commit(empty + 8 * s);
+                    #pragma unroll
+                    for (int e = 0; e < kRowStep / 16; ++e)
+                        if (e < steps)
+                            tc_mma_ss_pair(tmem + d * kSide, dn + 128 * e, dk + 128 * e, idesc, r > 0 || e > 0);
+                    tc_commit_pair(empty + 8 * s, both);
                 }
                 __syncwarp();
             }
             if (lost) break;
-            if (elect_one()) tc_commit(dfull + 8 * d);
+            if (elect_one()) tc_commit_pair(dfull + 8 * d, both);
             __syncwarp();
             ++n;
         }
-        if (elect_one()) tc_commit(drained);
+        if (elect_one()) tc_commit_pair(drained, both);
         __syncwarp();
         drain_wait(drained, 0);
-    } else {
-        // Lane l of a warp holds row 32 (warp % 4) + l of the tile; 32 rows and 128 bytes of
-        // each leave as one box.
+    } else if (warp == kWgStore0 + kWgStoreWarps) {
+        const uint32_t to = cluster_address(ready, rank & ~1);
+        int i = 0;
+        uint32_t tails = 0;
+        for (int id = id0; id < tiles && !lost; id += step) {
+            const WgTile t = wg_tile(a, tab_rows, id, part, split);
+            const int steps = (t.rows + kRowStep - 1) / kRowStep;
+            i += steps;
+            if (t.rows % 16 == 0) continue;
+            const int s = (i - 1) % kWgStages;
+            lost = !__all_sync(0xffffffffu, mbar_wait(tail + 8 * s, (tails >> s) & 1, abort_flag, a.err));
+            if (lost) break;
+            tails ^= 1u << s;
+            clear_rows(smem + s * kWgStage, t.rows - (steps - 1) * kRowStep);
+            if (lane == 0) mbar_arrive_cluster(to + 8 * s);
+            __syncwarp();
+        }
+    } else if (warp >= kWgStore0) {
+        // Lane l of a warp holds row 32 (warp % 4) + l of this CTA's half of the tile; 32 rows
+        // and 128 bytes of each go through shared memory and leave as whole lines.
         const int sub = warp % 4;
+        const uint32_t lanes = tmem + (uint32_t(32 * sub) << 16), done = cluster_address(dempty, rank & ~1);
         unsigned char *buf = smem + kWgOffStore + (warp - kWgStore0) * kStoreBox;
+        float *join = reinterpret_cast<float *>(smem) + (32 * sub + lane) * kSide;
         constexpr int kCols = F32 ? 32 : 64;
         int n = 0;
-        for (int id = blockIdx.x; id < tiles; id += gridDim.x) {
-            const WgTile t = wg_tile(a, tab_rows, id);
-            const int d = n & 1, width = min(kTileK, a.K - t.k0);
+        for (int id = id0; id < tiles; id += step) {
+            const WgTile t = wg_tile(a, tab_rows, id, part, split);
+            const int d = n & 1, width = min(kSide, a.K - t.k0), row = t.n0 + half * kHalf + 32 * sub;
             if (t.rows && !lost) {
                 lost = !__all_sync(0xffffffffu, mbar_wait(dfull + 8 * d, (n / 2) & 1, abort_flag, a.err));
                 tc_fence_after();
@@ -178,7 +237,7 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmap_dy, const __grid_c
                     #pragma unroll
                     for (int e = 0; e < kCols; e += 16) {
                         uint32_t w[16];
-                        tc_ld_32x32b_x16(tmem + (uint32_t(32 * sub) << 16) + d * kTileK + c + e, w);
+                        tc_ld_32x32b_x16(lanes + d * kSide + c + e, w);
                         tc_wait_ld_of(w);
                         #pragma unroll
                         for (int j = 0; j < 16; ++j) v[e + j] = w[j];
@@ -187,13 +246,21 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmap_dy, const __grid_c
                     #pragma unroll
                     for (int j = 0; j < kCols; ++j) v[j] = lost ? 0x7fffffffu : 0u;
                 }
-                if (lane == 0) bulk_wait_read<0>();      // the box before has left the buffer
-                __syncwarp();
+                if (split > 1) {
+                    // over the ring, whose boxes this tile's last MMAs have read; pieces of 16 bytes
+                    // placed so that eight rows' meet in no bank
+                    #pragma unroll
+                    for (int q = 0; q < kCols / 4; ++q)
+                        *reinterpret_cast<uint4 *>(join + 4 * ((c / 4 + q) ^ (lane & 7))) =
+                            make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                    __syncwarp();
+                    continue;
+                }
                 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
                     uint4 p;
                     if (F32) {
-                        p = make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                        p = make_uint4(v[4 * q % kCols], v[(4 * q + 1) % kCols], v[(4 * q + 2) % kCols], v[(4 * q + 3) % kCols]);
                     } else {
                         uint32_t h[4];
                         #pragma unroll
@@ -204,38 +271,71 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmap_dy, const __grid_c
                     }
                     *reinterpret_cast<uint4 *>(buf + lane * 128 + ((q ^ (lane & 7)) << 4)) = p;
                 }
-                fence_proxy_async();
                 __syncwarp();
-                if (lane == 0) {
-                    if (t.n0 + 32 * sub < a.N)
-                        tma_store_3d(&tmap_dw, t.k0 + c, t.n0 + 32 * sub, t.group, smem_u32(buf));
-                    bulk_commit();
+                #pragma unroll
+                for (int k = 0; k < 32; k += 4) {
+                    const int r = k + lane / 8, q = lane % 8, col = t.k0 + c + q * (kCols / 8);
+                    if (row + r < a.N && col < a.K)
+                        *reinterpret_cast<uint4 *>(static_cast<char *>(a.dw) +
+                                                   (((long long)t.group * a.N + row + r) * a.K + col) * (F32 ? 4 : 2)) =
+                            *reinterpret_cast<const uint4 *>(buf + r * 128 + ((q ^ (r & 7)) << 4));
                 }
                 __syncwarp();                            // tcgen05.ld takes the whole warp
             }
+            if (split > 1) break;                        // a cluster has one tile
             if (t.rows) {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0 && !lost) mbar_arrive(dempty + 8 * d);
+                if (lane == 0 && !lost) mbar_arrive_cluster(done + 8 * d);
                 ++n;
             }
         }
-        if (lane == 0) bulk_wait_all();
-        __syncwarp();
     }
     tc_fence_before();
     __syncthreads();
+    cluster_arrive();                                    // the pair's MMAs have read both CTAs' memory
+    cluster_wait();
+    if (split > 1) {
+        // Rows part, part + split, ... of this half of the tile, a warp a row, 8 columns a lane.
+        int gone = 0;                                    // a wait ran out: copies may have landed on the sums
+        for (int k = 0; k < 2 * split; ++k) gone |= ld_cluster1(&s_abort, k);
+        const WgTile t = wg_tile(a, tab_rows, id0, part, split);
+        for (int r = part + split * warp; r < min(kHalf, a.N - t.n0 - half * kHalf); r += split * (kWgThreads / 32)) {
+            float4 s[2];
+            for (int k = 0; k < split; ++k)
+                #pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int q = 2 * lane + h;
+                    const float4 v = ld_cluster4(reinterpret_cast<float *>(smem) + r * kSide + 4 * (q ^ (r & 7)), half + 2 * k);
+                    if (k == 0) s[h] = v;
+                    else s[h].x += v.x, s[h].y += v.y, s[h].z += v.z, s[h].w += v.w;
+                }
+            if (gone) s[0].x = s[0].y = s[0].z = s[0].w = s[1].x = s[1].y = s[1].z = s[1].w = __int_as_float(0x7fffffff);
+            const int col = t.k0 + 8 * lane;
+            if (col >= a.K) continue;
+            const long long at = ((long long)t.group * a.N + t.n0 + half * kHalf + r) * a.K + col;
+            if (F32) {
+                float4 *w = reinterpret_cast<float4 *>(static_cast<float *>(a.dw) + at);
+                w[0] = s[0], w[1] = s[1];
+            } else {
+                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.dw) + at) =
+                    make_uint4(pack_bf16x2_rn(s[0].x, s[0].y), pack_bf16x2_rn(s[0].z, s[0].w),
+                               pack_bf16x2_rn(s[1].x, s[1].y), pack_bf16x2_rn(s[1].z, s[1].w));
+            }
+        }
+        cluster_arrive();                                // the others have read this CTA's part
+        cluster_wait();
+    }
     tc_fence_after();
-    if (warp == 1) tc_dealloc(tmem, 2 * kTileK);
+    if (warp == 1) tc_dealloc_pair(tmem, 2 * kSide);
 }
 
 bool aligned(const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 int ceil_div(long long x, long long y) { return int((x + y - 1) / y); }
 
 template <bool F32>
-cudaError_t launch_grouped_wgrad(const GroupWgradArgs &a, const uint16_t *dy, const uint16_t *x, void *dw, int sms,
-                                 cudaStream_t s) {
-    CUtensorMap ty, tx, tw;
+cudaError_t launch_grouped_wgrad(const GroupWgradArgs &a, const uint16_t *dy, const uint16_t *x, int sms, cudaStream_t s) {
+    CUtensorMap ty, tx;
     const cuuint32_t box[2] = {64, kRowStep};
     const cuuint64_t ydim[2] = {cuuint64_t(a.N), cuuint64_t(a.M)}, ystride[1] = {2 * ydim[0]};
     cudaError_t e = encode_tensor_map(&ty, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, dy, ydim, ystride, box,
@@ -244,18 +344,17 @@ cudaError_t launch_grouped_wgrad(const GroupWgradArgs &a, const uint16_t *dy, co
     const cuuint64_t xdim[2] = {cuuint64_t(a.K), cuuint64_t(a.M)}, xstride[1] = {2 * xdim[0]};
     e = encode_tensor_map(&tx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, x, xdim, xstride, box, CU_TENSOR_MAP_SWIZZLE_128B);
     if (e != cudaSuccess) return e;
-    const size_t each = F32 ? 4 : 2;
-    const cuuint64_t wdim[3] = {cuuint64_t(a.K), cuuint64_t(a.N), cuuint64_t(a.groups)};
-    const cuuint64_t wstride[2] = {a.K * each, a.K * each * a.N};
-    const cuuint32_t wbox[3] = {cuuint32_t(128 / each), 32, 1};
-    e = encode_tensor_map(&tw, F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, dw, wdim,
-                          wstride, wbox, CU_TENSOR_MAP_SWIZZLE_128B);
-    if (e != cudaSuccess) return e;
     e = allow_smem<grouped_wgrad_kernel<F32>>(kTensorMaxSmem - 256);
     if (e != cudaSuccess) return e;
     const long long tiles = (long long)a.groups * a.n_tiles * a.k_tiles;
-    return launch_chained(grouped_wgrad_kernel<F32>, dim3(unsigned(tiles < sms ? tiles : sms)), kWgThreads,
-                          wgrad_smem(a.groups), 1, s, ty, tx, tw, a);
+    const int pairs = sms / 2;
+    // Pairs that share a tile: as long as all find a place and a part holds a few stages of a
+    // group's rows, if the groups are even.
+    int split = 1;
+    while (split < 4 && tiles * split * 2 <= pairs && a.M / a.groups >= 8 * kRowStep * split) split *= 2;
+    const int clusters = int(split > 1 || tiles < pairs ? tiles : pairs);
+    return launch_chained(grouped_wgrad_kernel<F32>, dim3(clusters * 2 * split), kWgThreads, wgrad_smem(a.groups),
+                          2 * split, s, ty, tx, a);
 }
 
 }  // namespace
@@ -286,11 +385,11 @@ extern "C" w4a16_status w4a16_gemm_grouped_wgrad(const w4a16_bf16 *dY, const w4a
     int sms = 0;
     if (device_sm_count(&sms) != 0 || sms < 1) return W4A16_ERR_CUDA;
     GroupWgradArgs a = {};
-    a.m_sizes = M_sizes_dev, a.status = status_dev, a.err = device_error_word();
+    a.m_sizes = M_sizes_dev, a.status = status_dev, a.err = device_error_word(), a.dw = dW;
     if (!a.err) return W4A16_ERR_CUDA;
     a.M = M_total, a.N = N, a.K = K, a.groups = num_groups;
-    a.n_tiles = ceil_div(N, kTileN), a.k_tiles = ceil_div(K, kTileK);
-    const cudaError_t e = dw_bytes == 4 ? launch_grouped_wgrad<true>(a, dY, X, dW, sms, s)
-                                        : launch_grouped_wgrad<false>(a, dY, X, dW, sms, s);
+    a.n_tiles = ceil_div(N, kSide), a.k_tiles = ceil_div(K, kSide);
+    const cudaError_t e = dw_bytes == 4 ? launch_grouped_wgrad<true>(a, dY, X, sms, s)
+                                        : launch_grouped_wgrad<false>(a, dY, X, sms, s);
     return e == cudaSuccess ? W4A16_OK : W4A16_ERR_CUDA;
 }
