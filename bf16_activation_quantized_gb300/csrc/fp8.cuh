@@ -26,10 +26,11 @@ struct Fp8Args {
 };
 
 // How a product is cut.  size 16 to 128: the kernel for few rows, of that template size,
-// with bt rows of x per tile and `split` CTAs (a cluster) that share a tile's sum; 0: the
-// kernel for many rows, split 2: pairs of CTAs.  CTAs launched and per SM.
+// with bt rows of x per tile; 0: the kernel for many rows, with pairs of CTAs or without.
+// split: CTAs of a cluster, which share a tile's sum or are a pair.  ctas: launched.
 struct Fp8Plan {
     int size, bt, split, ctas, occupancy;
+    bool pair;
 };
 Fp8Plan fp8_plan(int M, int out, int blocks, int groups, bool grouped, int sms);
 

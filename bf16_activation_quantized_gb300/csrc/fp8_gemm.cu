@@ -23,6 +23,7 @@
 #include "internal.h"
 #include "launch.cuh"
 #include "lora.cuh"
+#include "stall.cuh"
 #include "tc05.cuh"
 
 namespace w4a16 {
@@ -36,10 +37,9 @@ constexpr int kSlots = 4;                          // blocks whose sums and scal
 template <int BT>
 struct Fp8Shape {
     static constexpr int kTmem = kSlots * BT;
-    static constexpr int kChunk = BT >= 32 ? 16 : 8;    // columns a load from tensor memory brings
+    static constexpr int kChunk = BT == 128 ? 32 : BT == 32 ? 16 : 8;    // columns a load from tensor memory brings
     static constexpr int kChunks = BT / 2 / kChunk;            // per warp
     static constexpr int kAhead = 4;            // blocks whose scales a warp fetches ahead
-    static constexpr int kLoads = BT == 128 ? 2 : 1;           // chunks in registers
     static constexpr int kOccupancy = BT <= 64 ? 2 : 1;
 };
 
@@ -103,27 +103,37 @@ __device__ __forceinline__ void load_sums(uint32_t addr, uint32_t (&v)[N]) {
 }
 
 // One warp: rows first, first + SPLIT * warps, ... of a tile that SPLIT CTAs share, four
-// columns a lane; 8 parts are under way at once, a row's are added in the order of the CTAs.
+// columns a lane; several parts are under way at once, a row's are added in the order of
+// the CTAs.
 template <int SPLIT>
 __device__ __forceinline__ void join_rows(const Fp8Args &a, const Fp8Tile &t, const float *join, int first, int lost) {
-    constexpr int kAtOnce = 8 / SPLIT, kStep = SPLIT * (kFp8Threads / 32);
+    constexpr int kParts = SPLIT < 4 ? SPLIT : 4, kAtOnce = 4 / kParts, kStep = SPLIT * (kFp8Threads / 32);
     const int lane = threadIdx.x % 32, col0 = t.tile * kFp8Block + 4 * lane, cols = a.out - col0;
     for (int r0 = first; r0 < t.rows; r0 += kAtOnce * kStep) {
-        float4 v[kAtOnce][SPLIT];
+        float4 s[kAtOnce];
         #pragma unroll
-        for (int j = 0; j < kAtOnce; ++j)
+        for (int k0 = 0; k0 < SPLIT; k0 += kParts) {
+            float4 v[kAtOnce][kParts];
             #pragma unroll
-            for (int k = 0; k < SPLIT; ++k)
-                if (r0 + j * kStep < t.rows) v[j][k] = ld_cluster4(join + (r0 + j * kStep) * kFp8Block + 4 * lane, k);
+            for (int j = 0; j < kAtOnce; ++j)
+                #pragma unroll
+                for (int k = 0; k < kParts; ++k)
+                    if (r0 + j * kStep < t.rows)
+                        v[j][k] = ld_cluster4(join + (r0 + j * kStep) * kFp8Block + 4 * lane, k0 + k);
+            #pragma unroll
+            for (int j = 0; j < kAtOnce; ++j)
+                #pragma unroll
+                for (int k = 0; k < kParts; ++k) {
+                    if (k0 + k == 0) s[j] = v[j][0];
+                    else s[j].x += v[j][k].x, s[j].y += v[j][k].y, s[j].z += v[j][k].z, s[j].w += v[j][k].w;
+                }
+        }
         #pragma unroll
         for (int j = 0; j < kAtOnce; ++j) {
             if (r0 + j * kStep >= t.rows) break;
-            float4 s = v[j][0];
-            #pragma unroll
-            for (int k = 1; k < SPLIT; ++k) s.x += v[j][k].x, s.y += v[j][k].y, s.z += v[j][k].z, s.w += v[j][k].w;
-            if (lost) s.x = s.y = s.z = s.w = __int_as_float(0x7fffffff);
+            if (lost) s[j].x = s[j].y = s[j].z = s[j].w = __int_as_float(0x7fffffff);
             uint16_t *y = a.y + (long long)(t.row0 + r0 + j * kStep) * a.out + col0;
-            const uint32_t lo = pack_bf16x2_rn(s.x, s.y), hi = pack_bf16x2_rn(s.z, s.w);
+            const uint32_t lo = pack_bf16x2_rn(s[j].x, s[j].y), hi = pack_bf16x2_rn(s[j].z, s[j].w);
             if (a.vec) {
                 if (cols > 0) *reinterpret_cast<uint2 *>(y) = make_uint2(lo, hi);
             } else {
@@ -214,7 +224,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
                 const bool ok = i < NS || mbar_wait(empty + 8 * s, phase, abort_flag, a.err);
                 lost = !__all_sync(0xffffffffu, ok);
                 if (lost) break;
-                if (elect_one()) {
+                if (!stalled(i) && elect_one()) {
                     const uint32_t dst = ring + s * L.stage;
                     if (i >= early) {
                         mbar_arrive_expect_tx(full + 8 * s, stage_bytes);
@@ -323,25 +333,23 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
                 if (lost) break;
                 tc_fence_after();
                 const float *sc = scales + d * BT + c0;
-                // With registers to spare a chunk's load is under way while the one before is added.
-                uint32_t v[S::kLoads][S::kChunk];
-                if (S::kLoads == 2 && left > 0) load_sums(lanes + d * BT + c0, v[0]);
                 #pragma unroll
                 for (int c = 0; c < S::kChunks; ++c) {
                     if (c * S::kChunk < left) {
-                        uint32_t (&now)[S::kChunk] = v[c % S::kLoads];
-                        if (S::kLoads == 1) load_sums(lanes + d * BT + c0 + c * S::kChunk, now);
-                        tc_wait_ld_of(now);
-                        if (S::kLoads == 2 && c + 1 < S::kChunks && (c + 1) * S::kChunk < left)
-                            load_sums(lanes + d * BT + c0 + (c + 1) * S::kChunk, v[(c + 1) % S::kLoads]);
+                        uint32_t v[S::kChunk];
+                        load_sums(lanes + d * BT + c0 + c * S::kChunk, v);
+                        float4 f[S::kChunk / 4];
+                        #pragma unroll
+                        for (int e = 0; e < S::kChunk / 4; ++e)
+                            f[e] = *reinterpret_cast<const float4 *>(sc + c * S::kChunk + 4 * e);
+                        tc_wait_ld_of(v);
                         #pragma unroll
                         for (int e = 0; e < S::kChunk; e += 4) {
-                            const float4 f = *reinterpret_cast<const float4 *>(sc + c * S::kChunk + e);
                             float *s = acc + c * S::kChunk + e;
-                            s[0] = fmaf(__uint_as_float(now[e]), f.x, s[0]);
-                            s[1] = fmaf(__uint_as_float(now[e + 1]), f.y, s[1]);
-                            s[2] = fmaf(__uint_as_float(now[e + 2]), f.z, s[2]);
-                            s[3] = fmaf(__uint_as_float(now[e + 3]), f.w, s[3]);
+                            s[0] = fmaf(__uint_as_float(v[e]), f[e / 4].x, s[0]);
+                            s[1] = fmaf(__uint_as_float(v[e + 1]), f[e / 4].y, s[1]);
+                            s[2] = fmaf(__uint_as_float(v[e + 2]), f[e / 4].z, s[2]);
+                            s[3] = fmaf(__uint_as_float(v[e + 3]), f[e / 4].w, s[3]);
                         }
                     }
                 }
@@ -436,36 +444,44 @@ cudaError_t launch_trans(const Fp8Plan &p, const Fp8Args &a, const CUtensorMap &
 
 }  // namespace
 
+// The forms compared by their time in microseconds, as they measured on 152 SMs with the
+// weights in L2 (2560 x 9728, 8192 x 8192, 19456 x 2560, 4096 x 2048 and 1024 x 4096, 144 to
+// 4096 rows): 3.5 for the launch and the first and last tile; a block of 128 that is summed
+// over 0.30 (64 rows and fewer; with two CTAs on an SM 0.45, 32 rows and fewer 0.36), 0.365
+// (128 rows), 0.45 (128 rows, 256 columns), 0.41 (a pair's 256 and 256); 1.8 between tiles;
+// sums that CTAs share 1 and 0.3 for each (few rows) or 2 and 1.6 (many).  Groups fill half of their last tile.
 Fp8Plan fp8_plan(int M, int out, int blocks, int groups, bool grouped, int sms) {
-    Fp8Plan p;
-    const int used = grouped && groups < M ? groups : grouped ? M : 1;      // groups with rows at most
+    const int used = !grouped ? 1 : groups < M ? groups : M;                // groups with rows at most
     const int rows = ceil_div(M, used);                                     // a group's, if they are even
-    p.split = 1;
-    if (rows > 128) {
-        const int out_tiles = ceil_div(out, 2 * kFp8Block);
-        // A pair fetches less of the weights and runs a tile in 0.84 to 0.9 of the time (198
-        // against 236 us for 4096 x 8192 x 8192, 142 against 129 us where 64 groups of 256 rows
-        // on average have 1000 summed columns), but its tiles hold 256 rows: a group's last is
-        // half empty on average.
-        auto waves = [&](int tile_rows, int places) {
-            const long long tiles = (long long)ceil_div(M, tile_rows) * out_tiles;
-            return ceil_div(tiles + (grouped ? (long long)used * out_tiles / 2 : 0), places);
-        };
-        if (0.88 * waves(256, sms / 2) < waves(128, sms)) p.split = 2;
-        p.size = 0, p.bt = 128, p.occupancy = 1;
-        const long long tiles = (long long)out_tiles * (grouped ? M / (128 * p.split) + used : ceil_div(M, 128 * p.split));
-        p.ctas = p.split * int(tiles < sms / p.split ? tiles : sms / p.split);
-        return p;
+    Fp8Plan best = {};
+    double best_time = 0;
+    auto consider = [&](int size, int tile_rows, bool pair, int split) {
+        Fp8Plan p = {};
+        p.size = size, p.pair = pair, p.occupancy = size && size <= 64 ? 2 : 1;
+        p.bt = size == 0 ? 128 : grouped ? size : (ceil_div(rows, ceil_div(rows, size)) + 15) & ~15;
+        const int per = pair ? 2 : split, slots = p.occupancy * sms / per;
+        const long long cols = ceil_div(out, size ? kFp8Block : 2 * kFp8Block);
+        const long long most = cols * (grouped ? M / tile_rows + used : ceil_div(M, tile_rows));
+        if (split > 1 && (most > slots || blocks < 2 * split)) return;
+        const long long tiles = grouped ? cols * (2LL * M / tile_rows + used + 1) / 2 : most;
+        const double block = pair ? 0.41 : size == 0 ? 0.45 : size == 128 ? 0.365
+                             : tiles * split <= sms ? 0.30 : size == 64 ? 0.45 : 0.36;
+        const int waves = ceil_div(tiles, slots);
+        const double time = waves * (ceil_div(blocks, split) * block + 1.8) +
+                            (split == 1 ? 0.0 : size ? 1.0 + 0.3 * split : 2.0 + 1.6 * split);
+        p.split = per;
+        p.ctas = per * int(most < slots ? most : slots);
+        if (best_time == 0 || time < best_time) best = p, best_time = time;
+    };
+    const int size = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    for (int split = 1; split <= kMaxCluster; split *= 2) consider(size, size, false, split);
+    if (rows <= 64) return best;
+    for (int split = 1; split <= kMaxCluster; split *= 2) {
+        consider(128, 128, false, split);
+        consider(0, 128, false, split);
     }
-    const int out_tiles = ceil_div(out, kFp8Block);
-    p.size = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
-    p.occupancy = p.size <= 64 ? 2 : 1;
-    p.bt = grouped ? p.size : (rows + 15) & ~15;
-    const int slots = p.occupancy * sms;
-    const long long tiles = (long long)out_tiles * (grouped ? M / p.bt + used : 1);      // at most
-    while (p.split < kMaxCluster && tiles * p.split * 2 <= slots && blocks >= 4 * p.split) p.split *= 2;
-    p.ctas = int(p.split > 1 ? tiles * p.split : tiles < slots ? tiles : slots);
-    return p;
+    consider(0, 256, true, 1);
+    return best;
 }
 
 cudaError_t launch_fp8_gemm(const Fp8Plan &p, Fp8Args a, const uint8_t *x, const uint8_t *w, int N, int K, bool trans,
@@ -502,3 +518,5 @@ cudaError_t launch_fp8_gemm(const Fp8Plan &p, Fp8Args a, const uint8_t *x, const
 }
 
 }  // namespace w4a16
+
+W4A16_STALL_ENTRY(w4a16_test_stall_few)

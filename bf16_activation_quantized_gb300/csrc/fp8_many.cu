@@ -10,6 +10,9 @@
 // weights, which the pair's MMAs (cta_group::2) read from both.  That halves what an SM
 // has to fetch of the weights.
 //
+// With few tiles `split` CTAs (a cluster) share one, each a run of the blocks that are
+// summed over; the parts stand in shared memory and are added in the order of the CTAs.
+//
 // Warps: 0 copies (TMA) the tiles, 1 issues the MMAs, 4 to 11 add.
 #include "async.cuh"
 #include "common.cuh"
@@ -18,6 +21,7 @@
 #include "internal.h"
 #include "launch.cuh"
 #include "lora.cuh"
+#include "stall.cuh"
 #include "tc05.cuh"
 
 namespace w4a16 {
@@ -28,6 +32,7 @@ constexpr int kManyThreads = 384, kAddWarp0 = 4, kAddWarps = 8;
 // Registers a thread of the first four warps and of the adding ones: the launch's
 // (168 x 384) are what the two shares draw on.
 constexpr int kRegsIn = 72, kRegsAdd = 216;
+constexpr int kSumBytes = 128 * 256 * 4;           // a tile's fp32 sums
 static_assert(128 * kRegsIn + 256 * kRegsAdd <= 168 * kManyThreads, "registers");
 
 constexpr int kRows = 128, kCols = 256;
@@ -39,6 +44,7 @@ struct ManyShape {
     static constexpr int kStage = PAIR ? 2 * kTile : 3 * kTile;
     static constexpr int kStages = PAIR ? 6 : 4;
     static constexpr int kOffStore = kStages * kStage;
+    static_assert(kSumBytes <= kOffStore, "a tile's sums lie over the ring");
     static constexpr int kOffBar = kOffStore + kAddWarps * 32 * 64;
     static constexpr int kOffTab = kOffBar + (2 * kStages + 5) * 8 + 8;
     static size_t smem(int groups, bool grouped) { return kOffTab + (grouped ? 2 * (groups + 1) * 4 : 0) + 1024; }
@@ -84,6 +90,44 @@ __device__ __forceinline__ float fetch(const float *p) {
     return v;
 }
 
+// A tile's sums in shared memory: pieces of 16 bytes placed so that eight rows' meet in no bank.
+__device__ __forceinline__ float *sum_at(unsigned char *smem, int row, int piece) {
+    return reinterpret_cast<float *>(smem) + row * kCols + 4 * (piece ^ (row & 7));
+}
+
+// One warp: rows first, first + SPLIT * warps, ... of a tile that SPLIT CTAs share, eight
+// columns a lane.
+template <int SPLIT>
+__device__ __forceinline__ void join_rows(const Fp8Args &a, const ManyTile &t, unsigned char *smem, int first, int lost) {
+    constexpr int kParts = SPLIT < 4 ? SPLIT : 4;
+    const int lane = threadIdx.x % 32, col = t.tile * kCols + 8 * lane;
+    for (int r = first; r < t.rows; r += SPLIT * (kManyThreads / 32)) {
+        float s[8];
+        #pragma unroll
+        for (int k0 = 0; k0 < SPLIT; k0 += kParts) {
+            float4 v[kParts][2];
+            #pragma unroll
+            for (int k = 0; k < kParts; ++k)
+                #pragma unroll
+                for (int h = 0; h < 2; ++h) v[k][h] = ld_cluster4(sum_at(smem, r, 2 * lane + h), k0 + k);
+            #pragma unroll
+            for (int k = 0; k < kParts; ++k)
+                #pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float u[4] = {v[k][h].x, v[k][h].y, v[k][h].z, v[k][h].w};
+                    #pragma unroll
+                    for (int e = 0; e < 4; ++e) s[4 * h + e] = k0 + k == 0 ? u[e] : s[4 * h + e] + u[e];
+                }
+        }
+        if (lost)
+            #pragma unroll
+            for (int e = 0; e < 8; ++e) s[e] = __int_as_float(0x7fffffff);
+        uint16_t *y = a.y + (long long)(t.row0 + r) * a.out + col;
+        store_cols8(y, a.out - col, a.vec, make_uint4(pack_bf16x2_rn(s[0], s[1]), pack_bf16x2_rn(s[2], s[3]),
+                                                      pack_bf16x2_rn(s[4], s[5]), pack_bf16x2_rn(s[6], s[7])));
+    }
+}
+
 template <bool TRANS, bool PAIR>
 __global__ void __launch_bounds__(kManyThreads, 1)
 fp8_many_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w,
@@ -95,6 +139,8 @@ fp8_many_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
     __shared__ int s_abort;
     __shared__ uint32_t s_tmem;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, part = PAIR ? cluster_rank() : 0;
+    const int split = PAIR ? 1 : cluster_size(), share = PAIR ? 0 : cluster_rank();
+    const int b0 = int((long long)a.blocks * share / split), b1 = int((long long)a.blocks * (share + 1) / split);
     const uint32_t ring = smem_u32(smem), full = ring + S::kOffBar, empty = full + 8 * NS;
     const uint32_t dfull = empty + 8 * NS, dempty = dfull + 16, drained = dempty + 16;
     int *tab_rows = reinterpret_cast<int *>(smem + S::kOffTab), *tab_tiles = tab_rows + a.groups + 1;
@@ -125,7 +171,7 @@ fp8_many_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
     tc_fence_after();
     const uint32_t tmem = s_tmem;
     volatile int *abort_flag = &s_abort;
-    const int id0 = PAIR ? blockIdx.x / 2 : blockIdx.x, step = PAIR ? gridDim.x / 2 : gridDim.x;
+    const int per = PAIR ? 2 : split, id0 = int(blockIdx.x) / per, step = int(gridDim.x) / per;
     ManyTile t;
     if (warp < kAddWarp0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIn));
@@ -133,12 +179,12 @@ fp8_many_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
         int i = 0;
         if (warp == 0) {
             for (int id = id0; !lost && many_tile<PAIR>(a, tab_rows, tab_tiles, id, part, t); id += step)
-                for (int b = 0; b < a.blocks; ++b, ++i) {
+                for (int b = b0; b < b1; ++b, ++i) {
                     const int s = i % NS;
                     const bool ok = i < NS || mbar_wait(empty + 8 * s, (i / NS - 1) & 1, abort_flag, a.err);
                     lost = !__all_sync(0xffffffffu, ok);
                     if (lost) break;
-                    if (elect_one()) {
+                    if (!stalled(i) && elect_one()) {
                         const uint32_t dst = ring + s * S::kStage;
                         const int at = b * kFp8Block, col = t.tile * kCols + part * kFp8Block;
                         if (PAIR) {
@@ -163,7 +209,7 @@ fp8_many_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
         } else if (warp == 1 && part == 0) {
             constexpr uint32_t idesc = tc_idesc_e4m3((PAIR ? 2 : 1) * kRows, kCols) | (TRANS ? kTcBMajorN : 0u);
             for (int id = id0; !lost && many_tile<PAIR>(a, tab_rows, tab_tiles, id, part, t); id += step)
-                for (int b = 0; b < a.blocks; ++b, ++i) {
+                for (int b = b0; b < b1; ++b, ++i) {
                     const int s = i % NS, d = i & 1;
                     const bool ok = mbar_wait(full + 8 * s, (i / NS) & 1, abort_flag, a.err) &&
                                     (i < 2 || mbar_wait(dempty + 8 * d, (i / 2 - 1) & 1, abort_flag, a.err));
@@ -205,11 +251,11 @@ fp8_many_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
         // Rows past the tile's and columns past the last are not stored: any scale does.
         auto enter = [&]() {
             const int wt = min(2 * t.tile + half, (a.out - 1) / kFp8Block);
-            xs = a.xs + min(t.row0 + row, a.M - 1);
-            ws = a.ws + t.group * a.ws_group + (long long)wt * a.ws_tile;
+            xs = a.xs + (long long)b0 * a.M + min(t.row0 + row, a.M - 1);
+            ws = a.ws + t.group * a.ws_group + (long long)wt * a.ws_tile + (long long)b0 * a.ws_block;
             #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
-                if (u < a.blocks) fx[u] = fetch(xs), fw[u] = fetch(ws);
+                if (b0 + u < b1) fx[u] = fetch(xs), fw[u] = fetch(ws);
                 xs += a.M, ws += a.ws_block;
             }
         };
@@ -221,13 +267,13 @@ fp8_many_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
             float acc[kFp8Block];
             #pragma unroll
             for (int j = 0; j < kFp8Block; ++j) acc[j] = 0.f;
-            for (int b = 0; b < a.blocks && !lost; b += kAhead) {
+            for (int b = b0; b < b1 && !lost; b += kAhead) {
                 #pragma unroll
                 for (int u = 0; u < kAhead; ++u) {
-                    if (b + u >= a.blocks || lost) break;
+                    if (b + u >= b1 || lost) break;
                     const int d = i & 1;
                     const float scale = fx[u] * fw[u];
-                    if (b + u + kAhead < a.blocks) fx[u] = fetch(xs), fw[u] = fetch(ws);
+                    if (b + u + kAhead < b1) fx[u] = fetch(xs), fw[u] = fetch(ws);
                     xs += a.M, ws += a.ws_block;
                     lost = !__all_sync(0xffffffffu, mbar_wait(dfull + 8 * d, (i / 2) & 1, abort_flag, a.err));
                     if (lost) break;
@@ -264,6 +310,14 @@ fp8_many_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
             if (lost) {
                 #pragma unroll
                 for (int j = 0; j < kFp8Block; ++j) acc[j] = __int_as_float(0x7fffffff);
+            }
+            if (!PAIR && split > 1) {
+                // over the ring, whose tiles this one's last MMAs have read; a cluster has one tile
+                #pragma unroll
+                for (int q = 0; q < kFp8Block / 4; ++q)
+                    *reinterpret_cast<float4 *>(sum_at(smem, row, half * (kFp8Block / 4) + q)) =
+                        make_float4(acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]);
+                break;
             }
             // 32 rows and 32 columns at a time through shared memory (16-byte pieces placed so
             // that eight rows' meet in no bank).
@@ -302,6 +356,22 @@ fp8_many_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
     tc_fence_before();
     __syncthreads();
     if (PAIR) cluster_arrive(), cluster_wait();          // the pair's MMAs have read both CTAs' memory
+    if (!PAIR && split > 1) {
+        cluster_arrive();
+        cluster_wait();
+        int lost = 0;                                    // a wait ran out: copies may have landed on the sums
+        #pragma unroll
+        for (int k = 0; k < kMaxCluster; ++k)
+            if (k < split) lost |= ld_cluster1(&s_abort, k);
+        if (many_tile<PAIR>(a, tab_rows, tab_tiles, id0, part, t)) {
+            const int first = share + split * warp;
+            if (split == 2) join_rows<2>(a, t, smem, first, lost);
+            else if (split == 4) join_rows<4>(a, t, smem, first, lost);
+            else join_rows<8>(a, t, smem, first, lost);
+        }
+        cluster_arrive();                                // the others have read this CTA's part
+        cluster_wait();
+    }
     tc_fence_after();
     if (warp == 1) {
         if (PAIR) tc_dealloc_pair(tmem, 2 * kCols);
@@ -315,15 +385,17 @@ cudaError_t launch_many_form(const Fp8Plan &p, const Fp8Args &a, const CUtensorM
     const cudaError_t e = allow_smem<fp8_many_kernel<TRANS, PAIR>>(kTensorMaxSmem - 256);
     if (e != cudaSuccess) return e;
     return launch_chained(fp8_many_kernel<TRANS, PAIR>, dim3(p.ctas), kManyThreads,
-                          ManyShape<PAIR>::smem(a.groups, a.m_sizes != nullptr), PAIR ? 2 : 1, s, tx, tw, a);
+                          ManyShape<PAIR>::smem(a.groups, a.m_sizes != nullptr), p.split, s, tx, tw, a);
 }
 
 }  // namespace
 
 cudaError_t launch_fp8_many(const Fp8Plan &p, const Fp8Args &a, const CUtensorMap &tx, const CUtensorMap &tw,
                             bool trans, cudaStream_t s) {
-    if (p.split == 2) return trans ? launch_many_form<true, true>(p, a, tx, tw, s) : launch_many_form<false, true>(p, a, tx, tw, s);
+    if (p.pair) return trans ? launch_many_form<true, true>(p, a, tx, tw, s) : launch_many_form<false, true>(p, a, tx, tw, s);
     return trans ? launch_many_form<true, false>(p, a, tx, tw, s) : launch_many_form<false, false>(p, a, tx, tw, s);
 }
 
 }  // namespace w4a16
+
+W4A16_STALL_ENTRY(w4a16_test_stall_many)

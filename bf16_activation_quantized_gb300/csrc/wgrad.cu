@@ -22,6 +22,7 @@
 #include "internal.h"
 #include "launch.cuh"
 #include "lora.cuh"
+#include "stall.cuh"
 #include "tc05.cuh"
 #include "w4a16.h"
 
@@ -137,7 +138,7 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmap_dy, const __grid_c
                 lost = !__all_sync(0xffffffffu, ok);
                 if (lost) break;
                 const bool last = (t.rows - r < kRowStep) && t.rows % 16;
-                if (elect_one()) {
+                if (!stalled(i) && elect_one()) {
                     const uint32_t dst = ring + s * kWgStage, bar = (last ? own : even) + 8 * s;
                     if (last) mbar_arrive_expect_tx(tail + 8 * s, kWgStage);
                     else if (half == 0) mbar_arrive_expect_tx(full + 8 * s, 2 * kWgStage);
@@ -393,3 +394,5 @@ extern "C" w4a16_status w4a16_gemm_grouped_wgrad(const w4a16_bf16 *dY, const w4a
                                         : launch_grouped_wgrad<false>(a, dY, X, sms, s);
     return e == cudaSuccess ? W4A16_OK : W4A16_ERR_CUDA;
 }
+
+W4A16_STALL_ENTRY(w4a16_test_stall_wgrad)
