@@ -464,10 +464,10 @@ Fp8Plan fp8_plan(int M, int out, int blocks, int groups, bool grouped, int sms) 
         const long long most = cols * (grouped ? M / tile_rows + used : ceil_div(M, tile_rows));
         if (split > 1 && (most > slots || blocks < 2 * split)) return;
         const long long tiles = grouped ? cols * (2LL * M / tile_rows + used + 1) / 2 : most;
-        const double block = pair ? 0.41 : size == 0 ? 0.45 : size == 128 ? 0.365
+        const double block = pair ? 0.41 : size == 0 ? 0.46 : size == 128 ? 0.365
                              : tiles * split <= sms ? 0.30 : size == 64 ? 0.45 : 0.36;
         const int waves = ceil_div(tiles, slots);
-        const double time = waves * (ceil_div(blocks, split) * block + 1.8) +
+        const double time = waves * (ceil_div(blocks, split) * block + (size ? 1.8 : 1.0)) +
                             (split == 1 ? 0.0 : size ? 1.0 + 0.3 * split : 2.0 + 1.6 * split);
         p.split = per;
         p.ctas = per * int(most < slots ? most : slots);

@@ -13,7 +13,10 @@
 // With few tiles `split` CTAs (a cluster) share one, each a run of the blocks that are
 // summed over; the parts stand in shared memory and are added in the order of the CTAs.
 //
-// Warps: 0 copies (TMA) the tiles, 1 issues the MMAs, 4 to 11 add.
+// A tile's rounded sums go through shared memory to two warps that store them while the
+// next tile's blocks are added; the last tile's are stored by the adding warps too.
+//
+// Warps: 0 copies (TMA) the tiles, 1 issues the MMAs, 2 and 3 store, 4 to 11 add.
 #include "async.cuh"
 #include "common.cuh"
 #include "fp8.cuh"
@@ -42,11 +45,12 @@ constexpr int kAhead = 4;                          // blocks whose scales are fe
 template <bool PAIR>
 struct ManyShape {
     static constexpr int kStage = PAIR ? 2 * kTile : 3 * kTile;
-    static constexpr int kStages = PAIR ? 6 : 4;
-    static constexpr int kOffStore = kStages * kStage;
+    static constexpr int kStages = PAIR ? 4 : 3;
+    static constexpr int kOffStore = kStages * kStage;                       // a tile's results: rows of 512 bytes
     static_assert(kSumBytes <= kOffStore, "a tile's sums lie over the ring");
-    static constexpr int kOffBar = kOffStore + kAddWarps * 32 * 64;
-    static constexpr int kOffTab = kOffBar + (2 * kStages + 5) * 8 + 8;
+    static constexpr int kOffBar = kOffStore + kRows * kCols * 2;
+    static constexpr int kOffTab = kOffBar + (2 * kStages + 7) * 8 + 8;
+    static_assert(kOffTab + 2 * (kMaxGroups + 1) * 4 + 1024 <= kTensorMaxSmem - 256, "shared memory");
     static size_t smem(int groups, bool grouped) { return kOffTab + (grouped ? 2 * (groups + 1) * 4 : 0) + 1024; }
 };
 
@@ -128,6 +132,29 @@ __device__ __forceinline__ void join_rows(const Fp8Args &a, const ManyTile &t, u
     }
 }
 
+// One warp: rows first, first + step, ... of a tile from shared memory, a row of 512 bytes
+// at a time.
+__device__ __forceinline__ void store_rows(const Fp8Args &a, const ManyTile &t, const unsigned char *store, int first,
+                                           int step, bool lost) {
+    constexpr int kAtOnce = 8;
+    const int lane = threadIdx.x % 32, col = t.tile * kCols + 8 * lane;
+    uint16_t *y = a.y + (long long)t.row0 * a.out + col;
+    #pragma unroll 1
+    for (int r0 = first; r0 < t.rows; r0 += kAtOnce * step) {
+        uint4 v[kAtOnce];
+        #pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+            const int r = (r0 + j * step) % kRows;
+            v[j] = *reinterpret_cast<const uint4 *>(store + r * 512 + ((lane ^ (r & 7)) << 4));
+            // a wait that ran out: this tile and the CTA's later ones are NaN
+            if (lost) v[j] = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+        }
+        #pragma unroll
+        for (int j = 0; j < kAtOnce; ++j)
+            if (r0 + j * step < t.rows) store_cols8(y + (long long)(r0 + j * step) * a.out, a.out - col, a.vec, v[j]);
+    }
+}
+
 template <bool TRANS, bool PAIR>
 __global__ void __launch_bounds__(kManyThreads, 1)
 fp8_many_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w,
@@ -142,12 +169,12 @@ fp8_many_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
     const int split = PAIR ? 1 : cluster_size(), share = PAIR ? 0 : cluster_rank();
     const int b0 = int((long long)a.blocks * share / split), b1 = int((long long)a.blocks * (share + 1) / split);
     const uint32_t ring = smem_u32(smem), full = ring + S::kOffBar, empty = full + 8 * NS;
-    const uint32_t dfull = empty + 8 * NS, dempty = dfull + 16, drained = dempty + 16;
+    const uint32_t dfull = empty + 8 * NS, dempty = dfull + 16, sfull = dempty + 16, sempty = sfull + 8, drained = sempty + 8;
     int *tab_rows = reinterpret_cast<int *>(smem + S::kOffTab), *tab_tiles = tab_rows + a.groups + 1;
     if (threadIdx.x == 0) {
         for (int i = 0; i < NS; ++i) mbar_init(full + 8 * i, 1), mbar_init(empty + 8 * i, 1);
         for (int i = 0; i < 2; ++i) mbar_init(dfull + 8 * i, 1), mbar_init(dempty + 8 * i, (PAIR ? 2 : 1) * kAddWarps);
-        mbar_init(drained, 1);
+        mbar_init(sfull, kAddWarps), mbar_init(sempty, 2), mbar_init(drained, 1);
         s_abort = 0;
         fence_barrier_init();
     }
@@ -237,13 +264,23 @@ fp8_many_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
             }
             __syncwarp();
             drain_wait(drained, 0);
+        } else if (warp >= 2 && split == 1) {
+            for (int id = id0; many_tile<PAIR>(a, tab_rows, tab_tiles, id, part, t); ++i) {
+                const ManyTile now = t;
+                id += step;
+                const bool last = !many_tile<PAIR>(a, tab_rows, tab_tiles, id, part, t);
+                lost = lost || !__all_sync(0xffffffffu, mbar_wait(sfull, i & 1, abort_flag, a.err));
+                store_rows(a, now, smem + S::kOffStore, warp - 2, last ? 2 + kAddWarps : 2, lost);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sempty);
+                if (last) break;
+            }
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsAdd));
         const int sub = warp % 4, half = (warp - kAddWarp0) / 4;
         const uint32_t from = tmem + (uint32_t(32 * sub) << 16) + half * kFp8Block;
         const uint32_t done = PAIR ? cluster_address(dempty, 0) : dempty;
-        unsigned char *store = smem + S::kOffStore + (warp - kAddWarp0) * 32 * 64;
         const int row = 32 * sub + lane;
         // This lane's scales of x and of the weights, fetched kAhead blocks before their use.
         float fx[kAhead], fw[kAhead];
@@ -259,11 +296,12 @@ fp8_many_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
                 xs += a.M, ws += a.ws_block;
             }
         };
-        int i = 0;
+        int i = 0, tiles = 0;
         bool lost = false, more = many_tile<PAIR>(a, tab_rows, tab_tiles, id0, part, t);
         if (more) enter();
-        for (int id = id0; more; ) {
-            const ManyTile at = t;
+        ManyTile now = t;
+        for (int id = id0; more;) {
+            now = t;
             float acc[kFp8Block];
             #pragma unroll
             for (int j = 0; j < kFp8Block; ++j) acc[j] = 0.f;
@@ -302,55 +340,40 @@ fp8_many_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
                     }
                 }
             }
-            // The next tile's first scales come while this one is stored.
+            // The next tile's first scales come while this one is rounded.
             id += step;
             more = many_tile<PAIR>(a, tab_rows, tab_tiles, id, part, t);
             if (more) enter();
-            // A wait that ran out: this tile and the CTA's later ones are NaN.
-            if (lost) {
-                #pragma unroll
-                for (int j = 0; j < kFp8Block; ++j) acc[j] = __int_as_float(0x7fffffff);
-            }
             if (!PAIR && split > 1) {
                 // over the ring, whose tiles this one's last MMAs have read; a cluster has one tile
+                // (where a wait ran out the join finds the flag)
                 #pragma unroll
                 for (int q = 0; q < kFp8Block / 4; ++q)
                     *reinterpret_cast<float4 *>(sum_at(smem, row, half * (kFp8Block / 4) + q)) =
                         make_float4(acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]);
                 break;
             }
-            // 32 rows and 32 columns at a time through shared memory (16-byte pieces placed so
-            // that eight rows' meet in no bank).
+            // This row's 128 columns to the store warps, in pieces of 16 bytes placed so that
+            // eight rows' meet in no bank.  Where a wait ran out they write NaN.
+            if (tiles > 0 && !lost)
+                lost = !__all_sync(0xffffffffu, mbar_wait(sempty, (tiles - 1) & 1, abort_flag, a.err));
+            ++tiles;
+            if (lost) continue;
             #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const int col = at.tile * kCols + half * kFp8Block + 32 * c;
+            for (int q = 0; q < kFp8Block / 8; ++q) {
+                uint32_t p[4];
                 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t p[4];
-                    #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        p[j] = pack_bf16x2_rn(acc[32 * c + 8 * q + 2 * j], acc[32 * c + 8 * q + 2 * j + 1]);
-                    *reinterpret_cast<uint4 *>(store + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) =
-                        make_uint4(p[0], p[1], p[2], p[3]);
-                }
-                __syncwarp();
-                uint16_t *y = a.y + (long long)(at.row0 + 32 * sub) * a.out + col;
-                const int left = at.rows - 32 * sub;
-                if (a.vec) {
-                    #pragma unroll
-                    for (int k = 0; k < 32; k += 8) {
-                        const int r = k + lane / 4, q = lane % 4;
-                        if (r < left && col + 8 * q < a.out)
-                            *reinterpret_cast<uint4 *>(y + (long long)r * a.out + 8 * q) =
-                                *reinterpret_cast<const uint4 *>(store + r * 64 + ((q ^ ((r >> 1) & 3)) << 4));
-                    }
-                } else if (col + lane < a.out) {
-                    for (int r = 0; r < min(left, 32); ++r)
-                        y[(long long)r * a.out + lane] = *reinterpret_cast<const uint16_t *>(
-                            store + r * 64 + (((lane / 8) ^ ((r >> 1) & 3)) << 4) + 2 * (lane % 8));
-                }
-                __syncwarp();                            // tcgen05.ld takes the whole warp
+                for (int j = 0; j < 4; ++j) p[j] = pack_bf16x2_rn(acc[8 * q + 2 * j], acc[8 * q + 2 * j + 1]);
+                *reinterpret_cast<uint4 *>(smem + S::kOffStore + row * 512 + (((half * 16 + q) ^ (row & 7)) << 4)) =
+                    make_uint4(p[0], p[1], p[2], p[3]);
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(sfull);
+        }
+        // Nothing is left to add: these warps help to store the last tile.
+        if (split == 1 && tiles > 0) {
+            lost = lost || !__all_sync(0xffffffffu, mbar_wait(sfull, (tiles - 1) & 1, abort_flag, a.err));
+            store_rows(a, now, smem + S::kOffStore, warp - kAddWarp0 + 2, 2 + kAddWarps, lost);
         }
     }
     tc_fence_before();
