@@ -14,8 +14,9 @@
 // lands in one of several buffers of tensor memory; eight warps read it, multiply by
 // both scales and add in registers, in fp32, while the next block's MMAs run.
 //
-// Warps: 0 copies (TMA) the tiles, 1 issues the MMAs, 2 and 3 form the products of the
-// scales, 4 to 11 add.
+// Warps: 0 copies (TMA) the tiles, 1 and 2 issue the MMAs of every second block each (one
+// warp takes 480 cycles for a block's waits, four MMAs and two commits), 3 forms the
+// products of the scales, 4 to 11 add.
 #include "async.cuh"
 #include "common.cuh"
 #include "fp8.cuh"
@@ -170,7 +171,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
         for (int i = 0; i < NS; ++i) mbar_init(full + 8 * i, 1), mbar_init(empty + 8 * i, 1);
         for (int i = 0; i < kSlots; ++i)                   // full: the MMAs' end and the scales
             mbar_init(dfull + 8 * i, 2), mbar_init(dempty + 8 * i, kAddWarps);
-        mbar_init(drained, 1);
+        mbar_init(drained, 2);
         s_abort = 0;
         fence_barrier_init();
     }
@@ -239,17 +240,21 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
         // Every copy lands before the CTA ends.
         if (*abort_flag)
             for (int u = i > NS ? i - NS : 0; u < i; ++u) drain_wait(full + 8 * (u % NS), (u / NS) & 1);
-    } else if (warp == 1) {
+    } else if (warp <= 2) {
         // The slot is a counter: a division by the ring's depth would cost more than a block's MMAs.
-        int i = 0, s = 0;
+        int i = 0, s = warp - 1;
         uint32_t phase = 0;
         bool lost = false;
         for (int id = id0; !lost && fp8_tile(a, tab_rows, tab_tiles, id, t); id += step) {
             const uint32_t idesc = tc_idesc_e4m3(kFp8Block, (t.rows + 15) & ~15) | (TRANS ? kTcAMajorM : 0u);
             for (int b = b0; b < b1; ++b, ++i) {
+                if ((i & 1) != warp - 1) continue;
                 const int d = i % kSlots;
-                bool ok = mbar_wait(full + 8 * s, phase, abort_flag, a.err);
-                ok = ok && (i < kSlots || mbar_wait(dempty + 8 * d, (i / kSlots - 1) & 1, abort_flag, a.err));
+                // The sums' slot first: with an odd ring this warp meets a ring slot every second lap,
+                // and its parity would also fit two laps before.  The block that had the sums' slot
+                // has been added, so the ring slot's lap before, kSlots blocks back at least, is over.
+                bool ok = i < kSlots || mbar_wait(dempty + 8 * d, (i / kSlots - 1) & 1, abort_flag, a.err);
+                ok = ok && mbar_wait(full + 8 * s, phase, abort_flag, a.err);
                 lost = !__all_sync(0xffffffffu, ok);
                 if (lost) break;
                 tc_fence_after();
@@ -264,22 +269,21 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
                     tc_commit(dfull + 8 * d);
                 }
                 __syncwarp();
-                if (++s == NS) s = 0, phase ^= 1;
+                s += 2;
+                if (s >= NS) s -= NS, phase ^= 1;
             }
         }
         if (elect_one()) tc_commit(drained);
         __syncwarp();
         drain_wait(drained, 0);
     } else if (warp < kAddWarp0) {
-        // Products of the scales, one block after the other: this warp every second one, fetched
-        // kAhead of its blocks before their use.
+        // Products of the scales, fetched kAhead blocks before their use.
         constexpr int kEach = BT < 32 ? 1 : BT / 32, kAhead = S::kAhead;
         int i = 0;
         bool lost = false;
         for (int id = id0; !lost && fp8_tile(a, tab_rows, tab_tiles, id, t); id += step) {
-            const int first = b0 + ((warp ^ i) & 1);
-            const float *ws = a.ws + t.group * a.ws_group + (long long)t.tile * a.ws_tile + (long long)first * a.ws_block;
-            const float *xs = a.xs + (long long)first * a.M + t.row0;
+            const float *ws = a.ws + t.group * a.ws_group + (long long)t.tile * a.ws_tile + (long long)b0 * a.ws_block;
+            const float *xs = a.xs + (long long)b0 * a.M + t.row0;
             int r[kEach];
             #pragma unroll
             for (int j = 0; j < kEach; ++j) r[j] = min(lane + 32 * j, t.rows - 1);   // no row's scale: never used
@@ -291,14 +295,14 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
             };
             #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
-                if (first + 2 * u < b1) load(u);
-                ws += 2 * a.ws_block, xs += 2LL * a.M;
+                if (b0 + u < b1) load(u);
+                ws += a.ws_block, xs += a.M;
             }
-            for (int b = first; b < b1 && !lost; b += 2 * kAhead) {
+            for (int b = b0; b < b1 && !lost; b += kAhead) {
                 #pragma unroll
                 for (int u = 0; u < kAhead; ++u) {
-                    if (b + 2 * u >= b1) break;
-                    const int k = i + b + 2 * u - b0, s = k % kSlots;
+                    if (b + u >= b1) break;
+                    const int k = i + b + u - b0, s = k % kSlots;
                     const bool ok = k < kSlots || mbar_wait(dempty + 8 * s, (k / kSlots - 1) & 1, abort_flag, a.err);
                     lost = !__all_sync(0xffffffffu, ok);
                     if (lost) break;
@@ -307,8 +311,8 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
                         if (BT >= 32 || lane < BT) scales[s * BT + lane + 32 * j] = v[u][j] * w[u];
                     __syncwarp();
                     if (lane == 0) mbar_arrive(dfull + 8 * s);
-                    if (b + 2 * (u + kAhead) < b1) load(u);
-                    ws += 2 * a.ws_block, xs += 2LL * a.M;
+                    if (b + u + kAhead < b1) load(u);
+                    ws += a.ws_block, xs += a.M;
                 }
             }
             i += b1 - b0;
@@ -464,8 +468,8 @@ Fp8Plan fp8_plan(int M, int out, int blocks, int groups, bool grouped, int sms) 
         const long long most = cols * (grouped ? M / tile_rows + used : ceil_div(M, tile_rows));
         if (split > 1 && (most > slots || blocks < 2 * split)) return;
         const long long tiles = grouped ? cols * (2LL * M / tile_rows + used + 1) / 2 : most;
-        const double block = pair ? 0.41 : size == 0 ? 0.46 : size == 128 ? 0.365
-                             : tiles * split <= sms ? 0.30 : size == 64 ? 0.45 : 0.36;
+        const double block = pair ? 0.41 : size == 0 ? 0.46 : size == 128 ? 0.36
+                             : tiles * split <= sms ? (size == 64 ? 0.29 : 0.20) : size == 64 ? 0.46 : 0.28;
         const int waves = ceil_div(tiles, slots);
         const double time = waves * (ceil_div(blocks, split) * block + (size ? 1.8 : 1.0)) +
                             (split == 1 ? 0.0 : size ? 1.0 + 0.3 * split : 2.0 + 1.6 * split);
@@ -507,6 +511,8 @@ cudaError_t launch_fp8_gemm(const Fp8Plan &p, Fp8Args a, const uint8_t *x, const
     const int rest = fp8_smem(p.size, p.bt, 0, a.groups).total + 64 * 16;
     a.stages = (budget - rest) / (kWTile + p.bt * kFp8Block);
     if (a.stages > 16) a.stages = 16;
+    // An odd ring has to hold as many blocks as there are slots for sums (see the MMA warps).
+    if (a.stages % 2 && a.stages < kSlots) --a.stages;
     if (a.stages < 2) return cudaErrorInvalidValue;
     const size_t smem = fp8_smem(p.size, p.bt, a.stages, a.groups).total + 1024;
     switch (p.size) {

@@ -160,3 +160,71 @@ def test_kernels_wait_before_they_let_the_next_one_start(name, kernels):
     assert len(starts) == kernels
     for at in starts:
         assert 0 < text.index("pdl_wait();", at) < text.index("pdl_launch_dependents();", at)
+
+
+def test_mma_warps_wait_for_the_sums_before_the_ring():
+    """Two warps issue every second block's MMAs.  With an odd ring each meets a ring slot every
+    second lap, where the slot's parity alone also fits two laps before; the wait for the
+    block kSlots back rules that out, if it comes first and the ring is not shorter."""
+    text = source("fp8_gemm.cu")
+    part = text[text.index("} else if (warp <= 2) {"):text.index("} else if (warp < kAddWarp0) {")]
+    assert part.index("mbar_wait(dempty") < part.index("mbar_wait(full")
+    assert "if (a.stages % 2 && a.stages < kSlots) --a.stages;" in text
+
+
+def walk(ring, slots, seed, waits, blocks=23):
+    """The waits of the producer, the two MMA warps and the adding warps on a model of the
+    barriers, in a random order that they allow, copies landing in any order: fails where a
+    warp passes a wait whose phase is not over.  waits: an MMA warp's, in order."""
+    full, empty, dfull, dempty = [0] * ring, [0] * ring, [0] * slots, [0] * slots        # phases over
+    loads, add, mma, at, lap, step = 0, 0, [0, 1], [0, 1], [0, 0], [0, 0]
+    issued, flying, landed = set(), [], set()
+
+    def over(phases, parity):
+        return phases % 2 != parity
+
+    for _ in range(8000):
+        seed = (seed * 1103515245 + 12345) % 2**31
+        who = (seed >> 16) % 5
+        if who == 0 and loads < blocks:
+            if loads < ring or over(empty[loads % ring], (loads // ring - 1) % 2):
+                assert all(b % ring != loads % ring for b in flying), (ring, loads)
+                flying.append(loads)
+                loads += 1
+        elif who == 4 and flying:
+            b = flying.pop((seed >> 8) % len(flying))
+            full[b % ring] += 1
+            landed.add(b)
+        elif who in (1, 2) and mma[who - 1] < blocks:
+            w, i = who - 1, mma[who - 1]
+            d, s = i % slots, at[w]
+            if waits[step[w]] == "dempty":
+                step[w] += i < slots or over(dempty[d], (i // slots - 1) % 2)
+            else:
+                step[w] += over(full[s], lap[w])
+            if step[w] == 2:
+                assert i in landed, (ring, i)
+                issued.add(i)
+                empty[s] += 1
+                dfull[d] += 1
+                step[w], mma[w], at[w] = 0, i + 2, s + 2
+                if at[w] >= ring:
+                    at[w] -= ring
+                    lap[w] ^= 1
+        elif who == 3 and add < blocks and over(dfull[add % slots], add // slots % 2):
+            assert add in issued, (ring, add)
+            dempty[add % slots] += 1
+            add += 1
+    assert add == blocks, (ring, add)
+
+
+def test_ring_walks_never_pass_a_landing_copy():
+    slots = int(re.search(r"kSlots = (\d+);", source("fp8_gemm.cu")).group(1))
+    for ring in (2, 4, 5, 6, 7, 9, 16):
+        for order in range(40):
+            walk(ring, slots, order * 7919 + ring, ("dempty", "full"))
+    # the model sees the other order's fault, and that of a shorter odd ring
+    for ring, waits in ((5, ("full", "dempty")), (3, ("dempty", "full"))):
+        with pytest.raises(AssertionError):
+            for order in range(200):
+                walk(ring, slots, order * 7919 + ring, waits)
