@@ -8,6 +8,18 @@ namespace w4a16 {
 
 __device__ __forceinline__ int row_tiles(int rows, int bt) { return (rows + bt - 1) / bt; }
 
+// Tile r of a grid of `rows` by `cols`, in bands of kBand rows, down a band's columns: the
+// tiles that run at the same time form a block and share both operands' tiles in L2.  (Row
+// by row, the weight gradient of 4096 x 8192 x 8192 takes 304 us instead of 284, the 8-bit
+// product of these sizes 193 instead of 187; bands of 4, 8 and 32 lie between.)
+constexpr int kBand = 16;
+__device__ __forceinline__ void banded(int r, int rows, int cols, int &row, int &col) {
+    const int band = r / (kBand * cols), in_band = r - band * (kBand * cols);
+    const int height = min(kBand, rows - band * kBand);
+    col = in_band / height;
+    row = band * kBand + in_band - col * height;
+}
+
 // One warp: tab_rows[g] and tab_tiles[g], the first row and the first tile of each group
 // (unless nullptr) and the ends in [groups], where a group of n rows has ceil(n / bt) * per tiles.  A
 // negative size counts as 0 (status bit 0), rows at or past M belong to no group (bit 1).

@@ -22,6 +22,8 @@ namespace w4a16 {
 //                          gradient lora_wgrad_kernel)
 //   lora_wgrad_kernel      the sort               (n - 1: lora_sum_kernel)
 //   wgrad_sum_kernel       the sort               (n - 1: lora_up_kernel)
+//   fp8_gemm_kernel        the weights, where the caller says that nothing on the stream
+//                          still writes them (else they are only brought to L2)
 // Every kernel waits at some point, in CTAs enough to end after the one before it.
 // cluster > 1: clusters of that many CTAs along x.
 template <typename... Params, typename... Args>
