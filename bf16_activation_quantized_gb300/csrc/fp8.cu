@@ -14,6 +14,7 @@
 #include "async.cuh"
 #include "common.cuh"
 #include "fp8.cuh"
+#include "groups.cuh"
 #include "internal.h"
 #include "launch.cuh"
 #include "w4a16.h"
@@ -210,7 +211,7 @@ w4a16_status fp8_product(const uint8_t *X, const float *x_scales, const uint8_t 
     if (M > 0 && (!X || !x_scales || !W || !w_scales || !Y)) return W4A16_ERR_INVALID_ARG;
     if (!aligned(X, 16) || !aligned(W, 16) || !aligned(x_scales, 4) || !aligned(w_scales, 4) || !aligned(Y, 2))
         return W4A16_ERR_INVALID_ARG;
-    if (M == 0) return from_cuda(cudaMemsetAsync(status, 0, sizeof *status, s));
+    if (M == 0) return from_cuda(launch_group_status(m_sizes, groups, status, s));
     int sms = 0;
     if (device_sm_count(&sms) != 0 || sms < 1) return W4A16_ERR_CUDA;
     const int n_blocks = (N + kFp8Block - 1) / kFp8Block, k_blocks = K / kFp8Block;

@@ -3,8 +3,12 @@
 #pragma once
 
 #include <cstdint>
+#include <cuda_runtime.h>
 
 namespace w4a16 {
+
+// The status word alone, for calls without rows.
+cudaError_t launch_group_status(const int32_t *m_sizes, int groups, int *status, cudaStream_t s);
 
 __device__ __forceinline__ int row_tiles(int rows, int bt) { return (rows + bt - 1) / bt; }
 

@@ -387,7 +387,7 @@ extern "C" w4a16_status w4a16_gemm_grouped_wgrad(const w4a16_bf16 *dY, const w4a
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (M_total == 0) {
         if (cudaMemsetAsync(dW, 0, size_t(num_groups) * N * K * dw_bytes, s) != cudaSuccess) return W4A16_ERR_CUDA;
-        return cudaMemsetAsync(status_dev, 0, sizeof *status_dev, s) == cudaSuccess ? W4A16_OK : W4A16_ERR_CUDA;
+        return launch_group_status(M_sizes_dev, num_groups, status_dev, s) == cudaSuccess ? W4A16_OK : W4A16_ERR_CUDA;
     }
     int sms = 0;
     if (device_sm_count(&sms) != 0 || sms < 1) return W4A16_ERR_CUDA;

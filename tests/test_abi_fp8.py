@@ -153,7 +153,8 @@ def test_register_shares_fit_the_launch(report):
     assert text.count("setmaxnreg") == 2
 
 
-@pytest.mark.parametrize("name,kernels", [("fp8.cu", 2), ("fp8_gemm.cu", 1), ("fp8_many.cu", 1), ("wgrad.cu", 1)])
+@pytest.mark.parametrize("name,kernels", [("fp8.cu", 2), ("fp8_gemm.cu", 1), ("fp8_many.cu", 1), ("wgrad.cu", 1),
+                                          ("groups.cu", 1)])
 def test_kernels_wait_before_they_let_the_next_one_start(name, kernels):
     text = source(name)
     starts = [m.start() for m in re.finditer(r"__global__", text)]

@@ -48,6 +48,21 @@ def test_most_groups(M, N, K, transposed):
         check(w4.gemm_fp8(x[rows], xs[:, rows].contiguous(), w[e], ws[e], transposed=transposed), want, bound)
 
 
+# without rows any row a size names is past the last
+@pytest.mark.parametrize("sizes,want", [([0, 0], 0), ([3, 0], 2), ([0, -1], 1), ([-4, 1], 3), ([0] * 1023 + [1], 2)])
+def test_status_without_rows(sizes, want):
+    E = len(sizes)
+    m = torch.tensor(sizes, dtype=torch.int32, device="cuda")
+    x, xs, w, ws = problem(gen(0), 0, 128, 128, False, E)
+    for transposed in (False, True):
+        status = torch.full((4,), 9, dtype=torch.int32, device="cuda")
+        assert w4.gemm_fp8_grouped(x, xs, w, ws, m, transposed=transposed, status=status)[0].shape == (0, 128)
+        assert int(status[0]) == want
+    empty = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda")
+    dw, status = w4.gemm_grouped_wgrad(empty, empty, m, out=torch.ones(E, 64, 64, device="cuda"))
+    assert not dw.any() and int(status[0]) == want
+
+
 @pytest.mark.parametrize("M", [1, 30, 150])
 def test_longest_sums(M):
     """2^20 summed columns, and 2^20 summed rows of the weights."""
