@@ -223,8 +223,7 @@ __device__ __forceinline__ uint32_t cluster_address(uint32_t a, int rank) {
 // Arrive on a barrier of a CTA of the cluster (`bar` from cluster_address).  Orders no
 // writes of this thread to memory for the other CTA (that takes a release at the
 // cluster's scope, a fence of about a microsecond): what it hands over is tensor memory
-// that has been read, or shared memory written before a proxy fence that only the tensor
-// core reads.
+// that has been read.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }

@@ -458,10 +458,11 @@ cudaError_t launch_trans(const Fp8Plan &p, const Fp8Args &a, const CUtensorMap &
 
 // The forms compared by their time in microseconds, as they measured on 152 SMs with the
 // weights in L2 (2560 x 9728, 8192 x 8192, 19456 x 2560, 4096 x 2048 and 1024 x 4096, 144 to
-// 4096 rows): 3.5 for the launch and the first and last tile; a block of 128 that is summed
-// over 0.30 (64 rows and fewer; with two CTAs on an SM 0.45, 32 rows and fewer 0.36), 0.365
-// (128 rows), 0.45 (128 rows, 256 columns), 0.41 (a pair's 256 and 256); 1.8 between tiles;
-// sums that CTAs share 1 and 0.3 for each (few rows) or 2 and 1.6 (many).  Groups fill half of their last tile.
+// 4096 rows), beside what all have in common: a block of 128 that is summed over 0.20 (32
+// rows and fewer; with two CTAs on an SM 0.28), 0.29 (64 rows; 0.46), 0.36 (128 rows), 0.46
+// (128 rows, 256 columns), 0.41 (a pair's 256 and 256); from a tile to the next 1.8 (few
+// rows) or 1.0 (many); sums that CTAs share 1 and 0.3 for each (few rows) or 2 and 1.6
+// (many).  Groups fill half of their last tile.
 Fp8Plan fp8_plan(int M, int out, int blocks, int groups, bool grouped, int sms) {
     const int used = !grouped ? 1 : groups < M ? groups : M;                // groups with rows at most
     const int rows = ceil_div(M, used);                                     // a group's, if they are even

@@ -14,7 +14,7 @@ __device__ __forceinline__ int row_tiles(int rows, int bt) { return (rows + bt -
 
 // Tile r of a grid of `rows` by `cols`, in bands of kBand rows, down a band's columns: the
 // tiles that run at the same time form a block and share both operands' tiles in L2.  (Row
-// by row, the weight gradient of 4096 x 8192 x 8192 takes 304 us instead of 284, the 8-bit
+// by row, the weight gradient of 4096 x 8192 x 8192 took 304 us instead of 284, the 8-bit
 // product of these sizes 193 instead of 187; bands of 4, 8 and 32 lie between.)
 constexpr int kBand = 16;
 __device__ __forceinline__ void banded(int r, int rows, int cols, int &row, int &col) {

@@ -7,21 +7,23 @@
 // transpose.  Two CTAs share a tile of 256 columns of each (cta_group::2): a CTA loads
 // 128 columns of dY and 128 of X and holds the sums of its 128 rows of dW.
 //
-// A group may end anywhere: the rows of a box past the last are the next group's, and
-// those that share an MMA's step of 16 with it are overwritten with zeros in shared
-// memory, on both sides of the product and in both CTAs.
+// A group may end anywhere.  Its last rows come in boxes of 16, 8, 4, 2 and 1 rows, and
+// what they leave of an MMA's step of 16 in boxes past the last row of all, which TMA fills
+// with zeros: 32 boxes at most, one a lane, counted with the others.  Rows of the next
+// group are never loaded.
 //
 // With few tiles and many rows `split` pairs (a cluster of 2 split CTAs) share a tile's
 // rows; the parts stand in shared memory and are added in the order of the pairs.
 //
-// What bounds it: the tensor cores, 284 us for 4096 rows of 8192 and 8192 columns (1.02 of
+// What bounds it: the tensor cores, 280 us for 4096 rows of 8192 and 8192 columns (1.04 of
 // the measured cuBLAS rate; without pairs 356); with few rows a group L2, which carries the
-// operands of every tile and the results: 4096 rows of 8 groups, 2048 x 4096 in fp32, 73 us
-// (results stored by TMA in boxes of 4 KB: 107; rows past the last cleared by the warp that
-// issues the MMAs: 97).
+// operands of every tile and the results: 4096 rows of 8 groups, 2048 x 4096 in fp32, 68 us
+// (results stored by TMA in boxes of 4 KB: 107 us where 73 were).  Six stages: with five 73.
+// Rows past a group's last cleared in shared memory instead take as long (70.8 us for
+// 69.7 with groups of 511), with a hand-over between the CTAs for each group's last boxes.
 //
 // Warps: 0 copies (TMA) the boxes, 1 issues the MMAs, 2 to 5 empty one of two
-// accumulators while the next tile is summed into the other, 6 clears rows past the last.
+// accumulators while the next tile is summed into the other.
 #include "async.cuh"
 #include "common.cuh"
 #include "groups.cuh"
@@ -39,9 +41,15 @@ namespace {
 constexpr int kRowStep = 64;                       // rows of a stage
 constexpr int kSide = 256, kHalf = 128;            // columns of dY and of X of a tile, of a CTA
 constexpr int kBox = kRowStep * 128;               // bytes of 64 rows x 64 columns
-constexpr int kWgStage = 4 * kBox, kWgStages = 5;
-constexpr int kWgThreads = 224, kWgStore0 = 2, kWgStoreWarps = 4;
+constexpr int kWgStage = 4 * kBox, kWgStages = 6;
+constexpr int kWgThreads = 192, kWgStore0 = 2, kWgStoreWarps = 4;
 constexpr int kStoreBox = 32 * 128;                // bytes of 32 rows of dW, 128 bytes of each
+
+constexpr int kTailBoxes = 5;                      // heights 16, 8, 4, 2, 1
+
+struct GroupWgradMaps {
+    CUtensorMap full[2], tail[2][kTailBoxes];      // dY, X
+};
 
 struct GroupWgradArgs {
     const int32_t *m_sizes;
@@ -51,7 +59,7 @@ struct GroupWgradArgs {
 };
 
 constexpr int kWgOffStore = kWgStages * kWgStage, kWgOffBar = kWgOffStore + kWgStoreWarps * kStoreBox;
-constexpr int kWgOffTab = kWgOffBar + (4 * kWgStages + 5) * 8 + 8;
+constexpr int kWgOffTab = kWgOffBar + (2 * kWgStages + 5) * 8 + 8;
 inline size_t wgrad_smem(int groups) { return kWgOffTab + (groups + 1) * sizeof(int) + 1024; }
 static_assert(kWgOffTab + (kMaxGroups + 1) * 4 + 1024 <= kTensorMaxSmem - 256, "shared memory");
 static_assert(kHalf * kSide * 4 <= kWgOffStore, "a tile's sums lie over the ring");
@@ -77,21 +85,31 @@ __device__ __forceinline__ WgTile wg_tile(const GroupWgradArgs &a, const int *ta
     return t;
 }
 
-// One warp: zeros in rows `rows` to the end of the last step of 16, in the stage's boxes.
-__device__ __forceinline__ void clear_rows(unsigned char *stage, int rows) {
-    const int lane = threadIdx.x % 32;
-    for (int r = rows + lane / 8; r < ((rows + 15) & ~15); r += 4)
-        #pragma unroll
-        for (int box = 0; box < 4; ++box)
-            *reinterpret_cast<uint4 *>(stage + box * kBox + r * 128 + lane % 8 * 16) = make_uint4(0, 0, 0, 0);
-    fence_proxy_async();
-    __syncwarp();
+// Piece i of the rows below the last full step, `rows` of them: its first row and the
+// height, 16 >> box; past the rows it is one of zeros.  False: there are no more.
+__device__ __forceinline__ bool tail_piece(int rows, int i, int &first, int &box, bool &zeros) {
+    first = 16 * i, box = 0, zeros = false;
+    if (i < rows / 16) return true;
+    const int rest = rows % 16;
+    if (rest == 0) return false;
+    i -= rows / 16;
+    const int mine = __popc(rest);
+    zeros = i >= mine;
+    if (zeros) i -= mine;
+    int bits = zeros ? 16 - rest : rest;               // a piece for each bit, the highest first
+    first = rows / 16 * 16 + (zeros ? rest : 0);
+    for (; i > 0 && bits; --i) {
+        const int high = 1 << (31 - __clz(bits));
+        first += high, bits -= high;
+    }
+    if (!bits) return false;
+    box = 4 - (31 - __clz(bits));
+    return true;
 }
 
 template <bool F32>
 __global__ void __launch_bounds__(kWgThreads, 1)
-grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmap_dy, const __grid_constant__ CUtensorMap tmap_x,
-                     const GroupWgradArgs a) {
+grouped_wgrad_kernel(const __grid_constant__ GroupWgradMaps maps, const GroupWgradArgs a) {
     extern __shared__ unsigned char s_raw[];
     unsigned char *smem = s_raw + (-smem_u32(s_raw) & 1023);
     __shared__ int s_abort;
@@ -99,24 +117,18 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmap_dy, const __grid_c
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int rank = cluster_rank(), split = cluster_size() / 2, half = rank & 1, part = rank / 2;
     const uint32_t ring = smem_u32(smem), full = ring + kWgOffBar, empty = full + 8 * kWgStages;
-    // full: both CTAs' boxes have landed (counted in the even one).  The last boxes of a part
-    // that ends inside a step: tail, this CTA's have landed; ready (in the even one), both
-    // CTAs' rows past the last are cleared.
-    const uint32_t tail = empty + 8 * kWgStages, ready = tail + 8 * kWgStages;
-    const uint32_t dfull = ready + 8 * kWgStages, dempty = dfull + 16, drained = dempty + 16;
+    // full: both CTAs' boxes have landed (counted in the even one)
+    const uint32_t dfull = empty + 8 * kWgStages, dempty = dfull + 16, drained = dempty + 16;
     int *tab_rows = reinterpret_cast<int *>(smem + kWgOffTab);
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kWgStages; ++i) {
-            mbar_init(full + 8 * i, 1), mbar_init(empty + 8 * i, 1);
-            mbar_init(tail + 8 * i, 1), mbar_init(ready + 8 * i, 2);
-        }
+        for (int i = 0; i < kWgStages; ++i) mbar_init(full + 8 * i, 1), mbar_init(empty + 8 * i, 1);
         for (int i = 0; i < 2; ++i) mbar_init(dfull + 8 * i, 1), mbar_init(dempty + 8 * i, 2 * kWgStoreWarps);
         mbar_init(drained, 1);
         s_abort = 0;
         fence_barrier_init();
     }
     if (warp == 1) tc_alloc_pair(smem_u32(&s_tmem), 2 * kSide);
-    if (warp == 0 && lane == 0) tma_prefetch_desc(&tmap_dy), tma_prefetch_desc(&tmap_x);
+    if (warp == 0 && lane == 0) tma_prefetch_desc(&maps.full[0]), tma_prefetch_desc(&maps.full[1]);
     pdl_wait();
     pdl_launch_dependents();
     if (warp == 0)
@@ -134,8 +146,9 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmap_dy, const __grid_c
     bool lost = false;
     if (warp == 0) {
         int i = 0;
-        uint32_t uses = 0, tails = 0;                    // parities of the slots' full and tail barriers
-        const uint32_t even = cluster_address(full, rank & ~1), own = cluster_address(tail, rank);
+        const uint32_t even = cluster_address(full, rank & ~1);
+        // a lane's box of a part's last rows: dY or X, 64 columns
+        const int side = lane / 2 % 2, c = lane % 2;
         for (int id = id0; id < tiles && !lost; id += step) {
             const WgTile t = wg_tile(a, tab_rows, id, part, split);
             for (int r = 0; r < t.rows; r += kRowStep, ++i) {
@@ -143,32 +156,36 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmap_dy, const __grid_c
                 const bool ok = i < kWgStages || mbar_wait(empty + 8 * s, (i / kWgStages - 1) & 1, abort_flag, a.err);
                 lost = !__all_sync(0xffffffffu, ok);
                 if (lost) break;
-                const bool last = (t.rows - r < kRowStep) && t.rows % 16;
-                if (!stalled(i) && elect_one()) {
-                    const uint32_t dst = ring + s * kWgStage, bar = (last ? own : even) + 8 * s;
-                    if (last) mbar_arrive_expect_tx(tail + 8 * s, kWgStage);
-                    else if (half == 0) mbar_arrive_expect_tx(full + 8 * s, 2 * kWgStage);
-                    #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        tma_load_2d_pair(dst + c * kBox, &tmap_dy, t.n0 + half * kHalf + 64 * c, t.row0 + r, bar);
-                        tma_load_2d_pair(dst + (2 + c) * kBox, &tmap_x, t.k0 + half * kHalf + 64 * c, t.row0 + r, bar);
+                const uint32_t dst = ring + s * kWgStage, bar = even + 8 * s;
+                const int y = t.row0 + r, rows = t.rows - r, n0 = t.n0 + half * kHalf, k0 = t.k0 + half * kHalf;
+                if (stalled(i)) continue;
+                if (rows >= kRowStep) {
+                    if (elect_one()) {
+                        if (half == 0) mbar_arrive_expect_tx(full + 8 * s, 2 * kWgStage);
+                        #pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            tma_load_2d_pair(dst + j * kBox, &maps.full[0], n0 + 64 * j, y, bar);
+                            tma_load_2d_pair(dst + (2 + j) * kBox, &maps.full[1], k0 + 64 * j, y, bar);
+                        }
                     }
+                } else {
+                    if (half == 0 && lane == 0) mbar_arrive_expect_tx(full + 8 * s, 2 * 4 * 128 * ((rows + 15) & ~15));
+                    __syncwarp();
+                    int first, box;
+                    bool zeros;
+                    if (tail_piece(rows, lane / 4, first, box, zeros))
+                        tma_load_2d_pair(dst + (2 * side + c) * kBox + first * 128, &maps.tail[side][box],
+                                         (side ? k0 : n0) + 64 * c, zeros ? a.M : y + first, bar);
                 }
                 __syncwarp();
-                if (last) tails ^= 1u << s;
-                else uses ^= 1u << s;
             }
         }
         // Every copy lands before the CTA ends (the pair's are counted in the even one).
-        if (*abort_flag)
-            for (int s = 0; s < kWgStages; ++s) {
-                if (half == 0) drain_wait(full + 8 * s, ~(uses >> s) & 1);
-                drain_wait(tail + 8 * s, ~(tails >> s) & 1);
-            }
+        if (*abort_flag && half == 0)
+            for (int u = i > kWgStages ? i - kWgStages : 0; u < i; ++u) drain_wait(full + 8 * (u % kWgStages), (u / kWgStages) & 1);
     } else if (warp == 1 && half == 0) {
         constexpr uint32_t idesc = tc_idesc_bf16(kSide, kSide) | kTcAMajorM | kTcBMajorN;
         int i = 0, n = 0;
-        uint32_t uses = 0, tails = 0;                    // parities of the slots' full and ready barriers
         for (int id = id0; id < tiles && !lost; id += step) {
             const WgTile t = wg_tile(a, tab_rows, id, part, split);
             if (t.rows == 0) continue;
@@ -178,13 +195,8 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmap_dy, const __grid_c
             if (lost) break;
             for (int r = 0; r < t.rows; r += kRowStep, ++i) {
                 const int s = i % kWgStages, rows = min(kRowStep, t.rows - r), steps = (rows + 15) / 16;
-                const bool last = rows % 16;
-                const bool ok = last ? mbar_wait(ready + 8 * s, (tails >> s) & 1, abort_flag, a.err)
-                                     : mbar_wait(full + 8 * s, (uses >> s) & 1, abort_flag, a.err);
-                lost = !__all_sync(0xffffffffu, ok);
+                lost = !__all_sync(0xffffffffu, mbar_wait(full + 8 * s, (i / kWgStages) & 1, abort_flag, a.err));
                 if (lost) break;
-                if (last) tails ^= 1u << s;
-                else uses ^= 1u << s;
                 tc_fence_after();
                 const uint32_t st = ring + s * kWgStage;
                 const uint64_t dn = tc_sdesc_sw128_mn(st, kBox), dk = tc_sdesc_sw128_mn(st + 2 * kBox, kBox);
@@ -205,23 +217,6 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmap_dy, const __grid_c
         if (elect_one()) tc_commit_pair(drained, both);
         __syncwarp();
         drain_wait(drained, 0);
-    } else if (warp == kWgStore0 + kWgStoreWarps) {
-        const uint32_t to = cluster_address(ready, rank & ~1);
-        int i = 0;
-        uint32_t tails = 0;
-        for (int id = id0; id < tiles && !lost; id += step) {
-            const WgTile t = wg_tile(a, tab_rows, id, part, split);
-            const int steps = (t.rows + kRowStep - 1) / kRowStep;
-            i += steps;
-            if (t.rows % 16 == 0) continue;
-            const int s = (i - 1) % kWgStages;
-            lost = !__all_sync(0xffffffffu, mbar_wait(tail + 8 * s, (tails >> s) & 1, abort_flag, a.err));
-            if (lost) break;
-            tails ^= 1u << s;
-            clear_rows(smem + s * kWgStage, t.rows - (steps - 1) * kRowStep);
-            if (lane == 0) mbar_arrive_cluster(to + 8 * s);
-            __syncwarp();
-        }
     } else if (warp >= kWgStore0) {
         // Lane l of a warp holds row 32 (warp % 4) + l of this CTA's half of the tile; 32 rows
         // and 128 bytes of each go through shared memory and leave as whole lines.
@@ -342,16 +337,18 @@ int ceil_div(long long x, long long y) { return int((x + y - 1) / y); }
 
 template <bool F32>
 cudaError_t launch_grouped_wgrad(const GroupWgradArgs &a, const uint16_t *dy, const uint16_t *x, int sms, cudaStream_t s) {
-    CUtensorMap ty, tx;
-    const cuuint32_t box[2] = {64, kRowStep};
-    const cuuint64_t ydim[2] = {cuuint64_t(a.N), cuuint64_t(a.M)}, ystride[1] = {2 * ydim[0]};
-    cudaError_t e = encode_tensor_map(&ty, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, dy, ydim, ystride, box,
-                                      CU_TENSOR_MAP_SWIZZLE_128B);
-    if (e != cudaSuccess) return e;
-    const cuuint64_t xdim[2] = {cuuint64_t(a.K), cuuint64_t(a.M)}, xstride[1] = {2 * xdim[0]};
-    e = encode_tensor_map(&tx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, x, xdim, xstride, box, CU_TENSOR_MAP_SWIZZLE_128B);
-    if (e != cudaSuccess) return e;
-    e = allow_smem<grouped_wgrad_kernel<F32>>(kTensorMaxSmem - 256);
+    GroupWgradMaps maps;
+    for (int side = 0; side < 2; ++side) {
+        const cuuint64_t dim[2] = {cuuint64_t(side ? a.K : a.N), cuuint64_t(a.M)}, stride[1] = {2 * dim[0]};
+        for (int i = 0; i <= kTailBoxes; ++i) {
+            const cuuint32_t box[2] = {64, cuuint32_t(i == kTailBoxes ? kRowStep : 16 >> i)};
+            const cudaError_t e = encode_tensor_map(i == kTailBoxes ? &maps.full[side] : &maps.tail[side][i],
+                                                    CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, side ? x : dy, dim, stride, box,
+                                                    CU_TENSOR_MAP_SWIZZLE_128B);
+            if (e != cudaSuccess) return e;
+        }
+    }
+    const cudaError_t e = allow_smem<grouped_wgrad_kernel<F32>>(kTensorMaxSmem - 256);
     if (e != cudaSuccess) return e;
     const long long tiles = (long long)a.groups * a.n_tiles * a.k_tiles;
     const int pairs = sms / 2;
@@ -361,7 +358,7 @@ cudaError_t launch_grouped_wgrad(const GroupWgradArgs &a, const uint16_t *dy, co
     while (split < 4 && tiles * split * 2 <= pairs && a.M / a.groups >= 8 * kRowStep * split) split *= 2;
     const int clusters = int(split > 1 || tiles < pairs ? tiles : pairs);
     return launch_chained(grouped_wgrad_kernel<F32>, dim3(clusters * 2 * split), kWgThreads, wgrad_smem(a.groups),
-                          2 * split, s, ty, tx, a);
+                          2 * split, s, maps, a);
 }
 
 }  // namespace

@@ -118,6 +118,27 @@ def test_gradients_past_32_bits():
         row += n
 
 
+# every number of rows below and past a step, each before rows that are not its own
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("down", [False, True])
+def test_every_end_of_a_group(dtype, down):
+    sizes, N, K = list(range(132)), 72, 264
+    if down:
+        sizes.reverse()
+    M = sum(sizes)
+    g = gen(6)
+    dy = torch.randn(M, N, device="cuda", generator=g).bfloat16()
+    x = torch.randn(M, K, device="cuda", generator=g).bfloat16()
+    dw, _ = w4.gemm_grouped_wgrad(dy, x, torch.tensor(sizes, dtype=torch.int32, device="cuda"), dtype=dtype)
+    row = 0
+    for e, n in enumerate(sizes):
+        a, b = dy[row:row + n].double(), x[row:row + n].double()
+        want = a.t() @ b
+        bound = n * 2.0 ** -23 * (a.abs().t() @ b.abs()) + (2.0 ** -8 * want.abs() if dtype == torch.bfloat16 else 0.0)
+        assert bool(((dw[e].double() - want).abs() <= bound).all()), n
+        row += n
+
+
 # pairs that share a tile's rows: groups without rows, with fewer steps than pairs, rows behind
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("sizes,M,N,K", [([5000, 0], 5000, 256, 512), ([3, 2100], 2103, 512, 264),
