@@ -15,15 +15,20 @@
 // With few tiles and many rows `split` pairs (a cluster of 2 split CTAs) share a tile's
 // rows; the parts stand in shared memory and are added in the order of the pairs.
 //
-// What bounds it: the tensor cores, 280 us for 4096 rows of 8192 and 8192 columns (1.04 of
+// The tensor core cuts its sums off instead of rounding them, so that those of many rows
+// drift: with 16384 rows in one sum the result's error is 4.4e-6 of it, with 65536 1.9e-5.  A
+// sum of 512 rows is therefore handed over and added in registers, in fp32: 4.8e-7 for both
+// (256 rows: 2.4e-7, and 4 to 8 % of the time; sums of 32 bits in order have 4 to 6e-7).
+//
+// What bounds it: the tensor cores, 283 us for 4096 rows of 8192 and 8192 columns (1.03 of
 // the measured cuBLAS rate; without pairs 356); with few rows a group L2, which carries the
-// operands of every tile and the results: 4096 rows of 8 groups, 2048 x 4096 in fp32, 68 us
+// operands of every tile and the results: 4096 rows of 8 groups, 2048 x 4096 in fp32, 69 us
 // (results stored by TMA in boxes of 4 KB: 107 us where 73 were).  Six stages: with five 73.
 // Rows past a group's last cleared in shared memory instead take as long (70.8 us for
 // 69.7 with groups of 511), with a hand-over between the CTAs for each group's last boxes.
 //
-// Warps: 0 copies (TMA) the boxes, 1 issues the MMAs, 2 to 5 empty one of two
-// accumulators while the next tile is summed into the other.
+// Warps: 0 copies (TMA) the boxes, 1 issues the MMAs, 4 to 11 empty one of two accumulators
+// while the next rows are summed into the other.
 #include "async.cuh"
 #include "common.cuh"
 #include "groups.cuh"
@@ -42,8 +47,13 @@ constexpr int kRowStep = 64;                       // rows of a stage
 constexpr int kSide = 256, kHalf = 128;            // columns of dY and of X of a tile, of a CTA
 constexpr int kBox = kRowStep * 128;               // bytes of 64 rows x 64 columns
 constexpr int kWgStage = 4 * kBox, kWgStages = 6;
-constexpr int kWgThreads = 192, kWgStore0 = 2, kWgStoreWarps = 4;
-constexpr int kStoreBox = 32 * 128;                // bytes of 32 rows of dW, 128 bytes of each
+constexpr int kWgThreads = 384, kAddWarp0 = 4, kAddWarps = 8;
+// Registers a thread of the first four warps and of the adding ones: the launch's
+// (168 x 384) are what the two shares draw on.
+constexpr int kRegsIn = 72, kRegsAdd = 216;
+static_assert(128 * kRegsIn + 256 * kRegsAdd <= 168 * kWgThreads, "registers");
+constexpr int kStoreBox = 16 * 128;                // bytes of 16 rows of dW, 128 bytes of each
+constexpr int kPart = 512;                         // rows that the tensor core sums before registers add
 
 constexpr int kTailBoxes = 5;                      // heights 16, 8, 4, 2, 1
 
@@ -58,7 +68,7 @@ struct GroupWgradArgs {
     int M, N, K, groups, n_tiles, k_tiles;
 };
 
-constexpr int kWgOffStore = kWgStages * kWgStage, kWgOffBar = kWgOffStore + kWgStoreWarps * kStoreBox;
+constexpr int kWgOffStore = kWgStages * kWgStage, kWgOffBar = kWgOffStore + kAddWarps * kStoreBox;
 constexpr int kWgOffTab = kWgOffBar + (2 * kWgStages + 5) * 8 + 8;
 inline size_t wgrad_smem(int groups) { return kWgOffTab + (groups + 1) * sizeof(int) + 1024; }
 static_assert(kWgOffTab + (kMaxGroups + 1) * 4 + 1024 <= kTensorMaxSmem - 256, "shared memory");
@@ -122,7 +132,7 @@ grouped_wgrad_kernel(const __grid_constant__ GroupWgradMaps maps, const GroupWgr
     int *tab_rows = reinterpret_cast<int *>(smem + kWgOffTab);
     if (threadIdx.x == 0) {
         for (int i = 0; i < kWgStages; ++i) mbar_init(full + 8 * i, 1), mbar_init(empty + 8 * i, 1);
-        for (int i = 0; i < 2; ++i) mbar_init(dfull + 8 * i, 1), mbar_init(dempty + 8 * i, 2 * kWgStoreWarps);
+        for (int i = 0; i < 2; ++i) mbar_init(dfull + 8 * i, 1), mbar_init(dempty + 8 * i, 2 * kAddWarps);
         mbar_init(drained, 1);
         s_abort = 0;
         fence_barrier_init();
@@ -144,152 +154,209 @@ grouped_wgrad_kernel(const __grid_constant__ GroupWgradMaps maps, const GroupWgr
     const int step = int(gridDim.x) / (2 * split);
     const uint16_t both = uint16_t(3u << (rank & ~1));
     bool lost = false;
-    if (warp == 0) {
-        int i = 0;
-        const uint32_t even = cluster_address(full, rank & ~1);
-        // a lane's box of a part's last rows: dY or X, 64 columns
-        const int side = lane / 2 % 2, c = lane % 2;
-        for (int id = id0; id < tiles && !lost; id += step) {
-            const WgTile t = wg_tile(a, tab_rows, id, part, split);
-            for (int r = 0; r < t.rows; r += kRowStep, ++i) {
-                const int s = i % kWgStages;
-                const bool ok = i < kWgStages || mbar_wait(empty + 8 * s, (i / kWgStages - 1) & 1, abort_flag, a.err);
-                lost = !__all_sync(0xffffffffu, ok);
-                if (lost) break;
-                const uint32_t dst = ring + s * kWgStage, bar = even + 8 * s;
-                const int y = t.row0 + r, rows = t.rows - r, n0 = t.n0 + half * kHalf, k0 = t.k0 + half * kHalf;
-                if (stalled(i)) continue;
-                if (rows >= kRowStep) {
-                    if (elect_one()) {
-                        if (half == 0) mbar_arrive_expect_tx(full + 8 * s, 2 * kWgStage);
-                        #pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            tma_load_2d_pair(dst + j * kBox, &maps.full[0], n0 + 64 * j, y, bar);
-                            tma_load_2d_pair(dst + (2 + j) * kBox, &maps.full[1], k0 + 64 * j, y, bar);
+    if (warp < kAddWarp0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIn));
+        if (warp == 0) {
+            int i = 0;
+            const uint32_t even = cluster_address(full, rank & ~1);
+            // a lane's box of a part's last rows: dY or X, 64 columns
+            const int side = lane / 2 % 2, c = lane % 2;
+            for (int id = id0; id < tiles && !lost; id += step) {
+                const WgTile t = wg_tile(a, tab_rows, id, part, split);
+                for (int r = 0; r < t.rows; r += kRowStep, ++i) {
+                    const int s = i % kWgStages;
+                    const bool ok = i < kWgStages || mbar_wait(empty + 8 * s, (i / kWgStages - 1) & 1, abort_flag, a.err);
+                    lost = !__all_sync(0xffffffffu, ok);
+                    if (lost) break;
+                    const uint32_t dst = ring + s * kWgStage, bar = even + 8 * s;
+                    const int y = t.row0 + r, rows = t.rows - r, n0 = t.n0 + half * kHalf, k0 = t.k0 + half * kHalf;
+                    if (stalled(i)) continue;
+                    if (rows >= kRowStep) {
+                        if (elect_one()) {
+                            if (half == 0) mbar_arrive_expect_tx(full + 8 * s, 2 * kWgStage);
+                            #pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                tma_load_2d_pair(dst + j * kBox, &maps.full[0], n0 + 64 * j, y, bar);
+                                tma_load_2d_pair(dst + (2 + j) * kBox, &maps.full[1], k0 + 64 * j, y, bar);
+                            }
                         }
+                    } else {
+                        if (half == 0 && lane == 0) mbar_arrive_expect_tx(full + 8 * s, 2 * 4 * 128 * ((rows + 15) & ~15));
+                        __syncwarp();
+                        int first, box;
+                        bool zeros;
+                        if (tail_piece(rows, lane / 4, first, box, zeros))
+                            tma_load_2d_pair(dst + (2 * side + c) * kBox + first * 128, &maps.tail[side][box],
+                                             (side ? k0 : n0) + 64 * c, zeros ? a.M : y + first, bar);
                     }
-                } else {
-                    if (half == 0 && lane == 0) mbar_arrive_expect_tx(full + 8 * s, 2 * 4 * 128 * ((rows + 15) & ~15));
                     __syncwarp();
-                    int first, box;
-                    bool zeros;
-                    if (tail_piece(rows, lane / 4, first, box, zeros))
-                        tma_load_2d_pair(dst + (2 * side + c) * kBox + first * 128, &maps.tail[side][box],
-                                         (side ? k0 : n0) + 64 * c, zeros ? a.M : y + first, bar);
                 }
-                __syncwarp();
             }
-        }
-        // Every copy lands before the CTA ends (the pair's are counted in the even one).
-        if (*abort_flag && half == 0)
-            for (int u = i > kWgStages ? i - kWgStages : 0; u < i; ++u) drain_wait(full + 8 * (u % kWgStages), (u / kWgStages) & 1);
-    } else if (warp == 1 && half == 0) {
-        constexpr uint32_t idesc = tc_idesc_bf16(kSide, kSide) | kTcAMajorM | kTcBMajorN;
-        int i = 0, n = 0;
-        for (int id = id0; id < tiles && !lost; id += step) {
-            const WgTile t = wg_tile(a, tab_rows, id, part, split);
-            if (t.rows == 0) continue;
-            const int d = n & 1;
-            const bool free = n < 2 || mbar_wait(dempty + 8 * d, (n / 2 - 1) & 1, abort_flag, a.err);
-            lost = !__all_sync(0xffffffffu, free);
-            if (lost) break;
-            for (int r = 0; r < t.rows; r += kRowStep, ++i) {
-                const int s = i % kWgStages, rows = min(kRowStep, t.rows - r), steps = (rows + 15) / 16;
-                lost = !__all_sync(0xffffffffu, mbar_wait(full + 8 * s, (i / kWgStages) & 1, abort_flag, a.err));
-                if (lost) break;
-                tc_fence_after();
-                const uint32_t st = ring + s * kWgStage;
-                const uint64_t dn = tc_sdesc_sw128_mn(st, kBox), dk = tc_sdesc_sw128_mn(st + 2 * kBox, kBox);
-                if (elect_one()) {
-                    #pragma unroll
-                    for (int e = 0; e < kRowStep / 16; ++e)
-                        if (e < steps)
-                            tc_mma_ss_pair(tmem + d * kSide, dn + 128 * e, dk + 128 * e, idesc, r > 0 || e > 0);
-                    tc_commit_pair(empty + 8 * s, both);
+            // Every copy lands before the CTA ends (the pair's are counted in the even one).
+            if (*abort_flag && half == 0)
+                for (int u = i > kWgStages ? i - kWgStages : 0; u < i; ++u) drain_wait(full + 8 * (u % kWgStages), (u / kWgStages) & 1);
+        } else if (warp == 1 && half == 0) {
+            constexpr uint32_t idesc = tc_idesc_bf16(kSide, kSide) | kTcAMajorM | kTcBMajorN;
+            int i = 0, n = 0;
+            for (int id = id0; id < tiles && !lost; id += step) {
+                const WgTile t = wg_tile(a, tab_rows, id, part, split);
+                for (int r = 0; r < t.rows; r += kRowStep, ++i) {
+                    const int s = i % kWgStages, d = n & 1, steps = (min(kRowStep, t.rows - r) + 15) / 16;
+                    bool ok = r % kPart || n < 2 || mbar_wait(dempty + 8 * d, (n / 2 - 1) & 1, abort_flag, a.err);
+                    ok = ok && mbar_wait(full + 8 * s, (i / kWgStages) & 1, abort_flag, a.err);
+                    lost = !__all_sync(0xffffffffu, ok);
+                    if (lost) break;
+                    tc_fence_after();
+                    const uint32_t st = ring + s * kWgStage;
+                    const uint64_t dn = tc_sdesc_sw128_mn(st, kBox), dk = tc_sdesc_sw128_mn(st + 2 * kBox, kBox);
+                    const bool ends = (r + kRowStep) % kPart == 0 || r + kRowStep >= t.rows;
+                    if (elect_one()) {
+                        #pragma unroll
+                        for (int e = 0; e < kRowStep / 16; ++e)
+                            if (e < steps)
+                                tc_mma_ss_pair(tmem + d * kSide, dn + 128 * e, dk + 128 * e, idesc, r % kPart > 0 || e > 0);
+                        tc_commit_pair(empty + 8 * s, both);
+                        if (ends) tc_commit_pair(dfull + 8 * d, both);
+                    }
+                    __syncwarp();
+                    n += ends;
                 }
-                __syncwarp();
             }
-            if (lost) break;
-            if (elect_one()) tc_commit_pair(dfull + 8 * d, both);
+            if (elect_one()) tc_commit_pair(drained, both);
             __syncwarp();
-            ++n;
+            drain_wait(drained, 0);
         }
-        if (elect_one()) tc_commit_pair(drained, both);
-        __syncwarp();
-        drain_wait(drained, 0);
-    } else if (warp >= kWgStore0) {
-        // Lane l of a warp holds row 32 (warp % 4) + l of this CTA's half of the tile; 32 rows
-        // and 128 bytes of each go through shared memory and leave as whole lines.
-        const int sub = warp % 4;
-        const uint32_t lanes = tmem + (uint32_t(32 * sub) << 16), done = cluster_address(dempty, rank & ~1);
-        unsigned char *buf = smem + kWgOffStore + (warp - kWgStore0) * kStoreBox;
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsAdd));
+        // Lane l of a warp holds row 32 (warp % 4) + l of this CTA's half of the tile, 128 of its
+        // columns; 16 rows and 128 bytes of each go through shared memory and leave as whole lines.
+        const int sub = warp % 4, side = (warp - kAddWarp0) / 4;
+        const uint32_t from = tmem + (uint32_t(32 * sub) << 16) + side * kHalf;
+        const uint32_t done = cluster_address(dempty, rank & ~1);
+        unsigned char *buf = smem + kWgOffStore + (warp - kAddWarp0) * kStoreBox;
         float *join = reinterpret_cast<float *>(smem) + (32 * sub + lane) * kSide;
-        constexpr int kCols = F32 ? 32 : 64;
         int n = 0;
         for (int id = id0; id < tiles; id += step) {
             const WgTile t = wg_tile(a, tab_rows, id, part, split);
-            const int d = n & 1, width = min(kSide, a.K - t.k0), row = t.n0 + half * kHalf + 32 * sub;
-            if (t.rows && !lost) {
-                lost = !__all_sync(0xffffffffu, mbar_wait(dfull + 8 * d, (n / 2) & 1, abort_flag, a.err));
-                tc_fence_after();
-            }
-            for (int c = 0; c < width; c += kCols) {
-                uint32_t v[kCols];
-                if (t.rows && !lost) {
+            constexpr int kCols = 32;
+            const int row = t.n0 + half * kHalf + 32 * sub, col0 = t.k0 + side * kHalf;
+            // 32 columns: fp32 in two halves of 16 rows and 128 bytes of each, bf16 in 32 rows and 64
+            // bytes; pieces of 16 bytes lie so that eight of them meet in no bank.
+            auto put = [&](const uint32_t *v, int c) {
+                if (F32) {
                     #pragma unroll
-                    for (int e = 0; e < kCols; e += 16) {
-                        uint32_t w[16];
-                        tc_ld_32x32b_x16(lanes + d * kSide + c + e, w);
-                        tc_wait_ld_of(w);
+                    for (int h = 0; h < 2; ++h) {
+                        if (lane / 16 == h)
+                            #pragma unroll
+                            for (int q = 0; q < 8; ++q)
+                                *reinterpret_cast<uint4 *>(buf + lane % 16 * 128 + ((q ^ (lane & 7)) << 4)) =
+                                    make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                        __syncwarp();
                         #pragma unroll
-                        for (int j = 0; j < 16; ++j) v[e + j] = w[j];
+                        for (int k = 0; k < 16; k += 4) {
+                            const int r = k + lane / 8, q = lane % 8, col = col0 + c + 4 * q, at = row + 16 * h + r;
+                            if (at < a.N && col < a.K)
+                                *reinterpret_cast<uint4 *>(static_cast<float *>(a.dw) + ((long long)t.group * a.N + at) * a.K + col) =
+                                    *reinterpret_cast<const uint4 *>(buf + r * 128 + ((q ^ (r & 7)) << 4));
+                        }
+                        __syncwarp();
                     }
                 } else {
                     #pragma unroll
-                    for (int j = 0; j < kCols; ++j) v[j] = lost ? 0x7fffffffu : 0u;
-                }
-                if (split > 1) {
-                    // over the ring, whose boxes this tile's last MMAs have read; pieces of 16 bytes
-                    // placed so that eight rows' meet in no bank
-                    #pragma unroll
-                    for (int q = 0; q < kCols / 4; ++q)
-                        *reinterpret_cast<uint4 *>(join + 4 * ((c / 4 + q) ^ (lane & 7))) =
-                            make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-                    __syncwarp();
-                    continue;
-                }
-                #pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    uint4 p;
-                    if (F32) {
-                        p = make_uint4(v[4 * q % kCols], v[(4 * q + 1) % kCols], v[(4 * q + 2) % kCols], v[(4 * q + 3) % kCols]);
-                    } else {
-                        uint32_t h[4];
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t p[4];
                         #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            h[j] = pack_bf16x2_rn(__uint_as_float(v[(8 * q + 2 * j) % kCols]),
-                                                  __uint_as_float(v[(8 * q + 2 * j + 1) % kCols]));
-                        p = make_uint4(h[0], h[1], h[2], h[3]);
+                            p[j] = pack_bf16x2_rn(__uint_as_float(v[8 * q + 2 * j]), __uint_as_float(v[8 * q + 2 * j + 1]));
+                        *reinterpret_cast<uint4 *>(buf + lane * 64 + ((q ^ (lane / 2 & 3)) << 4)) = make_uint4(p[0], p[1], p[2], p[3]);
                     }
-                    *reinterpret_cast<uint4 *>(buf + lane * 128 + ((q ^ (lane & 7)) << 4)) = p;
+                    __syncwarp();
+                    #pragma unroll
+                    for (int k = 0; k < 32; k += 8) {
+                        const int r = k + lane / 4, q = lane % 4, col = col0 + c + 8 * q, at = row + r;
+                        if (at < a.N && col < a.K)
+                            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.dw) + ((long long)t.group * a.N + at) * a.K + col) =
+                                *reinterpret_cast<const uint4 *>(buf + r * 64 + ((q ^ (r / 2 & 3)) << 4));
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
-                #pragma unroll
-                for (int k = 0; k < 32; k += 4) {
-                    const int r = k + lane / 8, q = lane % 8, col = t.k0 + c + q * (kCols / 8);
-                    if (row + r < a.N && col < a.K)
-                        *reinterpret_cast<uint4 *>(static_cast<char *>(a.dw) +
-                                                   (((long long)t.group * a.N + row + r) * a.K + col) * (F32 ? 4 : 2)) =
-                            *reinterpret_cast<const uint4 *>(buf + r * 128 + ((q ^ (r & 7)) << 4));
+            };
+            if (split == 1 && t.rows <= kPart) {
+                // The tensor core has the whole sum: it leaves as it is read (8 groups of 64 rows, 2048 x
+                // 4096 in fp32: 46.8 us, through the sums in registers 50.9).
+                const int d = n & 1;
+                if (t.rows && !lost) {
+                    lost = !__all_sync(0xffffffffu, mbar_wait(dfull + 8 * d, (n / 2) & 1, abort_flag, a.err));
+                    tc_fence_after();
                 }
-                __syncwarp();                            // tcgen05.ld takes the whole warp
+                #pragma unroll 1
+                for (int c = 0; c < kHalf && col0 + c < a.K; c += kCols) {
+                    uint32_t v[kCols];
+                    if (t.rows && !lost) {
+                        #pragma unroll
+                        for (int e = 0; e < kCols; e += 16) {
+                            uint32_t u[16];
+                            tc_ld_32x32b_x16(from + d * kSide + c + e, u);
+                            tc_wait_ld_of(u);
+                            #pragma unroll
+                            for (int j = 0; j < 16; ++j) v[e + j] = u[j];
+                        }
+                    } else {
+                        #pragma unroll
+                        for (int j = 0; j < kCols; ++j) v[j] = lost ? 0x7fffffffu : 0u;
+                    }
+                    put(v, c);
+                }
+                if (t.rows) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0 && !lost) mbar_arrive_cluster(done + 8 * d);
+                    ++n;
+                }
+                continue;
             }
-            if (split > 1) break;                        // a cluster has one tile
-            if (t.rows) {
+            float acc[kHalf];
+            #pragma unroll
+            for (int j = 0; j < kHalf; ++j) acc[j] = 0.f;
+            for (int r = 0; r < t.rows && !lost; r += kPart, ++n) {
+                const int d = n & 1;
+                lost = !__all_sync(0xffffffffu, mbar_wait(dfull + 8 * d, (n / 2) & 1, abort_flag, a.err));
+                if (lost) break;
+                tc_fence_after();
+                constexpr int kChunk = 16;
+                #pragma unroll
+                for (int c = 0; c < kHalf; c += kChunk) {
+                    uint32_t v[kChunk];
+                    tc_ld_32x32b_x16(from + d * kSide + c, v);
+                    tc_wait_ld_of(v);
+                    #pragma unroll
+                    for (int e = 0; e < kChunk; ++e) acc[c + e] += __uint_as_float(v[e]);
+                }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0 && !lost) mbar_arrive_cluster(done + 8 * d);
-                ++n;
+                if (lane == 0) mbar_arrive_cluster(done + 8 * d);
+            }
+            // A wait that ran out: this tile and the pair's later ones are NaN.
+            if (lost) {
+                #pragma unroll
+                for (int j = 0; j < kHalf; ++j) acc[j] = __int_as_float(0x7fffffff);
+            }
+            if (split > 1) {
+                // over the ring, whose boxes this tile's last MMAs have read; pieces of 16 bytes
+                // placed so that eight rows' meet in no bank; a cluster has one tile
+                #pragma unroll
+                for (int q = 0; q < kHalf / 4; ++q)
+                    *reinterpret_cast<float4 *>(join + 4 * ((side * (kHalf / 4) + q) ^ (lane & 7))) =
+                        make_float4(acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]);
+                break;
+            }
+            #pragma unroll
+            for (int c = 0; c < kHalf; c += kCols) {
+                if (col0 + c >= a.K) break;
+                uint32_t v[kCols];
+                #pragma unroll
+                for (int j = 0; j < kCols; ++j) v[j] = __float_as_uint(acc[c + j]);
+                put(v, c);
             }
         }
     }

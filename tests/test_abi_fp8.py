@@ -139,13 +139,15 @@ def test_no_spills(report, kernel):
         assert r["spill"] == 0, name
 
 
-def test_register_shares_fit_the_launch(report):
+@pytest.mark.parametrize("file,threads,kernel", [("fp8_many.cu", "kManyThreads", "fp8_many_kernel"),
+                                                 ("wgrad.cu", "kWgThreads", "grouped_wgrad_kernel")])
+def test_register_shares_fit_the_launch(report, file, threads, kernel):
     """setmaxnreg waits until the block's registers at launch cover what it asks for: a share
     above them would wait forever."""
-    text = source("fp8_many.cu")
-    threads = int(re.search(r"kManyThreads = (\d+)", text).group(1))
+    text = source(file)
+    threads = int(re.search(threads + r" = (\d+)", text).group(1))
     few, more = (int(v) for v in re.search(r"kRegsIn = (\d+), kRegsAdd = (\d+)", text).groups())
-    hits = {k: v["regs"] for k, v in report.items() if "fp8_many_kernel" in k}
+    hits = {k: v["regs"] for k, v in report.items() if kernel in k}
     assert hits
     for name, regs in hits.items():
         assert regs == 168, name

@@ -139,6 +139,20 @@ def test_every_end_of_a_group(dtype, down):
         row += n
 
 
+def test_long_sums_do_not_drift():
+    """The tensor core cuts off at 2^-23 of a sum, 2^-24 of it on average and all one way.  Over 512
+    rows (32 steps) whose sums are 512^1/2 in the end and 15 on average that is 32 x 15 x 2^-24, one
+    way in a part and any in the next: 64 parts come to 64^1/2 of it, 2.3e-4, 1.3e-6 of the
+    result's 32768^1/2.  Adding the parts rounds 64 times by 2^-25 of up to that: 2.4e-7."""
+    M = 32768
+    g = gen(8)
+    dy = torch.randn(M, 256, device="cuda", generator=g).bfloat16()
+    x = torch.randn(M, 256, device="cuda", generator=g).bfloat16()
+    dw, _ = w4.gemm_grouped_wgrad(dy, x, torch.tensor([M], dtype=torch.int32, device="cuda"))
+    want = dy.double().t() @ x.double()
+    assert float((dw[0].double() - want).norm() / want.norm()) <= 1.6e-6
+
+
 # pairs that share a tile's rows: groups without rows, with fewer steps than pairs, rows behind
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("sizes,M,N,K", [([5000, 0], 5000, 256, 512), ([3, 2100], 2103, 512, 264),
