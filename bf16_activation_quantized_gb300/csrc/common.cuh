@@ -122,7 +122,6 @@ __device__ __forceinline__ uint4 ldg_stream16(const void *p) {
     return r;
 }
 
-// Read-only 16-byte load cached in L1 (activations shared by a CTA's warps).
 // d = a * b + c for one m16n8k16 bf16 tile with fp32 accumulation.  Not
 // volatile: a pure function of its operands, so the compiler may schedule it
 // freely.
@@ -154,10 +153,11 @@ __device__ __forceinline__ void mma_16816_f16_acc(float (&c)[4], const uint32_t 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// Read-only 16-byte load cached in L1 (activations shared by a CTA's warps).  volatile: it stays behind pdl_wait.
 __device__ __forceinline__ uint4 ldg_nc16(const void *p) {
     uint4 r;
-    asm("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
-        : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+    asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
     return r;
 }
 

@@ -24,12 +24,14 @@ namespace w4a16 {
 namespace {
 
 // Eight bf16 as they lie in memory; element by element where rows start anywhere.
+// volatile: the load stays behind pdl_wait (the rows are what the stream's previous kernel
+// wrote, as a rule).
 __device__ __forceinline__ uint4 load8(const uint16_t *p, int left, bool vec) {
     uint4 v = make_uint4(0, 0, 0, 0);
     if (left <= 0) return v;
     if (vec) {
-        asm("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-            : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+        asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
         return v;
     }
     uint32_t w[4];

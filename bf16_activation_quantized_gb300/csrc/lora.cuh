@@ -89,13 +89,14 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // Eight bf16 from column p, `left` of them inside the row.  vec: the row
-// starts on 16 bytes and its width is a multiple of 8.
+// starts on 16 bytes and its width is a multiple of 8.  volatile: the load stays
+// behind pdl_wait.
 __device__ __forceinline__ uint4 load_cols8(const uint16_t *p, int left, int vec) {
     uint4 v = make_uint4(0, 0, 0, 0);
     if (vec) {
         if (left > 0)
-            asm("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+            asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
         return v;
     }
     uint32_t w[4];
