@@ -98,7 +98,8 @@ constexpr int kQuantThreads = 128, kQuantRows = kQuantThreads / 16;
 // A CTA takes 8 rows and J blocks of 128 columns, half a warp a row; the scales leave
 // through shared memory, since those of neighbouring rows stand together.  65536 x 4096:
 // 122 us, 0.98 of the measured copy bandwidth (16 rows, 4 blocks: 133 us; 2 blocks: 156).
-template <int J, bool VEC>
+// PAD: the last block of a row has columns past the width.
+template <int J, bool VEC, bool PAD>
 __global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(const uint16_t *x, uint8_t *codes,
                                                                       float *scales, int rows, int width,
                                                                       int blocks) {
@@ -127,6 +128,12 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(const uint
         const int j = i / kQuantRows, r = i % kQuantRows;
         if (block0 + j < blocks && row0 + r < rows)
             scales[(long long)(block0 + j) * rows + row0 + r] = s_scale[j][r];
+    }
+    // In a block that holds a NaN the columns past the width, 0 times NaN, become zeros again.
+    const int last = blocks - 1 - block0;
+    if (PAD && last < J && row < rows && s_scale[last][half] != s_scale[last][half]) {
+        const int left = width - (blocks - 1) * kFp8Block - 8 * piece;
+        for (int e = max(left, 0); e < 8; ++e) codes[(row * blocks + blocks - 1) * kFp8Block + 8 * piece + e] = 0;
     }
 }
 
@@ -180,14 +187,15 @@ cudaError_t launch_quantize_rows(const uint16_t *x, uint8_t *codes, float *scale
     const dim3 grid((rows + kQuantRows - 1) / kQuantRows);
     // Eight blocks a CTA once that leaves every SM several CTAs, else one for latency.
     constexpr int J = 8;
-    if ((long long)grid.x * blocks >= 8192) {
-        const dim3 g(grid.x, (blocks + J - 1) / J);
-        return vec ? launch_chained(quantize_rows_kernel<J, true>, g, kQuantThreads, 0, 1, s, x, codes, scales, rows, width, blocks)
-                   : launch_chained(quantize_rows_kernel<J, false>, g, kQuantThreads, 0, 1, s, x, codes, scales, rows, width, blocks);
-    }
-    const dim3 g(grid.x, blocks);
-    return vec ? launch_chained(quantize_rows_kernel<1, true>, g, kQuantThreads, 0, 1, s, x, codes, scales, rows, width, blocks)
-               : launch_chained(quantize_rows_kernel<1, false>, g, kQuantThreads, 0, 1, s, x, codes, scales, rows, width, blocks);
+    const bool many = (long long)grid.x * blocks >= 8192;
+    const dim3 g(grid.x, many ? (blocks + J - 1) / J : blocks);
+    const auto launch = [&](auto kernel) {
+        return launch_chained(kernel, g, kQuantThreads, 0, 1, s, x, codes, scales, rows, width, blocks);
+    };
+    if (width % kFp8Block == 0 && vec)
+        return many ? launch(quantize_rows_kernel<J, true, false>) : launch(quantize_rows_kernel<1, true, false>);
+    if (vec) return many ? launch(quantize_rows_kernel<J, true, true>) : launch(quantize_rows_kernel<1, true, true>);
+    return many ? launch(quantize_rows_kernel<J, false, true>) : launch(quantize_rows_kernel<1, false, true>);
 }
 
 cudaError_t launch_quantize_blocks(const uint16_t *w, uint8_t *codes, float *scales, int groups, int rows,

@@ -471,12 +471,12 @@ w4a16_status w4a16_lora_add_backward(const w4a16_bf16 *dY, const w4a16_bf16 *X, 
  * w4a16_quantize_fp8: rows of X.  Block b of a row holds columns 128 b .. 128 b + 127:
  *   scales[b][m] = max |x| / 448,   codes[m][c] = e4m3(448 x / max |x|),
  * the nearest code of the exact quotient, ties to even.  A block of zeros has scale 0
- * and codes 0; in one that holds a NaN all codes and the scale are NaN; an infinity
- * gives scale infinity and the code NaN, finite elements beside it 0.  (Below about
+ * and codes 0; in one that holds a NaN all its elements' codes and the scale are NaN; an
+ * infinity gives scale infinity and the code NaN, finite elements beside it 0.  (Below about
  * 2^-110 the scale is subnormal and holds fewer bits.)
  *  X:      device bf16 [rows][width], any width >= 1 (at most 2^20).
  *  codes:  device e4m3 [rows][Wp], Wp = width rounded up to a multiple of 128; the
- *          columns past width are written as zeros.
+ *          columns past width are written as zeros, whatever the block holds.
  *  scales: device fp32 [Wp / 128][rows]: the scales of a block of all rows stand
  *          together.
  * w4a16_quantize_fp8_blocks: num_groups weights [N][K] at once (K a multiple of 128):
@@ -496,7 +496,7 @@ w4a16_status w4a16_quantize_fp8_blocks(const w4a16_bf16 *W, uint8_t *codes, floa
  *                   with X the quantised gradient of the product's result, the
  *                   gradient of its rows, from the weights as they lie.
  * P_b is summed by the tensor core, the blocks in fp32 in a fixed order; Y is rounded
- * once.
+ * once. 
  *  X:        device e4m3 [M][C], C = K, transposed: N rounded up to a multiple of 128
  *            (the columns past N have to be finite: they meet zeros).
  *  x_scales: device fp32 [C / 128][M].
