@@ -740,7 +740,9 @@ def gemm_fp8(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scales:
     ``transposed=True`` multiplies by W instead, from the same weights: x is [M, N]
     (N rounded up to a multiple of 128, the columns past N finite), the result bf16
     [M, K]; with the quantised gradient of Y that is the gradient of X.  Sums over a
-    block of 128 are the tensor core's, over the blocks fp32; one rounding.
+    block of 128 are the tensor core's, over the blocks fp32; one rounding.  A row's scale
+    times a weight block's has to be a normal float32 or 0 because one of them is 0 (so it
+    is where blocks' largest magnitudes are 0 or between 2^-54 and 2^72).
     ``resident_weights`` as for gemm.  Not recorded for autograd."""
     dev, M, N, K, cols = _need_fp8(x, x_scales, w, w_scales, 2, transposed)
     if out is None:

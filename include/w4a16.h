@@ -496,7 +496,12 @@ w4a16_status w4a16_quantize_fp8_blocks(const w4a16_bf16 *W, uint8_t *codes, floa
  *                   with X the quantised gradient of the product's result, the
  *                   gradient of its rows, from the weights as they lie.
  * P_b is summed by the tensor core, the blocks in fp32 in a fixed order; Y is rounded
- * once. 
+ * once.  The product of the two scales is formed first, in fp32: it has to be a normal
+ * number (2^-126 or more, below 2^128) or 0 because a scale is.  A smaller one loses bits
+ * or becomes 0 although a block's sum may be 2^24 times larger, a larger one becomes
+ * infinite and NaN with a sum of 0.  Scales from w4a16_quantize_fp8 are in that range where
+ * every block's largest magnitude is 0 or between 2^-54 and 2^72.  Infinite and NaN scales
+ * make their rows (columns) infinite or NaN.
  *  X:        device e4m3 [M][C], C = K, transposed: N rounded up to a multiple of 128
  *            (the columns past N have to be finite: they meet zeros).
  *  x_scales: device fp32 [C / 128][M].
