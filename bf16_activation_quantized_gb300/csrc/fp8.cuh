@@ -5,9 +5,9 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
-namespace w4a16 {
+#include "split_plan.h"
 
-constexpr int kFp8Block = 128;       // elements of a row per scale; weights: 128 x 128
+namespace w4a16 {
 
 // Both kernels multiply a row's scale by the weights' first, one product a row and block.
 // Where fp32 does not hold it (below 2^-126, from 2^128 on) a term that it would hold is
@@ -29,15 +29,6 @@ struct Fp8Args {
     int vec;                 // rows of y start on 16 bytes and hold a multiple of 8 columns
     int resident;            // the weights may be read before the stream's previous kernel has ended
 };
-
-// How a product is cut.  size 16 to 128: the kernel for few rows, of that template size,
-// with bt rows of x per tile; 0: the kernel for many rows, with pairs of CTAs or without.
-// split: CTAs of a cluster, which share a tile's sum or are a pair.  ctas: launched.
-struct Fp8Plan {
-    int size, bt, split, ctas, occupancy;
-    bool pair;
-};
-Fp8Plan fp8_plan(int M, int out, int blocks, int groups, bool grouped, int sms);
 
 cudaError_t launch_fp8_gemm(const Fp8Plan &p, Fp8Args a, const uint8_t *x, const uint8_t *w, int N, int K,
                             bool trans, cudaStream_t s);

@@ -35,6 +35,7 @@
 #include "internal.h"
 #include "launch.cuh"
 #include "lora.cuh"
+#include "split_plan.h"
 #include "stall.cuh"
 #include "tc05.cuh"
 #include "w4a16.h"
@@ -400,7 +401,6 @@ grouped_wgrad_kernel(const __grid_constant__ GroupWgradMaps maps, const GroupWgr
 }
 
 bool aligned(const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
-int ceil_div(long long x, long long y) { return int((x + y - 1) / y); }
 
 template <bool F32>
 cudaError_t launch_grouped_wgrad(const GroupWgradArgs &a, const uint16_t *dy, const uint16_t *x, int sms, cudaStream_t s) {
@@ -419,10 +419,7 @@ cudaError_t launch_grouped_wgrad(const GroupWgradArgs &a, const uint16_t *dy, co
     if (e != cudaSuccess) return e;
     const long long tiles = (long long)a.groups * a.n_tiles * a.k_tiles;
     const int pairs = sms / 2;
-    // Pairs that share a tile: as long as all find a place and a part holds a few stages of a
-    // group's rows, if the groups are even.
-    int split = 1;
-    while (split < 4 && tiles * split * 2 <= pairs && a.M / a.groups >= 8 * kRowStep * split) split *= 2;
+    const int split = wgrad_split(tiles, pairs, a.M, a.groups, kRowStep);
     const int clusters = int(split > 1 || tiles < pairs ? tiles : pairs);
     return launch_chained(grouped_wgrad_kernel<F32>, dim3(clusters * 2 * split), kWgThreads, wgrad_smem(a.groups),
                           2 * split, s, maps, a);
