@@ -16,11 +16,14 @@
 // A tile's rounded sums go through shared memory to two warps that store them while the
 // next tile's blocks are added; the last tile's are stored by the adding warps too.
 //
-// What bounds it: the adding warps.  A block's MMAs take 512 cycles, its loads from tensor
-// memory and FMAs 360 by themselves, 570 with the handshakes over two buffers (tensor
-// memory holds no third), 740 in the kernel.  Sixteen adding warps, packed FMAs and MMAs of
-// 128 columns were slower (279, 320 and 278 us where this had 238, 273 and 238).  4096 x
-// 8192 x 8192: 187 us, 2.9 PFLOP/s (without pairs 236); 2858 x 19456 x 2560: 111 us.
+// What bounds it: a block takes 740 cycles in the kernel, where its MMAs take 512 and its loads
+// from tensor memory and FMAs 360 by themselves, 570 with the handshakes over two buffers
+// (tensor memory holds no third).  wgrad.cu brings as much to an SM, 32 KB, for MMAs as long (64
+// bytes a clock would be needed to hide it) and takes 0.32 us a stage where this kernel takes 0.42, a
+// tile's end included in both: the loads set three quarters of a block's time, the cause of
+// the last is not known.  Sixteen adding warps, packed FMAs and MMAs of 128
+// columns were slower (279, 320 and 278 us where this had 238, 273 and 238).  4096 x 8192 x
+// 8192: 187 us, 2.9 PFLOP/s (without pairs 236); 2858 x 19456 x 2560: 113 us.
 //
 // Warps: 0 copies (TMA) the tiles, 1 issues the MMAs, 2 and 3 store, 4 to 11 add.
 #include "async.cuh"

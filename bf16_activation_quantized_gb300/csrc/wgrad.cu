@@ -21,9 +21,11 @@
 // (256 rows: 2.4e-7, and 4 to 8 % of the time; sums of 32 bits in order have 4 to 6e-7).
 //
 // What bounds it: the tensor cores, 283 us for 4096 rows of 8192 and 8192 columns (1.03 of
-// the measured cuBLAS rate; without pairs 356); with few rows a group L2, which carries the
-// operands of every tile and the results: 4096 rows of 8 groups, 2048 x 4096 in fp32, 69 us
-// (results stored by TMA in boxes of 4 KB: 107 us where 73 were).  Six stages: with five 73.
+// the measured cuBLAS rate; without pairs 356).  8 groups of 512 rows, 2048 x 4096 in fp32: 63
+// us, where the results alone take 47 (groups of 64 rows) and the MMAs alone 36: the two
+// overlap in part only.  4096 rows in uneven groups: 69 to 74 (tiles are dealt out by number,
+// whatever their rows).  (Results stored by TMA in boxes of 4 KB: 107 us where 73 were.)
+// Six stages: with five 73.
 // Rows past a group's last cleared in shared memory instead take as long (70.8 us for
 // 69.7 with groups of 511), with a hand-over between the CTAs for each group's last boxes.
 //
